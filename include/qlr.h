@@ -76,7 +76,10 @@ typedef enum {
   QLR_OP_LINEAR_DBA = 3,
   QLR_OP_QUANTIZE_OUTLIERS = 4, /* M = the outlier count k, N = rows, K = cols */
   QLR_OP_LINEAR_OUTLIERS = 5,
-  QLR_OP_LINEAR_WHA = 6 /* r is ignored */
+  QLR_OP_LINEAR_WHA = 6, /* r is ignored */
+  QLR_OP_LINEAR_I8 = 7,
+  QLR_OP_LINEAR_GROUPED = 8,    /* these two: qlr_grouped_workspace_bytes */
+  QLR_OP_LINEAR_GROUPED_BWD = 9
 } qlr_op;
 
 /*
@@ -154,6 +157,20 @@ typedef struct {
    * forward skip work it would otherwise do to find this out on the device. */
   int64_t max_group_nnz;
 } qlr_sparse;
+
+/*
+ * Rows held in 8-bit integers with one scale per row (tokens, or the output
+ * channels of a weight): row i stands for scale[i] * q[i][:].
+ */
+typedef struct {
+  int64_t rows;
+  int64_t cols;
+  int8_t* q;    /* device, rows x cols */
+  float* scale; /* device, rows */
+} qlr_i8rows;
+
+/* Most experts of a grouped call. */
+#define QLR_MAX_EXPERTS 4096
 
 /* Library version (major*10000 + minor*100 + patch). */
 int qlr_version(void);
@@ -424,6 +441,107 @@ qlr_status qlr_linear_bwd(const void* dy, qlr_dtype dydt, const void* x, qlr_dty
                           const qlr_qweight* w, const void* A, const void* B, qlr_dtype abdt, int32_t r,
                           float scale, void* dx, qlr_dtype dxdt, float* dA, float* dB, void* ws,
                           size_t ws_bytes, void* stream);
+
+/*
+ * Quantize rows to 8-bit integers.  X (device) rows x cols in dt (f32, f16 or
+ * bf16, widened exactly to float32); out (host struct with its two device
+ * buffers; out->rows and out->cols must equal rows and cols) gets, per row, the
+ * scale s = fl32(max|x| / 127) and q = the integer nearest x / s, ties to
+ * even, within [-127, 127] (decided exactly; s == 0 gives q = 0).  A row that
+ * holds a NaN or an Inf gets a NaN scale and q = 0, so that every product with
+ * it is NaN.  rows may be 0 (nothing is launched).  Asynchronous, no workspace.
+ * Errors: QLR_ERR_NULL, QLR_ERR_SHAPE, QLR_ERR_DTYPE, QLR_ERR_ALIGN,
+ * QLR_ERR_HIP.
+ */
+qlr_status qlr_quantize_i8(const void* X, qlr_dtype dt, int64_t rows, int64_t cols, qlr_i8rows* out,
+                           void* stream);
+
+/*
+ * Forward of a frozen base held in 8-bit integers (w: N x K, one scale per
+ * output channel), multiplied in integers, with the unmerged adapter:
+ *     y[m][n] = (sum_k xq[m][k] wq[n][k]) sx[m] sw[n] + scale (x A^T) B^T
+ * xq, sx the tokens as qlr_quantize_i8 holds them: given by the caller (xq,
+ * M x K, so that several linears of one x share it) or, with xq NULL, made by
+ * the call from x.  x (device) M x K in xdt (f32 or bf16) is read for the
+ * quantization and for the adapter, which multiplies the unquantized x; it may
+ * be NULL (and xdt is ignored) when xq is given and r == 0.  A, B bf16 as in
+ * qlr_linear_fwd (abdt must be QLR_BF16 when r > 0); y (device) M x N in ydt
+ * (f32 or bf16).  K % 16 == 0 and K <= 131072 (the integer sums stay below
+ * 2^31); N M as in qlr_linear_fwd, M may be 0.  Integer sums are exact; each
+ * result takes three float32 roundings (within 2e-7 of it, plus half a bf16
+ * ulp for a bf16 y; intermediate results beyond float32's range overflow),
+ * and the adapter term 1e-4 of the sum of its terms' absolute values.
+ * qlr_force_path: QLR_PATH_GEMV (M <= 16) and QLR_PATH_GEMM select the decode
+ * and the tiled kernel (the same values without an adapter); QLR_PATH_F32 is refused.  ws
+ * (device) >= qlr_workspace_bytes(QLR_OP_LINEAR_I8, M, N, K, r).
+ * Asynchronous, allocation-free.
+ * Errors: QLR_ERR_NULL, QLR_ERR_SHAPE, QLR_ERR_DTYPE, QLR_ERR_ALIGN,
+ * QLR_ERR_WORKSPACE, QLR_ERR_PATH, QLR_ERR_HIP.
+ */
+qlr_status qlr_linear_fwd_i8(const void* x, qlr_dtype xdt, int64_t M, const qlr_i8rows* xq, const qlr_i8rows* w,
+                             const void* A, const void* B, qlr_dtype abdt, int32_t r, float scale, void* y,
+                             qlr_dtype ydt, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Device workspace of the two grouped calls (op QLR_OP_LINEAR_GROUPED or
+ * QLR_OP_LINEAR_GROUPED_BWD) for T rows, a stacked weight of rows x cols, its
+ * number of experts and the adapters' rank: the float32 adapter products (T x r
+ * each), and for the backward B transposed and float32 partials of the adapter
+ * gradients.  0 when T or r is 0.  Contents need no initialisation.  Host only.
+ * Errors: QLR_ERR_NULL, QLR_ERR_SHAPE.
+ */
+qlr_status qlr_grouped_workspace_bytes(qlr_op op, int64_t T, int64_t rows, int64_t cols, int32_t experts,
+                                       int32_t r, size_t* bytes);
+
+/*
+ * Forward of an expert layer's linear: T rows sorted by expert, one frozen
+ * quantized weight W'_e and one adapter A_e, B_e per expert,
+ *     y[i] = x[i] W'_e^T + scale (x[i] A_e^T) B_e^T    for offsets[e] <= i < offsets[e + 1].
+ * w holds the experts' weights stacked by rows (quantized as one matrix:
+ * w->rows = experts * N, a multiple of experts; cols % 64 == 0).  offsets
+ * (device) are experts + 1 int32, nondecreasing, in [0, T]; they are read on the
+ * device when the call runs, so a router's results need not reach the host and
+ * a captured call follows them.  Experts may be empty.  Rows before offsets[0]
+ * and from offsets[experts] on belong to no expert: they are not read and their
+ * y is left as it was.  (Offsets outside [0, T] or decreasing are clamped:
+ * nothing outside the buffers is touched, the rows concerned get wrong values.)
+ * x (device) T x cols bf16; A (device) experts x r x cols and B (device) experts
+ * x N x r bf16, both NULL when r == 0; y (device) T x N in ydt (f32 or bf16).
+ * 1 <= experts <= QLR_MAX_EXPERTS, T <= 2^30, T may be 0.  Error bound per
+ * element as QLR_PATH_GEMM of qlr_linear_fwd: 5e-3 * S + 1e-5 (the weight enters
+ * rounded to bf16; sums are float32), plus half a bf16 ulp for a bf16 y.
+ * qlr_force_path: QLR_PATH_GEMM runs every expert on the tiled kernel (by
+ * default experts of few rows run on a kernel of their own); the others are
+ * refused.  ws (device) >= qlr_grouped_workspace_bytes(QLR_OP_LINEAR_GROUPED, ...).
+ * Asynchronous, allocation-free; results do not depend on timing.
+ * Errors: QLR_ERR_NULL, QLR_ERR_SHAPE, QLR_ERR_DTYPE, QLR_ERR_BITS,
+ * QLR_ERR_BLOCK, QLR_ERR_ALIGN, QLR_ERR_FORMAT, QLR_ERR_WORKSPACE,
+ * QLR_ERR_ALIAS (y overlaps an input), QLR_ERR_PATH, QLR_ERR_HIP.
+ */
+qlr_status qlr_linear_fwd_grouped(const void* x, qlr_dtype xdt, int64_t T, const qlr_qweight* w, int32_t experts,
+                                  const int32_t* offsets, const void* A, const void* B, qlr_dtype abdt, int32_t r,
+                                  float scale, void* y, qlr_dtype ydt, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward of qlr_linear_fwd_grouped for an upstream gradient dy (T x N bf16),
+ * with u = dy B_e and t = x A_e^T over each expert's rows:
+ *     dx = dy W'_e + scale * u A_e      (T x cols, f32 or bf16; NULL: skipped)
+ *     dA_e = scale * u_e^T x_e          (experts x r x cols float32)
+ *     dB_e = scale * dy_e^T t_e         (experts x N x r float32)
+ * dA and dB are overwritten (zero for an expert without rows) and required
+ * when r > 0; x is not read when r == 0 and may be NULL.  Rows of no expert are
+ * not read and their dx is left as it was.  N % 8 == 0.  Everything else as in
+ * the forward.  Per element dx is within 5e-3 * S + 1e-5 (plus half a bf16 ulp
+ * for a bf16 dx), dA and dB within 1e-4 * S + 1e-6 of the exact value, S the
+ * sum of the absolute values of the terms that define it.  No output may
+ * overlap an input or another output (QLR_ERR_ALIAS).  ws (device) >=
+ * qlr_grouped_workspace_bytes(QLR_OP_LINEAR_GROUPED_BWD, ...).  Asynchronous,
+ * allocation-free; results do not depend on timing.  Errors: as the forward.
+ */
+qlr_status qlr_linear_bwd_grouped(const void* dy, qlr_dtype dydt, const void* x, qlr_dtype xdt, int64_t T,
+                                  const qlr_qweight* w, int32_t experts, const int32_t* offsets, const void* A,
+                                  const void* B, qlr_dtype abdt, int32_t r, float scale, void* dx, qlr_dtype dxdt,
+                                  float* dA, float* dB, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Force the kernel family used by qlr_linear_fwd and qlr_linear_fwd_mixed on

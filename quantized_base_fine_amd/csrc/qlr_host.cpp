@@ -160,6 +160,39 @@ DbaLayout dba_layout(int64_t M, int64_t N, int64_t K, int R, int ell, int xdt) {
   return L;
 }
 
+// Workspace of an 8-bit-integer call: the adapter product's partials, then the
+// tokens' int8 values and scales (unused when the caller gives them).
+struct I8Layout {
+  size_t t, q, sx, total;
+};
+I8Layout i8_layout(int64_t M, int64_t K, int32_t r) {
+  auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
+  I8Layout L;
+  L.t = 0;
+  L.q = linear_ws_bytes(M, K, r);
+  L.sx = L.q + up((size_t)M * (size_t)K);
+  L.total = L.sx + up((size_t)M * 4);
+  return L;
+}
+
+// Workspace of the grouped calls: t = x A^T, and for the backward u = dy B, B
+// transposed per expert and the partials of the adapter gradients.
+struct GroupedLayout {
+  size_t t, u, bt, part, total;
+};
+GroupedLayout grouped_layout(bool bwd, int64_t T, int64_t rows, int64_t K, int32_t experts, int32_t r) {
+  GroupedLayout L{0, 0, 0, 0, 0};
+  if (r <= 0 || T <= 0) return L;
+  auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
+  const size_t tr = up((size_t)T * (size_t)r * sizeof(float));
+  L.u = L.total = tr;
+  if (!bwd) return L;
+  L.bt = L.u + tr;
+  L.part = L.bt + up((size_t)rows * (size_t)r * 2);
+  L.total = L.part + up(qlr::grouped_grad_floats(T, rows / experts, K, r, experts) * sizeof(float));
+  return L;
+}
+
 // choose the kernel family for a linear call
 // The Walsh-Hadamard branch is merged into the weight on the prefill GEMM when
 // the bf16 copy fits the dense-weight GEMM's 32-bit offsets.
@@ -266,6 +299,59 @@ qlr_status run_linear(const LinearCheck& c, float scale, char* ws, qlr_path path
   }
   if (e != hipSuccess) return hip_fail(e, "linear launch");
   return QLR_OK;
+}
+
+typedef std::pair<uintptr_t, uintptr_t> Span;
+Span span_of(const void* p, size_t n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, a + n};
+}
+bool overlaps(const Span& p, const Span& q) { return p.first < q.second && q.first < p.second; }
+
+qlr_status check_i8rows(const qlr_i8rows* q, const char* what) {
+  if (!q->q || !q->scale) return fail(QLR_ERR_NULL, "%s: a buffer is NULL", what);
+  if (!aligned16(q->q) || !aligned16(q->scale)) return fail(QLR_ERR_ALIGN, "%s: buffers must be 16-byte aligned", what);
+  return QLR_OK;
+}
+
+// The checks that the two grouped calls share.
+qlr_status check_grouped(int64_t T, const qlr_qweight* w, int32_t experts, const int32_t* offsets, int32_t r,
+                         qlr_dtype xdt, qlr_dtype abdt, qlr_dtype odt) {
+  qlr_status st = check_qweight(w);
+  if (st != QLR_OK) return st;
+  if (T < 0 || T > (INT64_C(1) << 30)) return fail(QLR_ERR_SHAPE, "T %lld not in [0, 2^30]", (long long)T);
+  if (r < 0 || r > (1 << 20)) return fail(QLR_ERR_SHAPE, "r %d not in [0, 2^20]", r);
+  if (experts < 1 || experts > QLR_MAX_EXPERTS)
+    return fail(QLR_ERR_SHAPE, "experts %d not in [1, %d]", experts, QLR_MAX_EXPERTS);
+  if (w->rows == 0 || w->cols == 0) return fail(QLR_ERR_SHAPE, "empty weight");
+  if (w->rows % experts != 0)
+    return fail(QLR_ERR_SHAPE, "rows %lld is not a multiple of experts %d", (long long)w->rows, experts);
+  if (w->cols % QLR_BLOCK != 0) return fail(QLR_ERR_SHAPE, "cols %lld is not a multiple of 64", (long long)w->cols);
+  if (w->cols > (1 << 20) || w->rows / experts > (1 << 20))
+    return fail(QLR_ERR_SHAPE, "an expert's weight is larger than 2^20 x 2^20");
+  if (xdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "x (dy) must be bf16");
+  if (r > 0 && abdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "the adapters must be bf16");
+  if (!(odt == QLR_F32 || odt == QLR_BF16)) return fail(QLR_ERR_DTYPE, "y (dx) dtype must be f32 or bf16");
+  if (!offsets) return fail(QLR_ERR_NULL, "offsets is NULL");
+  if ((reinterpret_cast<uintptr_t>(offsets) & 3u) != 0) return fail(QLR_ERR_ALIGN, "offsets must be 4-byte aligned");
+  return QLR_OK;
+}
+
+qlr::TileArgs grouped_args(int64_t T, const qlr_qweight* w, int32_t experts, const int32_t* offsets, int32_t r, float scale) {
+  qlr::TileArgs a{};
+  a.M = T;
+  a.offsets = offsets;
+  a.experts = experts;
+  a.N = w->rows / experts;
+  a.K = w->cols;
+  a.bits = w->bits;
+  a.w = reinterpret_cast<const uint8_t*>(w->codes);
+  a.q8 = w->absmax_q8;
+  a.cst = w->absmax_c;
+  a.t_splits = 1;
+  a.r = r;
+  a.scale = scale;
+  return a;
 }
 
 qlr_status quantize_common(const void* W, qlr_dtype wdt, int64_t rows, int64_t cols, int32_t bits,
@@ -421,6 +507,11 @@ qlr_status qlr_workspace_bytes(qlr_op op, int64_t M, int64_t N, int64_t K, int32
     const size_t splits = M > 0 ? (size_t)qlr::dba_t_splits(M, K, qlr::DT_BF16, r, 1) : 1;
     auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
     *bytes = up(splits * (size_t)M * (size_t)lr2 * 4) + up((size_t)N * (size_t)lr2 * 2);
+    return QLR_OK;
+  }
+  if (op == QLR_OP_LINEAR_I8) {
+    if (M < 0 || N < 0 || K < 0 || r < 0) return fail(QLR_ERR_SHAPE, "negative size");
+    *bytes = i8_layout(M, K, r).total;
     return QLR_OK;
   }
   if (op != QLR_OP_LINEAR && op != QLR_OP_LINEAR_BWD) return fail(QLR_ERR_SHAPE, "unknown op %d", (int)op);
@@ -973,6 +1064,245 @@ qlr_status qlr_linear_fwd_wha(const void* x, qlr_dtype xdt, int64_t M, const qlr
     addend = C;
   }
   return run_linear(c, 0.0f, nullptr, path, s, addend);
+}
+
+qlr_status qlr_quantize_i8(const void* X, qlr_dtype dt, int64_t rows, int64_t cols, qlr_i8rows* out, void* stream) {
+  if (!out) return fail(QLR_ERR_NULL, "out is NULL");
+  if (!dtype_ok(dt)) return fail(QLR_ERR_DTYPE, "X dtype must be f32, f16 or bf16");
+  if (rows < 0 || cols <= 0) return fail(QLR_ERR_SHAPE, "rows must not be negative, cols must be positive");
+  if (rows > (INT64_C(1) << 40) / cols) return fail(QLR_ERR_SHAPE, "X too large");
+  if (out->rows != rows || out->cols != cols) return fail(QLR_ERR_SHAPE, "out header does not match rows/cols");
+  if (rows == 0) return QLR_OK;
+  if (!X) return fail(QLR_ERR_NULL, "X is NULL");
+  const qlr_status st = check_i8rows(out, "out");
+  if (st != QLR_OK) return st;
+  if (!aligned16(X)) return fail(QLR_ERR_ALIGN, "X must be 16-byte aligned");
+  const hipError_t e = qlr::launch_quantize_i8(X, (int)dt, rows, cols, out->q, out->scale, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "row quantization launch");
+  return QLR_OK;
+}
+
+qlr_status qlr_linear_fwd_i8(const void* x, qlr_dtype xdt, int64_t M, const qlr_i8rows* xq, const qlr_i8rows* w,
+                             const void* A, const void* B, qlr_dtype abdt, int32_t r, float scale, void* y,
+                             qlr_dtype ydt, void* ws, size_t ws_bytes, void* stream) {
+  if (!w) return fail(QLR_ERR_NULL, "w is NULL");
+  if (M < 0 || M > (INT64_C(1) << 30)) return fail(QLR_ERR_SHAPE, "M %lld not in [0, 2^30]", (long long)M);
+  if (r < 0) return fail(QLR_ERR_SHAPE, "r < 0");
+  const int64_t N = w->rows, K = w->cols;
+  if (N <= 0 || K <= 0) return fail(QLR_ERR_SHAPE, "empty weight");
+  if (N > (INT64_C(1) << 30)) return fail(QLR_ERR_SHAPE, "rows %lld above 2^30", (long long)N);
+  if (K % 16 != 0 || K > 131072)
+    return fail(QLR_ERR_SHAPE, "cols %lld must be a multiple of 16 and at most 131072", (long long)K);
+  qlr_status st = check_i8rows(w, "w");
+  if (st != QLR_OK) return st;
+  const bool need_x = !xq || r > 0;
+  if (need_x && !(xdt == QLR_F32 || xdt == QLR_BF16)) return fail(QLR_ERR_DTYPE, "x dtype must be f32 or bf16");
+  if (!(ydt == QLR_F32 || ydt == QLR_BF16)) return fail(QLR_ERR_DTYPE, "y dtype must be f32 or bf16");
+  if (r > 0 && abdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "the adapter must be bf16");
+  if (xq && (xq->rows != M || xq->cols != K)) return fail(QLR_ERR_SHAPE, "xq does not match M and w");
+  if (M > 0) {
+    if ((need_x && !x) || !y) return fail(QLR_ERR_NULL, "x or y is NULL");
+    if ((need_x && !aligned16(x)) || !aligned16(y)) return fail(QLR_ERR_ALIGN, "x and y must be 16-byte aligned");
+    if (xq && (st = check_i8rows(xq, "xq")) != QLR_OK) return st;
+  }
+  if (r > 0) {
+    if (!A || !B) return fail(QLR_ERR_NULL, "A or B is NULL with r > 0");
+    if (!aligned16(A) || !aligned16(B)) return fail(QLR_ERR_ALIGN, "A and B must be 16-byte aligned");
+  }
+  const I8Layout lay = i8_layout(M, K, r);
+  if (lay.total > 0 && (!ws || ws_bytes < lay.total))
+    return fail(QLR_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", lay.total, ws ? ws_bytes : (size_t)0);
+  if (lay.total > 0 && !aligned16(ws)) return fail(QLR_ERR_ALIGN, "workspace must be 16-byte aligned");
+  qlr_path path = t_path;
+  if (path == QLR_PATH_AUTO) path = M <= 16 ? QLR_PATH_GEMV : QLR_PATH_GEMM;
+  if (path == QLR_PATH_F32) return fail(QLR_ERR_PATH, "the 8-bit-integer product has no float32 family");
+  if (path == QLR_PATH_GEMV && M > 16) return fail(QLR_ERR_PATH, "the GEMV path takes M <= 16");
+  if (M == 0) return QLR_OK;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  char* wsp = reinterpret_cast<char*>(ws);
+  hipError_t e;
+  qlr::TileArgs a{};
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.w = reinterpret_cast<const uint8_t*>(w->q);
+  a.sw = w->scale;
+  a.r = r;
+  a.scale = scale;
+  a.ab = reinterpret_cast<const uint16_t*>(B);
+  a.y = y;
+  a.ydt = (int)ydt;
+  if (xq) {
+    a.x = xq->q;
+    a.sx = xq->scale;
+  } else {
+    int8_t* q = reinterpret_cast<int8_t*>(wsp + lay.q);
+    float* sx = reinterpret_cast<float*>(wsp + lay.sx);
+    e = qlr::launch_quantize_i8(x, (int)xdt, M, K, q, sx, s);
+    if (e != hipSuccess) return hip_fail(e, "token quantization launch");
+    a.x = q;
+    a.sx = sx;
+  }
+  if (r > 0) {
+    a.t = reinterpret_cast<const float*>(wsp + lay.t);
+    a.t_splits = qlr::lora_t_splits(M, K, r, (int)xdt, (int)abdt);
+    e = qlr::launch_lora_t(x, (int)xdt, M, K, A, (int)abdt, r, reinterpret_cast<float*>(wsp + lay.t), a.t_splits, s);
+    if (e != hipSuccess) return hip_fail(e, "adapter product launch");
+  }
+  e = path == QLR_PATH_GEMV ? qlr::launch_i8_few(a, s) : qlr::launch_i8_gemm(a, s);
+  if (e != hipSuccess) return hip_fail(e, "8-bit-integer linear launch");
+  return QLR_OK;
+}
+
+qlr_status qlr_grouped_workspace_bytes(qlr_op op, int64_t T, int64_t rows, int64_t cols, int32_t experts, int32_t r,
+                                       size_t* bytes) {
+  if (!bytes) return fail(QLR_ERR_NULL, "bytes is NULL");
+  if (op != QLR_OP_LINEAR_GROUPED && op != QLR_OP_LINEAR_GROUPED_BWD)
+    return fail(QLR_ERR_SHAPE, "op %d is not a grouped call", (int)op);
+  if (T < 0 || rows < 0 || cols < 0 || r < 0) return fail(QLR_ERR_SHAPE, "negative size");
+  if (experts < 1 || rows % experts != 0) return fail(QLR_ERR_SHAPE, "rows is not a multiple of experts");
+  *bytes = grouped_layout(op == QLR_OP_LINEAR_GROUPED_BWD, T, rows, cols, experts, r).total;
+  return QLR_OK;
+}
+
+qlr_status qlr_linear_fwd_grouped(const void* x, qlr_dtype xdt, int64_t T, const qlr_qweight* w, int32_t experts,
+                                  const int32_t* offsets, const void* A, const void* B, qlr_dtype abdt, int32_t r,
+                                  float scale, void* y, qlr_dtype ydt, void* ws, size_t ws_bytes, void* stream) {
+  qlr_status st = check_grouped(T, w, experts, offsets, r, xdt, abdt, ydt);
+  if (st != QLR_OK) return st;
+  const int64_t N = w->rows / experts, K = w->cols;
+  if (T > 0) {
+    if (!x || !y) return fail(QLR_ERR_NULL, "x or y is NULL");
+    if (!aligned16(x) || !aligned16(y)) return fail(QLR_ERR_ALIGN, "x and y must be 16-byte aligned");
+  }
+  if (r > 0) {
+    if (!A || !B) return fail(QLR_ERR_NULL, "A or B is NULL with r > 0");
+    if (!aligned16(A) || !aligned16(B)) return fail(QLR_ERR_ALIGN, "A and B must be 16-byte aligned");
+  }
+  if (T > 0) {
+    const Span out = span_of(y, (size_t)(T * N) * dtype_size(ydt));
+    std::vector<Span> ins = {span_of(x, (size_t)(T * K) * 2), span_of(offsets, ((size_t)experts + 1) * 4)};
+    if (r > 0) {
+      ins.push_back(span_of(A, (size_t)experts * (size_t)r * (size_t)K * 2));
+      ins.push_back(span_of(B, (size_t)w->rows * (size_t)r * 2));
+    }
+    for (const Span& in : ins)
+      if (overlaps(out, in)) return fail(QLR_ERR_ALIAS, "y overlaps an input");
+  }
+  const GroupedLayout lay = grouped_layout(false, T, w->rows, K, experts, r);
+  if (lay.total > 0 && (!ws || ws_bytes < lay.total))
+    return fail(QLR_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", lay.total, ws ? ws_bytes : (size_t)0);
+  if (lay.total > 0 && !aligned16(ws)) return fail(QLR_ERR_ALIGN, "workspace must be 16-byte aligned");
+  if (t_path != QLR_PATH_AUTO && t_path != QLR_PATH_GEMM)
+    return fail(QLR_ERR_PATH, "the grouped products have no float32 or single-row family");
+  if (T == 0) return QLR_OK;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  hipError_t e;
+  qlr::TileArgs a = grouped_args(T, w, experts, offsets, r, scale);
+  a.x = x;
+  a.ab = reinterpret_cast<const uint16_t*>(B);
+  a.y = y;
+  a.ydt = (int)ydt;
+  if (r > 0) {
+    float* t = reinterpret_cast<float*>(ws);
+    e = qlr::launch_grouped_t(reinterpret_cast<const uint16_t*>(x), T, K, reinterpret_cast<const uint16_t*>(A), r, offsets,
+                              experts, t, s);
+    if (e != hipSuccess) return hip_fail(e, "adapter product launch");
+    a.t = t;
+  }
+  const qlr::Levels lv = levels_arg(w->bits);
+  // experts of few rows on their own kernel; neither is launched where no expert
+  // can be its (or, by the mean, hardly one will)
+  const bool few = t_path == QLR_PATH_AUTO && T < (int64_t)experts * 64;
+  if (few) {
+    e = qlr::launch_grouped_few(a, lv, s);
+    if (e != hipSuccess) return hip_fail(e, "few-rows expert launch");
+  }
+  if (!few || T > qlr::kFewRows) {
+    a.min_rows = few ? qlr::kFewRows : 0;
+    e = qlr::launch_grouped_gemm(a, lv, s);
+    if (e != hipSuccess) return hip_fail(e, "expert product launch");
+  }
+  return QLR_OK;
+}
+
+qlr_status qlr_linear_bwd_grouped(const void* dy, qlr_dtype dydt, const void* x, qlr_dtype xdt, int64_t T,
+                                  const qlr_qweight* w, int32_t experts, const int32_t* offsets, const void* A,
+                                  const void* B, qlr_dtype abdt, int32_t r, float scale, void* dx, qlr_dtype dxdt,
+                                  float* dA, float* dB, void* ws, size_t ws_bytes, void* stream) {
+  qlr_status st = check_grouped(T, w, experts, offsets, r, dydt, abdt, dx ? dxdt : QLR_F32);
+  if (st != QLR_OK) return st;
+  const int64_t N = w->rows / experts, K = w->cols;
+  if (N % 8 != 0) return fail(QLR_ERR_SHAPE, "an expert's %lld rows are not a multiple of 8", (long long)N);
+  if (r > 0) {
+    if (xdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "x must be bf16");
+    if (!A || !B || !dA || !dB) return fail(QLR_ERR_NULL, "A, B, dA or dB is NULL with r > 0");
+    if (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB))
+      return fail(QLR_ERR_ALIGN, "A, B, dA and dB must be 16-byte aligned");
+  }
+  if (T > 0) {
+    if (!dy) return fail(QLR_ERR_NULL, "dy is NULL");
+    if (r > 0 && !x) return fail(QLR_ERR_NULL, "x is NULL with r > 0");
+    if (!aligned16(dy) || (dx && !aligned16(dx)) || (r > 0 && !aligned16(x)))
+      return fail(QLR_ERR_ALIGN, "dy, x and dx must be 16-byte aligned");
+  }
+  {
+    std::vector<Span> outs, ins = {span_of(offsets, ((size_t)experts + 1) * 4)};
+    const size_t ab = (size_t)experts * (size_t)r * (size_t)K, bb = (size_t)w->rows * (size_t)r;
+    if (T > 0 && dx) outs.push_back(span_of(dx, (size_t)(T * K) * dtype_size(dxdt)));
+    if (r > 0) {
+      outs.push_back(span_of(dA, ab * 4));
+      outs.push_back(span_of(dB, bb * 4));
+      ins.push_back(span_of(A, ab * 2));
+      ins.push_back(span_of(B, bb * 2));
+      if (T > 0) ins.push_back(span_of(x, (size_t)(T * K) * 2));
+    }
+    if (T > 0) ins.push_back(span_of(dy, (size_t)(T * N) * 2));
+    for (size_t i = 0; i < outs.size(); ++i) {
+      for (size_t j = i + 1; j < outs.size(); ++j)
+        if (overlaps(outs[i], outs[j])) return fail(QLR_ERR_ALIAS, "two outputs overlap");
+      for (const Span& in : ins)
+        if (overlaps(outs[i], in)) return fail(QLR_ERR_ALIAS, "an output overlaps an input");
+    }
+  }
+  const GroupedLayout lay = grouped_layout(true, T, w->rows, K, experts, r);
+  if (lay.total > 0 && (!ws || ws_bytes < lay.total))
+    return fail(QLR_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", lay.total, ws ? ws_bytes : (size_t)0);
+  if (lay.total > 0 && !aligned16(ws)) return fail(QLR_ERR_ALIGN, "workspace must be 16-byte aligned");
+  if (t_path != QLR_PATH_AUTO && t_path != QLR_PATH_GEMM)
+    return fail(QLR_ERR_PATH, "the grouped products have no float32 or single-row family");
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  char* wsp = reinterpret_cast<char*>(ws);
+  float* t = reinterpret_cast<float*>(wsp + lay.t);
+  float* u = reinterpret_cast<float*>(wsp + lay.u);
+  uint16_t* bt = reinterpret_cast<uint16_t*>(wsp + lay.bt);
+  const uint16_t* dyp = reinterpret_cast<const uint16_t*>(dy);
+  const uint16_t* xp = reinterpret_cast<const uint16_t*>(x);
+  hipError_t e;
+  if (r > 0 && T > 0) {
+    e = qlr::launch_grouped_transpose(reinterpret_cast<const uint16_t*>(B), experts, N, r, bt, s);
+    if (e != hipSuccess) return hip_fail(e, "adapter transpose launch");
+    e = qlr::launch_grouped_t(dyp, T, N, bt, r, offsets, experts, u, s);
+    if (e != hipSuccess) return hip_fail(e, "adapter product (dy B) launch");
+    e = qlr::launch_grouped_t(xp, T, K, reinterpret_cast<const uint16_t*>(A), r, offsets, experts, t, s);
+    if (e != hipSuccess) return hip_fail(e, "adapter product (x A^T) launch");
+  }
+  if (dx && T > 0) {
+    qlr::TileArgs a = grouped_args(T, w, experts, offsets, r, scale);
+    a.x = dy;
+    a.t = u;
+    a.ab = reinterpret_cast<const uint16_t*>(A);
+    a.y = dx;
+    a.ydt = (int)dxdt;
+    e = qlr::launch_grouped_dx(a, levels_arg(w->bits), s);
+    if (e != hipSuccess) return hip_fail(e, "input-gradient launch");
+  }
+  if (r > 0) {
+    e = qlr::launch_grouped_grads(u, t, xp, dyp, T, N, K, r, offsets, experts, scale, dA, dB,
+                                  reinterpret_cast<float*>(wsp + lay.part), s);
+    if (e != hipSuccess) return hip_fail(e, "adapter-gradient launch");
+  }
+  return QLR_OK;
 }
 
 qlr_status qlr_force_path(qlr_path path) {

@@ -1,0 +1,220 @@
+// The linear layer in 8-bit integers: y = (sum_k xq wq) sx[m] sw[n] with one
+// scale per token and one per output channel, plus the unmerged adapter branch
+// of the frozen base (LoRDBA page, "adapter mode").
+//
+// Row quantization (tokens and weight channels alike): s = fl32(max|x| / 127),
+// q = the integer nearest x / s, ties to even, in [-127, 127].
+#include "qlr_tile.h"
+
+namespace qlr {
+
+namespace {
+
+// ---------------------------------------------------------------- row quantization
+//
+// One workgroup per row.  Pieces of 8 elements stay in registers between the
+// maximum and the rounding (kQPieces per thread: rows up to 16384 elements);
+// longer rows read the rest again, from cache.  The quotient is decided
+// exactly: q0 = rint(x * fl(1/s)) is within one of x / s, the residual
+// x - q0 s is exact in float32 (a multiple of s's last place, below s), and
+// comparing twice the residual with s settles the nearest integer and ties.
+constexpr int kQPieces = 8;
+
+__device__ __forceinline__ int quantize_exact(float w, float s, float inv) {
+  const float q0 = __builtin_rintf(inv > 0.0f ? w * inv : w / s);
+  const float d = fmaf(-q0, s, w);
+  const float d2 = 2.0f * fabsf(d);
+  int q = (int)q0;
+  if (d2 > s || (d2 == s && (q & 1))) q += d > 0.0f ? 1 : -1;
+  return min(max(q, -127), 127);
+}
+
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+  if constexpr (DT == DT_F32) {
+    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(p) + i);
+    const f32x4_t b = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(p) + i + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = a[e];
+      v[4 + e] = b[e];
+    }
+  } else {
+    const u32x4_t a = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t w = a[e];
+      if constexpr (DT == DT_BF16) {
+        v[2 * e] = __uint_as_float(w << 16);
+        v[2 * e + 1] = __uint_as_float(w & 0xFFFF0000u);
+      } else {
+        v[2 * e] = f16_bits_to_f32((uint16_t)w);
+        v[2 * e + 1] = f16_bits_to_f32((uint16_t)(w >> 16));
+      }
+    }
+  }
+}
+
+// VEC: cols % 8 == 0 (16-byte loads, 8-byte stores); otherwise element by element.
+template <int DT, bool VEC>
+__global__ __launch_bounds__(256) void k_quantize_i8(const void* __restrict__ X, int64_t cols, int8_t* __restrict__ q,
+                                                     float* __restrict__ scale) {
+  __shared__ uint32_t red[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t row = blockIdx.x, base = row * cols;
+  // |x| as bits: ordered like the magnitudes, Inf and NaN above every finite value
+  uint32_t am = 0;
+  float v[kQPieces][8];
+  if constexpr (VEC) {
+#pragma unroll
+    for (int p = 0; p < kQPieces; ++p) {
+      const int64_t c = 8 * ((int64_t)p * 256 + tid);
+      if (c < cols) {
+        load8<DT>(X, base + c, v[p]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) am = max(am, __float_as_uint(fabsf(v[p][e])));
+      }
+    }
+    for (int64_t c = 8 * ((int64_t)kQPieces * 256 + tid); c < cols; c += 8 * 256) {
+      float w[8];
+      load8<DT>(X, base + c, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) am = max(am, __float_as_uint(fabsf(w[e])));
+    }
+  } else {
+    for (int64_t c = tid; c < cols; c += 256) am = max(am, __float_as_uint(fabsf(load_elem<DT>(X, base + c))));
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) am = max(am, (uint32_t)__shfl_xor((int)am, off, 64));
+  if (lane == 0) red[wave] = am;
+  __syncthreads();
+  am = max(max(red[0], red[1]), max(red[2], red[3]));
+  const bool finite = am < 0x7F800000u;
+  const float s = finite ? __uint_as_float(am) / 127.0f : __uint_as_float(0x7FC00000u);
+  if (tid == 0) scale[row] = s;
+  const bool live = finite && s > 0.0f;
+  // below 2^-125 the reciprocal could overflow: divide instead
+  const float inv = s >= 2.350988701644575e-38f ? 1.0f / s : 0.0f;
+  auto q1 = [&](float w) { return live ? quantize_exact(w, s, inv) : 0; };
+  auto put8 = [&](int64_t c, const float (&w)[8]) {
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      lo |= ((uint32_t)q1(w[e]) & 255u) << (8 * e);
+      hi |= ((uint32_t)q1(w[4 + e]) & 255u) << (8 * e);
+    }
+    *reinterpret_cast<uint2*>(q + base + c) = uint2{lo, hi};
+  };
+  if constexpr (VEC) {
+#pragma unroll
+    for (int p = 0; p < kQPieces; ++p) {
+      const int64_t c = 8 * ((int64_t)p * 256 + tid);
+      if (c < cols) put8(c, v[p]);
+    }
+    for (int64_t c = 8 * ((int64_t)kQPieces * 256 + tid); c < cols; c += 8 * 256) {
+      float w[8];
+      load8<DT>(X, base + c, w);
+      put8(c, w);
+    }
+  } else {
+    for (int64_t c = tid; c < cols; c += 256) q[base + c] = (int8_t)q1(load_elem<DT>(X, base + c));
+  }
+}
+
+template <int DT>
+hipError_t launch_quantize_dt(const void* X, int64_t rows, int64_t cols, int8_t* q, float* scale, hipStream_t s) {
+  for (int64_t r0 = 0; r0 < rows; r0 += 1 << 30) {  // the grid's x dimension holds 2^31 - 1 workgroups
+    const int64_t n = std::min<int64_t>(rows - r0, 1 << 30);
+    const char* x0 = reinterpret_cast<const char*>(X) + r0 * cols * (DT == DT_F32 ? 4 : 2);
+    if (cols % 8 == 0)
+      hipLaunchKernelGGL((k_quantize_i8<DT, true>), dim3((unsigned)n), dim3(256), 0, s, x0, cols, q + r0 * cols, scale + r0);
+    else
+      hipLaunchKernelGGL((k_quantize_i8<DT, false>), dim3((unsigned)n), dim3(256), 0, s, x0, cols, q + r0 * cols, scale + r0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// ---------------------------------------------------------------- M <= 16
+//
+// The weight's stream: a workgroup of 8 waves takes 16 weight rows, wave w the
+// 64-element steps [w n / 8, (w + 1) n / 8) of them, multiplied on 16x16x64
+// int8 MFMA (weight rows as A, the tokens as B; token lanes past M hold zeros).
+// The waves' integer sums are added through LDS; the adapter's t B^T is added
+// in float32 before the store.
+constexpr int kFewWaves = 8, kFewBatch = 8;
+
+template <int YDT>
+__global__ __launch_bounds__(512) void k_i8_few(TileArgs P) {
+  __shared__ int red[kFewWaves][256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n0 = blockIdx.x * 16;
+  const int M = (int)P.M;
+  const int64_t K = P.K, N = P.N;
+  const int row = lane & 15, g = lane >> 4;
+  const int8_t* wp = reinterpret_cast<const int8_t*>(P.w) + std::min<int64_t>(n0 + row, N - 1) * K + 16 * g;
+  const int8_t* xp = reinterpret_cast<const int8_t*>(P.x) + (int64_t)std::min(row, M - 1) * K + 16 * g;
+  const int nst = (int)((K + 63) / 64);
+  const int s0 = (int)((int64_t)nst * wave / kFewWaves), s1 = (int)((int64_t)nst * (wave + 1) / kFewWaves);
+  const i32x4_t zero = {0, 0, 0, 0};
+  i32x4_t acc = zero;
+  for (int b = s0; b < s1; b += kFewBatch) {
+    i32x4_t wv[kFewBatch], xv[kFewBatch];
+#pragma unroll
+    for (int i = 0; i < kFewBatch; ++i) {
+      const int64_t k = (int64_t)(b + i) * 64;
+      const bool ok = b + i < s1 && k + 16 * g < K;
+      wv[i] = ok ? *reinterpret_cast<const i32x4_t*>(wp + k) : zero;
+      xv[i] = ok && row < M ? *reinterpret_cast<const i32x4_t*>(xp + k) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < kFewBatch; ++i) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[i], xv[i], acc, 0, 0, 0);
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) red[wave][(lane & 15) * 16 + 4 * g + v] = acc[v];  // [token][row]
+  __syncthreads();
+  if (tid >= 256) return;
+  const int m = tid >> 4, n = n0 + (tid & 15);
+  if (m >= M || n >= N) return;
+  int sum = 0;
+#pragma unroll
+  for (int w = 0; w < kFewWaves; ++w) sum += red[w][tid];
+  float y = (float)sum * P.sx[m] * P.sw[n];
+  if (P.r > 0) {
+    float lo = 0.0f;
+    for (int j = 0; j < P.r; ++j) {
+      float tj = 0.0f;
+      for (int sp = 0; sp < P.t_splits; ++sp) tj += P.t[((int64_t)sp * M + m) * P.r + j];
+      lo = fmaf(tj, bf16_bits_to_f32(P.ab[(int64_t)n * P.r + j]), lo);
+    }
+    y = fmaf(P.scale, lo, y);
+  }
+  if constexpr (YDT == DT_F32) reinterpret_cast<float*>(P.y)[m * N + n] = y;
+  else reinterpret_cast<uint16_t*>(P.y)[m * N + n] = (uint16_t)f32_to_bf16_bits(y);
+}
+
+}  // namespace
+
+hipError_t launch_quantize_i8(const void* X, int dt, int64_t rows, int64_t cols, int8_t* q, float* scale, hipStream_t s) {
+  switch (dt) {
+    case DT_F32: return launch_quantize_dt<DT_F32>(X, rows, cols, q, scale, s);
+    case DT_F16: return launch_quantize_dt<DT_F16>(X, rows, cols, q, scale, s);
+    default: return launch_quantize_dt<DT_BF16>(X, rows, cols, q, scale, s);
+  }
+}
+
+hipError_t launch_i8_few(const TileArgs& a, hipStream_t s) {
+  if (a.M < 1 || a.M > 16 || a.K % 16 != 0) return hipErrorInvalidValue;
+  const unsigned grid = (unsigned)((a.N + 15) / 16);
+  if (a.ydt == DT_F32) hipLaunchKernelGGL(k_i8_few<DT_F32>, dim3(grid), dim3(512), 0, s, a);
+  else hipLaunchKernelGGL(k_i8_few<DT_BF16>, dim3(grid), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_i8_gemm(const TileArgs& a, hipStream_t s) {
+  static const Levels none{};
+  return launch_tile_t<TILE_I8, 4, 256>(a, none, s);
+}
+
+}  // namespace qlr

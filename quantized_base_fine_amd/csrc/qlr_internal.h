@@ -202,4 +202,54 @@ hipError_t launch_lora_grads(const float* u, int u_splits, const float* t, int t
                              const void* dy, int qdt, bool mfma, int64_t M, int64_t N, int64_t K, int r,
                              float scale, float* dA, float* dB, float* part, hipStream_t s);
 
+// ---- products over ranges of rows: expert-grouped linears and the 8-bit-integer linear
+struct TileArgs {
+  const void* x;           // M x K bf16 (TR: dy, M x N; the 8-bit product: int8 M x K)
+  int64_t M;               // rows of x, y and t
+  const int32_t* offsets;  // experts + 1 device offsets, or null: one range of M rows
+  int experts;
+  int64_t N, K;            // one expert's weight
+  int bits;
+  const uint8_t* w;        // packed codes of the stacked weight, or int8 values
+  const uint8_t* q8;
+  const float* cst;
+  const float* sx;         // 8-bit product: scale per token and per output channel
+  const float* sw;
+  const float* t;          // t_splits x M x r float32 partials of the adapter product (TR: of u)
+  int t_splits;
+  const uint16_t* ab;      // bf16 adapter operand: B (experts x N x r); TR: A (experts x r x K)
+  int r;
+  float scale;
+  void* y;
+  int ydt;
+  int min_rows;            // experts with at most this many rows are left out (the few-rows kernel takes them)
+  int ntiles;              // set by the launcher
+};
+// Rows of an expert up to which the few-rows kernel takes it.
+constexpr int kFewRows = 16;
+
+// q (rows x cols) and scale (rows) of rows of dtype dt.
+hipError_t launch_quantize_i8(const void* X, int dt, int64_t rows, int64_t cols, int8_t* q, float* scale, hipStream_t s);
+// y = (x w^T) sx sw + scale t B^T with int8 x, w (K % 16 == 0).
+hipError_t launch_i8_gemm(const TileArgs& a, hipStream_t s);
+hipError_t launch_i8_few(const TileArgs& a, hipStream_t s);  // M <= 16
+
+// Expert products of the coded weight: every expert of more than a.min_rows rows ...
+hipError_t launch_grouped_gemm(const TileArgs& a, const Levels& lv, hipStream_t s);
+// ... and those of 1 .. kFewRows rows.
+hipError_t launch_grouped_few(const TileArgs& a, const Levels& lv, hipStream_t s);
+// dx = dy W'_e + scale u A_e (N % 8 == 0, K % 64 == 0).
+hipError_t launch_grouped_dx(const TileArgs& a, const Levels& lv, hipStream_t s);
+// t (M x r float32) = x A_e^T over each expert's rows, A experts x r x K bf16, K % 8 == 0.
+hipError_t launch_grouped_t(const uint16_t* x, int64_t M, int64_t K, const uint16_t* A, int r, const int32_t* offsets,
+                            int experts, float* t, hipStream_t s);
+// Bt (experts x r x N) = B^T per expert, B experts x N x r bf16.
+hipError_t launch_grouped_transpose(const uint16_t* B, int experts, int64_t N, int r, uint16_t* Bt, hipStream_t s);
+// dA (experts x r x K) = scale u^T x and dB (experts x N x r) = scale dy^T t, float32, zero for experts
+// without rows; K % 8 == 0 and N % 8 == 0.  part: grouped_grad_floats() floats of scratch.
+size_t grouped_grad_floats(int64_t M, int64_t N, int64_t K, int r, int experts);
+hipError_t launch_grouped_grads(const float* u, const float* t, const uint16_t* x, const uint16_t* dy, int64_t M,
+                                int64_t N, int64_t K, int r, const int32_t* offsets, int experts, float scale, float* dA,
+                                float* dB, float* part, hipStream_t s);
+
 }  // namespace qlr

@@ -1,0 +1,563 @@
+// Tiled matrix product over ranges of rows: the core of the expert products
+// (rows grouped by expert, one stacked coded weight) and of the 8-bit-integer
+// product (one range, both operands int8).
+//
+//   KIND TILE_I8    y = (sum_k xq wq) sx[m] sw[n]          (+ adapter)
+//   KIND TILE_CODED y[m] = x[m] W'_e^T, e the row's expert  (+ adapter)
+//   KIND TILE_TR    y[m] = x[m] W'_e (x = dy, y = dx)       (+ adapter)
+//
+// Tiling.  A workgroup of 8 waves owns BM (64, 128 or 256) rows x 256 columns;
+// wave (mh, nh) = (w / 4, w % 4) the rows [mh BM / 2, + BM / 2) x columns
+// [64 nh, + 64).  A step contracts 128 bytes of each row of x: 64 bf16 or 128
+// int8 elements.  MFMA operands: A = weight rows, B = x rows (32x32x16 bf16 or
+// 32x32x32 int8), so a lane's results are 4 neighbouring columns of one output
+// row and the epilogue stages whole 8- or 16-byte pieces.
+//
+// Pipeline.  Two LDS buffers of BM + 256 rows of 128 bytes, 16-byte chunks
+// XOR-swizzled by row (swz) so that fragment reads and tile writes are free of
+// bank conflicts.  Step k multiplies buffer k % 2 while the operands of step
+// k + 1 are on their way in registers; they are written to the other buffer in
+// the same step, and one barrier ends the step.  With two waves per SIMD, one
+// wave's products cover the other's waits.  Coded weights are loaded two steps
+// ahead and dequantized to bf16 between the products (32 codes per thread and
+// step); each weight is dequantized once per tile.
+//
+// Adapter.  t = x A_e^T (float32 partial sums) enters after the last step as
+// blocks of 32 adapter columns: the x side holds [hi(s t) | lo(s t)] (two bf16
+// halves, about 16 significant bits of s t), the weight side [B | B].
+//
+// Ranges.  Expert e's rows are [offsets[e], offsets[e + 1]); every offset is
+// clamped into [0, M] and to its predecessor, so no offset can lead out of
+// bounds.  Each workgroup finds its tile by a wave scan over the experts' tile
+// counts; workgroups past the last tile exit before any barrier.
+#pragma once
+
+#include <algorithm>
+#include <climits>
+#include <mutex>
+#include <type_traits>
+
+#include "qlr_dequant.h"
+#include "qlr_internal.h"
+
+namespace qlr {
+
+enum { TILE_I8 = 0, TILE_CODED = 1, TILE_TR = 2 };
+
+namespace {
+
+constexpr int kTileN = 256;
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+// Rows [a, b) of expert e, clamped.
+__device__ __forceinline__ void expert_range(const int32_t* offsets, int e, int M, int& a, int& b) {
+  a = min(max(offsets[e], 0), M);
+  b = max(a, min(max(offsets[e + 1], 0), M));
+}
+
+// Tiles of BM rows over the ranges holding more than min_rows rows: with
+// `want` < 0 returns the tile count, else finds tile `want` (expert and its
+// first and end row).  Called by whole waves.
+template <int BM>
+__device__ __forceinline__ int tile_scan(const int32_t* offsets, int E, int M, int min_rows, int want, int& e_out,
+                                         int& row0, int& row_end) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    int a = 0, b = 0;
+    if (e0 + lane < E) expert_range(offsets, e0 + lane, M, a, b);
+    const int nt = b - a > min_rows ? (b - a + BM - 1) / BM : 0;
+    int inc = nt;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(inc, d, 64);
+      if (lane >= d) inc += up;
+    }
+    const int last = __shfl(inc, 63, 64);
+    if (want >= 0 && want < before + last) {
+      const uint64_t hit = __ballot(before + inc > want);
+      const int src = __ffsll((unsigned long long)hit) - 1;  // the first expert whose tiles reach past `want`
+      const int t0 = before + __shfl(inc - nt, src, 64);
+      e_out = e0 + src;
+      row0 = __shfl(a, src, 64) + (want - t0) * BM;
+      row_end = __shfl(b, src, 64);
+      return 0;
+    }
+    before += last;
+  }
+  return before;
+}
+
+template <int KIND, int BITS, int BM>
+struct TileLds {
+  static constexpr uint32_t kX = BM * 128, kW = 256 * 128;
+  static constexpr uint32_t kWOff = 2 * kX;
+  static constexpr uint32_t kTab = 2 * (kX + kW);  // level table of the widths that use one
+  static constexpr uint32_t kTabBytes = (KIND == TILE_I8 || BITS == 4) ? 0
+                                        : BITS == 8                    ? 256 * 16 * 4
+                                                                       : PairTableF32<BITS>::kBytes;
+  // the epilogue's staging of BM / 2 output rows (float32 at most) overlays the buffers
+  static constexpr uint32_t kStage = (BM / 2) * (256 * 4 + 16);
+  static constexpr uint32_t kBytes = kTab + kTabBytes > kStage ? kTab + kTabBytes : kStage;
+  static_assert(kBytes <= 160 * 1024, "LDS budget");
+};
+
+__device__ __forceinline__ f32x16_t tile_mfma(u32x4_t a, u32x4_t b, f32x16_t c) {
+  return mfma32x32x16(as_bf16x8(a), as_bf16x8(b), c);
+}
+__device__ __forceinline__ f32x16_t tile_mfma_i8(u32x4_t a, u32x4_t b, f32x16_t c) {
+  return __builtin_bit_cast(
+      f32x16_t, __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b),
+                                                      __builtin_bit_cast(i32x16_t, c), 0, 0, 0));
+}
+
+template <int KIND, int BITS, int BM>
+__global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
+  using L = TileLds<KIND, BITS, BM>;
+  constexpr int MT = BM / 64;  // 32-row tiles of a wave
+  constexpr int XL = BM / 64;  // 16-byte pieces of x per thread and step
+  extern __shared__ uint32_t smem[];
+  (void)smem;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int fr = lane & 31, h = lane >> 5;
+
+  // ---- which tile.  Workgroup b runs on XCD b % 8; each XCD takes a contiguous range of tiles.
+  const int ntiles = P.ntiles;
+  int e = 0, row0 = 0, row_end = (int)P.M, tile_n;
+  {
+    int mt_total;
+    if (P.offsets) mt_total = tile_scan<BM>(P.offsets, P.experts, (int)P.M, P.min_rows, -1, e, row0, row_end);
+    else mt_total = (int)((P.M + BM - 1) / BM);
+    const int64_t total = (int64_t)mt_total * ntiles;
+    const int64_t per = (total + 7) / 8, loc = blockIdx.x >> 3;
+    const int64_t tile = (int64_t)(blockIdx.x & 7) * per + loc;
+    if (loc >= per || tile >= total) return;  // the whole workgroup, before any barrier
+    const int mi = (int)(tile / ntiles);
+    if (P.offsets) {
+      row_end = 0;
+      tile_scan<BM>(P.offsets, P.experts, (int)P.M, P.min_rows, mi, e, row0, row_end);
+    } else {
+      row0 = mi * BM;
+    }
+    e = __builtin_amdgcn_readfirstlane(e);
+    row0 = __builtin_amdgcn_readfirstlane(row0);
+    row_end = __builtin_amdgcn_readfirstlane(row_end);
+    tile_n = (int)(tile % ntiles);
+  }
+  const int mrows = min(BM, row_end - row0);
+  const int64_t N = P.N, K = P.K;
+  const int64_t NO = KIND == TILE_TR ? K : N;            // output columns
+  const int n0 = tile_n * kTileN;
+  const uint32_t kbytes = (uint32_t)(KIND == TILE_I8 ? K : KIND == TILE_TR ? 2 * N : 2 * K);  // bytes of one x row
+  const int nsteps = (int)((kbytes + 127) / 128);
+
+  if constexpr (L::kTabBytes > 0) {
+    float* sL = reinterpret_cast<float*>(smem);
+    stage_levels<1 << BITS>(lv, sL);
+    __syncthreads();
+    if constexpr (BITS == 8) {
+      for (int i = tid; i < 256 * 16; i += 512)
+        *reinterpret_cast<__attribute__((address_space(3))) float*>((uintptr_t)(L::kTab + 4 * i)) = sL[i >> 4];
+    } else {
+      constexpr int NL = 1 << BITS;
+      for (int i = tid; i < PairTableF32<BITS>::kEntries * 32; i += 512) {
+        const int en = i >> 5;
+        *reinterpret_cast<__attribute__((address_space(3))) f32x2_t*>((uintptr_t)(L::kTab + 8 * i)) =
+            f32x2_t{sL[en & (NL - 1)], sL[en >> BITS]};
+      }
+    }
+    __syncthreads();
+  }
+
+  // ---- x loads: piece i of a thread = chunk tid % 8 of tile row tid / 8 + 64 i; rows past the
+  // range and chunks past the row's end read zero
+  const char* xbase = reinterpret_cast<const char*>(P.x) + (int64_t)row0 * kbytes;
+  const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(xbase), (short)0,
+                                                                      (int)((uint32_t)mrows * kbytes), 0x00020000);
+  const uint32_t ch = (uint32_t)tid & 7u, rq = (uint32_t)tid >> 3;
+  const uint32_t xg = rq * kbytes + 16u * ch;
+  const uint32_t xst = rq * 128u + ((ch ^ swz(rq & 15u)) << 4);  // 64-row strides keep row % 16
+  struct Xs { u32x4_t v[XL]; };
+  auto load_x = [&](int k, Xs& s) {
+    const uint32_t kb = (uint32_t)k * 128u;
+    const bool ok = kb + 16u * ch < kbytes;
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      uint32_t off = ok ? xg + kb + (uint32_t)i * 64u * kbytes : 0xFFFFFFF0u;
+      s.v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(xr, off, 0, 0));
+    }
+  };
+  auto store_x = [&](const Xs& s, int buf) {
+#pragma unroll
+    for (int i = 0; i < XL; ++i) lds_store_u32x4(xst + (uint32_t)buf * L::kX + 8192u * i, s.v[i]);
+  };
+
+  // ---- weight loads
+  // I8: as x, rows n0 .. n0 + 255 (rows past N zero).
+  // CODED: thread = row tid / 2, codes [32 dh, + 32) of the step's block.
+  // TR: thread = weight row 64 k + tid / 8, codes [32 dh, + 32) of block column n0 / 64 + bq.
+  struct Ws {
+    u32x4_t v[KIND == TILE_I8 ? 4 : 1];
+    Codes32<BITS> c;
+    uint32_t q8;
+    float sc;
+  };
+  const int wrows = (int)min<int64_t>(kTileN, N - n0);
+  const char* wbase = reinterpret_cast<const char*>(P.w) + (int64_t)n0 * K;
+  const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char*>(KIND == TILE_I8 ? wbase : nullptr), (short)0,
+      KIND == TILE_I8 ? (int)((uint32_t)wrows * kbytes) : 0, 0x00020000);
+  const int rr = KIND == TILE_TR ? (tid >> 3) : (tid >> 1), dh = tid & 1, bq = KIND == TILE_TR ? ((tid >> 1) & 3) : 0;
+  const int64_t nbK = K >> 6;
+  bool wv = true;
+  int64_t wblk = 0;
+  if constexpr (KIND == TILE_CODED) {
+    wv = n0 + rr < N;
+    wblk = ((int64_t)e * N + (wv ? n0 + rr : N - 1)) * nbK;
+  } else if constexpr (KIND == TILE_TR) {
+    const int64_t wcol = (n0 >> 6) + bq;
+    wv = wcol < nbK;
+    wblk = (int64_t)e * N * nbK + (wv ? wcol : nbK - 1);
+  }
+  uint32_t wst[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (KIND == TILE_TR)
+      wst[q] = L::kWOff + (uint32_t)(bq >> 1) * 16384u + (uint32_t)rr * 256u +
+               (tr_chunk((uint32_t)(8 * (bq & 1) + 4 * dh + q), (uint32_t)rr) << 4);
+    else
+      wst[q] = L::kWOff + (uint32_t)rr * 128u + ((((uint32_t)(4 * dh + q)) ^ swz((uint32_t)rr & 15u)) << 4);
+  }
+  const uint32_t tp = L::kTab + (BITS == 8 ? 4u * (lane & 15) : 8u * fr);
+  auto load_w = [&](int k, Ws& s) {
+    if constexpr (KIND == TILE_I8) {
+      const uint32_t kb = (uint32_t)k * 128u;
+      const bool ok = kb + 16u * ch < kbytes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t off = ok ? xg + kb + (uint32_t)i * 64u * kbytes : 0xFFFFFFF0u;
+        s.v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, off, 0, 0));
+      }
+    } else {
+      int64_t blk;
+      bool ok = wv;
+      if constexpr (KIND == TILE_CODED) {
+        blk = wblk + min(k, nsteps - 1);
+      } else {
+        const int64_t n = 64 * (int64_t)min(k, nsteps - 1) + rr;
+        ok = wv && n < N;  // rows past N: scale 0
+        blk = wblk + min<int64_t>(n, N - 1) * nbK;
+      }
+      s.c = load_codes32<BITS>(P.w + blk * (8 * BITS) + dh * (4 * BITS));
+      s.q8 = P.q8[blk];
+      s.sc = P.cst[blk >> 8];
+      if (!ok) s.q8 = 0;
+    }
+  };
+  // part I (0..3) of the thread's weights into buffer buf: I8 one loaded piece, coded 8 dequantized weights
+  auto store_w = [&](const Ws& s, const Lut4& lut, float ap, auto part, int buf) {
+    constexpr int I = decltype(part)::value;
+    if constexpr (KIND == TILE_I8) {
+      lds_store_u32x4(L::kWOff + xst + (uint32_t)buf * L::kW + 8192u * I, s.v[I]);
+    } else {
+      uint32_t o[16];
+      if constexpr (BITS == 4) lut4_word(s.c.w[I], lut, o + 4 * I);
+      else dequant_pairs<BITS, 4 * I, 4 * I + 4>(s.c, ap, tp, o);
+      lds_store_u32x4(wst[I] + (uint32_t)buf * L::kW, u32x4_t{o[4 * I], o[4 * I + 1], o[4 * I + 2], o[4 * I + 3]});
+    }
+  };
+  auto store_w_all = [&](const Ws& s, int buf) {
+    Lut4 lut{};
+    const float ap = KIND == TILE_I8 ? 0.0f : (float)s.q8 * s.sc;
+    if constexpr (KIND != TILE_I8 && BITS == 4) lut = make_lut4(lv, ap);
+    store_w(s, lut, ap, std::integral_constant<int, 0>{}, buf);
+    store_w(s, lut, ap, std::integral_constant<int, 1>{}, buf);
+    store_w(s, lut, ap, std::integral_constant<int, 2>{}, buf);
+    store_w(s, lut, ap, std::integral_constant<int, 3>{}, buf);
+  };
+
+  // ---- fragments: MFMA step s (0..3) of a buffer, row fr (+ 32 per tile), chunk 2 s + h
+  const int mh = wave >> 2, nh = wave & 3;
+  uint32_t xb[4], wb[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const uint32_t fo = (uint32_t)(fr * 128) + ((((uint32_t)(2 * s + h)) ^ swz((uint32_t)fr & 15u)) << 4);
+    xb[s] = (uint32_t)(mh * (BM / 2) * 128) + fo;
+    wb[s] = L::kWOff + (uint32_t)(nh * 64 * 128) + fo;
+  }
+  uint32_t tbo[2];
+  {
+    const uint32_t g = (uint32_t)lane >> 4, sp = (uint32_t)lane & 15u;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t chunk = 8u * (uint32_t)(nh & 1) + 4u * c + 2u * (g & 1u) + ((sp >> 1) & 1u);
+      tbo[c] = L::kWOff + (uint32_t)(nh >> 1) * 16384u + (8u * h + (sp >> 2)) * 256u + (tr_chunk(chunk, sp >> 2) << 4) +
+               8u * (sp & 1u);
+    }
+  }
+  u32x4_t fx[2][MT], fw[2][2];
+  auto read_frags = [&](int buf, int s, int slot) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) fx[slot][i] = lds_u32x4(xb[s] + (uint32_t)buf * L::kX + 4096u * i);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if constexpr (KIND == TILE_TR) {
+        const uint32_t ad = tbo[c] + (uint32_t)buf * L::kW + 4096u * s;
+        const u16x4_t lo = lds_tr16(ad), hi = lds_tr16(ad + 1024u);
+        fw[slot][c] = u32x4_t{__builtin_bit_cast(uint2, lo).x, __builtin_bit_cast(uint2, lo).y,
+                              __builtin_bit_cast(uint2, hi).x, __builtin_bit_cast(uint2, hi).y};
+      } else {
+        fw[slot][c] = lds_u32x4(wb[s] + (uint32_t)buf * L::kW + 4096u * c);
+      }
+    }
+  };
+  f32x16_t acc[MT][2];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][c][v] = 0.0f;  // also the integer zero
+  auto mfmas = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if constexpr (KIND == TILE_I8) acc[i][c] = tile_mfma_i8(fw[slot][c], fx[slot][i], acc[i][c]);
+        else acc[i][c] = tile_mfma(fw[slot][c], fx[slot][i], acc[i][c]);
+      }
+  };
+
+  // ---- the steps.  I8 loads its weights with x, one step ahead; coded weights two.
+  Xs xs;
+  Ws wa, wn;
+  load_x(0, xs);
+  load_w(0, wa);
+  if constexpr (KIND != TILE_I8) load_w(1, wn);
+  store_x(xs, 0);
+  store_w_all(wa, 0);
+  __syncthreads();
+  auto step = [&](int k, int buf, Ws& cur, Ws& nxt) {
+    // cur: the weights of step k + 1 (coded); nxt: room for step k + 2
+    __builtin_amdgcn_sched_barrier(0);
+    load_x(k + 1, xs);
+    if constexpr (KIND == TILE_I8) load_w(k + 1, cur);
+    else load_w(k + 2, nxt);
+    __builtin_amdgcn_sched_barrier(0);
+    read_frags(buf, 0, 0);
+    Lut4 lut{};
+    const float ap = KIND == TILE_I8 ? 0.0f : (float)cur.q8 * cur.sc;
+    if constexpr (KIND != TILE_I8 && BITS == 4) lut = make_lut4(lv, ap);
+    auto sub = [&](auto spos) {
+      constexpr int S = decltype(spos)::value;
+      if constexpr (S < 3) read_frags(buf, S + 1, (S + 1) & 1);
+      mfmas(S & 1);
+      if constexpr (KIND != TILE_I8) store_w(cur, lut, ap, spos, buf ^ 1);
+    };
+    sub(std::integral_constant<int, 0>{});
+    sub(std::integral_constant<int, 1>{});
+    sub(std::integral_constant<int, 2>{});
+    sub(std::integral_constant<int, 3>{});
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (KIND == TILE_I8) store_w_all(cur, buf ^ 1);
+    store_x(xs, buf ^ 1);
+    __syncthreads();
+  };
+  int k = 0;
+  for (; k + 1 < nsteps; k += 2) {
+    step(k, 0, wn, wa);
+    step(k + 1, 1, wa, wn);
+  }
+  if (k < nsteps) step(k, 0, wn, wa);
+
+  // ---- row and column scales of the integer product
+  if constexpr (KIND == TILE_I8) {
+    float sx[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int m = mh * (BM / 2) + 32 * i + fr;
+      sx[i] = P.sx[row0 + min(m, mrows - 1)];
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int n = n0 + 64 * nh + 32 * c + 8 * (v >> 2) + 4 * h + (v & 3);
+        const float sw = P.sw[min<int64_t>(n, N - 1)];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i][c][v] = (float)__float_as_int(acc[i][c][v]) * sx[i] * sw;
+      }
+  }
+
+  // ---- adapter blocks (buffer 0 is free: the last barrier has passed)
+  if (P.r > 0) {
+    const int r = P.r;
+    const bool r8 = (r & 7) == 0;
+    const u32x4_t zero4 = {0u, 0u, 0u, 0u};
+    for (int j0 = 0; j0 < r; j0 += 32) {
+      // x side: row (idx / 4), adapter columns j0 + 8 (idx % 4) .. + 8
+      for (int idx = tid; idx < BM * 4; idx += 512) {
+        const int row = idx >> 2, c = idx & 3, jb = j0 + 8 * c;
+        float tv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) tv[i] = 0.0f;
+        if (row < mrows && jb < r) {
+          for (int sp = 0; sp < P.t_splits; ++sp) {
+            const float* tq = P.t + ((int64_t)sp * P.M + row0 + row) * r + jb;
+            if (r8) {
+              const f32x4_t v0 = *reinterpret_cast<const f32x4_t*>(tq), v1 = *reinterpret_cast<const f32x4_t*>(tq + 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                tv[i] += v0[i];
+                tv[4 + i] += v1[i];
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (jb + i < r) tv[i] += tq[i];
+            }
+          }
+        }
+        u32x4_t hv, lo;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u0 = P.scale * tv[2 * i], u1 = P.scale * tv[2 * i + 1];
+          const uint32_t h0 = f32_to_bf16_bits(u0), h1 = f32_to_bf16_bits(u1);
+          hv[i] = h0 | (h1 << 16);
+          lo[i] = pack_bf16x2(u0 - bf16_bits_to_f32(h0), u1 - bf16_bits_to_f32(h1));
+        }
+        const uint32_t xrow = (uint32_t)row * 128u;
+        lds_store_u32x4(xrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), hv);
+        lds_store_u32x4(xrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), lo);
+      }
+      if constexpr (KIND == TILE_TR) {
+        // A[j0 + row][n0 ..]: rows 0..31 and 32..63 hold the same 32 adapter rows
+        const uint16_t* Ae = P.ab + (int64_t)e * r * K;
+        for (int idx = tid; idx < 32 * 32; idx += 512) {
+          const int row = idx >> 5, c = idx & 31;
+          const int64_t col = n0 + 8 * c;
+          u32x4_t v = zero4;
+          if (j0 + row < r && col < K) v = *reinterpret_cast<const u32x4_t*>(Ae + (int64_t)(j0 + row) * K + col);
+          const uint32_t base = L::kWOff + (uint32_t)(c >> 4) * 16384u;
+          lds_store_u32x4(base + (uint32_t)row * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
+          lds_store_u32x4(base + (uint32_t)(row + 32) * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
+        }
+      } else {
+        // [B[n][j0 ..] | the same]
+        const uint16_t* Be = P.ab + (int64_t)e * N * r;
+        for (int idx = tid; idx < kTileN * 4; idx += 512) {
+          const int row = idx >> 2, c = idx & 3, jb = j0 + 8 * c;
+          u32x4_t v = zero4;
+          if (n0 + row < N && jb < r) {
+            const uint16_t* bp = Be + (int64_t)(n0 + row) * r + jb;
+            if (r8) {
+              v = *reinterpret_cast<const u32x4_t*>(bp);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = jb + 2 * i < r ? bp[2 * i] : 0u, hi = jb + 2 * i + 1 < r ? bp[2 * i + 1] : 0u;
+                v[i] = lo | (hi << 16);
+              }
+            }
+          }
+          const uint32_t wrow = L::kWOff + (uint32_t)row * 128u;
+          lds_store_u32x4(wrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), v);
+          lds_store_u32x4(wrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), v);
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        read_frags(0, s, 0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) acc[i][c] = tile_mfma(fw[0][c], fx[0][i], acc[i][c]);
+      }
+      __syncthreads();
+    }
+  }
+
+  // ---- output: the rows of one wave row-half at a time, staged row-major in LDS, stored in 16-byte pieces
+  const int es = P.ydt == DT_F32 ? 4 : 2;
+  const uint32_t rs = 256u * es + 16u;
+  const bool vec = (NO * es) % 16 == 0;
+  const int cpr = 16 * es;  // 16-byte pieces of a staged row
+  for (int p = 0; p < 2; ++p) {
+    if (p * (BM / 2) >= mrows) break;
+    if (mh == p) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t ad = (uint32_t)(32 * i + fr) * rs + (uint32_t)(64 * nh + 32 * c + 8 * q + 4 * h) * es;
+            const float v0 = acc[i][c][4 * q], v1 = acc[i][c][4 * q + 1], v2 = acc[i][c][4 * q + 2], v3 = acc[i][c][4 * q + 3];
+            if (es == 4) {
+              lds_store_f32x4(ad, f32x4_t{v0, v1, v2, v3});
+            } else {
+              *reinterpret_cast<__attribute__((address_space(3))) u32x2v_t*>((uintptr_t)ad) =
+                  u32x2v_t{pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)};
+            }
+          }
+    }
+    __syncthreads();
+    const int rows = min(BM / 2, mrows - p * (BM / 2));
+    for (int idx = tid; idx < rows * cpr; idx += 512) {
+      const int row = es == 4 ? idx >> 6 : idx >> 5, c = idx & (cpr - 1);
+      const int64_t col = n0 + c * (16 / es);
+      if (col >= NO) continue;
+      const u32x4_t v = lds_u32x4((uint32_t)row * rs + 16u * c);
+      char* dst = reinterpret_cast<char*>(P.y) + ((int64_t)(row0 + p * (BM / 2) + row) * NO + col) * es;
+      if (vec) {
+        *reinterpret_cast<u32x4_t*>(dst) = v;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = v[i];
+          if (es == 4) {
+            if (col + i < NO) reinterpret_cast<uint32_t*>(dst)[i] = w;
+          } else {
+            if (col + 2 * i < NO) reinterpret_cast<uint16_t*>(dst)[2 * i] = (uint16_t)w;
+            if (col + 2 * i + 1 < NO) reinterpret_cast<uint16_t*>(dst)[2 * i + 1] = (uint16_t)(w >> 16);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Upper bound of the row tiles of any `experts` ranges over M rows.
+inline int64_t tile_bound(int64_t M, int experts, int BM) { return M / BM + std::min<int64_t>(experts, M); }
+
+template <int KIND, int BITS, int BM>
+hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
+  auto kern = k_tile<KIND, BITS, BM>;
+  constexpr int shmem = (int)TileLds<KIND, BITS, BM>::kBytes;
+  static std::once_flag once;
+  static hipError_t setup;
+  std::call_once(once, [&] {
+    // the kernel addresses LDS from 0: it must not have static LDS
+    hipFuncAttributes fa;
+    setup = hipFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern));
+    if (setup == hipSuccess && fa.sharedSizeBytes != 0) setup = hipErrorInvalidKernelFile;
+  });
+  if (setup != hipSuccess) return setup;
+  const int64_t no = KIND == TILE_TR ? a.K : a.N;
+  a.ntiles = (int)((no + kTileN - 1) / kTileN);
+  const int64_t tiles = (a.offsets ? tile_bound(a.M, a.experts, BM) : (a.M + BM - 1) / BM) * a.ntiles;
+  if (tiles <= 0) return hipSuccess;
+  if (tiles > INT32_MAX - 8) return hipErrorInvalidValue;
+  hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, shmem);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(8 * ((tiles + 7) / 8))), dim3(512), shmem, s, a, lv);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace qlr

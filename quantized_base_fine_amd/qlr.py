@@ -25,6 +25,8 @@ QLR_F32, QLR_F16, QLR_BF16 = 0, 1, 2
 PATH_AUTO, PATH_F32, PATH_GEMV, PATH_GEMM = 0, 1, 2, 3
 OP_QUANTIZE, OP_LINEAR, OP_LINEAR_BWD, OP_LINEAR_DBA = 0, 1, 2, 3
 OP_QUANTIZE_OUTLIERS, OP_LINEAR_OUTLIERS, OP_LINEAR_WHA = 4, 5, 6
+OP_LINEAR_I8, OP_LINEAR_GROUPED, OP_LINEAR_GROUPED_BWD = 7, 8, 9
+MAX_EXPERTS = 4096
 
 STATUS = {
     0: "QLR_OK", 1: "QLR_ERR_NULL", 2: "QLR_ERR_SHAPE", 3: "QLR_ERR_DTYPE", 4: "QLR_ERR_BITS",
@@ -69,6 +71,10 @@ class CSparse(C.Structure):
     ]
 
 
+class CI8Rows(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("q", C.c_void_p), ("scale", C.c_void_p)]
+
+
 EXPORTS = {
     "qlr_version": (C.c_int, []),
     "qlr_status_string": (C.c_char_p, [C.c_int]),
@@ -108,6 +114,19 @@ EXPORTS = {
                                           C.c_void_p]),
     "qlr_linear_fwd_wha": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.POINTER(CQWeight), C.POINTER(CSparse),
                                      C.c_int32, C.c_void_p, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qlr_quantize_i8": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.POINTER(CI8Rows), C.c_void_p]),
+    "qlr_linear_fwd_i8": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.POINTER(CI8Rows), C.POINTER(CI8Rows),
+                                    C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_float, C.c_void_p, C.c_int,
+                                    C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qlr_grouped_workspace_bytes": (C.c_int, [C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_int32, C.c_int32,
+                                              C.POINTER(C.c_size_t)]),
+    "qlr_linear_fwd_grouped": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.POINTER(CQWeight), C.c_int32, C.c_void_p,
+                                         C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_float, C.c_void_p, C.c_int,
+                                         C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qlr_linear_bwd_grouped": (C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_int, C.c_int64, C.POINTER(CQWeight),
+                                         C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_float,
+                                         C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
+                                         C.c_void_p]),
     "qlr_force_path": (C.c_int, [C.c_int]),
 }
 
@@ -606,3 +625,246 @@ def sparse_from_csr(rows: int, cols: int, row_ptr, col, val, device) -> Sparse:
         sp.col[:nnz].copy_(torch.as_tensor(col, dtype=torch.int32))
         sp.val[:nnz].copy_(torch.as_tensor(val, dtype=torch.float32))
     return sp
+
+
+# ---------------------------------------------------------------- 8-bit-integer linear, expert-grouped linears
+
+def _rows2d(t, what: str, cols: Optional[int] = None, dtypes=None):
+    """t as the C ABI takes it: a 2-D GPU tensor, densely packed, of one of the dtypes."""
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous 2-D tensor")
+    if cols is not None and t.shape[1] != cols:
+        raise ValueError(f"{what} must have {cols} columns, not {t.shape[1]}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"{what} has dtype {t.dtype}; expected one of {tuple(dtypes)}")
+    return t
+
+
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+
+
+class _Launch:
+    """Runs a prepared C call with the buffers' device current (the kernels are launched there)."""
+
+    def __init__(self, fn, args, device):
+        torch = _torch()
+        self._fn, self._args = fn, args
+        self._index = device.index if device.index is not None else torch.cuda.current_device()
+        self._cuda = torch.cuda
+
+    def __call__(self):
+        if self._cuda.current_device() == self._index:
+            check(self._fn(*self._args))
+        else:
+            with self._cuda.device(self._index):
+                check(self._fn(*self._args))
+
+
+@dataclass
+class I8Rows:
+    """Rows in 8-bit integers: q (rows, cols) int8 and scale (rows,) float32, both on the GPU."""
+    rows: int
+    cols: int
+    q: "object"
+    scale: "object"
+
+    def c_struct(self) -> CI8Rows:
+        torch = _torch()
+        _require_cuda(self.q, self.scale)
+        if self.q.dtype != torch.int8 or tuple(self.q.shape) != (self.rows, self.cols) or not self.q.is_contiguous():
+            raise ValueError("q must be a contiguous int8 tensor of (rows, cols)")
+        if self.scale.dtype != torch.float32 or self.scale.numel() != self.rows or not self.scale.is_contiguous():
+            raise ValueError("scale must be a contiguous float32 tensor of rows values")
+        _same_device(self.q, scale=self.scale)
+        return CI8Rows(self.rows, self.cols, self.q.data_ptr(), self.scale.data_ptr())
+
+    @staticmethod
+    def empty(rows: int, cols: int, device) -> "I8Rows":
+        torch = _torch()
+        return I8Rows(rows, cols, torch.empty((rows, cols), dtype=torch.int8, device=device),
+                      torch.empty(rows, dtype=torch.float32, device=device))
+
+
+def quantize_i8(x, out: Optional[I8Rows] = None) -> I8Rows:
+    """Rows of a 2-D float32/float16/bfloat16 device tensor (tokens, or a weight's output
+    channels) as 8-bit integers with one scale per row."""
+    torch = _torch()
+    _require_cuda(x)
+    x = _rows2d(x.contiguous(), "x", dtypes=(torch.float32, torch.float16, torch.bfloat16))
+    rows, cols = x.shape
+    q = out if out is not None else I8Rows.empty(rows, cols, x.device)
+    cq = q.c_struct()
+    _same_device(x, out=q.q)
+    _Launch(lib().qlr_quantize_i8, (x.data_ptr(), _dt(x), rows, cols, C.byref(cq), _stream(x.device)), x.device)()
+    return q
+
+
+class LinearI8Call:
+    """A prepared ``qlr_linear_fwd_i8`` call: y = (xq wq^T) sx sw + scale (x A^T) B^T, the
+    tokens quantized by the call, or given as ``xq`` (``x`` is then read for the adapter
+    only and may be None without one).  Marshalled once (the stream current at construction is
+    used); the tensors are kept alive by the object, and two calls that can overlap in
+    time need workspaces of their own."""
+
+    def __init__(self, x, w: I8Rows, A=None, B=None, scale: float = 0.0, xq: Optional[I8Rows] = None, out_dtype=None,
+                 out=None, ws=None):
+        torch = _torch()
+        if x is None and (xq is None or A is not None):
+            raise ValueError("x is needed for the quantization (no xq) and for the adapter")
+        src = x if x is not None else xq.q
+        _require_cuda(x, A, B, out, ws)
+        M, r = src.shape[0], 0 if A is None else A.shape[0]
+        if x is not None:
+            _rows2d(x, "x", w.cols, (torch.float32, torch.bfloat16))
+        if (A is None) != (B is None) or (r > 0 and (A.shape != (r, w.cols) or B.shape != (w.rows, r))):
+            raise ValueError("A must be (r, K) and B (N, r)")
+        if A is not None:
+            _rows2d(A, "A", dtypes=(torch.bfloat16,))
+            _rows2d(B, "B", dtypes=(torch.bfloat16,))
+        if out is None:
+            dtype = out_dtype or (x.dtype if x is not None else torch.bfloat16)
+            out = torch.empty((M, w.rows), dtype=dtype, device=src.device)
+        _rows2d(out, "out", w.rows, (torch.float32, torch.bfloat16))
+        if out.shape[0] != M:
+            raise ValueError("out must have x's rows")
+        self.y = out
+        need = workspace_bytes(OP_LINEAR_I8, M, w.rows, w.cols, r)
+        if ws is None and need > 0:
+            ws = torch.empty(need, dtype=torch.uint8, device=src.device)
+        cw, cq = w.c_struct(), None if xq is None else xq.c_struct()
+        _same_device(src, w=w.q, A=A, B=B, out=out, ws=ws, xq=None if xq is None else xq.q)
+        self._keep = (x, w, A, B, xq, ws, cw, cq)
+        self._run = _Launch(lib().qlr_linear_fwd_i8,
+                            (_ptr(x), _dt(x) if x is not None else QLR_BF16, M, None if cq is None else C.byref(cq),
+                             C.byref(cw), _ptr(A), _ptr(B), QLR_BF16, r, float(scale), out.data_ptr(), _dt(out), _ptr(ws),
+                             0 if ws is None else ws.numel() * ws.element_size(), _stream(src.device)), src.device)
+
+    def __call__(self):
+        self._run()
+        return self.y
+
+
+def linear_i8(x, w: I8Rows, A=None, B=None, scale: float = 0.0, xq: Optional[I8Rows] = None, out_dtype=None):
+    """y = (xq wq^T) sx sw + scale (x A^T) B^T; see LinearI8Call."""
+    return LinearI8Call(x, w, A, B, scale, xq=xq, out_dtype=out_dtype)()
+
+
+def grouped_workspace_bytes(op: int, T: int, rows: int, cols: int, experts: int, r: int = 0) -> int:
+    out = C.c_size_t()
+    check(lib().qlr_grouped_workspace_bytes(op, T, rows, cols, experts, r, C.byref(out)))
+    return out.value
+
+
+def _grouped_operands(qw: QWeight, offsets, A, B):
+    """(experts, rows of one expert, rank) of a grouped call's operands, checked."""
+    torch = _torch()
+    if offsets.dim() != 1 or offsets.dtype != torch.int32 or not offsets.is_contiguous() or offsets.numel() < 2:
+        raise ValueError("offsets must be a contiguous int32 vector of experts + 1 row numbers")
+    E = offsets.numel() - 1
+    if qw.rows % E != 0:
+        raise ValueError(f"the stacked weight's {qw.rows} rows are not a multiple of {E} experts")
+    N, r = qw.rows // E, 0 if A is None else A.shape[1]
+    if (A is None) != (B is None) or (A is not None and (A.shape != (E, r, qw.cols) or B.shape != (E, N, r))):
+        raise ValueError("A must be (experts, r, K) and B (experts, N, r)")
+    for name, t in (("A", A), ("B", B)):
+        if t is not None and (t.dtype != torch.bfloat16 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bfloat16 tensor")
+    return E, N, r
+
+
+class GroupedCall:
+    """A prepared ``qlr_linear_fwd_grouped`` call: rows [offsets[e], offsets[e + 1]) of x (T, K)
+    take expert e of the stacked weight (experts N, K) and the adapter A[e] (r, K), B[e]
+    (N, r): y = x W'_e^T + scale (x A_e^T) B_e^T.  Rows of no expert keep what ``out`` holds (undefined when
+    the call makes its own output).  Marshalled once (the stream current at construction is
+    used; the offsets' values are read on the GPU at every call); the tensors are kept
+    alive by the object, and two calls that can overlap in time need workspaces of their own."""
+
+    def __init__(self, x, qw: QWeight, offsets, A=None, B=None, scale: float = 0.0, out_dtype=None, out=None, ws=None):
+        torch = _torch()
+        _require_cuda(x, offsets, A, B, out, ws)
+        E, N, r = _grouped_operands(qw, offsets, A, B)
+        _rows2d(x, "x", qw.cols, (torch.bfloat16,))
+        T = x.shape[0]
+        if out is None:
+            out = torch.empty((T, N), dtype=out_dtype or x.dtype, device=x.device)
+        _rows2d(out, "out", N, (torch.float32, torch.bfloat16))
+        if out.shape[0] != T:
+            raise ValueError("out must have x's rows")
+        self.y = out
+        need = grouped_workspace_bytes(OP_LINEAR_GROUPED, T, qw.rows, qw.cols, E, r)
+        if ws is None and need > 0:
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        _same_device(x, weight=qw.codes, offsets=offsets, A=A, B=B, out=out, ws=ws)
+        cw = qw.c_struct()
+        self._keep = (x, qw, offsets, A, B, ws, cw)
+        self._run = _Launch(lib().qlr_linear_fwd_grouped,
+                            (x.data_ptr(), _dt(x), T, C.byref(cw), E, offsets.data_ptr(), _ptr(A), _ptr(B), QLR_BF16, r,
+                             float(scale), out.data_ptr(), _dt(out), _ptr(ws),
+                             0 if ws is None else ws.numel() * ws.element_size(), _stream(x.device)), x.device)
+
+    def __call__(self):
+        self._run()
+        return self.y
+
+
+def linear_grouped(x, qw: QWeight, offsets, A=None, B=None, scale: float = 0.0, out_dtype=None, out=None):
+    """y = x W'_e^T + scale (x A_e^T) B_e^T for the rows of each expert e; see GroupedCall."""
+    return GroupedCall(x, qw, offsets, A, B, scale, out_dtype=out_dtype, out=out)()
+
+
+class GroupedBwdCall:
+    """A prepared ``qlr_linear_bwd_grouped`` call for an upstream gradient dy (T, N): over each
+    expert's rows dx = dy W'_e + scale (dy B_e) A_e, dA_e = scale (dy B_e)^T x, dB_e = scale
+    dy^T (x A_e^T).  dA (experts, r, K) and dB (experts, N, r) are float32, zero for an
+    expert without rows; rows of no expert keep what ``dx`` holds (undefined when the call makes
+    its own).  ``need_dx=False`` skips the input gradient; without an adapter x may be
+    None.  Marshalled once, as GroupedCall."""
+
+    def __init__(self, dy, x, qw: QWeight, offsets, A=None, B=None, scale: float = 0.0, dx_dtype=None,
+                 need_dx: bool = True, dx=None, dA=None, dB=None, ws=None):
+        torch = _torch()
+        _require_cuda(dy, x, offsets, A, B, dx, dA, dB, ws)
+        E, N, r = _grouped_operands(qw, offsets, A, B)
+        _rows2d(dy, "dy", N, (torch.bfloat16,))
+        T, dev = dy.shape[0], dy.device
+        if x is None and r > 0:
+            raise ValueError("x is needed for the adapter's gradients")
+        if x is not None and _rows2d(x, "x", qw.cols, (torch.bfloat16,)).shape[0] != T:
+            raise ValueError("x must have dy's rows")
+        if need_dx and dx is None:
+            dx = torch.empty((T, qw.cols), dtype=dx_dtype or dy.dtype, device=dev)
+        self.dx = dx if need_dx else None
+        if self.dx is not None and _rows2d(dx, "dx", qw.cols, (torch.float32, torch.bfloat16)).shape[0] != T:
+            raise ValueError("dx must have dy's rows")
+        self.dA = self.dB = None
+        if r > 0:
+            self.dA = dA if dA is not None else torch.empty((E, r, qw.cols), dtype=torch.float32, device=dev)
+            self.dB = dB if dB is not None else torch.empty((E, N, r), dtype=torch.float32, device=dev)
+            for name, t, shape in (("dA", self.dA, (E, r, qw.cols)), ("dB", self.dB, (E, N, r))):
+                if tuple(t.shape) != shape or t.dtype != torch.float32 or not t.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape}")
+        need = grouped_workspace_bytes(OP_LINEAR_GROUPED_BWD, T, qw.rows, qw.cols, E, r)
+        if ws is None and need > 0:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        _same_device(dy, x=x, weight=qw.codes, offsets=offsets, A=A, B=B, dx=self.dx, dA=self.dA, dB=self.dB, ws=ws)
+        cw = qw.c_struct()
+        self._keep = (dy, x, qw, offsets, A, B, ws, cw)
+        self._run = _Launch(lib().qlr_linear_bwd_grouped,
+                            (dy.data_ptr(), _dt(dy), _ptr(x), QLR_BF16, T, C.byref(cw), E, offsets.data_ptr(), _ptr(A),
+                             _ptr(B), QLR_BF16, r, float(scale), _ptr(self.dx),
+                             _dt(self.dx) if self.dx is not None else QLR_F32, _ptr(self.dA), _ptr(self.dB), _ptr(ws),
+                             0 if ws is None else ws.numel() * ws.element_size(), _stream(dev)), dev)
+
+    def __call__(self):
+        self._run()
+        return self.dx, self.dA, self.dB
+
+
+def linear_grouped_bwd(dy, x, qw: QWeight, offsets, A=None, B=None, scale: float = 0.0, dx_dtype=None,
+                       need_dx: bool = True):
+    """Gradients (dx, dA, dB) of linear_grouped for an upstream gradient dy; see GroupedBwdCall."""
+    return GroupedBwdCall(dy, x, qw, offsets, A, B, scale, dx_dtype=dx_dtype, need_dx=need_dx)()
