@@ -23,6 +23,8 @@ constexpr int kFewWaves = 8;
 template <int BITS>
 struct FewTab {
   static constexpr uint32_t kBytes = BITS == 4 ? 0 : BITS == 8 ? 256 * 16 * 4 : PairTableF32<BITS>::kBytes;
+  // the waves' sums (the staging of the levels shares the area)
+  __host__ __device__ static constexpr uint32_t kRedBytes(int G) { return kFewWaves * 16 * 16 * 4 * G; }
 };
 
 template <int BITS, int G>
@@ -60,6 +62,8 @@ __global__ __launch_bounds__(512) void k_grouped_few(TileArgs P, Levels lv) {
   int64_t wblk[G];
 #pragma unroll
   for (int i = 0; i < G; ++i) wblk[i] = ((int64_t)e * N + min<int64_t>(n0 + 16 * i + row, N - 1)) * nb;
+  FewAdapter<16 * G> ad;
+  ad.load(P.t, 1, P.M, a, rows, P.ab + (int64_t)e * N * P.r, n0, (int)min<int64_t>(16 * G, N - n0), P.r);
   f32x4_t acc[G];
 #pragma unroll
   for (int i = 0; i < G; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -116,6 +120,8 @@ __global__ __launch_bounds__(512) void k_grouped_few(TileArgs P, Levels lv) {
 #pragma unroll
   for (int i = 0; i < G; ++i)
     *reinterpret_cast<f32x4_t*>(red + (wave * 16 + row) * (16 * G) + 16 * i + 4 * g) = acc[i];
+  char* ad_lds = reinterpret_cast<char*>(smem) + kRed + FewTab<BITS>::kRedBytes(G);
+  ad.stage(ad_lds, 1, rows, P.r);
   __syncthreads();
   for (int idx = tid; idx < rows * 16 * G; idx += 512) {
     const int m = idx / (16 * G), c = idx % (16 * G);
@@ -124,13 +130,8 @@ __global__ __launch_bounds__(512) void k_grouped_few(TileArgs P, Levels lv) {
     float y = 0.0f;
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w) y += red[(w * 16 + m) * (16 * G) + c];
-    if (P.r > 0) {
-      const float* tq = P.t + (int64_t)(a + m) * P.r;
-      const uint16_t* bp = P.ab + ((int64_t)e * N + n) * P.r;
-      float lo = 0.0f;
-      for (int j = 0; j < P.r; ++j) lo = fmaf(tq[j], bf16_bits_to_f32(bp[j]), lo);
-      y = fmaf(P.scale, lo, y);
-    }
+    if (P.r > 0)
+      y = fmaf(P.scale, ad.dot(ad_lds, P.t, 1, P.M, a, m, P.ab + (int64_t)e * N * P.r, n0, c, P.r), y);
     const int64_t o = (int64_t)(a + m) * N + n;
     if (P.ydt == DT_F32) reinterpret_cast<float*>(P.y)[o] = y;
     else reinterpret_cast<uint16_t*>(P.y)[o] = (uint16_t)f32_to_bf16_bits(y);
@@ -140,7 +141,7 @@ __global__ __launch_bounds__(512) void k_grouped_few(TileArgs P, Levels lv) {
 template <int BITS, int G>
 hipError_t launch_few_g(const TileArgs& a, const Levels& lv, hipStream_t s) {
   auto kern = k_grouped_few<BITS, G>;
-  const size_t shmem = FewTab<BITS>::kBytes + std::max<size_t>(kFewWaves * 16 * 16 * G * 4, 1024);
+  const size_t shmem = FewTab<BITS>::kBytes + FewTab<BITS>::kRedBytes(G) + (a.r > 0 ? FewAdapter<16 * G>::kBytes : 0);
   const hipError_t e =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)shmem);
   if (e != hipSuccess) return e;

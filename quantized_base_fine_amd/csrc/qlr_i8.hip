@@ -147,6 +147,7 @@ constexpr int kFewWaves = 8, kFewBatch = 8;
 
 template <int YDT>
 __global__ __launch_bounds__(512) void k_i8_few(TileArgs P) {
+  __shared__ __attribute__((aligned(16))) char ad_lds[FewAdapter<16>::kBytes];
   __shared__ int red[kFewWaves][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n0 = blockIdx.x * 16;
@@ -157,6 +158,8 @@ __global__ __launch_bounds__(512) void k_i8_few(TileArgs P) {
   const int8_t* xp = reinterpret_cast<const int8_t*>(P.x) + (int64_t)std::min(row, M - 1) * K + 16 * g;
   const int nst = (int)((K + 63) / 64);
   const int s0 = (int)((int64_t)nst * wave / kFewWaves), s1 = (int)((int64_t)nst * (wave + 1) / kFewWaves);
+  FewAdapter<16> ad;
+  ad.load(P.t, P.t_splits, M, 0, M, P.ab, n0, (int)std::min<int64_t>(16, N - n0), P.r);
   const i32x4_t zero = {0, 0, 0, 0};
   i32x4_t acc = zero;
   for (int b = s0; b < s1; b += kFewBatch) {
@@ -173,6 +176,7 @@ __global__ __launch_bounds__(512) void k_i8_few(TileArgs P) {
   }
 #pragma unroll
   for (int v = 0; v < 4; ++v) red[wave][(lane & 15) * 16 + 4 * g + v] = acc[v];  // [token][row]
+  ad.stage(ad_lds, P.t_splits, M, P.r);
   __syncthreads();
   if (tid >= 256) return;
   const int m = tid >> 4, n = n0 + (tid & 15);
@@ -181,15 +185,7 @@ __global__ __launch_bounds__(512) void k_i8_few(TileArgs P) {
 #pragma unroll
   for (int w = 0; w < kFewWaves; ++w) sum += red[w][tid];
   float y = (float)sum * P.sx[m] * P.sw[n];
-  if (P.r > 0) {
-    float lo = 0.0f;
-    for (int j = 0; j < P.r; ++j) {
-      float tj = 0.0f;
-      for (int sp = 0; sp < P.t_splits; ++sp) tj += P.t[((int64_t)sp * M + m) * P.r + j];
-      lo = fmaf(tj, bf16_bits_to_f32(P.ab[(int64_t)n * P.r + j]), lo);
-    }
-    y = fmaf(P.scale, lo, y);
-  }
+  if (P.r > 0) y = fmaf(P.scale, ad.dot(ad_lds, P.t, P.t_splits, M, 0, m, P.ab, n0, tid & 15, P.r), y);
   if constexpr (YDT == DT_F32) reinterpret_cast<float*>(P.y)[m * N + n] = y;
   else reinterpret_cast<uint16_t*>(P.y)[m * N + n] = (uint16_t)f32_to_bf16_bits(y);
 }

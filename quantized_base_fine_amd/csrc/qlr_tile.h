@@ -15,12 +15,12 @@
 //
 // Pipeline.  Two LDS buffers of BM + 256 rows of 128 bytes, 16-byte chunks
 // XOR-swizzled by row (swz) so that fragment reads and tile writes are free of
-// bank conflicts.  Step k multiplies buffer k % 2 while the operands of step
-// k + 1 are on their way in registers; they are written to the other buffer in
-// the same step, and one barrier ends the step.  With two waves per SIMD, one
-// wave's products cover the other's waits.  Coded weights are loaded two steps
-// ahead and dequantized to bf16 between the products (32 codes per thread and
-// step); each weight is dequantized once per tile.
+// bank conflicts.  Step k multiplies buffer k % 2 and writes the operands of
+// step k + 1, loaded into registers during step k - 1, to the other buffer
+// between the products; one barrier ends the step.  With two waves per SIMD,
+// one wave's products cover the other's waits.  Coded weights are dequantized to
+// bf16 between the products (32 codes per thread and step); each weight is
+// dequantized once per tile.
 //
 // Adapter.  t = x A_e^T (float32 partial sums) enters after the last step as
 // blocks of 32 adapter columns: the x side holds [hi(s t) | lo(s t)] (two bf16
@@ -113,6 +113,15 @@ __device__ __forceinline__ f32x16_t tile_mfma_i8(u32x4_t a, u32x4_t b, f32x16_t 
                                                       __builtin_bit_cast(i32x16_t, c), 0, 0, 0));
 }
 
+// Buffer resource over n bytes from p, its words made scalar (a resource in vector
+// registers would turn every load into a loop over the lanes' values).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void* p, uint32_t n) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)lo | ((uint64_t)hi << 32)), (short)0,
+                                           (int)__builtin_amdgcn_readfirstlane(n), 0x00020000);
+}
+
 template <int KIND, int BITS, int BM>
 __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
   using L = TileLds<KIND, BITS, BM>;
@@ -144,7 +153,8 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
     e = __builtin_amdgcn_readfirstlane(e);
     row0 = __builtin_amdgcn_readfirstlane(row0);
     row_end = __builtin_amdgcn_readfirstlane(row_end);
-    tile_n = (int)(tile % ntiles);
+    // (scalar: the division runs on the vector unit, and a buffer resource needs scalar words)
+    tile_n = __builtin_amdgcn_readfirstlane((int)(tile % ntiles));
   }
   const int mrows = min(BM, row_end - row0);
   const int64_t N = P.N, K = P.K;
@@ -174,25 +184,22 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
   // ---- x loads: piece i of a thread = chunk tid % 8 of tile row tid / 8 + 64 i; rows past the
   // range and chunks past the row's end read zero
   const char* xbase = reinterpret_cast<const char*>(P.x) + (int64_t)row0 * kbytes;
-  const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(xbase), (short)0,
-                                                                      (int)((uint32_t)mrows * kbytes), 0x00020000);
+  const __amdgpu_buffer_rsrc_t xr = tile_rsrc(xbase, (uint32_t)mrows * kbytes);
   const uint32_t ch = (uint32_t)tid & 7u, rq = (uint32_t)tid >> 3;
   const uint32_t xg = rq * kbytes + 16u * ch;
   const uint32_t xst = rq * 128u + ((ch ^ swz(rq & 15u)) << 4);  // 64-row strides keep row % 16
-  struct Xs { u32x4_t v[XL]; };
-  auto load_x = [&](int k, Xs& s) {
+  // (a chunk past the row's end: an offset past every range, rows of at most 2^21 bytes added)
+  auto step_off = [&](int k) {
     const uint32_t kb = (uint32_t)k * 128u;
-    const bool ok = kb + 16u * ch < kbytes;
-#pragma unroll
-    for (int i = 0; i < XL; ++i) {
-      uint32_t off = ok ? xg + kb + (uint32_t)i * 64u * kbytes : 0xFFFFFFF0u;
-      s.v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(xr, off, 0, 0));
-    }
+    uint32_t off = xg + kb;
+    asm volatile("" : "+v"(off));  // keep the select a select (no branch around the loads)
+    return kb + 16u * ch < kbytes ? off : 0x80000000u;
   };
-  auto store_x = [&](const Xs& s, int buf) {
-#pragma unroll
-    for (int i = 0; i < XL; ++i) lds_store_u32x4(xst + (uint32_t)buf * L::kX + 8192u * i, s.v[i]);
+  struct Xs { u32x4_t v[XL]; };
+  auto load_xp = [&](uint32_t off, Xs& s, int i) {  // piece i of the step at offset off
+    s.v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(xr, off + (uint32_t)i * 64u * kbytes, 0, 0));
   };
+  auto store_xp = [&](const Xs& s, int buf, int i) { lds_store_u32x4(xst + (uint32_t)buf * L::kX + 8192u * i, s.v[i]); };
 
   // ---- weight loads
   // I8: as x, rows n0 .. n0 + 255 (rows past N zero).
@@ -206,9 +213,7 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
   };
   const int wrows = (int)min<int64_t>(kTileN, N - n0);
   const char* wbase = reinterpret_cast<const char*>(P.w) + (int64_t)n0 * K;
-  const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<char*>(KIND == TILE_I8 ? wbase : nullptr), (short)0,
-      KIND == TILE_I8 ? (int)((uint32_t)wrows * kbytes) : 0, 0x00020000);
+  const __amdgpu_buffer_rsrc_t wr = tile_rsrc(KIND == TILE_I8 ? wbase : nullptr, KIND == TILE_I8 ? (uint32_t)wrows * kbytes : 0u);
   const int rr = KIND == TILE_TR ? (tid >> 3) : (tid >> 1), dh = tid & 1, bq = KIND == TILE_TR ? ((tid >> 1) & 3) : 0;
   const int64_t nbK = K >> 6;
   bool wv = true;
@@ -231,16 +236,11 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
       wst[q] = L::kWOff + (uint32_t)rr * 128u + ((((uint32_t)(4 * dh + q)) ^ swz((uint32_t)rr & 15u)) << 4);
   }
   const uint32_t tp = L::kTab + (BITS == 8 ? 4u * (lane & 15) : 8u * fr);
+  auto load_wp = [&](uint32_t off, Ws& s, int i) {  // I8: piece i, as load_xp
+    s.v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, off + (uint32_t)i * 64u * kbytes, 0, 0));
+  };
   auto load_w = [&](int k, Ws& s) {
-    if constexpr (KIND == TILE_I8) {
-      const uint32_t kb = (uint32_t)k * 128u;
-      const bool ok = kb + 16u * ch < kbytes;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t off = ok ? xg + kb + (uint32_t)i * 64u * kbytes : 0xFFFFFFF0u;
-        s.v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, off, 0, 0));
-      }
-    } else {
+    if constexpr (KIND != TILE_I8) {
       int64_t blk;
       bool ok = wv;
       if constexpr (KIND == TILE_CODED) {
@@ -330,22 +330,40 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
       }
   };
 
-  // ---- the steps.  I8 loads its weights with x, one step ahead; coded weights two.
+  // ---- the steps
   Xs xs;
   Ws wa, wn;
-  load_x(0, xs);
-  load_w(0, wa);
-  if constexpr (KIND != TILE_I8) load_w(1, wn);
-  store_x(xs, 0);
-  store_w_all(wa, 0);
+  {
+    const uint32_t off0 = step_off(0), off1 = step_off(1);
+#pragma unroll
+    for (int i = 0; i < XL; ++i) load_xp(off0, xs, i);
+    if constexpr (KIND == TILE_I8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load_wp(off0, wa, i);
+    } else {
+      load_w(0, wa);
+      load_w(1, wn);
+    }
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      store_xp(xs, 0, i);
+      load_xp(off1, xs, i);
+    }
+    store_w_all(wa, 0);
+    if constexpr (KIND == TILE_I8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load_wp(off1, wa, i);
+    }
+  }
   __syncthreads();
-  auto step = [&](int k, int buf, Ws& cur, Ws& nxt) {
-    // cur: the weights of step k + 1 (coded); nxt: room for step k + 2
+  // Step k: xs (and the integer weights wi) hold step k + 1's pieces, loaded during step k - 1; each is written to the
+  // other buffer and its register loaded again for step k + 2 between the products, so a
+  // load has a whole step to arrive and the writes overlap the products.
+  // cur: the codes of step k + 1; nxt: room for those of step k + 2.
+  auto step = [&](int k, int buf, Ws& wi, Ws& cur, Ws& nxt) {
     __builtin_amdgcn_sched_barrier(0);
-    load_x(k + 1, xs);
-    if constexpr (KIND == TILE_I8) load_w(k + 1, cur);
-    else load_w(k + 2, nxt);
-    __builtin_amdgcn_sched_barrier(0);
+    const uint32_t off = step_off(k + 2);
+    if constexpr (KIND != TILE_I8) load_w(k + 2, nxt);
     read_frags(buf, 0, 0);
     Lut4 lut{};
     const float ap = KIND == TILE_I8 ? 0.0f : (float)cur.q8 * cur.sc;
@@ -353,24 +371,32 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
     auto sub = [&](auto spos) {
       constexpr int S = decltype(spos)::value;
       if constexpr (S < 3) read_frags(buf, S + 1, (S + 1) & 1);
+      __builtin_amdgcn_sched_barrier(0);
       mfmas(S & 1);
-      if constexpr (KIND != TILE_I8) store_w(cur, lut, ap, spos, buf ^ 1);
+      if constexpr (S < XL) {
+        store_xp(xs, buf ^ 1, S);
+        load_xp(off, xs, S);
+      }
+      if constexpr (KIND == TILE_I8) {
+        store_w(wi, lut, ap, spos, buf ^ 1);
+        load_wp(off, wi, S);
+      } else {
+        store_w(cur, lut, ap, spos, buf ^ 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     };
     sub(std::integral_constant<int, 0>{});
     sub(std::integral_constant<int, 1>{});
     sub(std::integral_constant<int, 2>{});
     sub(std::integral_constant<int, 3>{});
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (KIND == TILE_I8) store_w_all(cur, buf ^ 1);
-    store_x(xs, buf ^ 1);
     __syncthreads();
   };
   int k = 0;
   for (; k + 1 < nsteps; k += 2) {
-    step(k, 0, wn, wa);
-    step(k + 1, 1, wa, wn);
+    step(k, 0, wa, wn, wa);
+    step(k + 1, 1, wa, wa, wn);
   }
-  if (k < nsteps) step(k, 0, wn, wa);
+  if (k < nsteps) step(k, 0, wa, wn, wa);
 
   // ---- row and column scales of the integer product
   if constexpr (KIND == TILE_I8) {
@@ -530,6 +556,97 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
     __syncthreads();
   }
 }
+
+// The adapter branch of a few-rows kernel (512 threads, rows <= 16 of x against
+// NR weight rows): the operands are loaded into registers before the weight
+// stream and staged in LDS after it, so their latency hides behind it.
+//   t: splits x M x r partials in global memory (rows row0 ..), B: rows x r bf16.
+// staged() tells whether the sizes fit (r % 8 == 0 and the pieces a thread can hold);
+// otherwise the dot product reads global memory.
+template <int NR>
+struct FewAdapter {
+  static constexpr int kT = 8192;  // floats of t staged at most
+  static constexpr int kTPieces = 4, kBPieces = NR * 8 / 512 > 0 ? NR * 8 / 512 : 1;
+  static constexpr uint32_t kBytes = kT * 4 + NR * 64 * 2;
+  f32x4_t tv[kTPieces];
+  u32x4_t bv[kBPieces];
+  bool st;
+
+  __device__ __forceinline__ void load(const float* t, int splits, int64_t M, int row0, int rows, const uint16_t* B,
+                                       int64_t brow0, int brows, int r) {
+    const int tid = threadIdx.x;
+    st = r > 0 && r <= 64 && (r & 7) == 0 && splits * rows * r <= kT;
+    if (!st) return;
+    const int per = rows * r / 4;  // pieces of one split's rows
+#pragma unroll
+    for (int i = 0; i < kTPieces; ++i) {
+      const int p = tid + 512 * i;
+      if (p < splits * per)
+        tv[i] = *reinterpret_cast<const f32x4_t*>(t + ((int64_t)(p / per) * M + row0) * r + 4 * (p % per));
+    }
+    const int rp = r >> 3;
+#pragma unroll
+    for (int i = 0; i < kBPieces; ++i) {
+      const int p = tid + 512 * i;
+      if (p < NR * rp)
+        bv[i] = *reinterpret_cast<const u32x4_t*>(B + (brow0 + min(p / rp, brows - 1)) * r + 8 * (p % rp));
+    }
+  }
+  // called by the whole workgroup; lds: kBytes of it, free after the barrier that the caller has passed
+  __device__ __forceinline__ void stage(char* lds, int splits, int rows, int r) {
+    if (!st) return;
+    const int tid = threadIdx.x;
+    float* ts = reinterpret_cast<float*>(lds);
+    const int per = rows * r / 4;
+#pragma unroll
+    for (int i = 0; i < kTPieces; ++i) {
+      const int p = tid + 512 * i;
+      if (p < splits * per) *reinterpret_cast<f32x4_t*>(ts + 4 * p) = tv[i];
+    }
+    const int rp = r >> 3;
+#pragma unroll
+    for (int i = 0; i < kBPieces; ++i) {
+      const int p = tid + 512 * i;
+      if (p < NR * rp) *reinterpret_cast<u32x4_t*>(lds + kT * 4 + 16 * p) = bv[i];
+    }
+    __syncthreads();
+    if (splits > 1) {  // the split sums, in split order
+      for (int i = tid; i < rows * r; i += 512) {
+        float v = 0.0f;
+        for (int sp = 0; sp < splits; ++sp) v += ts[sp * rows * r + i];
+        ts[i] = v;
+      }
+      __syncthreads();
+    }
+  }
+  // sum_j t[m][j] B[n][j], m and n relative to the staged rows
+  __device__ __forceinline__ float dot(const char* lds, const float* t, int splits, int64_t M, int row0, int m,
+                                       const uint16_t* B, int64_t brow0, int n, int r) const {
+    float lo = 0.0f;
+    if (st) {
+      const float* ts = reinterpret_cast<const float*>(lds) + m * r;
+      const uint16_t* bs = reinterpret_cast<const uint16_t*>(lds + kT * 4) + n * r;
+      for (int j = 0; j < r; j += 8) {
+        const u32x4_t b = *reinterpret_cast<const u32x4_t*>(bs + j);
+        const f32x4_t t0 = *reinterpret_cast<const f32x4_t*>(ts + j), t1 = *reinterpret_cast<const f32x4_t*>(ts + j + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = b[i];
+          const float ta = i < 2 ? t0[2 * i] : t1[2 * i - 4], tb = i < 2 ? t0[2 * i + 1] : t1[2 * i - 3];
+          lo = fmaf(ta, __uint_as_float(w << 16), lo);
+          lo = fmaf(tb, __uint_as_float(w & 0xFFFF0000u), lo);
+        }
+      }
+      return lo;
+    }
+    for (int j = 0; j < r; ++j) {
+      float tj = 0.0f;
+      for (int sp = 0; sp < splits; ++sp) tj += t[((int64_t)sp * M + row0 + m) * r + j];
+      lo = fmaf(tj, bf16_bits_to_f32(B[(brow0 + n) * r + j]), lo);
+    }
+    return lo;
+  }
+};
 
 // Upper bound of the row tiles of any `experts` ranges over M rows.
 inline int64_t tile_bound(int64_t M, int experts, int BM) { return M / BM + std::min<int64_t>(experts, M); }
