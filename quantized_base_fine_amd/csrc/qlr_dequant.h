@@ -37,6 +37,31 @@ __device__ __forceinline__ Codes32<BITS> load_codes32(const uint8_t* p) {
   return c;
 }
 
+// The 16 codes [16 q, 16 q + 16) of a block whose codes start at p (16-byte aligned for 8-bit
+// codes, 4-byte for the others), in the low half of the words.
+template <int BITS>
+__device__ __forceinline__ Codes32<BITS> load_codes16(const uint8_t* p, int q) {
+  Codes32<BITS> c;
+#pragma unroll
+  for (int i = 0; i < BITS; ++i) c.w[i] = 0;
+  if constexpr (BITS == 2) {
+    c.w[0] = *reinterpret_cast<const uint32_t*>(p + 4 * q);
+  } else if constexpr (BITS == 3) {
+    // 6 bytes at 6 q: the two words around them
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p + ((6 * q) & ~3));
+    const uint32_t lo = w[0], hi = w[1], sh = 16u * (q & 1);
+    c.w[0] = __builtin_amdgcn_alignbit(hi, lo, sh);
+    c.w[1] = hi >> sh;
+  } else if constexpr (BITS == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p + 8 * q);
+    c.w[0] = u.x; c.w[1] = u.y;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p + 16 * q);
+    c.w[0] = u.x; c.w[1] = u.y; c.w[2] = u.z; c.w[3] = u.w;
+  }
+  return c;
+}
+
 // LDS accesses at a byte address of the dynamic LDS block, which starts at LDS
 // address 0 (the kernel has no static LDS; the launcher checks this).
 typedef float f32x2_t __attribute__((ext_vector_type(2)));

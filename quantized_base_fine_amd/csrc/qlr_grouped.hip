@@ -170,9 +170,9 @@ __global__ __launch_bounds__(512) void k_grouped_t(const uint16_t* __restrict__ 
                                                    int experts, float* __restrict__ t) {
   __shared__ float red[kFewWaves][RT * 16 * 64];
   int e = 0, row0 = 0, row_end = 0;
-  const int total = tile_scan<16 * RT>(offsets, experts, (int)M, 0, -1, e, row0, row_end);
+  const int total = tile_scan(offsets, experts, (int)M, 0, 16 * RT, -1, e, row0, row_end);
   if ((int)blockIdx.x >= total) return;  // the whole workgroup
-  tile_scan<16 * RT>(offsets, experts, (int)M, 0, blockIdx.x, e, row0, row_end);
+  tile_scan(offsets, experts, (int)M, 0, 16 * RT, blockIdx.x, e, row0, row_end);
   e = __builtin_amdgcn_readfirstlane(e);
   row0 = __builtin_amdgcn_readfirstlane(row0);
   row_end = __builtin_amdgcn_readfirstlane(row_end);

@@ -7,7 +7,7 @@ namespace {
 
 template <int BITS>
 hipError_t launch_b(const TileArgs& a, const Levels& lv, hipStream_t s) {
-  return launch_tile_t<TILE_TR, BITS, 256>(a, lv, s);
+  return launch_tile<TILE_TR, BITS>(a, lv, s);
 }
 
 }  // namespace

@@ -210,7 +210,7 @@ hipError_t launch_i8_few(const TileArgs& a, hipStream_t s) {
 
 hipError_t launch_i8_gemm(const TileArgs& a, hipStream_t s) {
   static const Levels none{};
-  return launch_tile_t<TILE_I8, 4, 256>(a, none, s);
+  return launch_tile<TILE_I8, 4>(a, none, s);
 }
 
 }  // namespace qlr

@@ -223,7 +223,7 @@ struct TileArgs {
   void* y;
   int ydt;
   int min_rows;            // experts with at most this many rows are left out (the few-rows kernel takes them)
-  int ntiles;              // set by the launcher
+  int ntiles, rest;        // set by the launcher: column tiles; whether a last partial round is split finer
 };
 // Rows of an expert up to which the few-rows kernel takes it.
 constexpr int kFewRows = 16;

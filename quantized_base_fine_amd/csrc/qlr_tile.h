@@ -6,14 +6,13 @@
 //   KIND TILE_CODED y[m] = x[m] W'_e^T, e the row's expert  (+ adapter)
 //   KIND TILE_TR    y[m] = x[m] W'_e (x = dy, y = dx)       (+ adapter)
 //
-// Tiling.  A workgroup of 8 waves owns BM (64, 128 or 256) rows x 256 columns;
-// wave (mh, nh) = (w / 4, w % 4) the rows [mh BM / 2, + BM / 2) x columns
-// [64 nh, + 64).  A step contracts 128 bytes of each row of x: 64 bf16 or 128
+// Tiling.  A workgroup of 8 waves owns BM rows x BN columns (256 x 256 down to 64
+// x 128), divided among WM x WN waves in 32 x 32 MFMA tiles.  A step contracts 128 bytes of each row of x: 64 bf16 or 128
 // int8 elements.  MFMA operands: A = weight rows, B = x rows (32x32x16 bf16 or
 // 32x32x32 int8), so a lane's results are 4 neighbouring columns of one output
 // row and the epilogue stages whole 8- or 16-byte pieces.
 //
-// Pipeline.  Two LDS buffers of BM + 256 rows of 128 bytes, 16-byte chunks
+// Pipeline.  Two LDS buffers of BM + BN rows of 128 bytes, 16-byte chunks
 // XOR-swizzled by row (swz) so that fragment reads and tile writes are free of
 // bank conflicts.  Step k multiplies buffer k % 2 and writes the operands of
 // step k + 1, loaded into registers during step k - 1, to the other buffer
@@ -46,8 +45,6 @@ enum { TILE_I8 = 0, TILE_CODED = 1, TILE_TR = 2 };
 
 namespace {
 
-constexpr int kTileN = 256;
-
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
@@ -57,12 +54,20 @@ __device__ __forceinline__ void expert_range(const int32_t* offsets, int e, int 
   b = max(a, min(max(offsets[e + 1], 0), M));
 }
 
+// 256 x 256 tiles run one to a CU.  A last round of at most kRestMax of them would
+// leave most of the 256 CUs idle for a whole tile's time: those tiles are
+// run as 128 x 128 ones (two to a CU) instead.  Returns the tiles that stay.
+constexpr int kCus = 256, kRestMax = 144;
+__host__ __device__ __forceinline__ int tile_split(int total) {
+  const int rest = total % kCus;
+  return total > kCus && rest <= kRestMax ? total - rest : total;
+}
+
 // Tiles of BM rows over the ranges holding more than min_rows rows: with
 // `want` < 0 returns the tile count, else finds tile `want` (expert and its
 // first and end row).  Called by whole waves.
-template <int BM>
-__device__ __forceinline__ int tile_scan(const int32_t* offsets, int E, int M, int min_rows, int want, int& e_out,
-                                         int& row0, int& row_end) {
+__device__ __forceinline__ int tile_scan(const int32_t* offsets, int E, int M, int min_rows, int BM, int want,
+                                         int& e_out, int& row0, int& row_end) {
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int e0 = 0; e0 < E; e0 += 64) {
@@ -90,16 +95,17 @@ __device__ __forceinline__ int tile_scan(const int32_t* offsets, int E, int M, i
   return before;
 }
 
-template <int KIND, int BITS, int BM>
+template <int KIND, int BITS, int BM, int BN>
 struct TileLds {
-  static constexpr uint32_t kX = BM * 128, kW = 256 * 128;
+  static constexpr uint32_t kX = BM * 128, kW = BN * 128;
   static constexpr uint32_t kWOff = 2 * kX;
   static constexpr uint32_t kTab = 2 * (kX + kW);  // level table of the widths that use one
   static constexpr uint32_t kTabBytes = (KIND == TILE_I8 || BITS == 4) ? 0
                                         : BITS == 8                    ? 256 * 16 * 4
                                                                        : PairTableF32<BITS>::kBytes;
-  // the epilogue's staging of BM / 2 output rows (float32 at most) overlays the buffers
-  static constexpr uint32_t kStage = (BM / 2) * (256 * 4 + 16);
+  // the epilogue's staging of BM / kPasses output rows (float32 at most) overlays the buffers
+  static constexpr int kPasses = BM * BN > 256 * 128 ? 2 : 1;
+  static constexpr uint32_t kStage = (BM / kPasses) * (BN * 4 + 16);
   static constexpr uint32_t kBytes = kTab + kTabBytes > kStage ? kTab + kTabBytes : kStage;
   static_assert(kBytes <= 160 * 1024, "LDS budget");
 };
@@ -122,44 +128,61 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void* p, uint3
                                            (int)__builtin_amdgcn_readfirstlane(n), 0x00020000);
 }
 
-template <int KIND, int BITS, int BM>
+template <int KIND, int BITS, int BM, int BN>
 __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
-  using L = TileLds<KIND, BITS, BM>;
-  constexpr int MT = BM / 64;  // 32-row tiles of a wave
+  using L = TileLds<KIND, BITS, BM, BN>;
+  constexpr int WM = (BN == 256 || BM == 64) ? 2 : 4, WN = 8 / WM;
+  constexpr int MT = BM / WM / 32, NT = BN / WN / 32;  // MFMA tiles of a wave
   constexpr int XL = BM / 64;  // 16-byte pieces of x per thread and step
+  constexpr int WL = BN / 64;  // the same of an int8 weight; 8-code parts of a coded one
+  constexpr int CPT = BN / 8;  // codes per thread and step
   extern __shared__ uint32_t smem[];
   (void)smem;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 31, h = lane >> 5;
 
   // ---- which tile.  Workgroup b runs on XCD b % 8; each XCD takes a contiguous range of tiles.
-  const int ntiles = P.ntiles;
+  // With P.rest the tiles are counted in 256 x 256 ones and those of a last partial
+  // round are left to the 128 x 128 kernel (tile_split): this kernel takes either part.
   int e = 0, row0 = 0, row_end = (int)P.M, tile_n;
   {
-    int mt_total;
-    if (P.offsets) mt_total = tile_scan<BM>(P.offsets, P.experts, (int)P.M, P.min_rows, -1, e, row0, row_end);
-    else mt_total = (int)((P.M + BM - 1) / BM);
-    const int64_t total = (int64_t)mt_total * ntiles;
-    const int64_t per = (total + 7) / 8, loc = blockIdx.x >> 3;
-    const int64_t tile = (int64_t)(blockIdx.x & 7) * per + loc;
-    if (loc >= per || tile >= total) return;  // the whole workgroup, before any barrier
-    const int mi = (int)(tile / ntiles);
+    constexpr int kBig = 256;
+    const bool sub = P.rest && BM < kBig;  // the 128 x 128 kernel on the rest of the 256 x 256 tiles
+    constexpr int kSubM = kBig / BM, kSub = kSubM * (kBig / BN);
+    const int step_m = sub ? kBig : BM, ntiles = sub ? (P.ntiles + kBig / BN - 1) / (kBig / BN) : P.ntiles;
+    const int mt_total = P.offsets ? tile_scan(P.offsets, P.experts, (int)P.M, P.min_rows, step_m, -1, e, row0, row_end)
+                                   : (int)((P.M + step_m - 1) / step_m);
+    const int total = mt_total * ntiles;
+    const int split = P.rest ? tile_split(total) : total;
+    const int first = sub ? split : 0, count = sub ? (total - split) * kSub : split;
+    const int per = (count + 7) / 8, loc = (int)(blockIdx.x >> 3);
+    const int tile = (int)(blockIdx.x & 7) * per + loc;
+    if (loc >= per || tile >= count) return;  // the whole workgroup, before any barrier
+    const int big = sub ? first + tile / kSub : tile;
+    const int mi = big / ntiles;
     if (P.offsets) {
       row_end = 0;
-      tile_scan<BM>(P.offsets, P.experts, (int)P.M, P.min_rows, mi, e, row0, row_end);
+      tile_scan(P.offsets, P.experts, (int)P.M, P.min_rows, step_m, mi, e, row0, row_end);
     } else {
-      row0 = mi * BM;
+      row0 = mi * step_m;
     }
+    tile_n = big % ntiles;
+    if (sub) {
+      const int q = tile % kSub;
+      row0 += (q % kSubM) * BM;
+      tile_n = tile_n * (kBig / BN) + q / kSubM;
+      if (row0 >= row_end || tile_n >= P.ntiles) return;
+    }
+    // (scalar: a buffer resource needs scalar words)
     e = __builtin_amdgcn_readfirstlane(e);
     row0 = __builtin_amdgcn_readfirstlane(row0);
     row_end = __builtin_amdgcn_readfirstlane(row_end);
-    // (scalar: the division runs on the vector unit, and a buffer resource needs scalar words)
-    tile_n = __builtin_amdgcn_readfirstlane((int)(tile % ntiles));
+    tile_n = __builtin_amdgcn_readfirstlane(tile_n);
   }
   const int mrows = min(BM, row_end - row0);
   const int64_t N = P.N, K = P.K;
   const int64_t NO = KIND == TILE_TR ? K : N;            // output columns
-  const int n0 = tile_n * kTileN;
+  const int n0 = tile_n * BN;
   const uint32_t kbytes = (uint32_t)(KIND == TILE_I8 ? K : KIND == TILE_TR ? 2 * N : 2 * K);  // bytes of one x row
   const int nsteps = (int)((kbytes + 127) / 128);
 
@@ -203,18 +226,19 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
 
   // ---- weight loads
   // I8: as x, rows n0 .. n0 + 255 (rows past N zero).
-  // CODED: thread = row tid / 2, codes [32 dh, + 32) of the step's block.
-  // TR: thread = weight row 64 k + tid / 8, codes [32 dh, + 32) of block column n0 / 64 + bq.
+  // CODED: thread = row tid / TPB, codes [CPT dh, + CPT) of the step's block (TPB threads share a block).
+  // TR: thread = weight row 64 k + tid / 8, codes [CPT dh, + CPT) of block column n0 / 64 + bq.
   struct Ws {
-    u32x4_t v[KIND == TILE_I8 ? 4 : 1];
+    u32x4_t v[KIND == TILE_I8 ? WL : 1];
     Codes32<BITS> c;
     uint32_t q8;
     float sc;
   };
-  const int wrows = (int)min<int64_t>(kTileN, N - n0);
+  const int wrows = (int)min<int64_t>(BN, N - n0);
   const char* wbase = reinterpret_cast<const char*>(P.w) + (int64_t)n0 * K;
   const __amdgpu_buffer_rsrc_t wr = tile_rsrc(KIND == TILE_I8 ? wbase : nullptr, KIND == TILE_I8 ? (uint32_t)wrows * kbytes : 0u);
-  const int rr = KIND == TILE_TR ? (tid >> 3) : (tid >> 1), dh = tid & 1, bq = KIND == TILE_TR ? ((tid >> 1) & 3) : 0;
+  constexpr int TPB = 64 / CPT;
+  const int rr = KIND == TILE_TR ? (tid >> 3) : tid / TPB, dh = tid % TPB, bq = KIND == TILE_TR ? (tid & 7) / TPB : 0;
   const int64_t nbK = K >> 6;
   bool wv = true;
   int64_t wblk = 0;
@@ -226,14 +250,14 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
     wv = wcol < nbK;
     wblk = (int64_t)e * N * nbK + (wv ? wcol : nbK - 1);
   }
-  uint32_t wst[4];
+  uint32_t wst[WL];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < WL; ++q) {
     if constexpr (KIND == TILE_TR)
       wst[q] = L::kWOff + (uint32_t)(bq >> 1) * 16384u + (uint32_t)rr * 256u +
-               (tr_chunk((uint32_t)(8 * (bq & 1) + 4 * dh + q), (uint32_t)rr) << 4);
+               (tr_chunk((uint32_t)(8 * (bq & 1) + WL * dh + q), (uint32_t)rr) << 4);
     else
-      wst[q] = L::kWOff + (uint32_t)rr * 128u + ((((uint32_t)(4 * dh + q)) ^ swz((uint32_t)rr & 15u)) << 4);
+      wst[q] = L::kWOff + (uint32_t)rr * 128u + ((((uint32_t)(WL * dh + q)) ^ swz((uint32_t)rr & 15u)) << 4);
   }
   const uint32_t tp = L::kTab + (BITS == 8 ? 4u * (lane & 15) : 8u * fr);
   auto load_wp = [&](uint32_t off, Ws& s, int i) {  // I8: piece i, as load_xp
@@ -250,13 +274,14 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
         ok = wv && n < N;  // rows past N: scale 0
         blk = wblk + min<int64_t>(n, N - 1) * nbK;
       }
-      s.c = load_codes32<BITS>(P.w + blk * (8 * BITS) + dh * (4 * BITS));
+      if constexpr (CPT == 32) s.c = load_codes32<BITS>(P.w + blk * (8 * BITS) + dh * (4 * BITS));
+      else s.c = load_codes16<BITS>(P.w + blk * (8 * BITS), dh);
       s.q8 = P.q8[blk];
       s.sc = P.cst[blk >> 8];
       if (!ok) s.q8 = 0;
     }
   };
-  // part I (0..3) of the thread's weights into buffer buf: I8 one loaded piece, coded 8 dequantized weights
+  // part I (0 .. WL - 1) of the thread's weights into buffer buf: I8 one loaded piece, coded 8 dequantized weights
   auto store_w = [&](const Ws& s, const Lut4& lut, float ap, auto part, int buf) {
     constexpr int I = decltype(part)::value;
     if constexpr (KIND == TILE_I8) {
@@ -274,35 +299,38 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
     if constexpr (KIND != TILE_I8 && BITS == 4) lut = make_lut4(lv, ap);
     store_w(s, lut, ap, std::integral_constant<int, 0>{}, buf);
     store_w(s, lut, ap, std::integral_constant<int, 1>{}, buf);
-    store_w(s, lut, ap, std::integral_constant<int, 2>{}, buf);
-    store_w(s, lut, ap, std::integral_constant<int, 3>{}, buf);
+    if constexpr (WL == 4) {
+      store_w(s, lut, ap, std::integral_constant<int, 2>{}, buf);
+      store_w(s, lut, ap, std::integral_constant<int, 3>{}, buf);
+    }
   };
 
   // ---- fragments: MFMA step s (0..3) of a buffer, row fr (+ 32 per tile), chunk 2 s + h
-  const int mh = wave >> 2, nh = wave & 3;
+  const int mh = wave / WN, nh = wave % WN;
   uint32_t xb[4], wb[4];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const uint32_t fo = (uint32_t)(fr * 128) + ((((uint32_t)(2 * s + h)) ^ swz((uint32_t)fr & 15u)) << 4);
-    xb[s] = (uint32_t)(mh * (BM / 2) * 128) + fo;
-    wb[s] = L::kWOff + (uint32_t)(nh * 64 * 128) + fo;
+    xb[s] = (uint32_t)(mh * (BM / WM) * 128) + fo;
+    wb[s] = L::kWOff + (uint32_t)(nh * (BN / WN) * 128) + fo;
   }
-  uint32_t tbo[2];
+  uint32_t tbo[NT];
   {
     const uint32_t g = (uint32_t)lane >> 4, sp = (uint32_t)lane & 15u;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint32_t chunk = 8u * (uint32_t)(nh & 1) + 4u * c + 2u * (g & 1u) + ((sp >> 1) & 1u);
-      tbo[c] = L::kWOff + (uint32_t)(nh >> 1) * 16384u + (8u * h + (sp >> 2)) * 256u + (tr_chunk(chunk, sp >> 2) << 4) +
+    for (int c = 0; c < NT; ++c) {
+      const uint32_t col = (uint32_t)(nh * (BN / WN) + 32 * c);
+      const uint32_t chunk = ((col & 127u) >> 3) + 2u * (g & 1u) + ((sp >> 1) & 1u);
+      tbo[c] = L::kWOff + (col >> 7) * 16384u + (8u * h + (sp >> 2)) * 256u + (tr_chunk(chunk, sp >> 2) << 4) +
                8u * (sp & 1u);
     }
   }
-  u32x4_t fx[2][MT], fw[2][2];
+  u32x4_t fx[2][MT], fw[2][NT];
   auto read_frags = [&](int buf, int s, int slot) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) fx[slot][i] = lds_u32x4(xb[s] + (uint32_t)buf * L::kX + 4096u * i);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < NT; ++c) {
       if constexpr (KIND == TILE_TR) {
         const uint32_t ad = tbo[c] + (uint32_t)buf * L::kW + 4096u * s;
         const u16x4_t lo = lds_tr16(ad), hi = lds_tr16(ad + 1024u);
@@ -313,18 +341,18 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
       }
     }
   };
-  f32x16_t acc[MT][2];
+  f32x16_t acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < NT; ++c)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][c][v] = 0.0f;  // also the integer zero
   auto mfmas = [&](int slot) {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < NT; ++c) {
         if constexpr (KIND == TILE_I8) acc[i][c] = tile_mfma_i8(fw[slot][c], fx[slot][i], acc[i][c]);
         else acc[i][c] = tile_mfma(fw[slot][c], fx[slot][i], acc[i][c]);
       }
@@ -339,7 +367,7 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
     for (int i = 0; i < XL; ++i) load_xp(off0, xs, i);
     if constexpr (KIND == TILE_I8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) load_wp(off0, wa, i);
+      for (int i = 0; i < WL; ++i) load_wp(off0, wa, i);
     } else {
       load_w(0, wa);
       load_w(1, wn);
@@ -352,7 +380,7 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
     store_w_all(wa, 0);
     if constexpr (KIND == TILE_I8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) load_wp(off1, wa, i);
+      for (int i = 0; i < WL; ++i) load_wp(off1, wa, i);
     }
   }
   __syncthreads();
@@ -378,10 +406,14 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
         load_xp(off, xs, S);
       }
       if constexpr (KIND == TILE_I8) {
-        store_w(wi, lut, ap, spos, buf ^ 1);
-        load_wp(off, wi, S);
-      } else {
+        if constexpr (S < WL) {
+          store_w(wi, lut, ap, spos, buf ^ 1);
+          load_wp(off, wi, S);
+        }
+      } else if constexpr (WL == 4) {
         store_w(cur, lut, ap, spos, buf ^ 1);
+      } else if constexpr (S % 2 == 0) {
+        store_w(cur, lut, ap, std::integral_constant<int, S / 2>{}, buf ^ 1);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -403,14 +435,14 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
     float sx[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      const int m = mh * (BM / 2) + 32 * i + fr;
+      const int m = mh * (BM / WM) + 32 * i + fr;
       sx[i] = P.sx[row0 + min(m, mrows - 1)];
     }
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < NT; ++c)
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const int n = n0 + 64 * nh + 32 * c + 8 * (v >> 2) + 4 * h + (v & 3);
+        const int n = n0 + nh * (BN / WN) + 32 * c + 8 * (v >> 2) + 4 * h + (v & 3);
         const float sw = P.sw[min<int64_t>(n, N - 1)];
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[i][c][v] = (float)__float_as_int(acc[i][c][v]) * sx[i] * sw;
@@ -461,8 +493,8 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
       if constexpr (KIND == TILE_TR) {
         // A[j0 + row][n0 ..]: rows 0..31 and 32..63 hold the same 32 adapter rows
         const uint16_t* Ae = P.ab + (int64_t)e * r * K;
-        for (int idx = tid; idx < 32 * 32; idx += 512) {
-          const int row = idx >> 5, c = idx & 31;
+        for (int idx = tid; idx < 32 * (BN / 8); idx += 512) {
+          const int row = idx / (BN / 8), c = idx % (BN / 8);
           const int64_t col = n0 + 8 * c;
           u32x4_t v = zero4;
           if (j0 + row < r && col < K) v = *reinterpret_cast<const u32x4_t*>(Ae + (int64_t)(j0 + row) * K + col);
@@ -473,7 +505,7 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
       } else {
         // [B[n][j0 ..] | the same]
         const uint16_t* Be = P.ab + (int64_t)e * N * r;
-        for (int idx = tid; idx < kTileN * 4; idx += 512) {
+        for (int idx = tid; idx < BN * 4; idx += 512) {
           const int row = idx >> 2, c = idx & 3, jb = j0 + 8 * c;
           u32x4_t v = zero4;
           if (n0 + row < N && jb < r) {
@@ -500,27 +532,29 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) acc[i][c] = tile_mfma(fw[0][c], fx[0][i], acc[i][c]);
+          for (int c = 0; c < NT; ++c) acc[i][c] = tile_mfma(fw[0][c], fx[0][i], acc[i][c]);
       }
       __syncthreads();
     }
   }
 
-  // ---- output: the rows of one wave row-half at a time, staged row-major in LDS, stored in 16-byte pieces
+  // ---- output: staged row-major in LDS (BM / kPasses rows at a time), stored in 16-byte pieces
+  constexpr int RP = BM / L::kPasses;
   const int es = P.ydt == DT_F32 ? 4 : 2;
-  const uint32_t rs = 256u * es + 16u;
+  const uint32_t rs = (uint32_t)BN * es + 16u;
   const bool vec = (NO * es) % 16 == 0;
-  const int cpr = 16 * es;  // 16-byte pieces of a staged row
-  for (int p = 0; p < 2; ++p) {
-    if (p * (BM / 2) >= mrows) break;
-    if (mh == p) {
+  const int cpr = BN * es / 16;  // 16-byte pieces of a staged row (a power of two)
+  for (int p = 0; p < L::kPasses; ++p) {
+    if (p * RP >= mrows) break;
+    if (mh * (BM / WM) / RP == p) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < NT; ++c)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint32_t ad = (uint32_t)(32 * i + fr) * rs + (uint32_t)(64 * nh + 32 * c + 8 * q + 4 * h) * es;
+            const uint32_t ad = (uint32_t)(mh * (BM / WM) - p * RP + 32 * i + fr) * rs +
+                                (uint32_t)(nh * (BN / WN) + 32 * c + 8 * q + 4 * h) * es;
             const float v0 = acc[i][c][4 * q], v1 = acc[i][c][4 * q + 1], v2 = acc[i][c][4 * q + 2], v3 = acc[i][c][4 * q + 3];
             if (es == 4) {
               lds_store_f32x4(ad, f32x4_t{v0, v1, v2, v3});
@@ -531,13 +565,13 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
           }
     }
     __syncthreads();
-    const int rows = min(BM / 2, mrows - p * (BM / 2));
+    const int rows = min(RP, mrows - p * RP);
     for (int idx = tid; idx < rows * cpr; idx += 512) {
-      const int row = es == 4 ? idx >> 6 : idx >> 5, c = idx & (cpr - 1);
+      const int row = es == 4 ? idx / (BN / 4) : idx / (BN / 8), c = idx & (cpr - 1);
       const int64_t col = n0 + c * (16 / es);
       if (col >= NO) continue;
       const u32x4_t v = lds_u32x4((uint32_t)row * rs + 16u * c);
-      char* dst = reinterpret_cast<char*>(P.y) + ((int64_t)(row0 + p * (BM / 2) + row) * NO + col) * es;
+      char* dst = reinterpret_cast<char*>(P.y) + ((int64_t)(row0 + p * RP + row) * NO + col) * es;
       if (vec) {
         *reinterpret_cast<u32x4_t*>(dst) = v;
       } else {
@@ -651,10 +685,10 @@ struct FewAdapter {
 // Upper bound of the row tiles of any `experts` ranges over M rows.
 inline int64_t tile_bound(int64_t M, int experts, int BM) { return M / BM + std::min<int64_t>(experts, M); }
 
-template <int KIND, int BITS, int BM>
+template <int KIND, int BITS, int BM, int BN>
 hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
-  auto kern = k_tile<KIND, BITS, BM>;
-  constexpr int shmem = (int)TileLds<KIND, BITS, BM>::kBytes;
+  auto kern = k_tile<KIND, BITS, BM, BN>;
+  constexpr int shmem = (int)TileLds<KIND, BITS, BM, BN>::kBytes;
   static std::once_flag once;
   static hipError_t setup;
   std::call_once(once, [&] {
@@ -665,14 +699,43 @@ hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
   });
   if (setup != hipSuccess) return setup;
   const int64_t no = KIND == TILE_TR ? a.K : a.N;
-  a.ntiles = (int)((no + kTileN - 1) / kTileN);
-  const int64_t tiles = (a.offsets ? tile_bound(a.M, a.experts, BM) : (a.M + BM - 1) / BM) * a.ntiles;
+  a.ntiles = (int)((no + BN - 1) / BN);
+  int64_t tiles = (a.offsets ? tile_bound(a.M, a.experts, BM) : (a.M + BM - 1) / BM) * a.ntiles;
+  if (a.rest && BM < 256) tiles = kRestMax * (256 / BM) * (256 / BN);
   if (tiles <= 0) return hipSuccess;
   if (tiles > INT32_MAX - 8) return hipErrorInvalidValue;
   hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, shmem);
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(kern, dim3((unsigned)(8 * ((tiles + 7) / 8))), dim3(512), shmem, s, a, lv);
   return hipGetLastError();
+}
+
+// The tile shape, from the sizes the host knows (the rows of an expert only by their
+// mean).  256 x 256 tiles multiply most per byte moved and watt, but need a
+// round of them to fill the 256 CUs and ranges of a few hundred rows to be
+// full: at 8192 x 4096 x 4096 in 8 ranges with 4-bit codes they took 359 us, 128 x 128 ones 434 and 64 x 128 ones
+// 629; at 777 rows in 64 ranges of 1408 x 2048 (2-bit) 55, 27 and 23 us.
+template <int KIND, int BITS>
+hipError_t launch_tile(TileArgs a, const Levels& lv, hipStream_t s) {
+  const int64_t no = KIND == TILE_TR ? a.K : a.N;
+  // tiles of b x c: whole ones, and half a partial one per range
+  auto count = [&](int64_t b, int64_t c) {
+    const int64_t nt = (no + c - 1) / c;
+    return a.offsets ? (a.M / b + (std::min<int64_t>(a.experts, a.M) + 1) / 2) * nt : (a.M + b - 1) / b * nt;
+  };
+  const bool short_ranges = a.offsets && a.M < (int64_t)a.experts * 96;
+  if (!short_ranges && count(256, 256) >= 192) {
+    a.rest = 1;
+    const hipError_t e = launch_tile_t<KIND, BITS, 256, 256>(a, lv, s);
+    if (e != hipSuccess) return e;
+    // the rest kernel: known not to be needed only without offsets
+    const int64_t total = a.offsets ? INT_MAX : count(256, 256);
+    if (!a.offsets && tile_split((int)total) == (int)total) return hipSuccess;
+    return launch_tile_t<KIND, BITS, 128, 128>(a, lv, s);
+  }
+  a.rest = 0;
+  if (a.M < (a.offsets ? (int64_t)a.experts * 64 : 65) || count(128, 128) < 256) return launch_tile_t<KIND, BITS, 64, 128>(a, lv, s);
+  return launch_tile_t<KIND, BITS, 128, 128>(a, lv, s);
 }
 
 }  // namespace
