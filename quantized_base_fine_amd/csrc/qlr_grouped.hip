@@ -10,126 +10,166 @@ namespace {
 
 // ---------------------------------------------------------------- experts of 1 .. 16 rows
 //
-// Bound by the stream of the experts' codes.  A workgroup of 8 waves takes 16 G
-// weight rows of one expert; the waves share K in pairs of 64-element blocks
-// (wave w the pairs w, w + 8, ...).  A lane holds 32 consecutive codes of one
-// weight row (row lane % 16, codes 32 (lane / 16) .. + 32 of the pair: one load),
-// dequantizes them to bf16 (scaled levels) straight into four MFMA A fragments
-// and multiplies them with the expert's rows as B (16x16x32, token lanes past
-// the expert's rows hold zeros).  The waves' sums are added through LDS in wave
-// order, then scale t B^T.
-constexpr int kFewWaves = 8;
+// Bound by the stream of the experts' codes, so the dequantization has to stay
+// off its way: levels come from a table in LDS (pairs of codes, bf16, 32 copies
+// that keep a wave's lookups on different banks: about 50 vector instructions per KB of
+// 4-bit codes, where forming scaled levels in registers took 144 and bound the kernel), and
+// the block's scale multiplies its products.
+//   y[m][n] = sum over blocks of scale[n][block] (sum_k x[m][k] level[n][k])
+// A workgroup of 8 waves takes 16 RS weight rows of one expert: RS sets of 16
+// rows, the 8 / RS waves of a set sharing K in ranges of 64-element blocks.  Per
+// block a lane loads 16 codes of one row, each quad of lanes a row's whole
+// block (8-byte pieces in MFMA fragment order read at 4.0 TB/s, quads on one row's bytes at 5.5),
+// lane permutes bring them to fragment order, and two 16x16x32 MFMAs (the expert's rows
+// as A) start from zero.  Codes are loaded kFewChunk to 2 kFewChunk blocks ahead; the rows' elements two
+// blocks ahead, four rows to a load, and go through a slice of LDS of the wave's
+// own (a wave's LDS accesses run in order).  The waves' sums are added through LDS
+// in wave order, then scale t B^T.
+constexpr int kFewWaves = 8, kFewChunk = 2;
+constexpr uint32_t kXRow = 256 + 16, kXSlice = 16 * kXRow;  // a wave's slice: two blocks of 16 rows, padded
 
 template <int BITS>
 struct FewTab {
-  static constexpr uint32_t kBytes = BITS == 4 ? 0 : BITS == 8 ? 256 * 16 * 4 : PairTableF32<BITS>::kBytes;
-  // the waves' sums (the staging of the levels shares the area)
-  __host__ __device__ static constexpr uint32_t kRedBytes(int G) { return kFewWaves * 16 * 16 * 4 * G; }
+  static constexpr int kEntries = BITS == 8 ? 256 : 1 << (2 * BITS);
+  static constexpr uint32_t kBytes = kEntries * 128;
 };
 
-template <int BITS, int G>
-__global__ __launch_bounds__(512) void k_grouped_few(TileArgs P, Levels lv) {
-  constexpr uint32_t kTab = 0, kRed = FewTab<BITS>::kBytes;
+// Words of a lane's 16 codes.
+template <int BITS>
+constexpr int kFewWords = BITS == 8 ? 4 : BITS == 2 ? 1 : 2;
+
+// bf16 levels of the lane's 16 codes, pairs in code order; tl = 4 (lane % 32).
+template <int BITS>
+__device__ __forceinline__ void few_levels(const uint32_t (&w)[kFewWords<BITS>], uint32_t tl, uint32_t (&o)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (BITS == 8) {
+      const uint32_t v = w[j >> 1] >> (16 * (j & 1));
+      o[j] = __builtin_amdgcn_perm(lds_word(((v >> 8) & 255u) << 7 | tl), lds_word((v & 255u) << 7 | tl), 0x05040100u);
+    } else if constexpr (BITS == 3) {
+      const int bit = 6 * j, wd = bit >> 5, sh = bit & 31;
+      const uint32_t v = sh + 6 > 32 ? __builtin_amdgcn_alignbit(w[wd < 1 ? wd + 1 : wd], w[wd], sh) : w[wd] >> sh;
+      o[j] = lds_word((v & 63u) << 7 | tl);
+    } else {
+      constexpr uint32_t mask = (1u << (2 * BITS)) - 1;
+      o[j] = lds_word(((w[(2 * BITS * j) >> 5] >> ((2 * BITS * j) & 31)) & mask) << 7 | tl);
+    }
+  }
+}
+
+template <int BITS, int RS>
+__global__ __launch_bounds__(512, 4) void k_grouped_few(TileArgs P, Levels lv) {
+  constexpr int NR = 16 * RS, KS = kFewWaves / RS, NW = kFewWords<BITS>;
+  typedef FewAdapter<NR, 1024> Adapter;
+  constexpr uint32_t kRed = FewTab<BITS>::kBytes;
   extern __shared__ uint32_t smem[];
   int a, b;
   const int e = blockIdx.y;
   expert_range(P.offsets, e, (int)P.M, a, b);
   const int rows = b - a;
   if (rows < 1 || rows > kFewRows) return;  // the whole workgroup
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if constexpr (BITS != 4) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t N = P.N, K = P.K, nb = K >> 6;
+  const int n0 = blockIdx.x * NR, rs = wave / KS, ks = wave % KS;
+  const int row = lane >> 2, g = lane & 3, src = (4 * (lane & 15) + (lane >> 4)) << 2;  // of the loads; the permute's source
+  const int frow = lane & 15, fg = lane >> 4;                                           // of the fragments
+  const int b0 = (int)(nb * ks / KS), b1 = (int)(nb * (ks + 1) / KS);
+  const int64_t wblk = ((int64_t)e * N + min<int64_t>(n0 + 16 * rs + row, N - 1)) * nb;
+  // x loads: piece lane % 16 of rows lane / 16 + 4 i of the two blocks
+  const int xr = lane >> 4, xc = lane & 15;
+  const uint16_t* xp = reinterpret_cast<const uint16_t*>(P.x) + (int64_t)a * K + 8 * xc;
+  struct Ld {
+    uint32_t c[kFewChunk][NW];
+    uint32_t q8[kFewChunk];
+    float sc[kFewChunk];
+  };
+  const u32x4_t zero4 = {0u, 0u, 0u, 0u};
+  auto load = [&](int bl, Ld& d) {  // (blocks past the wave's range repeat its last one and are not used)
+#pragma unroll
+    for (int i = 0; i < kFewChunk; ++i) {
+      const int64_t blk = wblk + max(min(bl + i, b1 - 1), 0);
+      const Codes32<BITS> c = load_codes16<BITS>(P.w + blk * (8 * BITS), g);
+#pragma unroll
+      for (int j = 0; j < NW; ++j) d.c[i][j] = c.w[j];
+      d.q8[i] = P.q8[blk];
+      d.sc[i] = P.cst[blk >> 8];
+    }
+  };
+  u32x4_t xv[4];
+  auto load_x = [&](int bl) {
+    const int64_t k = (int64_t)bl * 64;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * i < rows)  // (the same for the whole workgroup)
+        xv[i] = 4 * i + xr < rows && k + 8 * xc < K && bl < b1
+                    ? *reinterpret_cast<const u32x4_t*>(xp + (int64_t)(4 * i + xr) * K + k) : zero4;
+  };
+  Ld d0, d1;
+  load(b0, d0);
+  load_x(b0);
+  Adapter ad;
+  ad.load(P.t, 1, P.M, a, rows, P.ab + (int64_t)e * N * P.r, n0, (int)min<int64_t>(NR, N - n0), P.r);
+  // the level table, while the first loads are on their way
+  {
     float* sL = reinterpret_cast<float*>(smem) + kRed / 4;
     stage_levels<1 << BITS>(lv, sL);
     __syncthreads();
-    float* tab = reinterpret_cast<float*>(smem);
-    if constexpr (BITS == 8) {
-      for (int i = tid; i < 256 * 16; i += 512) tab[i] = sL[i >> 4];
-    } else {
-      constexpr int NL = 1 << BITS;
-      for (int i = tid; i < PairTableF32<BITS>::kEntries * 32; i += 512) {
-        tab[2 * i] = sL[(i >> 5) & (NL - 1)];
-        tab[2 * i + 1] = sL[(i >> 5) >> BITS];
-      }
+    constexpr int NL = 1 << BITS;
+    for (int i = tid; i < FewTab<BITS>::kEntries * 32; i += 512) {
+      const int en = i >> 5;
+      smem[i] = BITS == 8 ? f32_to_bf16_bits(sL[en]) : pack_bf16x2(sL[en & (NL - 1)], sL[en >> BITS]);
     }
     __syncthreads();
   }
-  const int64_t N = P.N, K = P.K, nb = K >> 6;
-  const int np = (int)((nb + 1) / 2);
-  const int n0 = blockIdx.x * 16 * G;
-  const int row = lane & 15, g = lane >> 4;
-  const uint32_t tp = kTab + (BITS == 8 ? 4u * (lane & 15) : 8u * (lane & 31));
-  const uint16_t* xp = reinterpret_cast<const uint16_t*>(P.x) + (int64_t)(a + min(row, rows - 1)) * K;
-  int64_t wblk[G];
+  const uint32_t tl = 4u * (lane & 31);
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  char* const xs = reinterpret_cast<char*>(smem) + kRed + wave * kXSlice;
+  auto compute = [&](int bl, const Ld& d) {
 #pragma unroll
-  for (int i = 0; i < G; ++i) wblk[i] = ((int64_t)e * N + min<int64_t>(n0 + 16 * i + row, N - 1)) * nb;
-  FewAdapter<16 * G> ad;
-  ad.load(P.t, 1, P.M, a, rows, P.ab + (int64_t)e * N * P.r, n0, (int)min<int64_t>(16 * G, N - n0), P.r);
-  f32x4_t acc[G];
+    for (int i = 0; i < kFewChunk; ++i) {
+      if (bl + i >= b1) return;  // (the same for the whole wave)
+      if (i % 2 == 0) {
 #pragma unroll
-  for (int i = 0; i < G; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const u32x4_t zero4 = {0u, 0u, 0u, 0u};
-  struct Ld {
-    u32x4_t x[4];
-    Codes32<BITS> c[G];
-    uint32_t q8[G];
-    float sc[G];
-  };
-  auto load = [&](int p, Ld& d) {
-    const int64_t blk = 2 * (int64_t)p + (g >> 1);
-    const bool ok = p < np && blk < nb;
-    const int64_t bl = ok ? blk : 0;
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      d.c[i] = load_codes32<BITS>(P.w + (wblk[i] + bl) * (8 * BITS) + (g & 1) * (4 * BITS));
-      d.q8[i] = ok ? P.q8[wblk[i] + bl] : 0u;
-      d.sc[i] = P.cst[(wblk[i] + bl) >> 8];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      d.x[i] = ok && row < rows ? *reinterpret_cast<const u32x4_t*>(xp + bl * 64 + 32 * (g & 1) + 8 * i) : zero4;
-  };
-  auto compute = [&](const Ld& d) {
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      const float ap = (float)d.q8[i] * d.sc[i];
-      uint32_t o[16];
-      if constexpr (BITS == 4) {
-        const Lut4 lut = make_lut4(lv, ap);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) lut4_word(d.c[i].w[j], lut, o + 4 * j);
-      } else {
-        dequant_pairs<BITS, 0, 16>(d.c[i], ap, tp, o);
+        for (int t = 0; t < 4; ++t)
+          if (4 * t < rows) *reinterpret_cast<u32x4_t*>(xs + (4 * t + xr) * kXRow + 16 * xc) = xv[t];
+        load_x(bl + i + 2);
       }
+      uint32_t w[NW], o[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i] = mfma16x16x32(as_bf16x8(u32x4_t{o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]}), as_bf16x8(d.x[j]),
-                              acc[i]);
+      for (int j = 0; j < NW; ++j) w[j] = (uint32_t)__builtin_amdgcn_ds_bpermute(src, (int)d.c[i][j]);
+      const float ap = __int_as_float(__builtin_amdgcn_ds_bpermute(src, __float_as_int((float)d.q8[i] * d.sc[i])));
+      few_levels<BITS>(w, tl, o);
+      const char* xf = xs + frow * kXRow + 128 * (i % 2) + 32 * fg;
+      // (rows past the expert's hold anything: they only reach results that are dropped)
+      f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+      s = mfma16x16x32(as_bf16x8(*reinterpret_cast<const u32x4_t*>(xf)), as_bf16x8(u32x4_t{o[0], o[1], o[2], o[3]}), s);
+      s = mfma16x16x32(as_bf16x8(*reinterpret_cast<const u32x4_t*>(xf + 16)), as_bf16x8(u32x4_t{o[4], o[5], o[6], o[7]}), s);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[v] = fmaf(ap, s[v], acc[v]);
     }
   };
-  Ld d0, d1;
-  load(wave, d0);
-  for (int p = wave; p < np; p += 2 * kFewWaves) {
-    load(p + kFewWaves, d1);
-    compute(d0);
-    load(p + 2 * kFewWaves, d0);
-    if (p + kFewWaves < np) compute(d1);
+  for (int bl = b0; bl < b1; bl += 2 * kFewChunk) {
+    load(bl + kFewChunk, d1);
+    compute(bl, d0);
+    if (bl + kFewChunk >= b1) break;
+    load(bl + 2 * kFewChunk, d0);
+    compute(bl + kFewChunk, d1);
   }
-  // [wave][token][weight row] sums
+  __syncthreads();  // (the sums overlay the waves' slices)
+  // [K range][token][weight row]: the lane's tokens 4 fg + v of weight row frow
   float* red = reinterpret_cast<float*>(smem) + kRed / 4;
-  if constexpr (BITS != 4) __syncthreads();  // the level staging above shared this area
 #pragma unroll
-  for (int i = 0; i < G; ++i)
-    *reinterpret_cast<f32x4_t*>(red + (wave * 16 + row) * (16 * G) + 16 * i + 4 * g) = acc[i];
-  char* ad_lds = reinterpret_cast<char*>(smem) + kRed + FewTab<BITS>::kRedBytes(G);
+  for (int v = 0; v < 4; ++v) red[(ks * 16 + 4 * fg + v) * NR + 16 * rs + frow] = acc[v];
+  char* ad_lds = reinterpret_cast<char*>(smem) + kRed + kFewWaves * kXSlice;
   ad.stage(ad_lds, 1, rows, P.r);
   __syncthreads();
-  for (int idx = tid; idx < rows * 16 * G; idx += 512) {
-    const int m = idx / (16 * G), c = idx % (16 * G);
+  for (int idx = tid; idx < rows * NR; idx += 512) {
+    const int m = idx / NR, c = idx % NR;
     const int n = n0 + c;
     if (n >= N) continue;
     float y = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) y += red[(w * 16 + m) * (16 * G) + c];
+    for (int k = 0; k < KS; ++k) y += red[(k * 16 + m) * NR + c];
     if (P.r > 0)
       y = fmaf(P.scale, ad.dot(ad_lds, P.t, 1, P.M, a, m, P.ab + (int64_t)e * N * P.r, n0, c, P.r), y);
     const int64_t o = (int64_t)(a + m) * N + n;
@@ -138,37 +178,42 @@ __global__ __launch_bounds__(512) void k_grouped_few(TileArgs P, Levels lv) {
   }
 }
 
-template <int BITS, int G>
-hipError_t launch_few_g(const TileArgs& a, const Levels& lv, hipStream_t s) {
-  auto kern = k_grouped_few<BITS, G>;
-  const size_t shmem = FewTab<BITS>::kBytes + FewTab<BITS>::kRedBytes(G) + (a.r > 0 ? FewAdapter<16 * G>::kBytes : 0);
+template <int BITS, int RS>
+hipError_t launch_few_r(const TileArgs& a, const Levels& lv, hipStream_t s) {
+  auto kern = k_grouped_few<BITS, RS>;
+  const size_t shmem = FewTab<BITS>::kBytes + kFewWaves * kXSlice + (a.r > 0 ? FewAdapter<16 * RS, 1024>::kBytes : 0);
   const hipError_t e =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)shmem);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)((a.N + 16 * G - 1) / (16 * G)), (unsigned)a.experts), dim3(512), shmem, s, a,
-                     lv);
+  hipLaunchKernelGGL(kern, dim3((unsigned)((a.N + 16 * RS - 1) / (16 * RS)), (unsigned)a.experts), dim3(512), shmem, s, a, lv);
   return hipGetLastError();
 }
 
 template <int BITS>
 hipError_t launch_few_b(const TileArgs& a, const Levels& lv, hipStream_t s) {
-  // workgroups of the experts that can have rows; 16 rows each until they fill the GPU
-  const int64_t wgs = std::min<int64_t>(a.experts, a.M) * ((a.N + 15) / 16);
-  if (wgs >= 4096) return launch_few_g<BITS, 4>(a, lv, s);
-  if (wgs >= 2048) return launch_few_g<BITS, 2>(a, lv, s);
-  return launch_few_g<BITS, 1>(a, lv, s);
+  // as many rows to a workgroup (one level table) as still gives the experts that can have rows 512 of them
+  const int64_t rows16 = std::min<int64_t>(a.experts, a.M) * ((a.N + 15) / 16);
+  if (rows16 >= 4 * 512) return launch_few_r<BITS, 4>(a, lv, s);
+  if (rows16 >= 2 * 512) return launch_few_r<BITS, 2>(a, lv, s);
+  return launch_few_r<BITS, 1>(a, lv, s);
 }
 
 // ---------------------------------------------------------------- t = x A_e^T
 //
-// A workgroup of 8 waves takes 16 RT rows of one expert x 64 adapter rows; the
+// A workgroup of W waves takes 16 RT rows of one expert x 16 JT adapter rows; the
 // waves split K in 32-element steps and multiply on 16x16x32 bf16 MFMA (x rows
-// as A, adapter rows as B); their sums are added through LDS in wave order.
-template <int RT>
-__global__ __launch_bounds__(512) void k_grouped_t(const uint16_t* __restrict__ x, int64_t M, int64_t K,
-                                                   const uint16_t* __restrict__ A, int r, const int32_t* offsets,
-                                                   int experts, float* __restrict__ t) {
-  __shared__ float red[kFewWaves][RT * 16 * 64];
+// as A, adapter rows as B).  Loads give each quad of lanes one row's 64 bytes; a
+// slice of LDS of the wave's own brings them to the fragment layout (80-byte
+// rows, free of bank conflicts).  NB steps of loads are in flight while the NB
+// before them are multiplied.  The waves' sums are added through LDS in wave order.
+constexpr uint32_t kTRowB = 80;
+
+template <int RT, int JT, int W, int NB>
+__global__ __launch_bounds__(64 * W) void k_grouped_t(const uint16_t* __restrict__ x, int64_t M, int64_t K,
+                                                      const uint16_t* __restrict__ A, int r, const int32_t* offsets,
+                                                      int experts, float* __restrict__ t) {
+  constexpr uint32_t kSlice = 16 * (RT + JT) * kTRowB, kSum = RT * 16 * JT * 16 * 4;
+  __shared__ __attribute__((aligned(16))) char lds[W * (kSlice > kSum ? kSlice : kSum)];
   int e = 0, row0 = 0, row_end = 0;
   const int total = tile_scan(offsets, experts, (int)M, 0, 16 * RT, -1, e, row0, row_end);
   if ((int)blockIdx.x >= total) return;  // the whole workgroup
@@ -177,62 +222,91 @@ __global__ __launch_bounds__(512) void k_grouped_t(const uint16_t* __restrict__ 
   row0 = __builtin_amdgcn_readfirstlane(row0);
   row_end = __builtin_amdgcn_readfirstlane(row_end);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int rows = min(16 * RT, row_end - row0), j0 = blockIdx.y * 64;
-  const int row = lane & 15, g = lane >> 4;
+  const int rows = min(16 * RT, row_end - row0), j0 = blockIdx.y * 16 * JT;
+  const int row = lane >> 2, g = lane & 3;     // of the loads
+  const int frow = lane & 15, fg = lane >> 4;  // of the fragments
   const uint16_t* xp[RT];
-  const uint16_t* ap[4];
+  const uint16_t* ap[JT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) xp[i] = x + (int64_t)(row0 + min(16 * i + row, rows - 1)) * K + 8 * g;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) ap[c] = A + ((int64_t)e * r + min(j0 + 16 * c + row, r - 1)) * K + 8 * g;
-  const int jt = min(4, (r - j0 + 15) / 16);
-  f32x4_t acc[RT][4];
+  for (int c = 0; c < JT; ++c) ap[c] = A + ((int64_t)e * r + min(j0 + 16 * c + row, r - 1)) * K + 8 * g;
+  f32x4_t acc[RT][JT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[i][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < JT; ++c) acc[i][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int nst = (int)((K + 31) / 32);
-  const int s0 = (int)((int64_t)nst * wave / kFewWaves), s1 = (int)((int64_t)nst * (wave + 1) / kFewWaves);
+  const int s0 = (int)((int64_t)nst * wave / W), s1 = (int)((int64_t)nst * (wave + 1) / W);
   const u32x4_t zero4 = {0u, 0u, 0u, 0u};
-  struct Ld { u32x4_t x[RT], a[4]; };
+  struct Ld { u32x4_t x[NB][RT], a[NB][JT]; };
+  // rows past the range or the adapter's rank repeat the last one: their results are dropped
   auto load = [&](int st, Ld& d) {
-    const int64_t k = (int64_t)st * 32;
-    const bool ok = st < s1 && k + 8 * g < K;  // past the range or the row's end: zeros
 #pragma unroll
-    for (int i = 0; i < RT; ++i) d.x[i] = ok ? *reinterpret_cast<const u32x4_t*>(xp[i] + k) : zero4;
+    for (int b = 0; b < NB; ++b) {
+      const int64_t k = (int64_t)(st + b) * 32;
+      const bool ok = st + b < s1 && k + 8 * g < K;  // past the range or the row's end: zeros
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      d.a[c] = ok && c < jt ? *reinterpret_cast<const u32x4_t*>(ap[c] + k) : zero4;
+      for (int i = 0; i < RT; ++i) d.x[b][i] = ok ? *reinterpret_cast<const u32x4_t*>(xp[i] + k) : zero4;
+#pragma unroll
+      for (int c = 0; c < JT; ++c) d.a[b][c] = ok ? *reinterpret_cast<const u32x4_t*>(ap[c] + k) : zero4;
+    }
   };
+  char* const sl = lds + wave * kSlice;
   auto compute = [&](const Ld& d) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int b = 0; b < NB; ++b) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[i][c] = mfma16x16x32(as_bf16x8(d.x[i]), as_bf16x8(d.a[c]), acc[i][c]);
+      for (int i = 0; i < RT; ++i) *reinterpret_cast<u32x4_t*>(sl + (16 * i + row) * kTRowB + 16 * g) = d.x[b][i];
+#pragma unroll
+      for (int c = 0; c < JT; ++c) *reinterpret_cast<u32x4_t*>(sl + (16 * (RT + c) + row) * kTRowB + 16 * g) = d.a[b][c];
+      bf16x8_t xf[RT], af[JT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) xf[i] = as_bf16x8(*reinterpret_cast<const u32x4_t*>(sl + (16 * i + frow) * kTRowB + 16 * fg));
+#pragma unroll
+      for (int c = 0; c < JT; ++c)
+        af[c] = as_bf16x8(*reinterpret_cast<const u32x4_t*>(sl + (16 * (RT + c) + frow) * kTRowB + 16 * fg));
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int c = 0; c < JT; ++c) acc[i][c] = mfma16x16x32(xf[i], af[c], acc[i][c]);
+    }
   };
   Ld d0, d1;
   load(s0, d0);
-  for (int st = s0; st < s1; st += 2) {
-    load(st + 1, d1);
+  for (int st = s0; st < s1; st += 2 * NB) {
+    load(st + NB, d1);
     compute(d0);
-    load(st + 2, d0);
+    if (st + NB >= s1) break;
+    load(st + 2 * NB, d0);
     compute(d1);
   }
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < JT; ++c)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) red[wave][(16 * i + 4 * g + v) * 64 + 16 * c + row] = acc[i][c][v];
+      for (int v = 0; v < 4; ++v)
+        red[wave * (RT * 16 * JT * 16) + (16 * i + 4 * fg + v) * (16 * JT) + 16 * c + frow] = acc[i][c][v];
   __syncthreads();
-  for (int idx = tid; idx < rows * 64; idx += 512) {
-    const int m = idx >> 6, j = j0 + (idx & 63);
+  for (int idx = tid; idx < rows * 16 * JT; idx += 64 * W) {
+    const int m = idx / (16 * JT), j = j0 + idx % (16 * JT);
     if (j >= r) continue;
     float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) sum += red[w][idx];
+    for (int w = 0; w < W; ++w) sum += red[w * (RT * 16 * JT * 16) + idx];
     t[(int64_t)(row0 + m) * r + j] = sum;
   }
+}
+
+template <int RT, int JT, int W, int NB>
+hipError_t launch_t(const uint16_t* x, int64_t M, int64_t K, const uint16_t* A, int r, const int32_t* offsets,
+                    int experts, float* t, hipStream_t s) {
+  hipLaunchKernelGGL((k_grouped_t<RT, JT, W, NB>), dim3((unsigned)tile_bound(M, experts, 16 * RT), (unsigned)((r + 16 * JT - 1) / (16 * JT))),
+                     dim3(64 * W), 0, s, x, M, K, A, r, offsets, experts, t);
+  return hipGetLastError();
 }
 
 // Bt[e][j][n] = B[e][n][j]
@@ -257,10 +331,13 @@ hipError_t launch_grouped_few(const TileArgs& a, const Levels& lv, hipStream_t s
 
 hipError_t launch_grouped_t(const uint16_t* x, int64_t M, int64_t K, const uint16_t* A, int r, const int32_t* offsets,
                             int experts, float* t, hipStream_t s) {
-  const unsigned jg = (unsigned)((r + 63) / 64);
-  const unsigned tiles = (unsigned)tile_bound(M, experts, 16);
-  hipLaunchKernelGGL(k_grouped_t<1>, dim3(tiles, jg), dim3(512), 0, s, x, M, K, A, r, offsets, experts, t);
-  return hipGetLastError();
+  // Few row tiles: 16 waves, 8 steps of loads in flight each (a decode call waits for one round trip).  Many: 32 rows
+  // against up to 64 adapter rows, which halves the reads of A.
+  const bool few = tile_bound(M, experts, 16) * ((r + 15) / 16) <= 256;
+  if (few) return launch_t<1, 1, 16, 4>(x, M, K, A, r, offsets, experts, t, s);
+  if (r <= 16) return launch_t<2, 1, 8, 4>(x, M, K, A, r, offsets, experts, t, s);
+  if (r <= 32) return launch_t<2, 2, 8, 2>(x, M, K, A, r, offsets, experts, t, s);
+  return launch_t<2, 4, 8, 2>(x, M, K, A, r, offsets, experts, t, s);
 }
 
 hipError_t launch_grouped_transpose(const uint16_t* B, int experts, int64_t N, int r, uint16_t* Bt, hipStream_t s) {

@@ -1114,9 +1114,9 @@ qlr_status qlr_linear_fwd_i8(const void* x, qlr_dtype xdt, int64_t M, const qlr_
     return fail(QLR_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", lay.total, ws ? ws_bytes : (size_t)0);
   if (lay.total > 0 && !aligned16(ws)) return fail(QLR_ERR_ALIGN, "workspace must be 16-byte aligned");
   qlr_path path = t_path;
-  if (path == QLR_PATH_AUTO) path = M <= 16 ? QLR_PATH_GEMV : QLR_PATH_GEMM;
+  if (path == QLR_PATH_AUTO) path = M <= qlr::kFewRows ? QLR_PATH_GEMV : QLR_PATH_GEMM;
   if (path == QLR_PATH_F32) return fail(QLR_ERR_PATH, "the 8-bit-integer product has no float32 family");
-  if (path == QLR_PATH_GEMV && M > 16) return fail(QLR_ERR_PATH, "the GEMV path takes M <= 16");
+  if (path == QLR_PATH_GEMV && M > qlr::kFewRows) return fail(QLR_ERR_PATH, "the GEMV path takes M <= %d", qlr::kFewRows);
   if (M == 0) return QLR_OK;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   char* wsp = reinterpret_cast<char*>(ws);

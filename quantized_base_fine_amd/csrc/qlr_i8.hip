@@ -139,54 +139,75 @@ hipError_t launch_quantize_dt(const void* X, int64_t rows, int64_t cols, int8_t*
 // ---------------------------------------------------------------- M <= 16
 //
 // The weight's stream: a workgroup of 8 waves takes 16 weight rows, wave w the
-// 64-element steps [w n / 8, (w + 1) n / 8) of them, multiplied on 16x16x64
-// int8 MFMA (weight rows as A, the tokens as B; token lanes past M hold zeros).
-// The waves' integer sums are added through LDS; the adapter's t B^T is added
-// in float32 before the store.
-constexpr int kFewWaves = 8, kFewBatch = 8;
+// w-th eighth of K in 64-element steps, multiplied on 16x16x64 int8 MFMA (the
+// tokens as A, weight rows as B; token lanes past M hold zeros).  Loads give
+// each quad of lanes one row's 64 bytes and lane permutes bring them to
+// fragment order (with every lane loading its own fragment piece the
+// 22016 x 8192 weight took 52 us, so 38).  NB steps are in flight
+// while the NB before them are multiplied.  The waves' integer sums are added
+// through LDS; the adapter's t B^T is added in float32 before the store.
+constexpr int kFewWaves = 8;
 
-template <int YDT>
+template <int NB>
 __global__ __launch_bounds__(512) void k_i8_few(TileArgs P) {
-  __shared__ __attribute__((aligned(16))) char ad_lds[FewAdapter<16>::kBytes];
+  typedef FewAdapter<16, 4096> Adapter;
+  __shared__ __attribute__((aligned(16))) char ad_lds[Adapter::kBytes];
   __shared__ int red[kFewWaves][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n0 = blockIdx.x * 16;
   const int M = (int)P.M;
   const int64_t K = P.K, N = P.N;
-  const int row = lane & 15, g = lane >> 4;
+  const int row = lane >> 2, g = lane & 3, src = (4 * (lane & 15) + (lane >> 4)) << 2;
   const int8_t* wp = reinterpret_cast<const int8_t*>(P.w) + std::min<int64_t>(n0 + row, N - 1) * K + 16 * g;
   const int8_t* xp = reinterpret_cast<const int8_t*>(P.x) + (int64_t)std::min(row, M - 1) * K + 16 * g;
   const int nst = (int)((K + 63) / 64);
   const int s0 = (int)((int64_t)nst * wave / kFewWaves), s1 = (int)((int64_t)nst * (wave + 1) / kFewWaves);
-  FewAdapter<16> ad;
-  ad.load(P.t, P.t_splits, M, 0, M, P.ab, n0, (int)std::min<int64_t>(16, N - n0), P.r);
-  const i32x4_t zero = {0, 0, 0, 0};
-  i32x4_t acc = zero;
-  for (int b = s0; b < s1; b += kFewBatch) {
-    i32x4_t wv[kFewBatch], xv[kFewBatch];
+  const u32x4_t zero = {0u, 0u, 0u, 0u};
+  i32x4_t acc = {0, 0, 0, 0};
+  struct Ld { u32x4_t w[NB], x[NB]; };
+  auto load = [&](int b, Ld& d) {
 #pragma unroll
-    for (int i = 0; i < kFewBatch; ++i) {
+    for (int i = 0; i < NB; ++i) {
       const int64_t k = (int64_t)(b + i) * 64;
       const bool ok = b + i < s1 && k + 16 * g < K;
-      wv[i] = ok ? *reinterpret_cast<const i32x4_t*>(wp + k) : zero;
-      xv[i] = ok && row < M ? *reinterpret_cast<const i32x4_t*>(xp + k) : zero;
+      d.w[i] = ok ? *reinterpret_cast<const u32x4_t*>(wp + k) : zero;
+      d.x[i] = ok && row < M ? *reinterpret_cast<const u32x4_t*>(xp + k) : zero;
     }
+  };
+  auto frag = [&](u32x4_t v) {
+    i32x4_t f;
 #pragma unroll
-    for (int i = 0; i < kFewBatch; ++i) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[i], xv[i], acc, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) f[i] = __builtin_amdgcn_ds_bpermute(src, (int)v[i]);
+    return f;
+  };
+  auto compute = [&](const Ld& d) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(frag(d.x[i]), frag(d.w[i]), acc, 0, 0, 0);
+  };
+  Ld d0, d1;
+  load(s0, d0);
+  Adapter ad;
+  ad.load(P.t, P.t_splits, M, 0, M, P.ab, n0, (int)std::min<int64_t>(16, N - n0), P.r);
+  for (int b = s0; b < s1; b += 2 * NB) {
+    load(b + NB, d1);
+    compute(d0);
+    if (b + NB >= s1) break;
+    load(b + 2 * NB, d0);
+    compute(d1);
   }
+  // [token][weight row]: the lane's tokens 4 (lane / 16) + v of weight row lane % 16
 #pragma unroll
-  for (int v = 0; v < 4; ++v) red[wave][(lane & 15) * 16 + 4 * g + v] = acc[v];  // [token][row]
+  for (int v = 0; v < 4; ++v) red[wave][(4 * (lane >> 4) + v) * 16 + (lane & 15)] = acc[v];
   ad.stage(ad_lds, P.t_splits, M, P.r);
   __syncthreads();
-  if (tid >= 256) return;
-  const int m = tid >> 4, n = n0 + (tid & 15);
+  const int m = tid >> 4, c = tid & 15, n = n0 + c;
   if (m >= M || n >= N) return;
   int sum = 0;
 #pragma unroll
   for (int w = 0; w < kFewWaves; ++w) sum += red[w][tid];
   float y = (float)sum * P.sx[m] * P.sw[n];
-  if (P.r > 0) y = fmaf(P.scale, ad.dot(ad_lds, P.t, P.t_splits, M, 0, m, P.ab, n0, tid & 15, P.r), y);
-  if constexpr (YDT == DT_F32) reinterpret_cast<float*>(P.y)[m * N + n] = y;
+  if (P.r > 0) y = fmaf(P.scale, ad.dot(ad_lds, P.t, P.t_splits, M, 0, m, P.ab, n0, c, P.r), y);
+  if (P.ydt == DT_F32) reinterpret_cast<float*>(P.y)[m * N + n] = y;
   else reinterpret_cast<uint16_t*>(P.y)[m * N + n] = (uint16_t)f32_to_bf16_bits(y);
 }
 
@@ -201,10 +222,8 @@ hipError_t launch_quantize_i8(const void* X, int dt, int64_t rows, int64_t cols,
 }
 
 hipError_t launch_i8_few(const TileArgs& a, hipStream_t s) {
-  if (a.M < 1 || a.M > 16 || a.K % 16 != 0) return hipErrorInvalidValue;
-  const unsigned grid = (unsigned)((a.N + 15) / 16);
-  if (a.ydt == DT_F32) hipLaunchKernelGGL(k_i8_few<DT_F32>, dim3(grid), dim3(512), 0, s, a);
-  else hipLaunchKernelGGL(k_i8_few<DT_BF16>, dim3(grid), dim3(512), 0, s, a);
+  if (a.M < 1 || a.M > kFewRows || a.K % 16 != 0) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((k_i8_few<4>), dim3((unsigned)((a.N + 15) / 16)), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 

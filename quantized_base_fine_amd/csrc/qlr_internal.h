@@ -225,14 +225,14 @@ struct TileArgs {
   int min_rows;            // experts with at most this many rows are left out (the few-rows kernel takes them)
   int ntiles, rest;        // set by the launcher: column tiles; whether a last partial round is split finer
 };
-// Rows of an expert up to which the few-rows kernel takes it.
+// Rows up to which the few-rows kernels take an expert, or a call of the 8-bit product.
 constexpr int kFewRows = 16;
 
 // q (rows x cols) and scale (rows) of rows of dtype dt.
 hipError_t launch_quantize_i8(const void* X, int dt, int64_t rows, int64_t cols, int8_t* q, float* scale, hipStream_t s);
 // y = (x w^T) sx sw + scale t B^T with int8 x, w (K % 16 == 0).
 hipError_t launch_i8_gemm(const TileArgs& a, hipStream_t s);
-hipError_t launch_i8_few(const TileArgs& a, hipStream_t s);  // M <= 16
+hipError_t launch_i8_few(const TileArgs& a, hipStream_t s);  // M <= kFewRows
 
 // Expert products of the coded weight: every expert of more than a.min_rows rows ...
 hipError_t launch_grouped_gemm(const TileArgs& a, const Levels& lv, hipStream_t s);

@@ -58,6 +58,11 @@ __device__ __forceinline__ void expert_range(const int32_t* offsets, int e, int 
 // leave most of the 256 CUs idle for a whole tile's time: those tiles are
 // run as 128 x 128 ones (two to a CU) instead.  Returns the tiles that stay.
 constexpr int kCus = 256, kRestMax = 144;
+// Tile order.  The 32 tiles that an XCD works on at a time cover kGroupM row
+// tiles x 32 / kGroupM column tiles, which share its L2: row by row (1 x 32), the int8
+// product of 2048 x 11008 x 4096 read 293 MB through the fabric (4.3 TB/s, its
+// bound) and took 149 us with its other launches; in blocks of 8 x 4, 135 us.
+constexpr int kGroupM = 8;
 __host__ __device__ __forceinline__ int tile_split(int total) {
   const int rest = total % kCus;
   return total > kCus && rest <= kRestMax ? total - rest : total;
@@ -159,14 +164,17 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
     const int tile = (int)(blockIdx.x & 7) * per + loc;
     if (loc >= per || tile >= count) return;  // the whole workgroup, before any barrier
     const int big = sub ? first + tile / kSub : tile;
-    const int mi = big / ntiles;
+    // order: blocks of kGroupM row tiles, their column tiles one after the other, row tiles innermost
+    const int grp = big / (kGroupM * ntiles), in = big - grp * kGroupM * ntiles;
+    const int gm = min(kGroupM, mt_total - grp * kGroupM);
+    const int mi = grp * kGroupM + in % gm;
+    tile_n = in / gm;
     if (P.offsets) {
       row_end = 0;
       tile_scan(P.offsets, P.experts, (int)P.M, P.min_rows, step_m, mi, e, row0, row_end);
     } else {
       row0 = mi * step_m;
     }
-    tile_n = big % ntiles;
     if (sub) {
       const int q = tile % kSub;
       row0 += (q % kSubM) * BM;
@@ -591,16 +599,16 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
   }
 }
 
-// The adapter branch of a few-rows kernel (512 threads, rows <= 16 of x against
-// NR weight rows): the operands are loaded into registers before the weight
+// The adapter branch of a few-rows kernel (rows <= 32 of x against
+// NR weight rows, NTH threads): the operands are loaded into registers before the weight
 // stream and staged in LDS after it, so their latency hides behind it.
 //   t: splits x M x r partials in global memory (rows row0 ..), B: rows x r bf16.
 // staged() tells whether the sizes fit (r % 8 == 0 and the pieces a thread can hold);
 // otherwise the dot product reads global memory.
-template <int NR>
+template <int NR, int KT, int NTH = 512>
 struct FewAdapter {
-  static constexpr int kT = 8192;  // floats of t staged at most
-  static constexpr int kTPieces = 4, kBPieces = NR * 8 / 512 > 0 ? NR * 8 / 512 : 1;
+  static constexpr int kT = KT;  // floats of t staged at most
+  static constexpr int kTPieces = (KT / 4 + NTH - 1) / NTH, kBPieces = (NR * 8 + NTH - 1) / NTH;
   static constexpr uint32_t kBytes = kT * 4 + NR * 64 * 2;
   f32x4_t tv[kTPieces];
   u32x4_t bv[kBPieces];
@@ -614,14 +622,14 @@ struct FewAdapter {
     const int per = rows * r / 4;  // pieces of one split's rows
 #pragma unroll
     for (int i = 0; i < kTPieces; ++i) {
-      const int p = tid + 512 * i;
+      const int p = tid + NTH * i;
       if (p < splits * per)
         tv[i] = *reinterpret_cast<const f32x4_t*>(t + ((int64_t)(p / per) * M + row0) * r + 4 * (p % per));
     }
     const int rp = r >> 3;
 #pragma unroll
     for (int i = 0; i < kBPieces; ++i) {
-      const int p = tid + 512 * i;
+      const int p = tid + NTH * i;
       if (p < NR * rp)
         bv[i] = *reinterpret_cast<const u32x4_t*>(B + (brow0 + min(p / rp, brows - 1)) * r + 8 * (p % rp));
     }
@@ -634,18 +642,18 @@ struct FewAdapter {
     const int per = rows * r / 4;
 #pragma unroll
     for (int i = 0; i < kTPieces; ++i) {
-      const int p = tid + 512 * i;
+      const int p = tid + NTH * i;
       if (p < splits * per) *reinterpret_cast<f32x4_t*>(ts + 4 * p) = tv[i];
     }
     const int rp = r >> 3;
 #pragma unroll
     for (int i = 0; i < kBPieces; ++i) {
-      const int p = tid + 512 * i;
+      const int p = tid + NTH * i;
       if (p < NR * rp) *reinterpret_cast<u32x4_t*>(lds + kT * 4 + 16 * p) = bv[i];
     }
     __syncthreads();
     if (splits > 1) {  // the split sums, in split order
-      for (int i = tid; i < rows * r; i += 512) {
+      for (int i = tid; i < rows * r; i += NTH) {
         float v = 0.0f;
         for (int sp = 0; sp < splits; ++sp) v += ts[sp * rows * r + i];
         ts[i] = v;
