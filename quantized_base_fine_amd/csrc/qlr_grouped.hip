@@ -8,6 +8,12 @@ namespace qlr {
 
 namespace {
 
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+// LDS transpose read of 16-bit elements (see lds_tr16) by pointer
+__device__ __forceinline__ s16x4_t lds_tr16p(const char* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(const_cast<char*>(p)));
+}
+
 // ---------------------------------------------------------------- experts of 1 .. 16 rows
 //
 // Bound by the stream of the experts' codes, so the dequantization has to stay
@@ -198,39 +204,60 @@ hipError_t launch_few_b(const TileArgs& a, const Levels& lv, hipStream_t s) {
   return launch_few_r<BITS, 1>(a, lv, s);
 }
 
-// ---------------------------------------------------------------- t = x A_e^T
+// ---------------------------------------------------------------- t = x A_e^T, u = dy B_e
 //
-// A workgroup of W waves takes 16 RT rows of one expert x 16 JT adapter rows; the
-// waves split K in 32-element steps and multiply on 16x16x32 bf16 MFMA (x rows
-// as A, adapter rows as B).  Loads give each quad of lanes one row's 64 bytes; a
-// slice of LDS of the wave's own brings them to the fragment layout (80-byte
-// rows, free of bank conflicts).  NB steps of loads are in flight while the NB
-// before them are multiplied.  The waves' sums are added through LDS in wave order.
+// A workgroup of W waves takes 16 RT rows of one expert x 16 JT adapter columns of
+// one product (the backward's two run in one launch); the waves split K in 32-element steps and multiply on 16x16x32 bf16
+// MFMA (x rows as A, the adapter as B).  Loads give each quad of lanes one row's
+// 64 bytes; a slice of LDS of the wave's own brings them to the fragment layout
+// (80-byte rows, free of bank conflicts).  An adapter given as K x r (the
+// backward's B) is staged row-major, 32 rows of K, and read with the LDS transpose
+// read.  NB steps of loads are in flight while the NB before them are
+// multiplied.  The waves' sums are added through LDS in wave order.
 constexpr uint32_t kTRowB = 80;
 
-template <int RT, int JT, int W, int NB>
-__global__ __launch_bounds__(64 * W) void k_grouped_t(const uint16_t* __restrict__ x, int64_t M, int64_t K,
-                                                      const uint16_t* __restrict__ A, int r, const int32_t* offsets,
-                                                      int experts, float* __restrict__ t) {
-  constexpr uint32_t kSlice = 16 * (RT + JT) * kTRowB, kSum = RT * 16 * JT * 16 * 4;
-  __shared__ __attribute__((aligned(16))) char lds[W * (kSlice > kSum ? kSlice : kSum)];
-  int e = 0, row0 = 0, row_end = 0;
-  const int total = tile_scan(offsets, experts, (int)M, 0, 16 * RT, -1, e, row0, row_end);
-  if ((int)blockIdx.x >= total) return;  // the whole workgroup
-  tile_scan(offsets, experts, (int)M, 0, 16 * RT, blockIdx.x, e, row0, row_end);
-  e = __builtin_amdgcn_readfirstlane(e);
-  row0 = __builtin_amdgcn_readfirstlane(row0);
-  row_end = __builtin_amdgcn_readfirstlane(row_end);
+struct TJob {
+  const uint16_t* x;  // M x K
+  const uint16_t* A;  // experts x r x K, or (BT) experts x K x r
+  int64_t K;
+  float* t;           // M x r
+};
+struct TJobs {
+  TJob j[2];
+  int64_t M;
+  int r, experts;
+  const int32_t* offsets;
+};
+
+// Bytes of row k of a staged K x r step (16 JT columns): rows 8 .. 15 of every 16 swap halves of a
+// 128-byte window where rows are 32 bytes, so that the transpose reads of rows {q .. q + 3} and {q + 8 .. q + 11} by
+// one half-wave hit distinct banks; longer rows are padded by 16 bytes.
+template <int JT>
+__device__ __forceinline__ uint32_t bt_off(uint32_t k) {
+  return JT == 1 ? (k * 32u) ^ (((k >> 3) & 1u) << 7) : k * (32u * JT + 16u);
+}
+
+template <int RT, int JT, int W, int NB, bool BT>
+__device__ __forceinline__ void t_tile(const TJob& job, int64_t M, int r, int e, int row0, int rows, int j0, char* lds) {
+  constexpr uint32_t kASlice = BT ? (JT == 1 ? 1024u : 32u * (32u * JT + 16u)) : 16u * JT * kTRowB;
+  constexpr uint32_t kSlice = 16 * RT * kTRowB + kASlice;
+  const int64_t K = job.K;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int rows = min(16 * RT, row_end - row0), j0 = blockIdx.y * 16 * JT;
   const int row = lane >> 2, g = lane & 3;     // of the loads
   const int frow = lane & 15, fg = lane >> 4;  // of the fragments
   const uint16_t* xp[RT];
   const uint16_t* ap[JT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) xp[i] = x + (int64_t)(row0 + min(16 * i + row, rows - 1)) * K + 8 * g;
+  for (int i = 0; i < RT; ++i) xp[i] = job.x + (int64_t)(row0 + min(16 * i + row, rows - 1)) * K + 8 * g;
+  // BT: load c of a step holds 16-byte pieces 64 c + lane of the 32 rows' 2 JT pieces each
+  int brow[JT], bcol[JT];
 #pragma unroll
-  for (int c = 0; c < JT; ++c) ap[c] = A + ((int64_t)e * r + min(j0 + 16 * c + row, r - 1)) * K + 8 * g;
+  for (int c = 0; c < JT; ++c) {
+    brow[c] = (64 * c + lane) / (2 * JT);
+    bcol[c] = 8 * ((64 * c + lane) % (2 * JT));
+    if constexpr (BT) ap[c] = job.A + ((int64_t)e * K + brow[c]) * r + min(j0 + bcol[c], r - 8);
+    else ap[c] = job.A + ((int64_t)e * r + min(j0 + 16 * c + row, r - 1)) * K + 8 * g;
+  }
   f32x4_t acc[RT][JT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
@@ -249,23 +276,39 @@ __global__ __launch_bounds__(64 * W) void k_grouped_t(const uint16_t* __restrict
 #pragma unroll
       for (int i = 0; i < RT; ++i) d.x[b][i] = ok ? *reinterpret_cast<const u32x4_t*>(xp[i] + k) : zero4;
 #pragma unroll
-      for (int c = 0; c < JT; ++c) d.a[b][c] = ok ? *reinterpret_cast<const u32x4_t*>(ap[c] + k) : zero4;
+      for (int c = 0; c < JT; ++c) {
+        if constexpr (BT) d.a[b][c] = st + b < s1 && k + brow[c] < K ? *reinterpret_cast<const u32x4_t*>(ap[c] + k * r) : zero4;
+        else d.a[b][c] = ok ? *reinterpret_cast<const u32x4_t*>(ap[c] + k) : zero4;
+      }
     }
   };
   char* const sl = lds + wave * kSlice;
+  char* const sa = sl + 16 * RT * kTRowB;
   auto compute = [&](const Ld& d) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) *reinterpret_cast<u32x4_t*>(sl + (16 * i + row) * kTRowB + 16 * g) = d.x[b][i];
 #pragma unroll
-      for (int c = 0; c < JT; ++c) *reinterpret_cast<u32x4_t*>(sl + (16 * (RT + c) + row) * kTRowB + 16 * g) = d.a[b][c];
+      for (int c = 0; c < JT; ++c) {
+        if constexpr (BT) *reinterpret_cast<u32x4_t*>(sa + bt_off<JT>(brow[c]) + 2 * bcol[c]) = d.a[b][c];
+        else *reinterpret_cast<u32x4_t*>(sa + (16 * c + row) * kTRowB + 16 * g) = d.a[b][c];
+      }
       bf16x8_t xf[RT], af[JT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) xf[i] = as_bf16x8(*reinterpret_cast<const u32x4_t*>(sl + (16 * i + frow) * kTRowB + 16 * fg));
 #pragma unroll
-      for (int c = 0; c < JT; ++c)
-        af[c] = as_bf16x8(*reinterpret_cast<const u32x4_t*>(sl + (16 * (RT + c) + frow) * kTRowB + 16 * fg));
+      for (int c = 0; c < JT; ++c) {
+        if constexpr (BT) {
+          // rows 8 fg + {0 .. 3} and {4 .. 7} of adapter column 16 c + lane % 16
+          const uint32_t kr = 8u * fg + (frow >> 2), co = 32u * c + 8u * (frow & 3);
+          const s16x4_t lo = lds_tr16p(sa + bt_off<JT>(kr) + co), hi = lds_tr16p(sa + bt_off<JT>(kr + 4) + co);
+          af[c] = as_bf16x8(u32x4_t{__builtin_bit_cast(uint2, lo).x, __builtin_bit_cast(uint2, lo).y,
+                                    __builtin_bit_cast(uint2, hi).x, __builtin_bit_cast(uint2, hi).y});
+        } else {
+          af[c] = as_bf16x8(*reinterpret_cast<const u32x4_t*>(sa + (16 * c + frow) * kTRowB + 16 * fg));
+        }
+      }
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -297,16 +340,44 @@ __global__ __launch_bounds__(64 * W) void k_grouped_t(const uint16_t* __restrict
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < W; ++w) sum += red[w * (RT * 16 * JT * 16) + idx];
-    t[(int64_t)(row0 + m) * r + j] = sum;
+    job.t[(int64_t)(row0 + m) * r + j] = sum;
   }
 }
 
+// blockIdx.z = 0: job 0 (adapter r x K); 1: job 1 (the backward's, adapter K x r, r % 8 == 0)
 template <int RT, int JT, int W, int NB>
-hipError_t launch_t(const uint16_t* x, int64_t M, int64_t K, const uint16_t* A, int r, const int32_t* offsets,
-                    int experts, float* t, hipStream_t s) {
-  hipLaunchKernelGGL((k_grouped_t<RT, JT, W, NB>), dim3((unsigned)tile_bound(M, experts, 16 * RT), (unsigned)((r + 16 * JT - 1) / (16 * JT))),
-                     dim3(64 * W), 0, s, x, M, K, A, r, offsets, experts, t);
+__global__ __launch_bounds__(64 * W) void k_grouped_t(TJobs J) {
+  constexpr uint32_t kA = 16u * JT * kTRowB, kB = JT == 1 ? 1024u : 32u * (32u * JT + 16u);
+  constexpr uint32_t kSlice = 16 * RT * kTRowB + (kA > kB ? kA : kB), kSum = RT * 16 * JT * 16 * 4;
+  __shared__ __attribute__((aligned(16))) char lds[W * (kSlice > kSum ? kSlice : kSum)];
+  int e = 0, row0 = 0, row_end = 0;
+  const int total = tile_scan(J.offsets, J.experts, (int)J.M, 0, 16 * RT, -1, e, row0, row_end);
+  if ((int)blockIdx.x >= total) return;  // the whole workgroup
+  tile_scan(J.offsets, J.experts, (int)J.M, 0, 16 * RT, blockIdx.x, e, row0, row_end);
+  e = __builtin_amdgcn_readfirstlane(e);
+  row0 = __builtin_amdgcn_readfirstlane(row0);
+  row_end = __builtin_amdgcn_readfirstlane(row_end);
+  const int rows = min(16 * RT, row_end - row0), j0 = blockIdx.y * 16 * JT;
+  if (blockIdx.z == 0) t_tile<RT, JT, W, NB, false>(J.j[0], J.M, J.r, e, row0, rows, j0, lds);
+  else t_tile<RT, JT, W, NB, true>(J.j[1], J.M, J.r, e, row0, rows, j0, lds);
+}
+
+template <int RT, int JT, int W, int NB>
+hipError_t launch_t(const TJobs& J, int jobs, hipStream_t s) {
+  hipLaunchKernelGGL((k_grouped_t<RT, JT, W, NB>),
+                     dim3((unsigned)tile_bound(J.M, J.experts, 16 * RT), (unsigned)((J.r + 16 * JT - 1) / (16 * JT)), (unsigned)jobs),
+                     dim3(64 * W), 0, s, J);
   return hipGetLastError();
+}
+
+hipError_t launch_t_jobs(const TJobs& J, int jobs, hipStream_t s) {
+  // Few row tiles: 16 waves, 8 steps of loads in flight each (a decode call waits for one round trip).  Many: 32 rows
+  // against up to 64 adapter columns, which halves the reads of A.
+  const bool few = tile_bound(J.M, J.experts, 16) * ((J.r + 15) / 16) <= 256;
+  if (few) return launch_t<1, 1, 16, 4>(J, jobs, s);
+  if (J.r <= 16) return launch_t<2, 1, 4, 4>(J, jobs, s);
+  if (J.r <= 32) return launch_t<2, 2, 4, 2>(J, jobs, s);
+  return launch_t<2, 4, 4, 2>(J, jobs, s);
 }
 
 // Bt[e][j][n] = B[e][n][j]
@@ -331,13 +402,27 @@ hipError_t launch_grouped_few(const TileArgs& a, const Levels& lv, hipStream_t s
 
 hipError_t launch_grouped_t(const uint16_t* x, int64_t M, int64_t K, const uint16_t* A, int r, const int32_t* offsets,
                             int experts, float* t, hipStream_t s) {
-  // Few row tiles: 16 waves, 8 steps of loads in flight each (a decode call waits for one round trip).  Many: 32 rows
-  // against up to 64 adapter rows, which halves the reads of A.
-  const bool few = tile_bound(M, experts, 16) * ((r + 15) / 16) <= 256;
-  if (few) return launch_t<1, 1, 16, 4>(x, M, K, A, r, offsets, experts, t, s);
-  if (r <= 16) return launch_t<2, 1, 8, 4>(x, M, K, A, r, offsets, experts, t, s);
-  if (r <= 32) return launch_t<2, 2, 8, 2>(x, M, K, A, r, offsets, experts, t, s);
-  return launch_t<2, 4, 8, 2>(x, M, K, A, r, offsets, experts, t, s);
+  TJobs J{};
+  J.j[0] = TJob{x, A, K, t};
+  J.M = M;
+  J.r = r;
+  J.experts = experts;
+  J.offsets = offsets;
+  return launch_t_jobs(J, 1, s);
+}
+
+hipError_t launch_grouped_tu(const uint16_t* x, const uint16_t* dy, int64_t M, int64_t N, int64_t K, const uint16_t* A,
+                             const uint16_t* B, int r, const int32_t* offsets, int experts, float* t, float* u,
+                             hipStream_t s) {
+  if (r % 8 != 0) return hipErrorInvalidValue;
+  TJobs J{};
+  J.j[0] = TJob{x, A, K, t};
+  J.j[1] = TJob{dy, B, N, u};
+  J.M = M;
+  J.r = r;
+  J.experts = experts;
+  J.offsets = offsets;
+  return launch_t_jobs(J, 2, s);
 }
 
 hipError_t launch_grouped_transpose(const uint16_t* B, int experts, int64_t N, int r, uint16_t* Bt, hipStream_t s) {

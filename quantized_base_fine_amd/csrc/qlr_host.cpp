@@ -1132,22 +1132,27 @@ qlr_status qlr_linear_fwd_i8(const void* x, qlr_dtype xdt, int64_t M, const qlr_
   a.ab = reinterpret_cast<const uint16_t*>(B);
   a.y = y;
   a.ydt = (int)ydt;
-  if (xq) {
-    a.x = xq->q;
-    a.sx = xq->scale;
-  } else {
-    int8_t* q = reinterpret_cast<int8_t*>(wsp + lay.q);
-    float* sx = reinterpret_cast<float*>(wsp + lay.sx);
-    e = qlr::launch_quantize_i8(x, (int)xdt, M, K, q, sx, s);
-    if (e != hipSuccess) return hip_fail(e, "token quantization launch");
-    a.x = q;
-    a.sx = sx;
-  }
+  float* t = reinterpret_cast<float*>(wsp + lay.t);
   if (r > 0) {
-    a.t = reinterpret_cast<const float*>(wsp + lay.t);
+    a.t = t;
     a.t_splits = qlr::lora_t_splits(M, K, r, (int)xdt, (int)abdt);
-    e = qlr::launch_lora_t(x, (int)xdt, M, K, A, (int)abdt, r, reinterpret_cast<float*>(wsp + lay.t), a.t_splits, s);
-    if (e != hipSuccess) return hip_fail(e, "adapter product launch");
+  }
+  int8_t* q = reinterpret_cast<int8_t*>(wsp + lay.q);
+  float* sx = reinterpret_cast<float*>(wsp + lay.sx);
+  a.x = xq ? xq->q : q;
+  a.sx = xq ? xq->scale : sx;
+  if (!xq && r > 0 && M <= 16 && xdt == QLR_BF16 && K % 64 == 0) {
+    e = qlr::launch_i8_prep(x, M, K, q, sx, A, r, a.t_splits, t, s);
+    if (e != hipSuccess) return hip_fail(e, "token quantization and adapter product launch");
+  } else {
+    if (!xq) {
+      e = qlr::launch_quantize_i8(x, (int)xdt, M, K, q, sx, s);
+      if (e != hipSuccess) return hip_fail(e, "token quantization launch");
+    }
+    if (r > 0) {
+      e = qlr::launch_lora_t(x, (int)xdt, M, K, A, (int)abdt, r, t, a.t_splits, s);
+      if (e != hipSuccess) return hip_fail(e, "adapter product launch");
+    }
   }
   e = path == QLR_PATH_GEMV ? qlr::launch_i8_few(a, s) : qlr::launch_i8_gemm(a, s);
   if (e != hipSuccess) return hip_fail(e, "8-bit-integer linear launch");
@@ -1280,12 +1285,19 @@ qlr_status qlr_linear_bwd_grouped(const void* dy, qlr_dtype dydt, const void* x,
   const uint16_t* xp = reinterpret_cast<const uint16_t*>(x);
   hipError_t e;
   if (r > 0 && T > 0) {
-    e = qlr::launch_grouped_transpose(reinterpret_cast<const uint16_t*>(B), experts, N, r, bt, s);
-    if (e != hipSuccess) return hip_fail(e, "adapter transpose launch");
-    e = qlr::launch_grouped_t(dyp, T, N, bt, r, offsets, experts, u, s);
-    if (e != hipSuccess) return hip_fail(e, "adapter product (dy B) launch");
-    e = qlr::launch_grouped_t(xp, T, K, reinterpret_cast<const uint16_t*>(A), r, offsets, experts, t, s);
-    if (e != hipSuccess) return hip_fail(e, "adapter product (x A^T) launch");
+    const uint16_t* Ap = reinterpret_cast<const uint16_t*>(A);
+    const uint16_t* Bp = reinterpret_cast<const uint16_t*>(B);
+    if (r % 8 == 0) {
+      e = qlr::launch_grouped_tu(xp, dyp, T, N, K, Ap, Bp, r, offsets, experts, t, u, s);
+      if (e != hipSuccess) return hip_fail(e, "adapter products (x A^T, dy B) launch");
+    } else {
+      e = qlr::launch_grouped_transpose(Bp, experts, N, r, bt, s);
+      if (e != hipSuccess) return hip_fail(e, "adapter transpose launch");
+      e = qlr::launch_grouped_t(dyp, T, N, bt, r, offsets, experts, u, s);
+      if (e != hipSuccess) return hip_fail(e, "adapter product (dy B) launch");
+      e = qlr::launch_grouped_t(xp, T, K, Ap, r, offsets, experts, t, s);
+      if (e != hipSuccess) return hip_fail(e, "adapter product (x A^T) launch");
+    }
   }
   if (dx && T > 0) {
     qlr::TileArgs a = grouped_args(T, w, experts, offsets, r, scale);

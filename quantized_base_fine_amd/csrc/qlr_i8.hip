@@ -4,6 +4,7 @@
 //
 // Row quantization (tokens and weight channels alike): s = fl32(max|x| / 127),
 // q = the integer nearest x / s, ties to even, in [-127, 127].
+#include "qlr_lora_t.h"
 #include "qlr_tile.h"
 
 namespace qlr {
@@ -12,14 +13,12 @@ namespace {
 
 // ---------------------------------------------------------------- row quantization
 //
-// One workgroup per row.  Pieces of 8 elements stay in registers between the
-// maximum and the rounding (kQPieces per thread: rows up to 16384 elements);
-// longer rows read the rest again, from cache.  The quotient is decided
-// exactly: q0 = rint(x * fl(1/s)) is within one of x / s, the residual
-// x - q0 s is exact in float32 (a multiple of s's last place, below s), and
-// comparing twice the residual with s settles the nearest integer and ties.
-constexpr int kQPieces = 8;
-
+// One workgroup per row.  Pieces of 8 elements stay in registers (as loaded)
+// between the maximum and the rounding, NP per thread; longer rows read the rest
+// again, from cache.  The quotient is decided exactly: q0 = rint(x * fl(1/s)) is
+// within one of x / s, the residual x - q0 s is exact in float32 (a multiple of
+// s's last place, below s), and comparing twice the residual with s settles the
+// nearest integer and ties.
 __device__ __forceinline__ int quantize_exact(float w, float s, float inv) {
   const float q0 = __builtin_rintf(inv > 0.0f ? w * inv : w / s);
   const float d = fmaf(-q0, s, w);
@@ -29,66 +28,71 @@ __device__ __forceinline__ int quantize_exact(float w, float s, float inv) {
   return min(max(q, -127), 127);
 }
 
+// Eight elements as loaded.
 template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
-  if constexpr (DT == DT_F32) {
-    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(p) + i);
-    const f32x4_t b = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(p) + i + 4);
+struct Raw8 { u32x4_t v[DT == DT_F32 ? 2 : 1]; };
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load8(const void* p, int64_t i) {
+  Raw8<DT> r;
+  const u32x4_t* q = reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(p) + i * (DT == DT_F32 ? 4 : 2));
+  r.v[0] = q[0];
+  if constexpr (DT == DT_F32) r.v[1] = q[1];
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void widen8(const Raw8<DT>& r, float (&v)[8]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = a[e];
-      v[4 + e] = b[e];
-    }
-  } else {
-    const u32x4_t a = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(p) + i);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t w = a[e];
-      if constexpr (DT == DT_BF16) {
-        v[2 * e] = __uint_as_float(w << 16);
-        v[2 * e + 1] = __uint_as_float(w & 0xFFFF0000u);
-      } else {
-        v[2 * e] = f16_bits_to_f32((uint16_t)w);
-        v[2 * e + 1] = f16_bits_to_f32((uint16_t)(w >> 16));
-      }
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t w = r.v[0][e];
+    if constexpr (DT == DT_F32) {
+      const uint32_t w2 = r.v[1][e];
+      v[e] = __uint_as_float(w);
+      v[4 + e] = __uint_as_float(w2);
+    } else if constexpr (DT == DT_BF16) {
+      v[2 * e] = __uint_as_float(w << 16);
+      v[2 * e + 1] = __uint_as_float(w & 0xFFFF0000u);
+    } else {
+      v[2 * e] = f16_bits_to_f32((uint16_t)w);
+      v[2 * e + 1] = f16_bits_to_f32((uint16_t)(w >> 16));
     }
   }
 }
 
 // VEC: cols % 8 == 0 (16-byte loads, 8-byte stores); otherwise element by element.
-template <int DT, bool VEC>
-__global__ __launch_bounds__(256) void k_quantize_i8(const void* __restrict__ X, int64_t cols, int8_t* __restrict__ q,
-                                                     float* __restrict__ scale) {
-  __shared__ uint32_t red[4];
+// Called by a whole workgroup of NTH threads; red: NTH / 64 words of LDS.
+template <int DT, bool VEC, int NP, int NTH>
+__device__ __forceinline__ void quantize_row(const void* __restrict__ X, int64_t row, int64_t cols,
+                                             int8_t* __restrict__ q, float* __restrict__ scale, uint32_t* red) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t row = blockIdx.x, base = row * cols;
+  const int64_t base = row * cols;
   // |x| as bits: ordered like the magnitudes, Inf and NaN above every finite value
   uint32_t am = 0;
-  float v[kQPieces][8];
+  Raw8<DT> v[NP];
+  auto amax8 = [&](const Raw8<DT>& r) {
+    float w[8];
+    widen8<DT>(r, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) am = max(am, __float_as_uint(fabsf(w[e])));
+  };
   if constexpr (VEC) {
 #pragma unroll
-    for (int p = 0; p < kQPieces; ++p) {
-      const int64_t c = 8 * ((int64_t)p * 256 + tid);
-      if (c < cols) {
-        load8<DT>(X, base + c, v[p]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) am = max(am, __float_as_uint(fabsf(v[p][e])));
-      }
+    for (int p = 0; p < NP; ++p) {
+      const int64_t c = 8 * ((int64_t)p * NTH + tid);
+      if (c < cols) v[p] = load8<DT>(X, base + c);
     }
-    for (int64_t c = 8 * ((int64_t)kQPieces * 256 + tid); c < cols; c += 8 * 256) {
-      float w[8];
-      load8<DT>(X, base + c, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) am = max(am, __float_as_uint(fabsf(w[e])));
-    }
+    for (int p = 0; p < NP; ++p)
+      if (8 * ((int64_t)p * NTH + tid) < cols) amax8(v[p]);
+    for (int64_t c = 8 * ((int64_t)NP * NTH + tid); c < cols; c += 8 * NTH) amax8(load8<DT>(X, base + c));
   } else {
-    for (int64_t c = tid; c < cols; c += 256) am = max(am, __float_as_uint(fabsf(load_elem<DT>(X, base + c))));
+    for (int64_t c = tid; c < cols; c += NTH) am = max(am, __float_as_uint(fabsf(load_elem<DT>(X, base + c))));
   }
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) am = max(am, (uint32_t)__shfl_xor((int)am, off, 64));
   if (lane == 0) red[wave] = am;
   __syncthreads();
-  am = max(max(red[0], red[1]), max(red[2], red[3]));
+#pragma unroll
+  for (int w = 0; w < NTH / 64; ++w) am = max(am, red[w]);
   const bool finite = am < 0x7F800000u;
   const float s = finite ? __uint_as_float(am) / 127.0f : __uint_as_float(0x7FC00000u);
   if (tid == 0) scale[row] = s;
@@ -96,7 +100,9 @@ __global__ __launch_bounds__(256) void k_quantize_i8(const void* __restrict__ X,
   // below 2^-125 the reciprocal could overflow: divide instead
   const float inv = s >= 2.350988701644575e-38f ? 1.0f / s : 0.0f;
   auto q1 = [&](float w) { return live ? quantize_exact(w, s, inv) : 0; };
-  auto put8 = [&](int64_t c, const float (&w)[8]) {
+  auto put8 = [&](int64_t c, const Raw8<DT>& r) {
+    float w[8];
+    widen8<DT>(r, w);
     uint32_t lo = 0, hi = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -107,29 +113,44 @@ __global__ __launch_bounds__(256) void k_quantize_i8(const void* __restrict__ X,
   };
   if constexpr (VEC) {
 #pragma unroll
-    for (int p = 0; p < kQPieces; ++p) {
-      const int64_t c = 8 * ((int64_t)p * 256 + tid);
+    for (int p = 0; p < NP; ++p) {
+      const int64_t c = 8 * ((int64_t)p * NTH + tid);
       if (c < cols) put8(c, v[p]);
     }
-    for (int64_t c = 8 * ((int64_t)kQPieces * 256 + tid); c < cols; c += 8 * 256) {
-      float w[8];
-      load8<DT>(X, base + c, w);
-      put8(c, w);
-    }
+    for (int64_t c = 8 * ((int64_t)NP * NTH + tid); c < cols; c += 8 * NTH) put8(c, load8<DT>(X, base + c));
   } else {
-    for (int64_t c = tid; c < cols; c += 256) q[base + c] = (int8_t)q1(load_elem<DT>(X, base + c));
+    for (int64_t c = tid; c < cols; c += NTH) q[base + c] = (int8_t)q1(load_elem<DT>(X, base + c));
   }
+}
+
+template <int DT, bool VEC, int NP>
+__global__ __launch_bounds__(256) void k_quantize_i8(const void* __restrict__ X, int64_t cols, int8_t* __restrict__ q,
+                                                     float* __restrict__ scale) {
+  __shared__ uint32_t red[4];
+  quantize_row<DT, VEC, NP, 256>(X, blockIdx.x, cols, q, scale, red);
+}
+
+// A decode call's tokens: the first M workgroups quantize a row each, the others
+// compute the partial sums of t = x A^T (both read x only), in one launch.
+__global__ __launch_bounds__(kLtWaves * 64) void k_i8_prep(const uint16_t* __restrict__ x, int64_t M, int64_t K,
+                                                           int8_t* __restrict__ q, float* __restrict__ scale,
+                                                           const uint16_t* __restrict__ A, int r, int jtiles, int splits,
+                                                           float* __restrict__ t) {
+  __shared__ float red[kLtWaves][256];
+  const int b = (int)blockIdx.x - (int)M;
+  if (b < 0) quantize_row<DT_BF16, true, 2, kLtWaves * 64>(x, blockIdx.x, K, q, scale, reinterpret_cast<uint32_t*>(&red[0][0]));
+  else lora_t_small_body(x, M, K, A, r, t, (b % jtiles) * 16, splits, b / jtiles, red);
 }
 
 template <int DT>
 hipError_t launch_quantize_dt(const void* X, int64_t rows, int64_t cols, int8_t* q, float* scale, hipStream_t s) {
   for (int64_t r0 = 0; r0 < rows; r0 += 1 << 30) {  // the grid's x dimension holds 2^31 - 1 workgroups
-    const int64_t n = std::min<int64_t>(rows - r0, 1 << 30);
+    const dim3 n((unsigned)std::min<int64_t>(rows - r0, 1 << 30)), b(256);
     const char* x0 = reinterpret_cast<const char*>(X) + r0 * cols * (DT == DT_F32 ? 4 : 2);
-    if (cols % 8 == 0)
-      hipLaunchKernelGGL((k_quantize_i8<DT, true>), dim3((unsigned)n), dim3(256), 0, s, x0, cols, q + r0 * cols, scale + r0);
-    else
-      hipLaunchKernelGGL((k_quantize_i8<DT, false>), dim3((unsigned)n), dim3(256), 0, s, x0, cols, q + r0 * cols, scale + r0);
+    int8_t* q0 = q + r0 * cols;
+    if (cols % 8 != 0) hipLaunchKernelGGL((k_quantize_i8<DT, false, 1>), n, b, 0, s, x0, cols, q0, scale + r0);
+    else if (cols <= 2 * 2048) hipLaunchKernelGGL((k_quantize_i8<DT, true, 2>), n, b, 0, s, x0, cols, q0, scale + r0);
+    else hipLaunchKernelGGL((k_quantize_i8<DT, true, 8>), n, b, 0, s, x0, cols, q0, scale + r0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -219,6 +240,15 @@ hipError_t launch_quantize_i8(const void* X, int dt, int64_t rows, int64_t cols,
     case DT_F16: return launch_quantize_dt<DT_F16>(X, rows, cols, q, scale, s);
     default: return launch_quantize_dt<DT_BF16>(X, rows, cols, q, scale, s);
   }
+}
+
+hipError_t launch_i8_prep(const void* x, int64_t M, int64_t K, int8_t* q, float* scale, const void* A, int r, int splits,
+                          float* t, hipStream_t s) {
+  if (M < 1 || M > 16 || K % 64 != 0 || r < 1 || splits < 1) return hipErrorInvalidValue;
+  const int jt = (r + 15) / 16;
+  hipLaunchKernelGGL(k_i8_prep, dim3((unsigned)(M + (int64_t)jt * splits)), dim3(kLtWaves * 64), 0, s,
+                     reinterpret_cast<const uint16_t*>(x), M, K, q, scale, reinterpret_cast<const uint16_t*>(A), r, jt, splits, t);
+  return hipGetLastError();
 }
 
 hipError_t launch_i8_few(const TileArgs& a, hipStream_t s) {

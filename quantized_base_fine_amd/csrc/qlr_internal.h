@@ -230,6 +230,9 @@ constexpr int kFewRows = 16;
 
 // q (rows x cols) and scale (rows) of rows of dtype dt.
 hipError_t launch_quantize_i8(const void* X, int dt, int64_t rows, int64_t cols, int8_t* q, float* scale, hipStream_t s);
+// The same for a few bf16 rows (M <= 16, K % 64 == 0), with t = x A^T as `splits` partial sums (lora_t_splits), in one launch.
+hipError_t launch_i8_prep(const void* x, int64_t M, int64_t K, int8_t* q, float* scale, const void* A, int r, int splits,
+                          float* t, hipStream_t s);
 // y = (x w^T) sx sw + scale t B^T with int8 x, w (K % 16 == 0).
 hipError_t launch_i8_gemm(const TileArgs& a, hipStream_t s);
 hipError_t launch_i8_few(const TileArgs& a, hipStream_t s);  // M <= kFewRows
@@ -243,6 +246,10 @@ hipError_t launch_grouped_dx(const TileArgs& a, const Levels& lv, hipStream_t s)
 // t (M x r float32) = x A_e^T over each expert's rows, A experts x r x K bf16, K % 8 == 0.
 hipError_t launch_grouped_t(const uint16_t* x, int64_t M, int64_t K, const uint16_t* A, int r, const int32_t* offsets,
                             int experts, float* t, hipStream_t s);
+// That and u (M x r) = dy B_e, B experts x N x r, in one launch; r, N and K multiples of 8.
+hipError_t launch_grouped_tu(const uint16_t* x, const uint16_t* dy, int64_t M, int64_t N, int64_t K, const uint16_t* A,
+                             const uint16_t* B, int r, const int32_t* offsets, int experts, float* t, float* u,
+                             hipStream_t s);
 // Bt (experts x r x N) = B^T per expert, B experts x N x r bf16.
 hipError_t launch_grouped_transpose(const uint16_t* B, int experts, int64_t N, int r, uint16_t* Bt, hipStream_t s);
 // dA (experts x r x K) = scale u^T x and dB (experts x N x r) = scale dy^T t, float32, zero for experts

@@ -247,17 +247,27 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
   const __amdgpu_buffer_rsrc_t wr = tile_rsrc(KIND == TILE_I8 ? wbase : nullptr, KIND == TILE_I8 ? (uint32_t)wrows * kbytes : 0u);
   constexpr int TPB = 64 / CPT;
   const int rr = KIND == TILE_TR ? (tid >> 3) : tid / TPB, dh = tid % TPB, bq = KIND == TILE_TR ? (tid & 7) / TPB : 0;
+  // Addresses of a coded weight's blocks: a scalar part (the tile's first block and the step) plus a 32-bit part
+  // per lane, fixed for all steps but TR's last, whose rows past N read row N - 1 with scale 0.
   const int64_t nbK = K >> 6;
-  bool wv = true;
-  int64_t wblk = 0;
+  const int64_t gb = KIND == TILE_TR ? (int64_t)e * N * nbK + (n0 >> 6) : ((int64_t)e * N + n0) * nbK;
+  bool wv = true, wv_last = true;
+  uint32_t lb = 0, lb_last = 0;  // the lane's block, relative
   if constexpr (KIND == TILE_CODED) {
-    wv = n0 + rr < N;
-    wblk = ((int64_t)e * N + (wv ? n0 + rr : N - 1)) * nbK;
+    wv = wv_last = n0 + rr < N;
+    lb = lb_last = (uint32_t)(min<int64_t>(rr, N - 1 - n0) * nbK);
   } else if constexpr (KIND == TILE_TR) {
-    const int64_t wcol = (n0 >> 6) + bq;
-    wv = wcol < nbK;
-    wblk = (int64_t)e * N * nbK + (wv ? wcol : nbK - 1);
+    wv = (n0 >> 6) + bq < nbK;
+    const uint32_t col = (uint32_t)min<int64_t>(bq, nbK - 1 - (n0 >> 6));
+    const int64_t nl = N - 64 * (int64_t)(nsteps - 1);  // rows of the last step
+    wv_last = wv && rr < nl;
+    lb = (uint32_t)((int64_t)rr * nbK) + col;
+    lb_last = (uint32_t)(min<int64_t>(rr, nl - 1) * nbK) + col;
   }
+  const uint8_t* const wb8 = P.w + (KIND == TILE_I8 ? 0 : gb * (8 * BITS));
+  const uint8_t* const qb8 = KIND == TILE_I8 ? nullptr : P.q8 + gb;
+  const float* const cb = KIND == TILE_I8 ? nullptr : P.cst + (gb >> 8);
+  const uint32_t gl = (uint32_t)(gb & 255);
   uint32_t wst[WL];
 #pragma unroll
   for (int q = 0; q < WL; ++q) {
@@ -273,21 +283,21 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
   };
   auto load_w = [&](int k, Ws& s) {
     if constexpr (KIND != TILE_I8) {
-      int64_t blk;
-      bool ok = wv;
-      if constexpr (KIND == TILE_CODED) {
-        blk = wblk + min(k, nsteps - 1);
-      } else {
-        const int64_t n = 64 * (int64_t)min(k, nsteps - 1) + rr;
-        ok = wv && n < N;  // rows past N: scale 0
-        blk = wblk + min<int64_t>(n, N - 1) * nbK;
-      }
-      if constexpr (CPT == 32) s.c = load_codes32<BITS>(P.w + blk * (8 * BITS) + dh * (4 * BITS));
-      else s.c = load_codes16<BITS>(P.w + blk * (8 * BITS), dh);
-      s.q8 = P.q8[blk];
-      s.sc = P.cst[blk >> 8];
-      if (!ok) s.q8 = 0;
+      const int kk = min(k, nsteps - 1);
+      const bool last = kk == nsteps - 1;  // (scalar)
+      const int64_t ks = KIND == TILE_TR ? 64 * (int64_t)kk * nbK : kk;  // the step's first block
+      const uint32_t l = last ? lb_last : lb;
+      const uint8_t* const wk = wb8 + ks * (8 * BITS);
+      if constexpr (CPT == 32) s.c = load_codes32<BITS>(wk + l * (uint32_t)(8 * BITS) + dh * (4 * BITS));
+      else s.c = load_codes16<BITS>(wk + l * (uint32_t)(8 * BITS), dh);
+      s.q8 = (qb8 + ks)[l];
+      s.sc = (cb + (ks >> 8))[(gl + (uint32_t)(ks & 255) + l) >> 8];
     }
+  };
+  // The scale of step k's weights, 0 outside the weight.  (Selected here, where it is used: a select next to the loads
+  // would wait for them.)
+  auto scale_of = [&](const Ws& s, int k) {
+    return KIND != TILE_I8 && (k < nsteps - 1 ? wv : wv_last) ? (float)s.q8 * s.sc : 0.0f;
   };
   // part I (0 .. WL - 1) of the thread's weights into buffer buf: I8 one loaded piece, coded 8 dequantized weights
   auto store_w = [&](const Ws& s, const Lut4& lut, float ap, auto part, int buf) {
@@ -301,9 +311,9 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
       lds_store_u32x4(wst[I] + (uint32_t)buf * L::kW, u32x4_t{o[4 * I], o[4 * I + 1], o[4 * I + 2], o[4 * I + 3]});
     }
   };
-  auto store_w_all = [&](const Ws& s, int buf) {
+  auto store_w_all = [&](const Ws& s, int k, int buf) {
     Lut4 lut{};
-    const float ap = KIND == TILE_I8 ? 0.0f : (float)s.q8 * s.sc;
+    const float ap = scale_of(s, k);
     if constexpr (KIND != TILE_I8 && BITS == 4) lut = make_lut4(lv, ap);
     store_w(s, lut, ap, std::integral_constant<int, 0>{}, buf);
     store_w(s, lut, ap, std::integral_constant<int, 1>{}, buf);
@@ -378,18 +388,22 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
       for (int i = 0; i < WL; ++i) load_wp(off0, wa, i);
     } else {
       load_w(0, wa);
+      // (loads in the steps' order, here and below: the compiler's wait counts at the loop's head are those of the worse path)
+      __builtin_amdgcn_sched_barrier(0);
       load_w(1, wn);
     }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
       store_xp(xs, 0, i);
       load_xp(off1, xs, i);
     }
-    store_w_all(wa, 0);
+    store_w_all(wa, 0, 0);
     if constexpr (KIND == TILE_I8) {
 #pragma unroll
       for (int i = 0; i < WL; ++i) load_wp(off1, wa, i);
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
   __syncthreads();
   // Step k: xs (and the integer weights wi) hold step k + 1's pieces, loaded during step k - 1; each is written to the
@@ -400,9 +414,17 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
     __builtin_amdgcn_sched_barrier(0);
     const uint32_t off = step_off(k + 2);
     if constexpr (KIND != TILE_I8) load_w(k + 2, nxt);
+    // (opaque from here: the compiler would otherwise start the codes' arithmetic right after their load, a
+    // step early, and wait for them there)
+    if constexpr (KIND != TILE_I8) {
+#pragma unroll
+      for (int i = 0; i < BITS; ++i) asm volatile("" : "+v"(cur.c.w[i]));
+      asm volatile("" : "+v"(cur.q8), "+v"(cur.sc));
+    }
+    __builtin_amdgcn_sched_barrier(0);
     read_frags(buf, 0, 0);
     Lut4 lut{};
-    const float ap = KIND == TILE_I8 ? 0.0f : (float)cur.q8 * cur.sc;
+    const float ap = scale_of(cur, k + 1);
     if constexpr (KIND != TILE_I8 && BITS == 4) lut = make_lut4(lv, ap);
     auto sub = [&](auto spos) {
       constexpr int S = decltype(spos)::value;
