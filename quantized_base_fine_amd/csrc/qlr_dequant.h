@@ -140,31 +140,37 @@ __device__ __forceinline__ void lut4_word(uint32_t w, const Lut4& t, uint32_t* o
   o[3] = perm(h47, l47, 0x07030602u);
 }
 
+// Float32 levels of codes 2 j, 2 j + 1 of one thread's 32 codes, for widths other
+// than 4 (from a lane-private LDS table; tp = this lane's copy).
+template <int BITS>
+__device__ __forceinline__ float2 level_pair(const Codes32<BITS>& c, int j, uint32_t tp) {
+  if constexpr (BITS == 8) {
+    // one float32 level per code; 16 lane copies, entry e of copy l at e*64 + 4l
+    const uint32_t w = c.w[j >> 1] >> (16 * (j & 1));
+    return make_float2(lds_f32(tp + ((w & 255u) << 6)), lds_f32(tp + (((w >> 8) & 255u) << 6)));
+  } else {
+    // float32 level pairs of two neighbouring codes; 32 lane copies, entry e at e*256 + 8l
+    uint32_t e;
+    if constexpr (BITS == 2) {
+      e = (c.w[j >> 3] >> (4 * (j & 7))) & 15u;
+    } else {
+      const int bit = 6 * j, wd = bit >> 5, sh = bit & 31;
+      uint32_t v = c.w[wd] >> sh;
+      if (sh + 6 > 32) v |= c.w[wd + 1] << (32 - sh);
+      e = v & 63u;
+    }
+    return lds_pair(tp + (e << 8));
+  }
+}
+
 // Pairs [J0, J1) of the 16 bf16 pairs of one thread's 32 codes, for widths
-// other than 4 (float32 levels from a lane-private LDS table; tp = this lane's
-// copy): o[j] = bf16 pair of codes 2j, 2j+1.
+// other than 4: o[j] = bf16 pair of codes 2j, 2j+1, scaled by ap.
 template <int BITS, int J0, int J1>
 __device__ __forceinline__ void dequant_pairs(const Codes32<BITS>& c, float ap, uint32_t tp, uint32_t (&o)[16]) {
 #pragma unroll
   for (int j = J0; j < J1; ++j) {
-    if constexpr (BITS == 8) {
-      // one float32 level per code; 16 lane copies, entry e of copy l at e*64 + 4l
-      const uint32_t w = c.w[j >> 1] >> (16 * (j & 1));
-      o[j] = cvt_pk_bf16(lds_f32(tp + ((w & 255u) << 6)) * ap, lds_f32(tp + (((w >> 8) & 255u) << 6)) * ap);
-    } else {
-      // float32 level pairs of two neighbouring codes; 32 lane copies, entry e at e*256 + 8l
-      uint32_t e;
-      if constexpr (BITS == 2) {
-        e = (c.w[j >> 3] >> (4 * (j & 7))) & 15u;
-      } else {
-        const int bit = 6 * j, wd = bit >> 5, sh = bit & 31;
-        uint32_t v = c.w[wd] >> sh;
-        if (sh + 6 > 32) v |= c.w[wd + 1] << (32 - sh);
-        e = v & 63u;
-      }
-      const float2 p = lds_pair(tp + (e << 8));
-      o[j] = cvt_pk_bf16(p.x * ap, p.y * ap);
-    }
+    const float2 p = level_pair<BITS>(c, j, tp);
+    o[j] = cvt_pk_bf16(p.x * ap, p.y * ap);
   }
 }
 

@@ -134,7 +134,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void* p, uint3
 }
 
 template <int KIND, int BITS, int BM, int BN>
-__global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
+__global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(TileArgs P, Levels lv) {
   using L = TileLds<KIND, BITS, BM, BN>;
   constexpr int WM = (BN == 256 || BM == 64) ? 2 : 4, WN = 8 / WM;
   constexpr int MT = BM / WM / 32, NT = BN / WN / 32;  // MFMA tiles of a wave
@@ -311,6 +311,23 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
       lds_store_u32x4(wst[I] + (uint32_t)buf * L::kW, u32x4_t{o[4 * I], o[4 * I + 1], o[4 * I + 2], o[4 * I + 3]});
     }
   };
+  // the same in two halves, for the widths whose levels come from LDS: the lookups before a run of products, the rest after
+  constexpr bool kLook = KIND != TILE_I8 && BITS != 4;
+  float2 look[4];
+  auto lookup_w = [&](const Ws& s, auto part) {
+    if constexpr (kLook) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) look[j] = level_pair<BITS>(s.c, 4 * decltype(part)::value + j, tp);
+    }
+  };
+  auto finish_w = [&](float ap, auto part, int buf) {
+    if constexpr (kLook) {
+      u32x4_t o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = cvt_pk_bf16(look[j].x * ap, look[j].y * ap);
+      lds_store_u32x4(wst[decltype(part)::value] + (uint32_t)buf * L::kW, o);
+    }
+  };
   auto store_w_all = [&](const Ws& s, int k, int buf) {
     Lut4 lut{};
     const float ap = scale_of(s, k);
@@ -429,6 +446,9 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
     auto sub = [&](auto spos) {
       constexpr int S = decltype(spos)::value;
       if constexpr (S < 3) read_frags(buf, S + 1, (S + 1) & 1);
+      constexpr bool kPart = WL == 4 || S % 2 == 0;
+      constexpr std::integral_constant<int, WL == 4 ? S : S / 2> wpart{};
+      if constexpr (kLook && kPart) lookup_w(cur, wpart);
       __builtin_amdgcn_sched_barrier(0);
       mfmas(S & 1);
       if constexpr (S < XL) {
@@ -440,10 +460,13 @@ __global__ __launch_bounds__(512, 1) void k_tile(TileArgs P, Levels lv) {
           store_w(wi, lut, ap, spos, buf ^ 1);
           load_wp(off, wi, S);
         }
-      } else if constexpr (WL == 4) {
-        store_w(cur, lut, ap, spos, buf ^ 1);
-      } else if constexpr (S % 2 == 0) {
-        store_w(cur, lut, ap, std::integral_constant<int, S / 2>{}, buf ^ 1);
+      } else if constexpr (kPart) {
+        if constexpr (kLook) {
+          __builtin_amdgcn_sched_barrier(0);
+          finish_w(ap, wpart, buf ^ 1);
+        } else {
+          store_w(cur, lut, ap, wpart, buf ^ 1);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -754,7 +777,7 @@ hipError_t launch_tile(TileArgs a, const Levels& lv, hipStream_t s) {
     return a.offsets ? (a.M / b + (std::min<int64_t>(a.experts, a.M) + 1) / 2) * nt : (a.M + b - 1) / b * nt;
   };
   const bool short_ranges = a.offsets && a.M < (int64_t)a.experts * 96;
-  if (!short_ranges && count(256, 256) >= 192) {
+  if (!short_ranges && count(256, 256) >= (a.offsets ? 320 : 192)) {  // (an even split has fewer tiles than the estimate)
     a.rest = 1;
     const hipError_t e = launch_tile_t<KIND, BITS, 256, 256>(a, lv, s);
     if (e != hipSuccess) return e;

@@ -29,6 +29,10 @@ class Layer:
         self.A = (torch.randn((self.E, r, K), generator=g) * K ** -0.5).to(BF) if r else None
         self.B = (torch.randn((self.E, N, r), generator=g) * 0.2).to(BF) if r else None
         self.scale = 0.75 if r else 0.0
+        # rows of no expert hold NaN: they must not be read
+        for t in (self.x, self.dy):
+            t[:lead] = float("nan")
+            t[int(self.off[-1]):] = float("nan")
         self.offsets = torch.tensor(self.off, dtype=torch.int32, device="cuda")
         self.xd, self.dyd = self.x.cuda(), self.dy.cuda()
         self.Ad, self.Bd = (None, None) if not r else (self.A.cuda(), self.B.cuda())
@@ -123,7 +127,7 @@ def test_forward_counts(bits, counts, path):
 
 
 @pytest.mark.parametrize("N,K", [(1, 64), (7, 128), (16, 64), (255, 320), (257, 64), (520, 1088), (96, 4096)])
-@pytest.mark.parametrize("r", [0, 3, 16, 40])
+@pytest.mark.parametrize("r", [0, 3, 16, 40, 72])
 @pytest.mark.parametrize("out", [BF, F32], ids=["bf16", "f32"])
 def test_forward_shapes(N, K, r, out):
     print(f"grouped fwd N={N} K={K} r={r}", flush=True)
@@ -150,6 +154,100 @@ def test_backward_long_experts_and_no_input_gradient():
     L = Layer([513, 512, 1, 1100], 48, 64, 4, 12, seed=5)
     check_backward(L)
     check_backward(L, need_dx=False)
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+def test_large_tiles_and_their_rest(bits):
+    """Enough rows and columns for the 256 x 256 tiles: 64 column tiles, 11, 13 and 9 row tiles, so a last round of 192 tiles
+    (kept whole), of 64 and of 64 (run as smaller tiles); the input gradient with 32 column tiles, 11 row tiles, 352 = 256 + 96."""
+    for counts in ([500, 700, 256, 3, 1000], [520, 700, 256, 3, 1100], [512, 300, 1, 513, 200]):
+        L = Layer(counts, 16384, 64, bits, 8, seed=sum(counts) + bits)
+        check_forward(L)
+    L = Layer([500, 0, 400, 900, 700], 64, 8192, bits, 8, seed=bits)
+    check_backward(L)
+
+
+def test_no_rows():
+    L = Layer([0, 0], 24, 128, 4, 8, seed=1)
+    assert qlr.linear_grouped(L.xd, L.qw, L.offsets, L.Ad, L.Bd, 1.0).shape == (0, 24)
+    dx, dA, dB = qlr.linear_grouped_bwd(L.dyd, L.xd, L.qw, L.offsets, L.Ad, L.Bd, 1.0)
+    torch.cuda.synchronize()
+    assert dx.shape == (0, 128) and (dA == 0).all() and (dB == 0).all()
+
+
+def test_offsets_out_of_range_or_decreasing_stay_inside_the_buffers():
+    """The kernels clamp every offset into [0, T] and to its predecessor: guard rows around y and dx keep their values."""
+    L = Layer([30, 40, 20], 40, 128, 4, 8, seed=2)
+    for bad in ([0, 200, -5, 90], [-7, 10, 1 << 30, 50], [90, 60, 30, 0], [0, 90, 0, 90]):
+        L.offsets.copy_(torch.tensor(bad, dtype=torch.int32))
+        y = torch.full((L.T + 64, L.N), 7.25, dtype=BF, device="cuda")
+        dx = torch.full((L.T + 64, L.K), 7.25, dtype=BF, device="cuda")
+        qlr.linear_grouped(L.xd, L.qw, L.offsets, L.Ad, L.Bd, 1.0, out=y[32:32 + L.T])
+        qlr.GroupedBwdCall(L.dyd, L.xd, L.qw, L.offsets, L.Ad, L.Bd, 1.0, dx=dx[32:32 + L.T])()
+        torch.cuda.synchronize()
+        for t in (y, dx):
+            assert (t[:32] == 7.25).all() and (t[32 + L.T:] == 7.25).all()
+
+
+def test_rows_and_codes_past_32_bit_offsets():
+    """x past 2^32 bytes and codes past 2^32 bytes: the last expert's rows against 64 bits."""
+    K, N, T = 2048, 64, 1_100_000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    W = torch.randn((3 * N, K), generator=g, device="cuda") * 0.05
+    qw = qlr.quantize(W, 4)
+    x = torch.empty((T, K), dtype=BF, device="cuda")
+    x.normal_(generator=g)
+    assert x.numel() * 2 > 1 << 32
+    for last in (9, 400_000):
+        off = torch.tensor([0, 5, T - last, T], dtype=torch.int32, device="cuda")
+        y = qlr.linear_grouped(x, qw, off)
+        w = qlr.dequantize(qw, F32).view(3, N, K)
+        for e, rows in ((2, slice(T - 9, T)), (1, slice(T - last - 300, T - last)), (0, slice(0, 5))):
+            xr = x[rows].cpu().double()
+            we = w[e].cpu().double()
+            close(y[rows], xr @ we.t(), xr.abs() @ we.abs().t(), 5e-3, 1e-5, f"rows of expert {e}")
+    del x, y
+    E, N, K = 70, 8192, 8192
+    qw = qlr.QWeight.empty(E * N, K, 8, "cuda")
+    assert qw.codes.numel() > 1 << 32
+    qw.codes.random_(0, 256, generator=g)
+    qw.absmax_q8.random_(100, 256, generator=g)
+    qw.absmax_c.fill_(1e-3)
+    one = N * K // 64
+    last = qlr.QWeight(8, N, K, qw.codes[(E - 1) * N * K:], qw.absmax_q8[(E - 1) * one:], qw.absmax_c[(E - 1) * one // 256:])
+    w = qlr.dequantize(last, F32).cpu().double()
+    for rows in (3, 90):
+        x = torch.randn((rows, K), generator=g, device="cuda").to(BF)
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[E] = rows
+        y = qlr.linear_grouped(x, qw, off, out_dtype=F32)
+        xr = x.cpu().double()
+        close(y, xr @ w.t(), xr.abs() @ w.abs().t(), 5e-3, 1e-5, "last expert")
+        dy = torch.randn((rows, N), generator=g, device="cuda").to(BF)
+        dx, _, _ = qlr.linear_grouped_bwd(dy, None, qw, off, dx_dtype=F32)
+        d = dy.cpu().double()
+        close(dx, d @ w, d.abs() @ w.abs(), 5e-3, 1e-5, "last expert's input gradient")
+
+
+def test_calls_on_two_streams():
+    """Two calls in flight on two streams, each with a workspace of its own."""
+    Ls = [Layer([50, 200, 9], 128, 512, 4, 16, seed=s) for s in (20, 21)]
+    torch.cuda.synchronize()
+    outs = []
+    for L in Ls:
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            outs.append([(qlr.linear_grouped(L.xd, L.qw, L.offsets, L.Ad, L.Bd, L.scale),
+                          *qlr.linear_grouped_bwd(L.dyd, L.xd, L.qw, L.offsets, L.Ad, L.Bd, L.scale)) for _ in range(5)])
+    torch.cuda.synchronize()
+    for L, o in zip(Ls, outs):
+        ref, S = L.forward()
+        (rx, Sx), (rA, SA), (rB, SB) = L.backward()
+        for y, dx, dA, dB in o:
+            close(y, ref, S, 5e-3, 1e-5, "y")
+            close(dx, rx, Sx, 5e-3, 1e-5, "dx")
+            close(dA, rA, SA, 1e-4, 1e-6, "dA")
+            close(dB, rB, SB, 1e-4, 1e-6, "dB")
 
 
 def test_many_experts():

@@ -155,6 +155,36 @@ def test_families_agree_without_adapter(M):
     assert torch.equal(torch.cat(ys), y)
 
 
+@pytest.mark.parametrize("M,N", [(700, 24576), (2060, 8000), (300, 25000), (520, 33000)])
+def test_large_tiles_and_their_rest(M, N):
+    """256 x 256 tiles: 3 x 96 = 256 + 32, 9 x 32 = 256 + 32 (odd rows), 2 x 98 = 196 (one round), 3 x 129 = 256 + 131."""
+    x, w, A, B = make(M, N, 128, 8, seed=N)
+    xd, wd, Ad, Bd = dev(x, w, A, B)
+    y = qlr.linear_i8(xd, qlr.quantize_i8(wd), Ad, Bd, 0.5)
+    torch.cuda.synchronize()
+    check(y, *reference(x, w, A, B, 0.5))
+
+
+def test_rows_past_32_bit_offsets():
+    """Tokens and outputs past 2^32 bytes: the last rows against 64 bits."""
+    M, N, K = 540_000, 2064, 8192
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q = torch.empty((M, K), dtype=torch.int8, device="cuda")
+    q.random_(-127, 128, generator=g)
+    s = torch.rand(M, generator=g, device="cuda") + 0.5
+    assert q.numel() > 1 << 32
+    w = rand(N, K, 7, "f32", 0.02)
+    w8 = qlr.quantize_i8(w.cuda())
+    y = qlr.linear_i8(None, w8, xq=qlr.I8Rows(M, K, q, s), out_dtype=torch.float32)
+    assert y.numel() * 4 > 1 << 32
+    torch.cuda.synchronize()
+    wq, sw = ref_rows(w)
+    for rows in (slice(0, 40), slice(M - 40, M)):
+        ref = q[rows].cpu().double() @ torch.from_numpy(wq).t() * s[rows].cpu().double()[:, None]
+        ref = ref * torch.from_numpy(sw.astype(np.float64))
+        check(y[rows], ref, 4e-7 * ref.abs() + 1e-30)
+
+
 def test_largest_sums_do_not_wrap():
     """Every product 127 * 127 with one sign over the longest row allowed: 2 114 060 288 < 2^31."""
     K = 131072
