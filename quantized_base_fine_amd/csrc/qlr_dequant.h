@@ -140,14 +140,26 @@ __device__ __forceinline__ void lut4_word(uint32_t w, const Lut4& t, uint32_t* o
   o[3] = perm(h47, l47, 0x07030602u);
 }
 
+// A lane's copy of the level table: at an LDS byte address, or behind a pointer.
+struct TabAt {
+  uint32_t tp;
+  __device__ __forceinline__ float one(uint32_t off) const { return lds_f32(tp + off); }
+  __device__ __forceinline__ float2 pair(uint32_t off) const { return lds_pair(tp + off); }
+};
+struct TabPtr {
+  const char* p;
+  __device__ __forceinline__ float one(uint32_t off) const { return *reinterpret_cast<const float*>(p + off); }
+  __device__ __forceinline__ float2 pair(uint32_t off) const { return *reinterpret_cast<const float2*>(p + off); }
+};
+
 // Float32 levels of codes 2 j, 2 j + 1 of one thread's 32 codes, for widths other
-// than 4 (from a lane-private LDS table; tp = this lane's copy).
-template <int BITS>
-__device__ __forceinline__ float2 level_pair(const Codes32<BITS>& c, int j, uint32_t tp) {
+// than 4.
+template <int BITS, typename Tab>
+__device__ __forceinline__ float2 level_pair(const Codes32<BITS>& c, int j, const Tab& tab) {
   if constexpr (BITS == 8) {
     // one float32 level per code; 16 lane copies, entry e of copy l at e*64 + 4l
     const uint32_t w = c.w[j >> 1] >> (16 * (j & 1));
-    return make_float2(lds_f32(tp + ((w & 255u) << 6)), lds_f32(tp + (((w >> 8) & 255u) << 6)));
+    return make_float2(tab.one((w & 255u) << 6), tab.one(((w >> 8) & 255u) << 6));
   } else {
     // float32 level pairs of two neighbouring codes; 32 lane copies, entry e at e*256 + 8l
     uint32_t e;
@@ -159,7 +171,7 @@ __device__ __forceinline__ float2 level_pair(const Codes32<BITS>& c, int j, uint
       if (sh + 6 > 32) v |= c.w[wd + 1] << (32 - sh);
       e = v & 63u;
     }
-    return lds_pair(tp + (e << 8));
+    return tab.pair(e << 8);
   }
 }
 
@@ -169,7 +181,7 @@ template <int BITS, int J0, int J1>
 __device__ __forceinline__ void dequant_pairs(const Codes32<BITS>& c, float ap, uint32_t tp, uint32_t (&o)[16]) {
 #pragma unroll
   for (int j = J0; j < J1; ++j) {
-    const float2 p = level_pair<BITS>(c, j, tp);
+    const float2 p = level_pair<BITS>(c, j, TabAt{tp});
     o[j] = cvt_pk_bf16(p.x * ap, p.y * ap);
   }
 }

@@ -108,9 +108,8 @@ struct TileLds {
   static constexpr uint32_t kTabBytes = (KIND == TILE_I8 || BITS == 4) ? 0
                                         : BITS == 8                    ? 256 * 16 * 4
                                                                        : PairTableF32<BITS>::kBytes;
-  // the epilogue's staging of BM / kPasses output rows (float32 at most) overlays the buffers
-  static constexpr int kPasses = BM * BN > 256 * 128 ? 2 : 1;
-  static constexpr uint32_t kStage = (BM / kPasses) * (BN * 4 + 16);
+  // the epilogue's staging of the output rows (float32 at most) overlays the buffers (256 x 256: inside them)
+  static constexpr uint32_t kStage = BM * BN == 256 * 256 ? 0 : BM * (BN * 4 + 16);
   static constexpr uint32_t kBytes = kTab + kTabBytes > kStage ? kTab + kTabBytes : kStage;
   static_assert(kBytes <= 160 * 1024, "LDS budget");
 };
@@ -141,10 +140,38 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   constexpr int XL = BM / 64;  // 16-byte pieces of x per thread and step
   constexpr int WL = BN / 64;  // the same of an int8 weight; 8-code parts of a coded one
   constexpr int CPT = BN / 8;  // codes per thread and step
+  // 256 x 256 tiles: direct loads into LDS.  The buffers are separate LDS variables, so that the compiler knows that the
+  // fragment reads of one do not touch the loads in flight into the other and does not wait for them.
+  constexpr bool kDma = BM * BN == 256 * 256;
   extern __shared__ uint32_t smem[];
+  __shared__ __attribute__((aligned(16))) char sX0[kDma ? L::kX : 16], sX1[kDma ? L::kX : 16];
+  __shared__ __attribute__((aligned(16))) char sW0[kDma ? L::kW : 16], sW1[kDma ? L::kW : 16];
+  __shared__ __attribute__((aligned(16))) char sT[kDma && L::kTabBytes ? L::kTabBytes : 16];
   (void)smem;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 31, h = lane >> 5;
+  // LDS accesses: byte `off` of x buffer / weight buffer `buf`
+  auto rd_x = [&](int buf, uint32_t off) -> u32x4_t {
+    if constexpr (kDma) return *reinterpret_cast<const u32x4_t*>((buf ? sX1 : sX0) + off);
+    else return lds_u32x4(off + (uint32_t)buf * L::kX);
+  };
+  auto st_x = [&](int buf, uint32_t off, u32x4_t v) {
+    if constexpr (kDma) *reinterpret_cast<u32x4_t*>((buf ? sX1 : sX0) + off) = v;
+    else lds_store_u32x4(off + (uint32_t)buf * L::kX, v);
+  };
+  auto rd_w = [&](int buf, uint32_t off) -> u32x4_t {
+    if constexpr (kDma) return *reinterpret_cast<const u32x4_t*>((buf ? sW1 : sW0) + off);
+    else return lds_u32x4(L::kWOff + off + (uint32_t)buf * L::kW);
+  };
+  auto st_w = [&](int buf, uint32_t off, u32x4_t v) {
+    if constexpr (kDma) *reinterpret_cast<u32x4_t*>((buf ? sW1 : sW0) + off) = v;
+    else lds_store_u32x4(L::kWOff + off + (uint32_t)buf * L::kW, v);
+  };
+  auto tr_w = [&](int buf, uint32_t off) -> u16x4_t {
+    if constexpr (kDma)
+      return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)((buf ? sW1 : sW0) + off));
+    else return lds_tr16(L::kWOff + off + (uint32_t)buf * L::kW);
+  };
 
   // ---- which tile.  Workgroup b runs on XCD b % 8; each XCD takes a contiguous range of tiles.
   // With P.rest the tiles are counted in 256 x 256 ones and those of a last partial
@@ -195,18 +222,18 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   const int nsteps = (int)((kbytes + 127) / 128);
 
   if constexpr (L::kTabBytes > 0) {
-    float* sL = reinterpret_cast<float*>(smem);
+    float* sL = kDma ? reinterpret_cast<float*>(sX0) : reinterpret_cast<float*>(smem);
     stage_levels<1 << BITS>(lv, sL);
     __syncthreads();
+    float* tab = kDma ? reinterpret_cast<float*>(sT) : reinterpret_cast<float*>(smem) + L::kTab / 4;
     if constexpr (BITS == 8) {
-      for (int i = tid; i < 256 * 16; i += 512)
-        *reinterpret_cast<__attribute__((address_space(3))) float*>((uintptr_t)(L::kTab + 4 * i)) = sL[i >> 4];
+      for (int i = tid; i < 256 * 16; i += 512) tab[i] = sL[i >> 4];
     } else {
       constexpr int NL = 1 << BITS;
       for (int i = tid; i < PairTableF32<BITS>::kEntries * 32; i += 512) {
         const int en = i >> 5;
-        *reinterpret_cast<__attribute__((address_space(3))) f32x2_t*>((uintptr_t)(L::kTab + 8 * i)) =
-            f32x2_t{sL[en & (NL - 1)], sL[en >> BITS]};
+        tab[2 * i] = sL[en & (NL - 1)];
+        tab[2 * i + 1] = sL[en >> BITS];
       }
     }
     __syncthreads();
@@ -230,7 +257,30 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   auto load_xp = [&](uint32_t off, Xs& s, int i) {  // piece i of the step at offset off
     s.v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(xr, off + (uint32_t)i * 64u * kbytes, 0, 0));
   };
-  auto store_xp = [&](const Xs& s, int buf, int i) { lds_store_u32x4(xst + (uint32_t)buf * L::kX + 8192u * i, s.v[i]); };
+  auto store_xp = [&](const Xs& s, int buf, int i) { st_x(buf, xst + 8192u * i, s.v[i]); };
+  // Direct loads: load j (0..3) of wave w fills tile rows 32 w + 8 j .. + 7 (1 KB, lane l at byte 16 l: row l / 8, slot
+  // l % 8), so lane l reads the chunk that the swizzle puts at its slot; it depends on j through j % 2 only.
+  const uint32_t t8 = (uint32_t)lane >> 3;
+  uint32_t dch[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) dch[p] = 16u * (((uint32_t)lane & 7u) ^ swz(t8 + 8u * p));
+  auto dma = [&](__amdgpu_buffer_rsrc_t rsrc, char* dst, int k) {
+    if constexpr (kDma) {
+      const uint32_t kb = (uint32_t)k * 128u;
+      uint32_t off[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        uint32_t o = (uint32_t)(32 * wave + t8) * kbytes + kb + dch[p];
+        asm volatile("" : "+v"(o));
+        off[p] = kb + dch[p] < kbytes ? o : 0x80000000u;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rsrc, (void __attribute__((address_space(3)))*)(dst + wave * 4096 + j * 1024), 16,
+            off[j & 1] + (uint32_t)j * 8u * kbytes, 0, 0, 0);
+    }
+  };
 
   // ---- weight loads
   // I8: as x, rows n0 .. n0 + 255 (rows past N zero).
@@ -272,12 +322,16 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
 #pragma unroll
   for (int q = 0; q < WL; ++q) {
     if constexpr (KIND == TILE_TR)
-      wst[q] = L::kWOff + (uint32_t)(bq >> 1) * 16384u + (uint32_t)rr * 256u +
+      wst[q] = (uint32_t)(bq >> 1) * 16384u + (uint32_t)rr * 256u +
                (tr_chunk((uint32_t)(8 * (bq & 1) + WL * dh + q), (uint32_t)rr) << 4);
     else
-      wst[q] = L::kWOff + (uint32_t)rr * 128u + ((((uint32_t)(WL * dh + q)) ^ swz((uint32_t)rr & 15u)) << 4);
+      wst[q] = (uint32_t)rr * 128u + ((((uint32_t)(WL * dh + q)) ^ swz((uint32_t)rr & 15u)) << 4);
   }
-  const uint32_t tp = L::kTab + (BITS == 8 ? 4u * (lane & 15) : 8u * fr);
+  const uint32_t tl = BITS == 8 ? 4u * (lane & 15) : 8u * fr;  // the lane's copy of the level table
+  const auto tab = [&] {
+    if constexpr (kDma) return TabPtr{sT + tl};
+    else return TabAt{L::kTab + tl};
+  }();
   auto load_wp = [&](uint32_t off, Ws& s, int i) {  // I8: piece i, as load_xp
     s.v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, off + (uint32_t)i * 64u * kbytes, 0, 0));
   };
@@ -303,12 +357,19 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   auto store_w = [&](const Ws& s, const Lut4& lut, float ap, auto part, int buf) {
     constexpr int I = decltype(part)::value;
     if constexpr (KIND == TILE_I8) {
-      lds_store_u32x4(L::kWOff + xst + (uint32_t)buf * L::kW + 8192u * I, s.v[I]);
+      st_w(buf, xst + 8192u * I, s.v[I]);
     } else {
-      uint32_t o[16];
-      if constexpr (BITS == 4) lut4_word(s.c.w[I], lut, o + 4 * I);
-      else dequant_pairs<BITS, 4 * I, 4 * I + 4>(s.c, ap, tp, o);
-      lds_store_u32x4(wst[I] + (uint32_t)buf * L::kW, u32x4_t{o[4 * I], o[4 * I + 1], o[4 * I + 2], o[4 * I + 3]});
+      uint32_t o[4];
+      if constexpr (BITS == 4) {
+        lut4_word(s.c.w[I], lut, o);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 p = level_pair<BITS>(s.c, 4 * I + j, tab);
+          o[j] = cvt_pk_bf16(p.x * ap, p.y * ap);
+        }
+      }
+      st_w(buf, wst[I], u32x4_t{o[0], o[1], o[2], o[3]});
     }
   };
   // the same in two halves, for the widths whose levels come from LDS: the lookups before a run of products, the rest after
@@ -317,7 +378,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   auto lookup_w = [&](const Ws& s, auto part) {
     if constexpr (kLook) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) look[j] = level_pair<BITS>(s.c, 4 * decltype(part)::value + j, tp);
+      for (int j = 0; j < 4; ++j) look[j] = level_pair<BITS>(s.c, 4 * decltype(part)::value + j, tab);
     }
   };
   auto finish_w = [&](float ap, auto part, int buf) {
@@ -325,7 +386,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       u32x4_t o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = cvt_pk_bf16(look[j].x * ap, look[j].y * ap);
-      lds_store_u32x4(wst[decltype(part)::value] + (uint32_t)buf * L::kW, o);
+      st_w(buf, wst[decltype(part)::value], o);
     }
   };
   auto store_w_all = [&](const Ws& s, int k, int buf) {
@@ -347,7 +408,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   for (int s = 0; s < 4; ++s) {
     const uint32_t fo = (uint32_t)(fr * 128) + ((((uint32_t)(2 * s + h)) ^ swz((uint32_t)fr & 15u)) << 4);
     xb[s] = (uint32_t)(mh * (BM / WM) * 128) + fo;
-    wb[s] = L::kWOff + (uint32_t)(nh * (BN / WN) * 128) + fo;
+    wb[s] = (uint32_t)(nh * (BN / WN) * 128) + fo;
   }
   uint32_t tbo[NT];
   {
@@ -356,23 +417,23 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     for (int c = 0; c < NT; ++c) {
       const uint32_t col = (uint32_t)(nh * (BN / WN) + 32 * c);
       const uint32_t chunk = ((col & 127u) >> 3) + 2u * (g & 1u) + ((sp >> 1) & 1u);
-      tbo[c] = L::kWOff + (col >> 7) * 16384u + (8u * h + (sp >> 2)) * 256u + (tr_chunk(chunk, sp >> 2) << 4) +
+      tbo[c] = (col >> 7) * 16384u + (8u * h + (sp >> 2)) * 256u + (tr_chunk(chunk, sp >> 2) << 4) +
                8u * (sp & 1u);
     }
   }
   u32x4_t fx[2][MT], fw[2][NT];
   auto read_frags = [&](int buf, int s, int slot) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) fx[slot][i] = lds_u32x4(xb[s] + (uint32_t)buf * L::kX + 4096u * i);
+    for (int i = 0; i < MT; ++i) fx[slot][i] = rd_x(buf, xb[s] + 4096u * i);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
       if constexpr (KIND == TILE_TR) {
-        const uint32_t ad = tbo[c] + (uint32_t)buf * L::kW + 4096u * s;
-        const u16x4_t lo = lds_tr16(ad), hi = lds_tr16(ad + 1024u);
+        const uint32_t ad = tbo[c] + 4096u * s;
+        const u16x4_t lo = tr_w(buf, ad), hi = tr_w(buf, ad + 1024u);
         fw[slot][c] = u32x4_t{__builtin_bit_cast(uint2, lo).x, __builtin_bit_cast(uint2, lo).y,
                               __builtin_bit_cast(uint2, hi).x, __builtin_bit_cast(uint2, hi).y};
       } else {
-        fw[slot][c] = lds_u32x4(wb[s] + (uint32_t)buf * L::kW + 4096u * c);
+        fw[slot][c] = rd_w(buf, wb[s] + 4096u * c);
       }
     }
   };
@@ -396,7 +457,19 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   // ---- the steps
   Xs xs;
   Ws wa, wn;
-  {
+  if constexpr (kDma) {
+    dma(xr, sX0, 0);
+    if constexpr (KIND == TILE_I8) {
+      dma(wr, sW0, 0);
+    } else {
+      load_w(0, wa);
+      // (loads in the steps' order: the compiler's wait counts at the loop's head are those of the worse path)
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(1, wn);
+      __builtin_amdgcn_sched_barrier(0);
+      store_w_all(wa, 0, 0);
+    }
+  } else {
     const uint32_t off0 = step_off(0), off1 = step_off(1);
 #pragma unroll
     for (int i = 0; i < XL; ++i) load_xp(off0, xs, i);
@@ -405,7 +478,6 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       for (int i = 0; i < WL; ++i) load_wp(off0, wa, i);
     } else {
       load_w(0, wa);
-      // (loads in the steps' order, here and below: the compiler's wait counts at the loop's head are those of the worse path)
       __builtin_amdgcn_sched_barrier(0);
       load_w(1, wn);
     }
@@ -425,11 +497,17 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   __syncthreads();
   // Step k: xs (and the integer weights wi) hold step k + 1's pieces, loaded during step k - 1; each is written to the
   // other buffer and its register loaded again for step k + 2 between the products, so a
-  // load has a whole step to arrive and the writes overlap the products.
+  // load has a whole step to arrive and the writes overlap the products.  Direct loads bring step k + 1 to the other buffer
+  // during step k.
   // cur: the codes of step k + 1; nxt: room for those of step k + 2.
   auto step = [&](int k, int buf, Ws& wi, Ws& cur, Ws& nxt) {
     __builtin_amdgcn_sched_barrier(0);
-    const uint32_t off = step_off(k + 2);
+    const uint32_t off = kDma ? 0u : step_off(k + 2);
+    if constexpr (kDma) {
+      dma(xr, buf ? sX0 : sX1, k + 1);
+      if constexpr (KIND == TILE_I8) dma(wr, buf ? sW0 : sW1, k + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     if constexpr (KIND != TILE_I8) load_w(k + 2, nxt);
     // (opaque from here: the compiler would otherwise start the codes' arithmetic right after their load, a
     // step early, and wait for them there)
@@ -451,12 +529,12 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       if constexpr (kLook && kPart) lookup_w(cur, wpart);
       __builtin_amdgcn_sched_barrier(0);
       mfmas(S & 1);
-      if constexpr (S < XL) {
+      if constexpr (!kDma && S < XL) {
         store_xp(xs, buf ^ 1, S);
         load_xp(off, xs, S);
       }
       if constexpr (KIND == TILE_I8) {
-        if constexpr (S < WL) {
+        if constexpr (!kDma && S < WL) {
           store_w(wi, lut, ap, spos, buf ^ 1);
           load_wp(off, wi, S);
         }
@@ -540,8 +618,8 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
           lo[i] = pack_bf16x2(u0 - bf16_bits_to_f32(h0), u1 - bf16_bits_to_f32(h1));
         }
         const uint32_t xrow = (uint32_t)row * 128u;
-        lds_store_u32x4(xrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), hv);
-        lds_store_u32x4(xrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), lo);
+        st_x(0, xrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), hv);
+        st_x(0, xrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), lo);
       }
       if constexpr (KIND == TILE_TR) {
         // A[j0 + row][n0 ..]: rows 0..31 and 32..63 hold the same 32 adapter rows
@@ -551,9 +629,9 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
           const int64_t col = n0 + 8 * c;
           u32x4_t v = zero4;
           if (j0 + row < r && col < K) v = *reinterpret_cast<const u32x4_t*>(Ae + (int64_t)(j0 + row) * K + col);
-          const uint32_t base = L::kWOff + (uint32_t)(c >> 4) * 16384u;
-          lds_store_u32x4(base + (uint32_t)row * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
-          lds_store_u32x4(base + (uint32_t)(row + 32) * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
+          const uint32_t base = (uint32_t)(c >> 4) * 16384u;
+          st_w(0, base + (uint32_t)row * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
+          st_w(0, base + (uint32_t)(row + 32) * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
         }
       } else {
         // [B[n][j0 ..] | the same]
@@ -573,9 +651,9 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
               }
             }
           }
-          const uint32_t wrow = L::kWOff + (uint32_t)row * 128u;
-          lds_store_u32x4(wrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), v);
-          lds_store_u32x4(wrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), v);
+          const uint32_t wrow = (uint32_t)row * 128u;
+          st_w(0, wrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), v);
+          st_w(0, wrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), v);
         }
       }
       __syncthreads();
@@ -591,56 +669,90 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     }
   }
 
-  // ---- output: staged row-major in LDS (BM / kPasses rows at a time), stored in 16-byte pieces
-  constexpr int RP = BM / L::kPasses;
+  // ---- output: staged row-major in LDS, stored in 16-byte pieces
   const int es = P.ydt == DT_F32 ? 4 : 2;
-  const uint32_t rs = (uint32_t)BN * es + 16u;
   const bool vec = (NO * es) % 16 == 0;
   const int cpr = BN * es / 16;  // 16-byte pieces of a staged row (a power of two)
-  for (int p = 0; p < L::kPasses; ++p) {
-    if (p * RP >= mrows) break;
-    if (mh * (BM / WM) / RP == p) {
+  auto put = [&](int row, int c, u32x4_t v) {  // piece c of tile row `row`
+    const int64_t col = n0 + c * (16 / es);
+    if (col >= NO) return;
+    char* dst = reinterpret_cast<char*>(P.y) + ((int64_t)(row0 + row) * NO + col) * es;
+    if (vec) {
+      *reinterpret_cast<u32x4_t*>(dst) = v;
+    } else {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t ad = (uint32_t)(mh * (BM / WM) - p * RP + 32 * i + fr) * rs +
-                                (uint32_t)(nh * (BN / WN) + 32 * c + 8 * q + 4 * h) * es;
-            const float v0 = acc[i][c][4 * q], v1 = acc[i][c][4 * q + 1], v2 = acc[i][c][4 * q + 2], v3 = acc[i][c][4 * q + 3];
-            if (es == 4) {
-              lds_store_f32x4(ad, f32x4_t{v0, v1, v2, v3});
-            } else {
-              *reinterpret_cast<__attribute__((address_space(3))) u32x2v_t*>((uintptr_t)ad) =
-                  u32x2v_t{pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)};
-            }
-          }
-    }
-    __syncthreads();
-    const int rows = min(RP, mrows - p * RP);
-    for (int idx = tid; idx < rows * cpr; idx += 512) {
-      const int row = es == 4 ? idx / (BN / 4) : idx / (BN / 8), c = idx & (cpr - 1);
-      const int64_t col = n0 + c * (16 / es);
-      if (col >= NO) continue;
-      const u32x4_t v = lds_u32x4((uint32_t)row * rs + 16u * c);
-      char* dst = reinterpret_cast<char*>(P.y) + ((int64_t)(row0 + p * RP + row) * NO + col) * es;
-      if (vec) {
-        *reinterpret_cast<u32x4_t*>(dst) = v;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = v[i];
-          if (es == 4) {
-            if (col + i < NO) reinterpret_cast<uint32_t*>(dst)[i] = w;
-          } else {
-            if (col + 2 * i < NO) reinterpret_cast<uint16_t*>(dst)[2 * i] = (uint16_t)w;
-            if (col + 2 * i + 1 < NO) reinterpret_cast<uint16_t*>(dst)[2 * i + 1] = (uint16_t)(w >> 16);
-          }
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = v[i];
+        if (es == 4) {
+          if (col + i < NO) reinterpret_cast<uint32_t*>(dst)[i] = w;
+        } else {
+          if (col + 2 * i < NO) reinterpret_cast<uint16_t*>(dst)[2 * i] = (uint16_t)w;
+          if (col + 2 * i + 1 < NO) reinterpret_cast<uint16_t*>(dst)[2 * i + 1] = (uint16_t)(w >> 16);
         }
       }
     }
+  };
+  if constexpr (kDma) {
+    // The four 32 KB buffers hold 64 bf16 or 32 float32 rows of 256 columns each, their 16-byte pieces XOR-swizzled by the
+    // row: all 256 bf16 rows at once, float32 rows in two passes of 128.
+    const int passes = es == 4 ? 2 : 1, rpb = es == 4 ? 32 : 64;
+    for (int p = 0; p < passes; ++p) {
+      if (p * 128 >= mrows) break;
+      if (es == 2 || mh == p) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          char* st = es == 4 ? (i < 2 ? (i ? sX1 : sX0) : (i == 3 ? sW1 : sW0)) : (mh ? (i < 2 ? sW0 : sW1) : (i < 2 ? sX0 : sX1));
+          const uint32_t lr = (uint32_t)(es == 4 ? fr : 32 * (i & 1) + fr);
+#pragma unroll
+          for (int c = 0; c < NT; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float v0 = acc[i][c][4 * q], v1 = acc[i][c][4 * q + 1], v2 = acc[i][c][4 * q + 2], v3 = acc[i][c][4 * q + 3];
+              if (es == 4) {
+                const uint32_t pc = (uint32_t)(16 * nh + 8 * c + 2 * q + h) ^ (lr & 31u);
+                *reinterpret_cast<f32x4_t*>(st + lr * 1024u + 16u * pc) = f32x4_t{v0, v1, v2, v3};
+              } else {
+                const uint32_t pc = (uint32_t)(8 * nh + 4 * c + q) ^ (lr & 31u);
+                *reinterpret_cast<u32x2v_t*>(st + lr * 512u + 16u * pc + 8u * h) = u32x2v_t{pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)};
+              }
+            }
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const char* st = b < 2 ? (b ? sX1 : sX0) : (b == 3 ? sW1 : sW0);
+        const int first = p * 128 + b * rpb, rows = min(rpb, mrows - first);
+        for (int idx = tid; idx < rows * cpr; idx += 512) {
+          const int lr = es == 4 ? idx >> 6 : idx >> 5, c = idx & (cpr - 1);
+          put(first + lr, c, *reinterpret_cast<const u32x4_t*>(st + lr * (256 * es) + 16 * (c ^ (lr & 31))));
+        }
+      }
+      __syncthreads();
+    }
+  } else {
+    const uint32_t rs = (uint32_t)BN * es + 16u;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t ad = (uint32_t)(mh * (BM / WM) + 32 * i + fr) * rs +
+                              (uint32_t)(nh * (BN / WN) + 32 * c + 8 * q + 4 * h) * es;
+          const float v0 = acc[i][c][4 * q], v1 = acc[i][c][4 * q + 1], v2 = acc[i][c][4 * q + 2], v3 = acc[i][c][4 * q + 3];
+          if (es == 4) {
+            lds_store_f32x4(ad, f32x4_t{v0, v1, v2, v3});
+          } else {
+            *reinterpret_cast<__attribute__((address_space(3))) u32x2v_t*>((uintptr_t)ad) =
+                u32x2v_t{pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)};
+          }
+        }
     __syncthreads();
+    for (int idx = tid; idx < mrows * cpr; idx += 512) {
+      const int row = es == 4 ? idx / (BN / 4) : idx / (BN / 8), c = idx & (cpr - 1);
+      put(row, c, lds_u32x4((uint32_t)row * rs + 16u * c));
+    }
   }
 }
 
@@ -741,14 +853,15 @@ inline int64_t tile_bound(int64_t M, int experts, int BM) { return M / BM + std:
 template <int KIND, int BITS, int BM, int BN>
 hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
   auto kern = k_tile<KIND, BITS, BM, BN>;
-  constexpr int shmem = (int)TileLds<KIND, BITS, BM, BN>::kBytes;
+  // 256 x 256 tiles have their LDS as variables; the others address dynamic LDS from 0: they must not have any static
+  constexpr bool dma = BM * BN == 256 * 256;
+  constexpr int shmem = dma ? 0 : (int)TileLds<KIND, BITS, BM, BN>::kBytes;
   static std::once_flag once;
   static hipError_t setup;
   std::call_once(once, [&] {
-    // the kernel addresses LDS from 0: it must not have static LDS
     hipFuncAttributes fa;
     setup = hipFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern));
-    if (setup == hipSuccess && fa.sharedSizeBytes != 0) setup = hipErrorInvalidKernelFile;
+    if (setup == hipSuccess && !dma && fa.sharedSizeBytes != 0) setup = hipErrorInvalidKernelFile;
   });
   if (setup != hipSuccess) return setup;
   const int64_t no = KIND == TILE_TR ? a.K : a.N;
@@ -757,8 +870,11 @@ hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
   if (a.rest && BM < 256) tiles = kRestMax * (256 / BM) * (256 / BN);
   if (tiles <= 0) return hipSuccess;
   if (tiles > INT32_MAX - 8) return hipErrorInvalidValue;
-  hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, shmem);
-  if (err != hipSuccess) return err;
+  if (!dma) {
+    const hipError_t err =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, shmem);
+    if (err != hipSuccess) return err;
+  }
   hipLaunchKernelGGL(kern, dim3((unsigned)(8 * ((tiles + 7) / 8))), dim3(512), shmem, s, a, lv);
   return hipGetLastError();
 }
