@@ -33,7 +33,6 @@
 
 #include <algorithm>
 #include <climits>
-#include <mutex>
 #include <type_traits>
 
 #include "qlr_dequant.h"
@@ -103,15 +102,10 @@ __device__ __forceinline__ int tile_scan(const int32_t* offsets, int E, int M, i
 template <int KIND, int BITS, int BM, int BN>
 struct TileLds {
   static constexpr uint32_t kX = BM * 128, kW = BN * 128;
-  static constexpr uint32_t kWOff = 2 * kX;
-  static constexpr uint32_t kTab = 2 * (kX + kW);  // level table of the widths that use one
   static constexpr uint32_t kTabBytes = (KIND == TILE_I8 || BITS == 4) ? 0
                                         : BITS == 8                    ? 256 * 16 * 4
                                                                        : PairTableF32<BITS>::kBytes;
-  // the epilogue's staging of the output rows (float32 at most) overlays the buffers (256 x 256: inside them)
-  static constexpr uint32_t kStage = BM * BN == 256 * 256 ? 0 : BM * (BN * 4 + 16);
-  static constexpr uint32_t kBytes = kTab + kTabBytes > kStage ? kTab + kTabBytes : kStage;
-  static_assert(kBytes <= 160 * 1024, "LDS budget");
+  static_assert(2 * (kX + kW) + kTabBytes <= 160 * 1024, "LDS budget");
 };
 
 __device__ __forceinline__ f32x16_t tile_mfma(u32x4_t a, u32x4_t b, f32x16_t c) {
@@ -137,40 +131,22 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   using L = TileLds<KIND, BITS, BM, BN>;
   constexpr int WM = (BN == 256 || BM == 64) ? 2 : 4, WN = 8 / WM;
   constexpr int MT = BM / WM / 32, NT = BN / WN / 32;  // MFMA tiles of a wave
-  constexpr int XL = BM / 64;  // 16-byte pieces of x per thread and step
-  constexpr int WL = BN / 64;  // the same of an int8 weight; 8-code parts of a coded one
+  constexpr int XL = BM / 64;  // direct loads of x per wave and step
+  constexpr int WL = BN / 64;  // the same of an int8 weight; 8-code parts of a coded one per thread
   constexpr int CPT = BN / 8;  // codes per thread and step
-  // 256 x 256 tiles: direct loads into LDS.  The buffers are separate LDS variables, so that the compiler knows that the
-  // fragment reads of one do not touch the loads in flight into the other and does not wait for them.
-  constexpr bool kDma = BM * BN == 256 * 256;
-  extern __shared__ uint32_t smem[];
-  __shared__ __attribute__((aligned(16))) char sX0[kDma ? L::kX : 16], sX1[kDma ? L::kX : 16];
-  __shared__ __attribute__((aligned(16))) char sW0[kDma ? L::kW : 16], sW1[kDma ? L::kW : 16];
-  __shared__ __attribute__((aligned(16))) char sT[kDma && L::kTabBytes ? L::kTabBytes : 16];
-  (void)smem;
+  // x and int8 weights are loaded straight into LDS.  The buffers are separate LDS variables, so that the compiler knows
+  // that the fragment reads of one do not touch the loads in flight into the other and does not wait for them.
+  __shared__ __attribute__((aligned(16))) char sX0[L::kX], sX1[L::kX], sW0[L::kW], sW1[L::kW];
+  // The small integer tile has little else to hide a load behind: a third buffer, its loads two steps ahead.
+  constexpr bool kThird = KIND == TILE_I8 && BM == 64;
+  __shared__ __attribute__((aligned(16))) char sX2[kThird ? L::kX : 16], sW2[kThird ? L::kW : 16];
+  __shared__ __attribute__((aligned(16))) char sT[L::kTabBytes ? L::kTabBytes : 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 31, h = lane >> 5;
-  // LDS accesses: byte `off` of x buffer / weight buffer `buf`
-  auto rd_x = [&](int buf, uint32_t off) -> u32x4_t {
-    if constexpr (kDma) return *reinterpret_cast<const u32x4_t*>((buf ? sX1 : sX0) + off);
-    else return lds_u32x4(off + (uint32_t)buf * L::kX);
-  };
-  auto st_x = [&](int buf, uint32_t off, u32x4_t v) {
-    if constexpr (kDma) *reinterpret_cast<u32x4_t*>((buf ? sX1 : sX0) + off) = v;
-    else lds_store_u32x4(off + (uint32_t)buf * L::kX, v);
-  };
-  auto rd_w = [&](int buf, uint32_t off) -> u32x4_t {
-    if constexpr (kDma) return *reinterpret_cast<const u32x4_t*>((buf ? sW1 : sW0) + off);
-    else return lds_u32x4(L::kWOff + off + (uint32_t)buf * L::kW);
-  };
-  auto st_w = [&](int buf, uint32_t off, u32x4_t v) {
-    if constexpr (kDma) *reinterpret_cast<u32x4_t*>((buf ? sW1 : sW0) + off) = v;
-    else lds_store_u32x4(L::kWOff + off + (uint32_t)buf * L::kW, v);
-  };
-  auto tr_w = [&](int buf, uint32_t off) -> u16x4_t {
-    if constexpr (kDma)
-      return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)((buf ? sW1 : sW0) + off));
-    else return lds_tr16(L::kWOff + off + (uint32_t)buf * L::kW);
+  auto st16 = [](char* p, u32x4_t v) { *reinterpret_cast<u32x4_t*>(p) = v; };
+  auto ld16 = [](const char* p) { return *reinterpret_cast<const u32x4_t*>(p); };
+  auto ld_tr = [](char* p) -> u16x4_t {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
   };
 
   // ---- which tile.  Workgroup b runs on XCD b % 8; each XCD takes a contiguous range of tiles.
@@ -222,10 +198,10 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   const int nsteps = (int)((kbytes + 127) / 128);
 
   if constexpr (L::kTabBytes > 0) {
-    float* sL = kDma ? reinterpret_cast<float*>(sX0) : reinterpret_cast<float*>(smem);
+    float* sL = reinterpret_cast<float*>(sX0);
     stage_levels<1 << BITS>(lv, sL);
     __syncthreads();
-    float* tab = kDma ? reinterpret_cast<float*>(sT) : reinterpret_cast<float*>(smem) + L::kTab / 4;
+    float* tab = reinterpret_cast<float*>(sT);
     if constexpr (BITS == 8) {
       for (int i = tid; i < 256 * 16; i += 512) tab[i] = sL[i >> 4];
     } else {
@@ -239,55 +215,39 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     __syncthreads();
   }
 
-  // ---- x loads: piece i of a thread = chunk tid % 8 of tile row tid / 8 + 64 i; rows past the
-  // range and chunks past the row's end read zero
+  // ---- x, and int8 weights: direct loads.  Load j of the J of wave w fills tile rows 8 (J w + j) .. + 7 (1 KB, lane l at
+  // byte 16 l: row l / 8, slot l % 8), so lane l reads the chunk that the swizzle puts at its slot; that depends on the load
+  // through (J w + j) % 2 only.  Rows past the range and chunks past the row's end read zero.
   const char* xbase = reinterpret_cast<const char*>(P.x) + (int64_t)row0 * kbytes;
   const __amdgpu_buffer_rsrc_t xr = tile_rsrc(xbase, (uint32_t)mrows * kbytes);
-  const uint32_t ch = (uint32_t)tid & 7u, rq = (uint32_t)tid >> 3;
-  const uint32_t xg = rq * kbytes + 16u * ch;
-  const uint32_t xst = rq * 128u + ((ch ^ swz(rq & 15u)) << 4);  // 64-row strides keep row % 16
-  // (a chunk past the row's end: an offset past every range, rows of at most 2^21 bytes added)
-  auto step_off = [&](int k) {
-    const uint32_t kb = (uint32_t)k * 128u;
-    uint32_t off = xg + kb;
-    asm volatile("" : "+v"(off));  // keep the select a select (no branch around the loads)
-    return kb + 16u * ch < kbytes ? off : 0x80000000u;
-  };
-  struct Xs { u32x4_t v[XL]; };
-  auto load_xp = [&](uint32_t off, Xs& s, int i) {  // piece i of the step at offset off
-    s.v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(xr, off + (uint32_t)i * 64u * kbytes, 0, 0));
-  };
-  auto store_xp = [&](const Xs& s, int buf, int i) { st_x(buf, xst + 8192u * i, s.v[i]); };
-  // Direct loads: load j (0..3) of wave w fills tile rows 32 w + 8 j .. + 7 (1 KB, lane l at byte 16 l: row l / 8, slot
-  // l % 8), so lane l reads the chunk that the swizzle puts at its slot; it depends on j through j % 2 only.
   const uint32_t t8 = (uint32_t)lane >> 3;
-  uint32_t dch[2];
+  const uint32_t dch0 = 16u * (((uint32_t)lane & 7u) ^ swz(t8)), dch1 = 16u * (((uint32_t)lane & 7u) ^ swz(t8 + 8u));
+  const uint32_t dchw = (wave & 1) ? dch1 : dch0;
+  auto direct = [&](__amdgpu_buffer_rsrc_t rsrc, char* dst, int k, auto loads) {
+    constexpr int J = decltype(loads)::value;
+    const uint32_t kb = (uint32_t)k * 128u;
+    uint32_t off[2];
 #pragma unroll
-  for (int p = 0; p < 2; ++p) dch[p] = 16u * (((uint32_t)lane & 7u) ^ swz(t8 + 8u * p));
-  auto dma = [&](__amdgpu_buffer_rsrc_t rsrc, char* dst, int k) {
-    if constexpr (kDma) {
-      const uint32_t kb = (uint32_t)k * 128u;
-      uint32_t off[2];
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        uint32_t o = (uint32_t)(32 * wave + t8) * kbytes + kb + dch[p];
-        asm volatile("" : "+v"(o));
-        off[p] = kb + dch[p] < kbytes ? o : 0x80000000u;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rsrc, (void __attribute__((address_space(3)))*)(dst + wave * 4096 + j * 1024), 16,
-            off[j & 1] + (uint32_t)j * 8u * kbytes, 0, 0, 0);
+    for (int p = 0; p < (J < 2 ? J : 2); ++p) {
+      const uint32_t chb = J == 1 ? dchw : p ? dch1 : dch0;
+      uint32_t o = ((uint32_t)(8 * J * wave) + t8) * kbytes + kb + chb;
+      asm volatile("" : "+v"(o));  // keep the select a select (no branch around the loads)
+      // (a chunk past the row's end: an offset past every range, rows of at most 2^21 bytes added)
+      off[p] = kb + chb < kbytes ? o : 0x80000000u;
     }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (void __attribute__((address_space(3)))*)(dst + (J * wave + j) * 1024), 16,
+                                               off[j & 1] + (uint32_t)j * 8u * kbytes, 0, 0, 0);
   };
+  constexpr std::integral_constant<int, XL> xloads{};
+  constexpr std::integral_constant<int, WL> wloads{};
 
   // ---- weight loads
-  // I8: as x, rows n0 .. n0 + 255 (rows past N zero).
+  // I8: as x, the rows from n0 (rows past N zero).
   // CODED: thread = row tid / TPB, codes [CPT dh, + CPT) of the step's block (TPB threads share a block).
   // TR: thread = weight row 64 k + tid / 8, codes [CPT dh, + CPT) of block column n0 / 64 + bq.
   struct Ws {
-    u32x4_t v[KIND == TILE_I8 ? WL : 1];
     Codes32<BITS> c;
     uint32_t q8;
     float sc;
@@ -328,13 +288,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       wst[q] = (uint32_t)rr * 128u + ((((uint32_t)(WL * dh + q)) ^ swz((uint32_t)rr & 15u)) << 4);
   }
   const uint32_t tl = BITS == 8 ? 4u * (lane & 15) : 8u * fr;  // the lane's copy of the level table
-  const auto tab = [&] {
-    if constexpr (kDma) return TabPtr{sT + tl};
-    else return TabAt{L::kTab + tl};
-  }();
-  auto load_wp = [&](uint32_t off, Ws& s, int i) {  // I8: piece i, as load_xp
-    s.v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, off + (uint32_t)i * 64u * kbytes, 0, 0));
-  };
+  const TabPtr tab{sT + tl};
   auto load_w = [&](int k, Ws& s) {
     if constexpr (KIND != TILE_I8) {
       const int kk = min(k, nsteps - 1);
@@ -353,12 +307,10 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   auto scale_of = [&](const Ws& s, int k) {
     return KIND != TILE_I8 && (k < nsteps - 1 ? wv : wv_last) ? (float)s.q8 * s.sc : 0.0f;
   };
-  // part I (0 .. WL - 1) of the thread's weights into buffer buf: I8 one loaded piece, coded 8 dequantized weights
-  auto store_w = [&](const Ws& s, const Lut4& lut, float ap, auto part, int buf) {
+  // part I (0 .. WL - 1) of the thread's coded weights, dequantized, into buffer buf
+  auto store_w = [&](const Ws& s, const Lut4& lut, float ap, auto part, char* buf) {
     constexpr int I = decltype(part)::value;
-    if constexpr (KIND == TILE_I8) {
-      st_w(buf, xst + 8192u * I, s.v[I]);
-    } else {
+    if constexpr (KIND != TILE_I8) {
       uint32_t o[4];
       if constexpr (BITS == 4) {
         lut4_word(s.c.w[I], lut, o);
@@ -369,7 +321,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
           o[j] = cvt_pk_bf16(p.x * ap, p.y * ap);
         }
       }
-      st_w(buf, wst[I], u32x4_t{o[0], o[1], o[2], o[3]});
+      st16(buf + wst[I], u32x4_t{o[0], o[1], o[2], o[3]});
     }
   };
   // the same in two halves, for the widths whose levels come from LDS: the lookups before a run of products, the rest after
@@ -381,26 +333,14 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       for (int j = 0; j < 4; ++j) look[j] = level_pair<BITS>(s.c, 4 * decltype(part)::value + j, tab);
     }
   };
-  auto finish_w = [&](float ap, auto part, int buf) {
+  auto finish_w = [&](float ap, auto part, char* buf) {
     if constexpr (kLook) {
       u32x4_t o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = cvt_pk_bf16(look[j].x * ap, look[j].y * ap);
-      st_w(buf, wst[decltype(part)::value], o);
+      st16(buf + wst[decltype(part)::value], o);
     }
   };
-  auto store_w_all = [&](const Ws& s, int k, int buf) {
-    Lut4 lut{};
-    const float ap = scale_of(s, k);
-    if constexpr (KIND != TILE_I8 && BITS == 4) lut = make_lut4(lv, ap);
-    store_w(s, lut, ap, std::integral_constant<int, 0>{}, buf);
-    store_w(s, lut, ap, std::integral_constant<int, 1>{}, buf);
-    if constexpr (WL == 4) {
-      store_w(s, lut, ap, std::integral_constant<int, 2>{}, buf);
-      store_w(s, lut, ap, std::integral_constant<int, 3>{}, buf);
-    }
-  };
-
   // ---- fragments: MFMA step s (0..3) of a buffer, row fr (+ 32 per tile), chunk 2 s + h
   const int mh = wave / WN, nh = wave % WN;
   uint32_t xb[4], wb[4];
@@ -422,18 +362,18 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     }
   }
   u32x4_t fx[2][MT], fw[2][NT];
-  auto read_frags = [&](int buf, int s, int slot) {
+  auto read_frags = [&](const char* bx, char* bw, int s, int slot) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) fx[slot][i] = rd_x(buf, xb[s] + 4096u * i);
+    for (int i = 0; i < MT; ++i) fx[slot][i] = ld16(bx + xb[s] + 4096u * i);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
       if constexpr (KIND == TILE_TR) {
-        const uint32_t ad = tbo[c] + 4096u * s;
-        const u16x4_t lo = tr_w(buf, ad), hi = tr_w(buf, ad + 1024u);
+        char* const ad = bw + tbo[c] + 4096u * s;
+        const u16x4_t lo = ld_tr(ad), hi = ld_tr(ad + 1024u);
         fw[slot][c] = u32x4_t{__builtin_bit_cast(uint2, lo).x, __builtin_bit_cast(uint2, lo).y,
                               __builtin_bit_cast(uint2, hi).x, __builtin_bit_cast(uint2, hi).y};
       } else {
-        fw[slot][c] = rd_w(buf, wb[s] + 4096u * c);
+        fw[slot][c] = ld16(bw + wb[s] + 4096u * c);
       }
     }
   };
@@ -455,59 +395,48 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   };
 
   // ---- the steps
-  Xs xs;
   Ws wa, wn;
-  if constexpr (kDma) {
-    dma(xr, sX0, 0);
-    if constexpr (KIND == TILE_I8) {
-      dma(wr, sW0, 0);
-    } else {
-      load_w(0, wa);
-      // (loads in the steps' order: the compiler's wait counts at the loop's head are those of the worse path)
-      __builtin_amdgcn_sched_barrier(0);
-      load_w(1, wn);
-      __builtin_amdgcn_sched_barrier(0);
-      store_w_all(wa, 0, 0);
+  direct(xr, sX0, 0, xloads);
+  if constexpr (KIND == TILE_I8) {
+    direct(wr, sW0, 0, wloads);
+    if constexpr (kThird) {
+      direct(xr, sX1, 1, xloads);
+      direct(wr, sW1, 1, wloads);
     }
   } else {
-    const uint32_t off0 = step_off(0), off1 = step_off(1);
-#pragma unroll
-    for (int i = 0; i < XL; ++i) load_xp(off0, xs, i);
-    if constexpr (KIND == TILE_I8) {
-#pragma unroll
-      for (int i = 0; i < WL; ++i) load_wp(off0, wa, i);
-    } else {
-      load_w(0, wa);
-      __builtin_amdgcn_sched_barrier(0);
-      load_w(1, wn);
-    }
+    load_w(0, wa);
+    // (loads in the steps' order: the compiler's wait counts at the loop's head are those of the worse path)
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < XL; ++i) {
-      store_xp(xs, 0, i);
-      load_xp(off1, xs, i);
-    }
-    store_w_all(wa, 0, 0);
-    if constexpr (KIND == TILE_I8) {
-#pragma unroll
-      for (int i = 0; i < WL; ++i) load_wp(off1, wa, i);
-    }
+    load_w(1, wn);
     __builtin_amdgcn_sched_barrier(0);
+    Lut4 lut{};
+    const float ap = scale_of(wa, 0);
+    if constexpr (BITS == 4) lut = make_lut4(lv, ap);
+    store_w(wa, lut, ap, std::integral_constant<int, 0>{}, sW0);
+    store_w(wa, lut, ap, std::integral_constant<int, 1>{}, sW0);
+    if constexpr (WL == 4) {
+      store_w(wa, lut, ap, std::integral_constant<int, 2>{}, sW0);
+      store_w(wa, lut, ap, std::integral_constant<int, 3>{}, sW0);
+    }
   }
-  __syncthreads();
-  // Step k: xs (and the integer weights wi) hold step k + 1's pieces, loaded during step k - 1; each is written to the
-  // other buffer and its register loaded again for step k + 2 between the products, so a
-  // load has a whole step to arrive and the writes overlap the products.  Direct loads bring step k + 1 to the other buffer
-  // during step k.
-  // cur: the codes of step k + 1; nxt: room for those of step k + 2.
-  auto step = [&](int k, int buf, Ws& wi, Ws& cur, Ws& nxt) {
-    __builtin_amdgcn_sched_barrier(0);
-    const uint32_t off = kDma ? 0u : step_off(k + 2);
-    if constexpr (kDma) {
-      dma(xr, buf ? sX0 : sX1, k + 1);
-      if constexpr (KIND == TILE_I8) dma(wr, buf ? sW0 : sW1, k + 1);
-      __builtin_amdgcn_sched_barrier(0);
+  // the end of a step: every wave's share of the next one is in LDS
+  auto step_barrier = [&] {
+    if constexpr (kThird) {
+      __builtin_amdgcn_s_waitcnt(0x0070 | (XL + WL));  // all but the last step's direct loads; no LDS access open
+      __builtin_amdgcn_s_barrier();
+    } else {
+      __syncthreads();
     }
+  };
+  step_barrier();
+  // Step k multiplies buffers bx, bw while the next step (with a third buffer: the one after) comes into ox, ow: x and int8
+  // weights by direct loads issued first, codes dequantized from registers between the products.
+  // cur: the codes of step k + 1; nxt: room for those of step k + 2.
+  auto step = [&](int k, char* bx, char* bw, char* ox, char* ow, Ws& cur, Ws& nxt) {
+    __builtin_amdgcn_sched_barrier(0);
+    direct(xr, ox, kThird ? k + 2 : k + 1, xloads);
+    if constexpr (KIND == TILE_I8) direct(wr, ow, kThird ? k + 2 : k + 1, wloads);
+    __builtin_amdgcn_sched_barrier(0);
     if constexpr (KIND != TILE_I8) load_w(k + 2, nxt);
     // (opaque from here: the compiler would otherwise start the codes' arithmetic right after their load, a
     // step early, and wait for them there)
@@ -517,34 +446,23 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       asm volatile("" : "+v"(cur.q8), "+v"(cur.sc));
     }
     __builtin_amdgcn_sched_barrier(0);
-    read_frags(buf, 0, 0);
+    read_frags(bx, bw, 0, 0);
     Lut4 lut{};
     const float ap = scale_of(cur, k + 1);
     if constexpr (KIND != TILE_I8 && BITS == 4) lut = make_lut4(lv, ap);
     auto sub = [&](auto spos) {
       constexpr int S = decltype(spos)::value;
-      if constexpr (S < 3) read_frags(buf, S + 1, (S + 1) & 1);
+      if constexpr (S < 3) read_frags(bx, bw, S + 1, (S + 1) & 1);
       constexpr bool kPart = WL == 4 || S % 2 == 0;
       constexpr std::integral_constant<int, WL == 4 ? S : S / 2> wpart{};
       if constexpr (kLook && kPart) lookup_w(cur, wpart);
       __builtin_amdgcn_sched_barrier(0);
       mfmas(S & 1);
-      if constexpr (!kDma && S < XL) {
-        store_xp(xs, buf ^ 1, S);
-        load_xp(off, xs, S);
-      }
-      if constexpr (KIND == TILE_I8) {
-        if constexpr (!kDma && S < WL) {
-          store_w(wi, lut, ap, spos, buf ^ 1);
-          load_wp(off, wi, S);
-        }
+      if constexpr (kLook && kPart) {
+        __builtin_amdgcn_sched_barrier(0);
+        finish_w(ap, wpart, ow);
       } else if constexpr (kPart) {
-        if constexpr (kLook) {
-          __builtin_amdgcn_sched_barrier(0);
-          finish_w(ap, wpart, buf ^ 1);
-        } else {
-          store_w(cur, lut, ap, wpart, buf ^ 1);
-        }
+        store_w(cur, lut, ap, wpart, ow);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -552,14 +470,23 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     sub(std::integral_constant<int, 1>{});
     sub(std::integral_constant<int, 2>{});
     sub(std::integral_constant<int, 3>{});
-    __syncthreads();
+    step_barrier();
   };
   int k = 0;
-  for (; k + 1 < nsteps; k += 2) {
-    step(k, 0, wa, wn, wa);
-    step(k + 1, 1, wa, wa, wn);
+  if constexpr (kThird) {
+    for (; k < nsteps; k += 3) {  // (up to two steps past the end: zeros)
+      step(k, sX0, sW0, sX2, sW2, wn, wa);
+      step(k + 1, sX1, sW1, sX0, sW0, wn, wa);
+      step(k + 2, sX2, sW2, sX1, sW1, wn, wa);
+    }
+    __syncthreads();  // the last direct loads too
+  } else {
+    for (; k + 1 < nsteps; k += 2) {
+      step(k, sX0, sW0, sX1, sW1, wn, wa);
+      step(k + 1, sX1, sW1, sX0, sW0, wa, wn);
+    }
+    if (k < nsteps) step(k, sX0, sW0, sX1, sW1, wn, wa);
   }
-  if (k < nsteps) step(k, 0, wa, wn, wa);
 
   // ---- row and column scales of the integer product
   if constexpr (KIND == TILE_I8) {
@@ -618,8 +545,8 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
           lo[i] = pack_bf16x2(u0 - bf16_bits_to_f32(h0), u1 - bf16_bits_to_f32(h1));
         }
         const uint32_t xrow = (uint32_t)row * 128u;
-        st_x(0, xrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), hv);
-        st_x(0, xrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), lo);
+        st16(sX0 + xrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), hv);
+        st16(sX0 + xrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), lo);
       }
       if constexpr (KIND == TILE_TR) {
         // A[j0 + row][n0 ..]: rows 0..31 and 32..63 hold the same 32 adapter rows
@@ -630,8 +557,8 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
           u32x4_t v = zero4;
           if (j0 + row < r && col < K) v = *reinterpret_cast<const u32x4_t*>(Ae + (int64_t)(j0 + row) * K + col);
           const uint32_t base = (uint32_t)(c >> 4) * 16384u;
-          st_w(0, base + (uint32_t)row * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
-          st_w(0, base + (uint32_t)(row + 32) * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
+          st16(sW0 + base + (uint32_t)row * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
+          st16(sW0 + base + (uint32_t)(row + 32) * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
         }
       } else {
         // [B[n][j0 ..] | the same]
@@ -652,14 +579,14 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
             }
           }
           const uint32_t wrow = (uint32_t)row * 128u;
-          st_w(0, wrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), v);
-          st_w(0, wrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), v);
+          st16(sW0 + wrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), v);
+          st16(sW0 + wrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), v);
         }
       }
       __syncthreads();
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        read_frags(0, s, 0);
+        read_frags(sX0, sW0, s, 0);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -692,67 +619,43 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       }
     }
   };
-  if constexpr (kDma) {
-    // The four 32 KB buffers hold 64 bf16 or 32 float32 rows of 256 columns each, their 16-byte pieces XOR-swizzled by the
-    // row: all 256 bf16 rows at once, float32 rows in two passes of 128.
-    const int passes = es == 4 ? 2 : 1, rpb = es == 4 ? 32 : 64;
-    for (int p = 0; p < passes; ++p) {
-      if (p * 128 >= mrows) break;
-      if (es == 2 || mh == p) {
+  // Each buffer holds rpb rows (of the 64-row tile only the weight's buffers, the others are half as large), their 16-byte
+  // pieces XOR-swizzled by the row.  All bf16 rows go at once, the float32 rows of a 256 x 256 tile in two passes.
+  constexpr int kBufs = BM == 64 ? 2 : 4;
+  auto sbuf = [&](int b) { return kBufs == 2 ? (b ? sW1 : sW0) : b < 2 ? (b ? sX1 : sX0) : (b == 3 ? sW1 : sW0); };
+  const int rpb = es == 4 ? 32 : 64;
+  const uint32_t rowb = (uint32_t)(BN * es), mask = min(31, cpr - 1);
+  for (int first = 0; first < mrows; first += kBufs * rpb) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          char* st = es == 4 ? (i < 2 ? (i ? sX1 : sX0) : (i == 3 ? sW1 : sW0)) : (mh ? (i < 2 ? sW0 : sW1) : (i < 2 ? sX0 : sX1));
-          const uint32_t lr = (uint32_t)(es == 4 ? fr : 32 * (i & 1) + fr);
+    for (int i = 0; i < MT; ++i) {
+      const int tr = mh * (BM / WM) + 32 * i - first;  // the MFMA tile's first row in this pass
+      if (tr >= 0 && tr < kBufs * rpb) {
+        const uint32_t lr = (uint32_t)((es == 4 ? 0 : tr & 32) + fr);
+        char* const st = sbuf(tr / rpb) + lr * rowb;
 #pragma unroll
-          for (int c = 0; c < NT; ++c)
+        for (int c = 0; c < NT; ++c)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float v0 = acc[i][c][4 * q], v1 = acc[i][c][4 * q + 1], v2 = acc[i][c][4 * q + 2], v3 = acc[i][c][4 * q + 3];
-              if (es == 4) {
-                const uint32_t pc = (uint32_t)(16 * nh + 8 * c + 2 * q + h) ^ (lr & 31u);
-                *reinterpret_cast<f32x4_t*>(st + lr * 1024u + 16u * pc) = f32x4_t{v0, v1, v2, v3};
-              } else {
-                const uint32_t pc = (uint32_t)(8 * nh + 4 * c + q) ^ (lr & 31u);
-                *reinterpret_cast<u32x2v_t*>(st + lr * 512u + 16u * pc + 8u * h) = u32x2v_t{pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)};
-              }
-            }
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const char* st = b < 2 ? (b ? sX1 : sX0) : (b == 3 ? sW1 : sW0);
-        const int first = p * 128 + b * rpb, rows = min(rpb, mrows - first);
-        for (int idx = tid; idx < rows * cpr; idx += 512) {
-          const int lr = es == 4 ? idx >> 6 : idx >> 5, c = idx & (cpr - 1);
-          put(first + lr, c, *reinterpret_cast<const u32x4_t*>(st + lr * (256 * es) + 16 * (c ^ (lr & 31))));
-        }
-      }
-      __syncthreads();
-    }
-  } else {
-    const uint32_t rs = (uint32_t)BN * es + 16u;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int c = 0; c < NT; ++c)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t ad = (uint32_t)(mh * (BM / WM) + 32 * i + fr) * rs +
-                              (uint32_t)(nh * (BN / WN) + 32 * c + 8 * q + 4 * h) * es;
-          const float v0 = acc[i][c][4 * q], v1 = acc[i][c][4 * q + 1], v2 = acc[i][c][4 * q + 2], v3 = acc[i][c][4 * q + 3];
-          if (es == 4) {
-            lds_store_f32x4(ad, f32x4_t{v0, v1, v2, v3});
-          } else {
-            *reinterpret_cast<__attribute__((address_space(3))) u32x2v_t*>((uintptr_t)ad) =
-                u32x2v_t{pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)};
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t col = (uint32_t)(nh * (BN / WN) + 32 * c + 8 * q);
+            const float v0 = acc[i][c][4 * q], v1 = acc[i][c][4 * q + 1], v2 = acc[i][c][4 * q + 2], v3 = acc[i][c][4 * q + 3];
+            if (es == 4)
+              *reinterpret_cast<f32x4_t*>(st + 16u * ((col / 4 + h) ^ (lr & mask))) = f32x4_t{v0, v1, v2, v3};
+            else
+              *reinterpret_cast<u32x2v_t*>(st + 16u * ((col / 8) ^ (lr & mask)) + 8u * h) =
+                  u32x2v_t{pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)};
           }
-        }
-    __syncthreads();
-    for (int idx = tid; idx < mrows * cpr; idx += 512) {
-      const int row = es == 4 ? idx / (BN / 4) : idx / (BN / 8), c = idx & (cpr - 1);
-      put(row, c, lds_u32x4((uint32_t)row * rs + 16u * c));
+      }
     }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < kBufs; ++b) {
+      const int r0 = first + b * rpb, rows = min(rpb, mrows - r0);
+      for (int idx = tid; idx < rows * cpr; idx += 512) {
+        const int lr = es == 4 ? idx / (BN / 4) : idx / (BN / 8), c = idx & (cpr - 1);
+        put(r0 + lr, c, ld16(sbuf(b) + lr * rowb + 16u * ((uint32_t)c ^ ((uint32_t)lr & mask))));
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -853,29 +756,13 @@ inline int64_t tile_bound(int64_t M, int experts, int BM) { return M / BM + std:
 template <int KIND, int BITS, int BM, int BN>
 hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
   auto kern = k_tile<KIND, BITS, BM, BN>;
-  // 256 x 256 tiles have their LDS as variables; the others address dynamic LDS from 0: they must not have any static
-  constexpr bool dma = BM * BN == 256 * 256;
-  constexpr int shmem = dma ? 0 : (int)TileLds<KIND, BITS, BM, BN>::kBytes;
-  static std::once_flag once;
-  static hipError_t setup;
-  std::call_once(once, [&] {
-    hipFuncAttributes fa;
-    setup = hipFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern));
-    if (setup == hipSuccess && !dma && fa.sharedSizeBytes != 0) setup = hipErrorInvalidKernelFile;
-  });
-  if (setup != hipSuccess) return setup;
   const int64_t no = KIND == TILE_TR ? a.K : a.N;
   a.ntiles = (int)((no + BN - 1) / BN);
   int64_t tiles = (a.offsets ? tile_bound(a.M, a.experts, BM) : (a.M + BM - 1) / BM) * a.ntiles;
   if (a.rest && BM < 256) tiles = kRestMax * (256 / BM) * (256 / BN);
   if (tiles <= 0) return hipSuccess;
   if (tiles > INT32_MAX - 8) return hipErrorInvalidValue;
-  if (!dma) {
-    const hipError_t err =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, shmem);
-    if (err != hipSuccess) return err;
-  }
-  hipLaunchKernelGGL(kern, dim3((unsigned)(8 * ((tiles + 7) / 8))), dim3(512), shmem, s, a, lv);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(8 * ((tiles + 7) / 8))), dim3(512), 0, s, a, lv);
   return hipGetLastError();
 }
 
