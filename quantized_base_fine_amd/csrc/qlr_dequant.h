@@ -38,7 +38,9 @@ __device__ __forceinline__ Codes32<BITS> load_codes32(const uint8_t* p) {
 }
 
 // The 16 codes [16 q, 16 q + 16) of a block whose codes start at p (16-byte aligned for 8-bit
-// codes, 4-byte for the others), in the low half of the words.
+// codes, 4-byte for the others), in the low half of the words; of 3-bit codes, 6 bytes at
+// 6 q, the two words around them, which place_codes16 shifts into place (apart, so that a
+// load well ahead of its use is not waited for by the shift).
 template <int BITS>
 __device__ __forceinline__ Codes32<BITS> load_codes16(const uint8_t* p, int q) {
   Codes32<BITS> c;
@@ -47,11 +49,8 @@ __device__ __forceinline__ Codes32<BITS> load_codes16(const uint8_t* p, int q) {
   if constexpr (BITS == 2) {
     c.w[0] = *reinterpret_cast<const uint32_t*>(p + 4 * q);
   } else if constexpr (BITS == 3) {
-    // 6 bytes at 6 q: the two words around them
     const uint32_t* w = reinterpret_cast<const uint32_t*>(p + ((6 * q) & ~3));
-    const uint32_t lo = w[0], hi = w[1], sh = 16u * (q & 1);
-    c.w[0] = __builtin_amdgcn_alignbit(hi, lo, sh);
-    c.w[1] = hi >> sh;
+    c.w[0] = w[0]; c.w[1] = w[1];
   } else if constexpr (BITS == 4) {
     const uint2 u = *reinterpret_cast<const uint2*>(p + 8 * q);
     c.w[0] = u.x; c.w[1] = u.y;
@@ -60,6 +59,15 @@ __device__ __forceinline__ Codes32<BITS> load_codes16(const uint8_t* p, int q) {
     c.w[0] = u.x; c.w[1] = u.y; c.w[2] = u.z; c.w[3] = u.w;
   }
   return c;
+}
+
+template <int BITS>
+__device__ __forceinline__ void place_codes16(Codes32<BITS>& c, int q) {
+  if constexpr (BITS == 3) {
+    const uint32_t sh = 16u * (q & 1);
+    c.w[0] = __builtin_amdgcn_alignbit(c.w[1], c.w[0], sh);
+    c.w[1] = c.w[1] >> sh;
+  }
 }
 
 // LDS accesses at a byte address of the dynamic LDS block, which starts at LDS

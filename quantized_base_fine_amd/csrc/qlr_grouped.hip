@@ -94,7 +94,8 @@ __global__ __launch_bounds__(512, 4) void k_grouped_few(TileArgs P, Levels lv) {
 #pragma unroll
     for (int i = 0; i < kFewChunk; ++i) {
       const int64_t blk = wblk + max(min(bl + i, b1 - 1), 0);
-      const Codes32<BITS> c = load_codes16<BITS>(P.w + blk * (8 * BITS), g);
+      Codes32<BITS> c = load_codes16<BITS>(P.w + blk * (8 * BITS), g);
+      place_codes16<BITS>(c, g);
 #pragma unroll
       for (int j = 0; j < NW; ++j) d.c[i][j] = c.w[j];
       d.q8[i] = P.q8[blk];

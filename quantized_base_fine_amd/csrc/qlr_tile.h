@@ -105,7 +105,10 @@ struct TileLds {
   static constexpr uint32_t kTabBytes = (KIND == TILE_I8 || BITS == 4) ? 0
                                         : BITS == 8                    ? 256 * 16 * 4
                                                                        : PairTableF32<BITS>::kBytes;
-  static_assert(2 * (kX + kW) + kTabBytes <= 160 * 1024, "LDS budget");
+  // Buffers.  Two; the 64 x 128 tiles, which run few to a CU and have little work to hide a load behind, have more: the
+  // integer one three of each operand, the coded ones four of x.
+  static constexpr int kXBufs = BM > 64 ? 2 : KIND == TILE_I8 ? 3 : 4, kWBufs = KIND == TILE_I8 ? kXBufs : 2;
+  static_assert(kXBufs * kX + kWBufs * kW + kTabBytes <= 160 * 1024, "LDS budget");
 };
 
 __device__ __forceinline__ f32x16_t tile_mfma(u32x4_t a, u32x4_t b, f32x16_t c) {
@@ -137,9 +140,8 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   // x and int8 weights are loaded straight into LDS.  The buffers are separate LDS variables, so that the compiler knows
   // that the fragment reads of one do not touch the loads in flight into the other and does not wait for them.
   __shared__ __attribute__((aligned(16))) char sX0[L::kX], sX1[L::kX], sW0[L::kW], sW1[L::kW];
-  // The small integer tile has little else to hide a load behind: a third buffer, its loads two steps ahead.
-  constexpr bool kThird = KIND == TILE_I8 && BM == 64;
-  __shared__ __attribute__((aligned(16))) char sX2[kThird ? L::kX : 16], sW2[kThird ? L::kW : 16];
+  __shared__ __attribute__((aligned(16))) char sX2[L::kXBufs > 2 ? L::kX : 16], sX3[L::kXBufs > 3 ? L::kX : 16];
+  __shared__ __attribute__((aligned(16))) char sW2[L::kWBufs > 2 ? L::kW : 16];
   __shared__ __attribute__((aligned(16))) char sT[L::kTabBytes ? L::kTabBytes : 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 31, h = lane >> 5;
@@ -249,7 +251,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   // TR: thread = weight row 64 k + tid / 8, codes [CPT dh, + CPT) of block column n0 / 64 + bq.
   struct Ws {
     Codes32<BITS> c;
-    uint32_t q8;
+    uint8_t q8;
     float sc;
   };
   const int wrows = (int)min<int64_t>(BN, N - n0);
@@ -395,20 +397,29 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   };
 
   // ---- the steps
-  Ws wa, wn;
+  // x (and int8 weights) of step k are loaded kAhead steps before, codes kSets steps before.
+  constexpr int kAhead = L::kXBufs - 1, kSets = L::kXBufs == 4 ? 4 : 2;
+  Ws wa, wb_, wc, wd;
   direct(xr, sX0, 0, xloads);
-  if constexpr (KIND == TILE_I8) {
-    direct(wr, sW0, 0, wloads);
-    if constexpr (kThird) {
-      direct(xr, sX1, 1, xloads);
-      direct(wr, sW1, 1, wloads);
-    }
-  } else {
+  if constexpr (KIND == TILE_I8) direct(wr, sW0, 0, wloads);
+  if constexpr (kAhead > 1) {
+    direct(xr, sX1, 1, xloads);
+    if constexpr (KIND == TILE_I8) direct(wr, sW1, 1, wloads);
+  }
+  if constexpr (kAhead > 2) direct(xr, sX2, 2, xloads);
+  if constexpr (KIND != TILE_I8) {
     load_w(0, wa);
     // (loads in the steps' order: the compiler's wait counts at the loop's head are those of the worse path)
     __builtin_amdgcn_sched_barrier(0);
-    load_w(1, wn);
+    load_w(1, wb_);
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kSets == 4) {
+      load_w(2, wc);
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(3, wd);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (CPT == 16) place_codes16<BITS>(wa.c, dh);
     Lut4 lut{};
     const float ap = scale_of(wa, 0);
     if constexpr (BITS == 4) lut = make_lut4(lv, ap);
@@ -419,31 +430,35 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       store_w(wa, lut, ap, std::integral_constant<int, 3>{}, sW0);
     }
   }
-  // the end of a step: every wave's share of the next one is in LDS
+  __syncthreads();
+  // The end of a step: every wave's share of the next one is in LDS.  Behind the loads that must have arrived there are those
+  // of the kAhead - 1 steps after the next: XL (+ WL) direct loads each and, from the next step's on, at least three of codes,
+  // scale and constant (loads return in order).
   auto step_barrier = [&] {
-    if constexpr (kThird) {
-      __builtin_amdgcn_s_waitcnt(0x0070 | (XL + WL));  // all but the last step's direct loads; no LDS access open
+    if constexpr (kAhead > 1) {
+      constexpr int kOpen = (kAhead - 1) * (XL + (KIND == TILE_I8 ? WL : 0)) + (KIND == TILE_I8 ? 0 : 3 * kAhead);
+      static_assert(kOpen < 16, "wait count");
+      __builtin_amdgcn_s_waitcnt(0x0070 | kOpen);  // and no LDS access open
       __builtin_amdgcn_s_barrier();
     } else {
       __syncthreads();
     }
   };
-  step_barrier();
-  // Step k multiplies buffers bx, bw while the next step (with a third buffer: the one after) comes into ox, ow: x and int8
-  // weights by direct loads issued first, codes dequantized from registers between the products.
-  // cur: the codes of step k + 1; nxt: room for those of step k + 2.
+  // Step k multiplies buffers bx, bw while step k + kAhead comes into ox (and ow) by direct loads issued first; the codes of
+  // step k + 1, in cur, are dequantized between the products (into ow), and those of step k + kSets loaded into nxt.
   auto step = [&](int k, char* bx, char* bw, char* ox, char* ow, Ws& cur, Ws& nxt) {
     __builtin_amdgcn_sched_barrier(0);
-    direct(xr, ox, kThird ? k + 2 : k + 1, xloads);
-    if constexpr (KIND == TILE_I8) direct(wr, ow, kThird ? k + 2 : k + 1, wloads);
+    direct(xr, ox, k + kAhead, xloads);
+    if constexpr (KIND == TILE_I8) direct(wr, ow, k + kAhead, wloads);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (KIND != TILE_I8) load_w(k + 2, nxt);
+    if constexpr (KIND != TILE_I8) load_w(k + kSets, nxt);
     // (opaque from here: the compiler would otherwise start the codes' arithmetic right after their load, a
     // step early, and wait for them there)
     if constexpr (KIND != TILE_I8) {
 #pragma unroll
       for (int i = 0; i < BITS; ++i) asm volatile("" : "+v"(cur.c.w[i]));
-      asm volatile("" : "+v"(cur.q8), "+v"(cur.sc));
+      asm volatile("" : "+v"(cur.sc));
+      if constexpr (CPT == 16) place_codes16<BITS>(cur.c, dh);
     }
     __builtin_amdgcn_sched_barrier(0);
     read_frags(bx, bw, 0, 0);
@@ -473,19 +488,36 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     step_barrier();
   };
   int k = 0;
-  if constexpr (kThird) {
-    for (; k < nsteps; k += 3) {  // (up to two steps past the end: zeros)
-      step(k, sX0, sW0, sX2, sW2, wn, wa);
-      step(k + 1, sX1, sW1, sX0, sW0, wn, wa);
-      step(k + 2, sX2, sW2, sX1, sW1, wn, wa);
+  if constexpr (kAhead == 2) {
+    for (;;) {
+      step(k, sX0, sW0, sX2, sW2, wa, wa);
+      if (++k >= nsteps) break;
+      step(k, sX1, sW1, sX0, sW0, wa, wa);
+      if (++k >= nsteps) break;
+      step(k, sX2, sW2, sX1, sW1, wa, wa);
+      if (++k >= nsteps) break;
     }
-    __syncthreads();  // the last direct loads too
+  } else if constexpr (kAhead == 3) {
+    for (;;) {
+      step(k, sX0, sW0, sX3, sW1, wb_, wa);
+      if (++k >= nsteps) break;
+      step(k, sX1, sW1, sX0, sW0, wc, wb_);
+      if (++k >= nsteps) break;
+      step(k, sX2, sW0, sX1, sW1, wd, wc);
+      if (++k >= nsteps) break;
+      step(k, sX3, sW1, sX2, sW0, wa, wd);
+      if (++k >= nsteps) break;
+    }
   } else {
     for (; k + 1 < nsteps; k += 2) {
-      step(k, sX0, sW0, sX1, sW1, wn, wa);
-      step(k + 1, sX1, sW1, sX0, sW0, wa, wn);
+      step(k, sX0, sW0, sX1, sW1, wb_, wa);
+      step(k + 1, sX1, sW1, sX0, sW0, wa, wb_);
     }
-    if (k < nsteps) step(k, sX0, sW0, sX1, sW1, wn, wa);
+    if (k < nsteps) step(k, sX0, sW0, sX1, sW1, wb_, wa);
+  }
+  if constexpr (kAhead > 1) {
+    __builtin_amdgcn_s_waitcnt(0x0070);  // the loads past the last step too, before the buffers are used again
+    __syncthreads();
   }
 
   // ---- row and column scales of the integer product
@@ -513,6 +545,33 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     const bool r8 = (r & 7) == 0;
     const u32x4_t zero4 = {0u, 0u, 0u, 0u};
     for (int j0 = 0; j0 < r; j0 += 32) {
+      // the weight side's pieces first, so that both sides' loads are on their way together
+      constexpr int kAP = BN / 128;
+      u32x4_t av[kAP];
+#pragma unroll
+      for (int u = 0; u < kAP; ++u) {
+        const int idx = tid + 512 * u;
+        av[u] = zero4;
+        if constexpr (KIND == TILE_TR) {  // A[j0 + row][n0 + 8 c ..]
+          const int row = idx / (BN / 8);
+          const int64_t col = n0 + 8 * (idx % (BN / 8));
+          if (j0 + row < r && col < K) av[u] = *reinterpret_cast<const u32x4_t*>(P.ab + ((int64_t)e * r + j0 + row) * K + col);
+        } else {  // B[n0 + row][j0 + 8 c ..]
+          const int row = idx >> 2, jb = j0 + 8 * (idx & 3);
+          if (n0 + row < N && jb < r) {
+            const uint16_t* bp = P.ab + ((int64_t)e * N + n0 + row) * r + jb;
+            if (r8) {
+              av[u] = *reinterpret_cast<const u32x4_t*>(bp);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = jb + 2 * i < r ? bp[2 * i] : 0u, hi = jb + 2 * i + 1 < r ? bp[2 * i + 1] : 0u;
+                av[u][i] = lo | (hi << 16);
+              }
+            }
+          }
+        }
+      }
       // x side: row (idx / 4), adapter columns j0 + 8 (idx % 4) .. + 8
       for (int idx = tid; idx < BM * 4; idx += 512) {
         const int row = idx >> 2, c = idx & 3, jb = j0 + 8 * c;
@@ -548,39 +607,20 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
         st16(sX0 + xrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), hv);
         st16(sX0 + xrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), lo);
       }
-      if constexpr (KIND == TILE_TR) {
-        // A[j0 + row][n0 ..]: rows 0..31 and 32..63 hold the same 32 adapter rows
-        const uint16_t* Ae = P.ab + (int64_t)e * r * K;
-        for (int idx = tid; idx < 32 * (BN / 8); idx += 512) {
-          const int row = idx / (BN / 8), c = idx % (BN / 8);
-          const int64_t col = n0 + 8 * c;
-          u32x4_t v = zero4;
-          if (j0 + row < r && col < K) v = *reinterpret_cast<const u32x4_t*>(Ae + (int64_t)(j0 + row) * K + col);
-          const uint32_t base = (uint32_t)(c >> 4) * 16384u;
-          st16(sW0 + base + (uint32_t)row * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
-          st16(sW0 + base + (uint32_t)(row + 32) * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), v);
-        }
-      } else {
-        // [B[n][j0 ..] | the same]
-        const uint16_t* Be = P.ab + (int64_t)e * N * r;
-        for (int idx = tid; idx < BN * 4; idx += 512) {
-          const int row = idx >> 2, c = idx & 3, jb = j0 + 8 * c;
-          u32x4_t v = zero4;
-          if (n0 + row < N && jb < r) {
-            const uint16_t* bp = Be + (int64_t)(n0 + row) * r + jb;
-            if (r8) {
-              v = *reinterpret_cast<const u32x4_t*>(bp);
-            } else {
+      // weight side, twice: [B | B], for A the rows 0..31 and 32..63
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = jb + 2 * i < r ? bp[2 * i] : 0u, hi = jb + 2 * i + 1 < r ? bp[2 * i + 1] : 0u;
-                v[i] = lo | (hi << 16);
-              }
-            }
-          }
+      for (int u = 0; u < kAP; ++u) {
+        const int idx = tid + 512 * u;
+        if constexpr (KIND == TILE_TR) {
+          const int row = idx / (BN / 8), c = idx % (BN / 8);
+          const uint32_t base = (uint32_t)(c >> 4) * 16384u;
+          st16(sW0 + base + (uint32_t)row * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), av[u]);
+          st16(sW0 + base + (uint32_t)(row + 32) * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), av[u]);
+        } else {
+          const int row = idx >> 2, c = idx & 3;
           const uint32_t wrow = (uint32_t)row * 128u;
-          st16(sW0 + wrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), v);
-          st16(sW0 + wrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), v);
+          st16(sW0 + wrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), av[u]);
+          st16(sW0 + wrow + ((((uint32_t)(4 + c)) ^ swz((uint32_t)row & 15u)) << 4), av[u]);
         }
       }
       __syncthreads();
