@@ -446,25 +446,28 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   };
   // Step k multiplies buffers bx, bw while step k + kAhead comes into ox (and ow) by direct loads issued first; the codes of
   // step k + 1, in cur, are dequantized between the products (into ow), and those of step k + kSets loaded into nxt.
+  // The first products wait for nothing but their fragments; addresses, the level table and the next codes' loads go between
+  // the products.
   auto step = [&](int k, char* bx, char* bw, char* ox, char* ow, Ws& cur, Ws& nxt) {
+    __builtin_amdgcn_sched_barrier(0);
+    read_frags(bx, bw, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
     direct(xr, ox, k + kAhead, xloads);
     if constexpr (KIND == TILE_I8) direct(wr, ow, k + kAhead, wloads);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (KIND != TILE_I8) load_w(k + kSets, nxt);
+    Lut4 lut{};
+    float ap = 0.0f;
     // (opaque from here: the compiler would otherwise start the codes' arithmetic right after their load, a
     // step early, and wait for them there)
-    if constexpr (KIND != TILE_I8) {
+    auto pin = [&] {
+      if constexpr (KIND != TILE_I8) {
 #pragma unroll
-      for (int i = 0; i < BITS; ++i) asm volatile("" : "+v"(cur.c.w[i]));
-      asm volatile("" : "+v"(cur.sc));
-      if constexpr (CPT == 16) place_codes16<BITS>(cur.c, dh);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    read_frags(bx, bw, 0, 0);
-    Lut4 lut{};
-    const float ap = scale_of(cur, k + 1);
-    if constexpr (KIND != TILE_I8 && BITS == 4) lut = make_lut4(lv, ap);
+        for (int i = 0; i < BITS; ++i) asm volatile("" : "+v"(cur.c.w[i]));
+        asm volatile("" : "+v"(cur.sc));
+        if constexpr (CPT == 16) place_codes16<BITS>(cur.c, dh);
+      }
+    };
+    if constexpr (kLook) pin();
     auto sub = [&](auto spos) {
       constexpr int S = decltype(spos)::value;
       if constexpr (S < 3) read_frags(bx, bw, S + 1, (S + 1) & 1);
@@ -473,11 +476,21 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       if constexpr (kLook && kPart) lookup_w(cur, wpart);
       __builtin_amdgcn_sched_barrier(0);
       mfmas(S & 1);
+      if constexpr (S == 0 && KIND != TILE_I8) {
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!kLook) pin();
+        ap = scale_of(cur, k + 1);
+        if constexpr (BITS == 4) lut = make_lut4(lv, ap);
+      }
       if constexpr (kLook && kPart) {
         __builtin_amdgcn_sched_barrier(0);
         finish_w(ap, wpart, ow);
       } else if constexpr (kPart) {
         store_w(cur, lut, ap, wpart, ow);
+      }
+      if constexpr (S == 1 && KIND != TILE_I8) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_w(k + kSets, nxt);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
