@@ -99,6 +99,78 @@ __device__ __forceinline__ int tile_scan(const int32_t* offsets, int E, int M, i
   return before;
 }
 
+// A workgroup's part of the rest: the 128 x 128 quarters of the 256 x 256 tiles split .. total - 1
+// that hold a row and a column, counted through (workgroups that find nothing to do must come last: among the
+// others they would leave some CUs two workgroups and others none, 80 us instead of 64 for a 4096 x 4096 backward of 8
+// ragged ranges).  ntiles: column tiles of 256; ncols: of 128; half: kRestRows words of LDS for each wave.  Returns the
+// tile, or -1.  Called by whole waves.
+constexpr int kRestRows = kRestMax + kGroupM;  // at most that many row tiles have tiles in the rest
+__device__ __forceinline__ int rest_tile(const int32_t* offsets, int E, int M, int min_rows, int split, int total,
+                                         int ntiles, int ncols, uint32_t* half, int& row_half, int& col_half) {
+  const int lane = threadIdx.x & 63;
+  const int lo = split / (kGroupM * ntiles) * kGroupM, mt_total = total / ntiles;
+  for (int i = lane; i < kRestRows; i += 64) half[i] = 2;
+  int before = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    int a = 0, b = 0;
+    if (e0 + lane < E) {
+      if (offsets) expert_range(offsets, e0 + lane, M, a, b);
+      else b = M;
+    }
+    const int nt = b - a > min_rows ? (b - a + 255) / 256 : 0;
+    int inc = nt;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(inc, d, 64);
+      if (lane >= d) inc += up;
+    }
+    const int at = before + inc - 1 - lo;  // the range's last row tile
+    if (nt > 0 && b - a - (nt - 1) * 256 <= 128 && at >= 0 && at < kRestRows) half[at] = 1;
+    before += __shfl(inc, 63, 64);
+  }
+  __builtin_amdgcn_wave_barrier();
+  // quarters of a lane's tiles, the tile's row and column halves
+  constexpr int kPer = (kRestMax + 63) / 64;
+  int cnt[kPer], rows[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int big = split + kPer * lane + i;
+    cnt[i] = rows[i] = 0;
+    if (big < total) {
+      const int grp = big / (kGroupM * ntiles), in = big - grp * kGroupM * ntiles;
+      const int gm = min(kGroupM, mt_total - grp * kGroupM);
+      rows[i] = (int)half[grp * kGroupM + in % gm - lo];
+      cnt[i] = rows[i] * (2 * (in / gm) + 1 < ncols ? 2 : 1);
+    }
+    sum += cnt[i];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(inc, d, 64);
+    if (lane >= d) inc += up;
+  }
+  const int all = __shfl(inc, 63, 64), per = (all + 7) / 8, loc = (int)(blockIdx.x >> 3);
+  const int want = (int)(blockIdx.x & 7) * per + loc;  // each XCD a contiguous range
+  if (loc >= per || want >= all) return -1;
+  int first = inc - sum, tile = -1, q = 0, nr = 1;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (want >= first && want < first + cnt[i]) {
+      tile = split + kPer * lane + i;
+      q = want - first;
+      nr = rows[i];
+    }
+    first += cnt[i];
+  }
+  const int src = __ffsll((unsigned long long)__ballot(tile >= 0)) - 1;
+  q = __shfl(q, src, 64);
+  nr = __shfl(nr, src, 64);
+  row_half = q % nr;
+  col_half = q / nr;
+  return __shfl(tile, src, 64);
+}
+
 template <int KIND, int BITS, int BM, int BN>
 struct TileLds {
   static constexpr uint32_t kX = BM * 128, kW = BN * 128;
@@ -108,6 +180,7 @@ struct TileLds {
   // Buffers.  Two; the 64 x 128 tiles, which run few to a CU and have little work to hide a load behind, have more: the
   // integer one three of each operand, the coded ones four of x.
   static constexpr int kXBufs = BM > 64 ? 2 : KIND == TILE_I8 ? 3 : 4, kWBufs = KIND == TILE_I8 ? kXBufs : 2;
+  static_assert(BM != 128 || kW >= 8 * kRestRows * 4, "rest_tile's words overlay a buffer");
   static_assert(kXBufs * kX + kWBufs * kW + kTabBytes <= 160 * 1024, "LDS budget");
 };
 
@@ -157,18 +230,23 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   int e = 0, row0 = 0, row_end = (int)P.M, tile_n;
   {
     constexpr int kBig = 256;
-    const bool sub = P.rest && BM < kBig;  // the 128 x 128 kernel on the rest of the 256 x 256 tiles
-    constexpr int kSubM = kBig / BM, kSub = kSubM * (kBig / BN);
+    const bool sub = BM == 128 && P.rest;  // the 128 x 128 kernel on the rest of the 256 x 256 tiles
     const int step_m = sub ? kBig : BM, ntiles = sub ? (P.ntiles + kBig / BN - 1) / (kBig / BN) : P.ntiles;
     const int mt_total = P.offsets ? tile_scan(P.offsets, P.experts, (int)P.M, P.min_rows, step_m, -1, e, row0, row_end)
                                    : (int)((P.M + step_m - 1) / step_m);
     const int total = mt_total * ntiles;
     const int split = P.rest ? tile_split(total) : total;
-    const int first = sub ? split : 0, count = sub ? (total - split) * kSub : split;
-    const int per = (count + 7) / 8, loc = (int)(blockIdx.x >> 3);
-    const int tile = (int)(blockIdx.x & 7) * per + loc;
-    if (loc >= per || tile >= count) return;  // the whole workgroup, before any barrier
-    const int big = sub ? first + tile / kSub : tile;
+    int big, row_half = 0, col_half = 0;
+    if (sub) {
+      // (its words lie in a buffer that no wave writes before the first barrier, which every wave reaches after reading them)
+      big = rest_tile(P.offsets, P.offsets ? P.experts : 1, (int)P.M, P.min_rows, split, total, ntiles, P.ntiles,
+                      reinterpret_cast<uint32_t*>(sW1) + wave * kRestRows, row_half, col_half);
+      if (big < 0) return;  // (as below)
+    } else {
+      const int per = (split + 7) / 8, loc = (int)(blockIdx.x >> 3);
+      big = (int)(blockIdx.x & 7) * per + loc;
+      if (loc >= per || big >= split) return;  // the whole workgroup, before any barrier
+    }
     // order: blocks of kGroupM row tiles, their column tiles one after the other, row tiles innermost
     const int grp = big / (kGroupM * ntiles), in = big - grp * kGroupM * ntiles;
     const int gm = min(kGroupM, mt_total - grp * kGroupM);
@@ -181,9 +259,8 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       row0 = mi * step_m;
     }
     if (sub) {
-      const int q = tile % kSub;
-      row0 += (q % kSubM) * BM;
-      tile_n = tile_n * (kBig / BN) + q / kSubM;
+      row0 += row_half * BM;
+      tile_n = tile_n * (kBig / BN) + col_half;
       if (row0 >= row_end || tile_n >= P.ntiles) return;
     }
     // (scalar: a buffer resource needs scalar words)
