@@ -67,6 +67,17 @@ __host__ __device__ __forceinline__ int tile_split(int total) {
   return total > kCus && rest <= kRestMax ? total - rest : total;
 }
 
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // rows of 16 lanes: shifts by 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 of rows 0 and 2 to rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to rows 2 and 3
+  return v;
+}
+
 // Tiles of BM rows over the ranges holding more than min_rows rows: with
 // `want` < 0 returns the tile count, else finds tile `want` (expert and its
 // first and end row).  Called by whole waves.
@@ -78,20 +89,15 @@ __device__ __forceinline__ int tile_scan(const int32_t* offsets, int E, int M, i
     int a = 0, b = 0;
     if (e0 + lane < E) expert_range(offsets, e0 + lane, M, a, b);
     const int nt = b - a > min_rows ? (b - a + BM - 1) / BM : 0;
-    int inc = nt;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(inc, d, 64);
-      if (lane >= d) inc += up;
-    }
-    const int last = __shfl(inc, 63, 64);
+    const int inc = wave_scan(nt);
+    const int last = __builtin_amdgcn_readlane(inc, 63);
     if (want >= 0 && want < before + last) {
       const uint64_t hit = __ballot(before + inc > want);
       const int src = __ffsll((unsigned long long)hit) - 1;  // the first expert whose tiles reach past `want`
-      const int t0 = before + __shfl(inc - nt, src, 64);
+      const int t0 = before + __builtin_amdgcn_readlane(inc - nt, src);
       e_out = e0 + src;
-      row0 = __shfl(a, src, 64) + (want - t0) * BM;
-      row_end = __shfl(b, src, 64);
+      row0 = __builtin_amdgcn_readlane(a, src) + (want - t0) * BM;
+      row_end = __builtin_amdgcn_readlane(b, src);
       return 0;
     }
     before += last;
@@ -118,15 +124,10 @@ __device__ __forceinline__ int rest_tile(const int32_t* offsets, int E, int M, i
       else b = M;
     }
     const int nt = b - a > min_rows ? (b - a + 255) / 256 : 0;
-    int inc = nt;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(inc, d, 64);
-      if (lane >= d) inc += up;
-    }
+    const int inc = wave_scan(nt);
     const int at = before + inc - 1 - lo;  // the range's last row tile
     if (nt > 0 && b - a - (nt - 1) * 256 <= 128 && at >= 0 && at < kRestRows) half[at] = 1;
-    before += __shfl(inc, 63, 64);
+    before += __builtin_amdgcn_readlane(inc, 63);
   }
   __builtin_amdgcn_wave_barrier();
   // quarters of a lane's tiles, the tile's row and column halves
@@ -137,20 +138,15 @@ __device__ __forceinline__ int rest_tile(const int32_t* offsets, int E, int M, i
     const int big = split + kPer * lane + i;
     cnt[i] = rows[i] = 0;
     if (big < total) {
-      const int grp = big / (kGroupM * ntiles), in = big - grp * kGroupM * ntiles;
-      const int gm = min(kGroupM, mt_total - grp * kGroupM);
-      rows[i] = (int)half[grp * kGroupM + in % gm - lo];
-      cnt[i] = rows[i] * (2 * (in / gm) + 1 < ncols ? 2 : 1);
+      int row = 0, in = big - lo * ntiles;  // the group's first row tile, from lo, and the place in the group
+      for (; in >= kGroupM * ntiles; in -= kGroupM * ntiles) row += kGroupM;
+      const uint32_t gm = (uint32_t)min(kGroupM, mt_total - lo - row), col = (uint32_t)in / gm;
+      rows[i] = (int)half[row + in - (int)(col * gm)];
+      cnt[i] = rows[i] * (2 * (int)col + 1 < ncols ? 2 : 1);
     }
     sum += cnt[i];
   }
-  int inc = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int up = __shfl_up(inc, d, 64);
-    if (lane >= d) inc += up;
-  }
-  const int all = __shfl(inc, 63, 64), per = (all + 7) / 8, loc = (int)(blockIdx.x >> 3);
+  const int inc = wave_scan(sum), all = __builtin_amdgcn_readlane(inc, 63), per = (all + 7) / 8, loc = (int)(blockIdx.x >> 3);
   const int want = (int)(blockIdx.x & 7) * per + loc;  // each XCD a contiguous range
   if (loc >= per || want >= all) return -1;
   int first = inc - sum, tile = -1, q = 0, nr = 1;
@@ -164,11 +160,10 @@ __device__ __forceinline__ int rest_tile(const int32_t* offsets, int E, int M, i
     first += cnt[i];
   }
   const int src = __ffsll((unsigned long long)__ballot(tile >= 0)) - 1;
-  q = __shfl(q, src, 64);
-  nr = __shfl(nr, src, 64);
-  row_half = q % nr;
-  col_half = q / nr;
-  return __shfl(tile, src, 64);
+  q = __builtin_amdgcn_readlane(q, src);  // 0 .. 3
+  row_half = __builtin_amdgcn_readlane(nr, src) == 2 ? q & 1 : 0;
+  col_half = __builtin_amdgcn_readlane(nr, src) == 2 ? q >> 1 : q;
+  return __builtin_amdgcn_readlane(tile, src);
 }
 
 template <int KIND, int BITS, int BM, int BN>
