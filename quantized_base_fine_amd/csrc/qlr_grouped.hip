@@ -353,8 +353,10 @@ __global__ __launch_bounds__(64 * W) void k_grouped_t(TJobs J) {
   __shared__ __attribute__((aligned(16))) char lds[W * (kSlice > kSum ? kSlice : kSum)];
   int e = 0, row0 = 0, row_end = 0;
   const int total = tile_scan(J.offsets, J.experts, (int)J.M, 0, 16 * RT, -1, e, row0, row_end);
-  if ((int)blockIdx.x >= total) return;  // the whole workgroup
-  tile_scan(J.offsets, J.experts, (int)J.M, 0, 16 * RT, blockIdx.x, e, row0, row_end);
+  // each XCD a contiguous range of row tiles (the grid's rows are a multiple of 8): an expert's adapter in few L2s
+  const int per = (total + 7) / 8, loc = (int)(blockIdx.x >> 3), tile = (int)(blockIdx.x & 7) * per + loc;
+  if (loc >= per || tile >= total) return;  // the whole workgroup
+  tile_scan(J.offsets, J.experts, (int)J.M, 0, 16 * RT, tile, e, row0, row_end);
   e = __builtin_amdgcn_readfirstlane(e);
   row0 = __builtin_amdgcn_readfirstlane(row0);
   row_end = __builtin_amdgcn_readfirstlane(row_end);
@@ -366,19 +368,21 @@ __global__ __launch_bounds__(64 * W) void k_grouped_t(TJobs J) {
 template <int RT, int JT, int W, int NB>
 hipError_t launch_t(const TJobs& J, int jobs, hipStream_t s) {
   hipLaunchKernelGGL((k_grouped_t<RT, JT, W, NB>),
-                     dim3((unsigned)tile_bound(J.M, J.experts, 16 * RT), (unsigned)((J.r + 16 * JT - 1) / (16 * JT)), (unsigned)jobs),
+                     dim3((unsigned)((tile_bound(J.M, J.experts, 16 * RT) + 7) / 8 * 8), (unsigned)((J.r + 16 * JT - 1) / (16 * JT)), (unsigned)jobs),
                      dim3(64 * W), 0, s, J);
   return hipGetLastError();
 }
 
 hipError_t launch_t_jobs(const TJobs& J, int jobs, hipStream_t s) {
   // Few row tiles: 16 waves, 8 steps of loads in flight each (a decode call waits for one round trip).  Many: 32 rows
-  // against up to 64 adapter columns, which halves the reads of A.
+  // against up to 64 adapter columns, which halves the reads of A; 64 rows where the ranges fill them and A is wide (8192
+  // rows of 4096, r = 64: 37 us with 32 rows, 30 with 64, of 13 for reading x).
   const bool few = tile_bound(J.M, J.experts, 16) * ((J.r + 15) / 16) <= 256;
   if (few) return launch_t<1, 1, 16, 4>(J, jobs, s);
-  if (J.r <= 16) return launch_t<2, 1, 4, 4>(J, jobs, s);
+  if (J.r <= 16) return launch_t<2, 1, 8, 2>(J, jobs, s);
   if (J.r <= 32) return launch_t<2, 2, 4, 2>(J, jobs, s);
-  return launch_t<2, 4, 4, 2>(J, jobs, s);
+  if (J.M < (int64_t)J.experts * 128) return launch_t<2, 4, 4, 2>(J, jobs, s);
+  return launch_t<4, 4, 8, 1>(J, jobs, s);
 }
 
 // Bt[e][j][n] = B[e][n][j]
