@@ -167,6 +167,15 @@ def test_large_tiles_and_their_rest(bits):
     check_backward(L)
 
 
+@pytest.mark.parametrize("r", [8, 24, 64, 72])
+def test_wide_adapters_and_half_filled_tiles(r):
+    """Input gradient: 32 column tiles, 12 row tiles of 256, of which four hold at most 128 rows, 384 = 256 + 128 of them; the
+    adapter products of ranges of 1 to 700 rows in steps of 32 and 64 rows."""
+    L = Layer([384, 90, 300, 530, 1, 700], 64, 8192, 4, r, seed=r)
+    check_backward(L)
+    check_forward(L)
+
+
 def test_no_rows():
     L = Layer([0, 0], 24, 128, 4, 8, seed=1)
     assert qlr.linear_grouped(L.xd, L.qw, L.offsets, L.Ad, L.Bd, 1.0).shape == (0, 24)
