@@ -123,11 +123,11 @@ __device__ __forceinline__ void quantize_row(const void* __restrict__ X, int64_t
   }
 }
 
-template <int DT, bool VEC, int NP>
-__global__ __launch_bounds__(256) void k_quantize_i8(const void* __restrict__ X, int64_t cols, int8_t* __restrict__ q,
+template <int DT, bool VEC, int NP, int NTH>
+__global__ __launch_bounds__(NTH) void k_quantize_i8(const void* __restrict__ X, int64_t cols, int8_t* __restrict__ q,
                                                      float* __restrict__ scale) {
-  __shared__ uint32_t red[4];
-  quantize_row<DT, VEC, NP, 256>(X, blockIdx.x, cols, q, scale, red);
+  __shared__ uint32_t red[NTH / 64];
+  quantize_row<DT, VEC, NP, NTH>(X, blockIdx.x, cols, q, scale, red);
 }
 
 // A decode call's tokens: the first M workgroups quantize a row each, the others
@@ -145,12 +145,12 @@ __global__ __launch_bounds__(kLtWaves * 64) void k_i8_prep(const uint16_t* __res
 template <int DT>
 hipError_t launch_quantize_dt(const void* X, int64_t rows, int64_t cols, int8_t* q, float* scale, hipStream_t s) {
   for (int64_t r0 = 0; r0 < rows; r0 += 1 << 30) {  // the grid's x dimension holds 2^31 - 1 workgroups
-    const dim3 n((unsigned)std::min<int64_t>(rows - r0, 1 << 30)), b(256);
+    const dim3 n((unsigned)std::min<int64_t>(rows - r0, 1 << 30));
     const char* x0 = reinterpret_cast<const char*>(X) + r0 * cols * (DT == DT_F32 ? 4 : 2);
     int8_t* q0 = q + r0 * cols;
-    if (cols % 8 != 0) hipLaunchKernelGGL((k_quantize_i8<DT, false, 1>), n, b, 0, s, x0, cols, q0, scale + r0);
-    else if (cols <= 2 * 2048) hipLaunchKernelGGL((k_quantize_i8<DT, true, 2>), n, b, 0, s, x0, cols, q0, scale + r0);
-    else hipLaunchKernelGGL((k_quantize_i8<DT, true, 8>), n, b, 0, s, x0, cols, q0, scale + r0);
+    if (cols % 8 != 0) hipLaunchKernelGGL((k_quantize_i8<DT, false, 1, 256>), n, dim3(256), 0, s, x0, cols, q0, scale + r0);
+    else if (cols <= 2 * 2048) hipLaunchKernelGGL((k_quantize_i8<DT, true, 2, 256>), n, dim3(256), 0, s, x0, cols, q0, scale + r0);
+    else hipLaunchKernelGGL((k_quantize_i8<DT, true, 2, 1024>), n, dim3(1024), 0, s, x0, cols, q0, scale + r0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -160,12 +160,15 @@ hipError_t launch_quantize_dt(const void* X, int64_t rows, int64_t cols, int8_t*
 // ---------------------------------------------------------------- M <= 16
 //
 // The weight's stream: a workgroup of 8 waves takes 16 weight rows, wave w the
-// w-th eighth of K in 64-element steps, multiplied on 16x16x64 int8 MFMA (the
-// tokens as A, weight rows as B; token lanes past M hold zeros).  Loads give
-// each quad of lanes one row's 64 bytes and lane permutes bring them to
-// fragment order (with every lane loading its own fragment piece the
-// 22016 x 8192 weight took 52 us, so 38).  NB steps are in flight
-// while the NB before them are multiplied.  The waves' integer sums are added
+// w-th eighth of K in 128-element steps, multiplied on 16x16x64 int8 MFMA (the
+// tokens as A, weight rows as B; token lanes past M hold zeros).  A load of the weight
+// covers whole 128-byte lines, 8 lanes to each of 8 rows: the memory behind the
+// caches is asked for full lines (22016 x 8192 from there: 64-byte pieces of
+// 16 rows 55.6 us a call, full lines 50.8, and read past the caches'
+// allocation, which a weight used once a token cannot profit from, 46).
+// Lane permutes bring both loads' rows to fragment order.  The tokens, which stay in L2, come in quads
+// of lanes on one row's 64 bytes.  NB steps are in flight while the NB before them are
+// multiplied.  The waves' integer sums are added
 // through LDS; the adapter's t B^T is added in float32 before the store.
 constexpr int kFewWaves = 8;
 
@@ -178,32 +181,49 @@ __global__ __launch_bounds__(512) void k_i8_few(TileArgs P) {
   const int n0 = blockIdx.x * 16;
   const int M = (int)P.M;
   const int64_t K = P.K, N = P.N;
-  const int row = lane >> 2, g = lane & 3, src = (4 * (lane & 15) + (lane >> 4)) << 2;
-  const int8_t* wp = reinterpret_cast<const int8_t*>(P.w) + std::min<int64_t>(n0 + row, N - 1) * K + 16 * g;
+  // weight: load 2 s + i of a step, rows n0 + 8 i + lane / 8, bytes 16 (lane % 8) of the step's 128
+  const int wr = lane >> 3, wc = lane & 7;
+  const int8_t* wp[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    wp[i] = reinterpret_cast<const int8_t*>(P.w) + std::min<int64_t>(n0 + 8 * i + wr, N - 1) * K + 16 * wc;
+  const int wsrc = (8 * (lane & 7) + (lane >> 4)) << 2;  // lane 16 g + n <- lane 8 (n % 8) + 4 half + g of load n / 8
+  const bool low = (lane & 15) < 8;
+  // tokens: quads, lane 16 g + n <- lane 4 n + g
+  const int row = lane >> 2, g = lane & 3, xsrc = (4 * (lane & 15) + (lane >> 4)) << 2;
   const int8_t* xp = reinterpret_cast<const int8_t*>(P.x) + (int64_t)std::min(row, M - 1) * K + 16 * g;
-  const int nst = (int)((K + 63) / 64);
+  const int nst = (int)((K + 127) / 128);
   const int s0 = (int)((int64_t)nst * wave / kFewWaves), s1 = (int)((int64_t)nst * (wave + 1) / kFewWaves);
   const u32x4_t zero = {0u, 0u, 0u, 0u};
   i32x4_t acc = {0, 0, 0, 0};
-  struct Ld { u32x4_t w[NB], x[NB]; };
+  struct Ld { u32x4_t w[NB][2], x[NB][2]; };
   auto load = [&](int b, Ld& d) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int64_t k = (int64_t)(b + i) * 64;
-      const bool ok = b + i < s1 && k + 16 * g < K;
-      d.w[i] = ok ? *reinterpret_cast<const u32x4_t*>(wp + k) : zero;
-      d.x[i] = ok && row < M ? *reinterpret_cast<const u32x4_t*>(xp + k) : zero;
-    }
-  };
-  auto frag = [&](u32x4_t v) {
-    i32x4_t f;
+    for (int s = 0; s < NB; ++s) {
+      const int64_t k = (int64_t)(b + s) * 128;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __builtin_amdgcn_ds_bpermute(src, (int)v[i]);
-    return f;
+      for (int i = 0; i < 2; ++i) {
+        d.w[s][i] = b + s < s1 && k + 16 * wc < K ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wp[i] + k)) : zero;
+        const int64_t kx = k + 64 * i;
+        d.x[s][i] = b + s < s1 && kx + 16 * g < K && row < M ? *reinterpret_cast<const u32x4_t*>(xp + kx) : zero;
+      }
+    }
   };
   auto compute = [&](const Ld& d) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(frag(d.x[i]), frag(d.w[i]), acc, 0, 0, 0);
+    for (int s = 0; s < NB; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // elements 64 i .. + 63 of the step
+        i32x4_t xf, wf;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          xf[j] = __builtin_amdgcn_ds_bpermute(xsrc, (int)d.x[s][i][j]);
+          const int w0 = __builtin_amdgcn_ds_bpermute(wsrc + 16 * i, (int)d.w[s][0][j]);
+          const int w1 = __builtin_amdgcn_ds_bpermute(wsrc + 16 * i, (int)d.w[s][1][j]);
+          wf[j] = low ? w0 : w1;
+        }
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(xf, wf, acc, 0, 0, 0);
+      }
   };
   Ld d0, d1;
   load(s0, d0);
@@ -253,7 +273,7 @@ hipError_t launch_i8_prep(const void* x, int64_t M, int64_t K, int8_t* q, float*
 
 hipError_t launch_i8_few(const TileArgs& a, hipStream_t s) {
   if (a.M < 1 || a.M > kFewRows || a.K % 16 != 0) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_i8_few<4>), dim3((unsigned)((a.N + 15) / 16)), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((k_i8_few<1>), dim3((unsigned)((a.N + 15) / 16)), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
