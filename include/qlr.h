@@ -446,7 +446,7 @@ qlr_status qlr_linear_bwd(const void* dy, qlr_dtype dydt, const void* x, qlr_dty
  * Quantize rows to 8-bit integers.  X (device) rows x cols in dt (f32, f16 or
  * bf16, widened exactly to float32); out (host struct with its two device
  * buffers; out->rows and out->cols must equal rows and cols) gets, per row, the
- * scale s = fl32(max|x| / 127) and q = the integer nearest x / s, ties to
+ * scale s = fl32(max|x| fl32(1 / 127)) and q = the integer nearest x / s, ties to
  * even, within [-127, 127] (decided exactly; s == 0 gives q = 0).  A row that
  * holds a NaN or an Inf gets a NaN scale and q = 0, so that every product with
  * it is NaN.  rows may be 0 (nothing is launched).  Asynchronous, no workspace.
@@ -467,7 +467,7 @@ qlr_status qlr_quantize_i8(const void* X, qlr_dtype dt, int64_t rows, int64_t co
  * be NULL (and xdt is ignored) when xq is given and r == 0.  A, B bf16 as in
  * qlr_linear_fwd (abdt must be QLR_BF16 when r > 0); y (device) M x N in ydt
  * (f32 or bf16).  K % 16 == 0 and K <= 131072 (the integer sums stay below
- * 2^31); N M as in qlr_linear_fwd, M may be 0.  Integer sums are exact; each
+ * 2^31); M may be 0.  Integer sums are exact; each
  * result takes three float32 roundings (within 2e-7 of it, plus half a bf16
  * ulp for a bf16 y; intermediate results beyond float32's range overflow),
  * and the adapter term 1e-4 of the sum of its terms' absolute values.
@@ -544,7 +544,8 @@ qlr_status qlr_linear_bwd_grouped(const void* dy, qlr_dtype dydt, const void* x,
                                   float* dA, float* dB, void* ws, size_t ws_bytes, void* stream);
 
 /*
- * Force the kernel family used by qlr_linear_fwd and qlr_linear_fwd_mixed on
+ * Force the kernel family used by qlr_linear_fwd, qlr_linear_fwd_mixed,
+ * qlr_linear_fwd_i8 and qlr_linear_fwd_grouped (as each describes) on
  * the calling thread (for tests, measurement, and callers that need a
  * family's error bound; see qlr_linear_fwd).  QLR_PATH_AUTO restores the
  * default choice: F32 for float32 x or float32 adapters, GEMV for M <= 16,

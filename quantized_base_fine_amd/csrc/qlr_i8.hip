@@ -2,8 +2,11 @@
 // scale per token and one per output channel, plus the unmerged adapter branch
 // of the frozen base (LoRDBA page, "adapter mode").
 //
-// Row quantization (tokens and weight channels alike): s = fl32(max|x| / 127),
-// q = the integer nearest x / s, ties to even, in [-127, 127].
+// Row quantization (tokens and weight channels alike): s = fl32(max|x| fl32(1 / 127)),
+// q = the integer nearest x / s, ties to even, in [-127, 127].  (The product, not
+// the quotient, which can be a last place away and then takes exact ties to the other
+// side: amax() / 127 on the GPU in PyTorch is this product, so rows quantized by
+// either agree bit for bit.)
 #include "qlr_lora_t.h"
 #include "qlr_tile.h"
 
@@ -94,7 +97,7 @@ __device__ __forceinline__ void quantize_row(const void* __restrict__ X, int64_t
 #pragma unroll
   for (int w = 0; w < NTH / 64; ++w) am = max(am, red[w]);
   const bool finite = am < 0x7F800000u;
-  const float s = finite ? __uint_as_float(am) / 127.0f : __uint_as_float(0x7FC00000u);
+  const float s = finite ? __uint_as_float(am) * (1.0f / 127.0f) : __uint_as_float(0x7FC00000u);
   if (tid == 0) scale[row] = s;
   const bool live = finite && s > 0.0f;
   // below 2^-125 the reciprocal could overflow: divide instead

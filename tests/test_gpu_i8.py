@@ -1,7 +1,7 @@
 """GPU tests of the 8-bit-integer linear layer: row quantization (exact), the product on both
 kernel families, the adapter, scales of non-finite and zero rows.
 
-The reference is numpy / torch on the CPU in 64 bits, from the definitions: s = fl32(max|x| / 127), q the integer
+The reference is numpy / torch on the CPU in 64 bits, from the definitions: s = fl32(max|x| fl32(1 / 127)), q the integer
 nearest x / s (ties to even), y = sx sw sum(xq wq) + scale (x A^T) B^T.
 
 Tolerance of the product: the integer sum is exact; its conversion and the two scale products round three
@@ -24,7 +24,7 @@ def ref_rows(x):
     v = x.float().numpy()
     bad = ~np.isfinite(v).all(1)
     am = np.where(bad, 0.0, np.abs(np.where(np.isfinite(v), v, 0)).max(1)).astype(np.float32)
-    s = (am / np.float32(127)).astype(np.float32)
+    s = (am * (np.float32(1) / np.float32(127))).astype(np.float32)
     with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
         q = np.rint(v.astype(np.float64) / s.astype(np.float64)[:, None])
     q = np.clip(np.where((s > 0)[:, None] & ~bad[:, None], q, 0), -127, 127)
@@ -60,6 +60,15 @@ def test_quantize_ties_go_to_even_and_borders_keep_their_side():
     assert np.array_equal(q.scale.cpu().numpy(), rs)
     assert np.array_equal(q.q.cpu().numpy().astype(np.float64), rq)
     assert q.q[0, 0].item() == -126 and q.q[0, 126].item() == 0  # -126.5 -> -126, -0.5 -> 0
+
+
+def test_quantize_agrees_with_torch_on_the_gpu():
+    """The same scales and integers as amax() / 127 and a division on the GPU (short rows: many exact ties)."""
+    x = rand(2000, 264, 9).cuda()
+    q = qlr.quantize_i8(x)
+    s = x.float().abs().amax(1) / 127
+    assert torch.equal(q.scale, s)
+    assert torch.equal(q.q.double(), torch.round(x.double() / s.double()[:, None]).clamp(-127, 127))
 
 
 def test_quantize_extreme_rows():
