@@ -12,14 +12,22 @@
 // 32x32x32 int8), so a lane's results are 4 neighbouring columns of one output
 // row and the epilogue stages whole 8- or 16-byte pieces.
 //
-// Pipeline.  Two LDS buffers of BM + BN rows of 128 bytes, 16-byte chunks
+// Pipeline.  LDS buffers of BM + BN rows of 128 bytes, 16-byte chunks
 // XOR-swizzled by row (swz) so that fragment reads and tile writes are free of
-// bank conflicts.  Step k multiplies buffer k % 2 and writes the operands of
-// step k + 1, loaded into registers during step k - 1, to the other buffer
-// between the products; one barrier ends the step.  With two waves per SIMD,
-// one wave's products cover the other's waits.  Coded weights are dequantized to
-// bf16 between the products (32 codes per thread and step); each weight is
-// dequantized once per tile.
+// bank conflicts.  While step k is multiplied, x (and int8 weights) of a later step come
+// into another buffer by direct loads, and the codes of step k + 1, loaded into registers
+// before, are dequantized to bf16 between the products (32 or 16 codes per thread and
+// step); one barrier ends the step.  Each weight is dequantized once per tile.  The
+// first products of a step wait for their fragments only: with addresses and the level
+// table before them, mid-size products took 3 to 7 % longer.
+//
+// What bounds it (counters at the sizes named): the 256 x 256 tiles keep the matrix pipes busy
+// 53 % of the cycles of 8192 x 4096 x 4096 in 8 ranges with 4-bit codes (1.03 PFLOP/s over the 512 tiles; the same loop on
+// zeros runs a step in 1.3 us, on random values in 1.8: the clock falls with the
+// power) and 50 % of those of the transposed product; the vector units are busy 37 % with the codes.
+// The smaller tiles spend more on the codes than on the products: 128 x 128 ones on the last 64 tiles of
+// that call keep the vector units busy 41 % and the matrix pipes 25 %, 64 x 128 ones on 777 rows in 64 ranges of
+// 1408 x 2048 (3-bit, transposed) 50 and 19 %; the rest is waiting at the barriers.
 //
 // Adapter.  t = x A_e^T (float32 partial sums) enters after the last step as
 // blocks of 32 adapter columns: the x side holds [hi(s t) | lo(s t)] (two bf16
@@ -60,7 +68,7 @@ constexpr int kCus = 256, kRestMax = 144;
 // Tile order.  The 32 tiles that an XCD works on at a time cover kGroupM row
 // tiles x 32 / kGroupM column tiles, which share its L2: row by row (1 x 32), the int8
 // product of 2048 x 11008 x 4096 read 293 MB through the fabric (4.3 TB/s, its
-// bound) and took 149 us with its other launches; in blocks of 8 x 4, 135 us.
+// bound) and took 149 us with its other launches; in blocks of 8 x 4 it read 193 MB and took 135.
 constexpr int kGroupM = 8;
 __host__ __device__ __forceinline__ int tile_split(int total) {
   const int rest = total % kCus;
@@ -788,7 +796,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
 // NR weight rows, NTH threads): the operands are loaded into registers before the weight
 // stream and staged in LDS after it, so their latency hides behind it.
 //   t: splits x M x r partials in global memory (rows row0 ..), B: rows x r bf16.
-// staged() tells whether the sizes fit (r % 8 == 0 and the pieces a thread can hold);
+// st tells whether the sizes fit (r % 8 == 0 and the pieces a thread can hold);
 // otherwise the dot product reads global memory.
 template <int NR, int KT, int NTH = 512>
 struct FewAdapter {
@@ -883,7 +891,9 @@ hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
   auto kern = k_tile<KIND, BITS, BM, BN>;
   const int64_t no = KIND == TILE_TR ? a.K : a.N;
   a.ntiles = (int)((no + BN - 1) / BN);
-  int64_t tiles = (a.offsets ? tile_bound(a.M, a.experts, BM) : (a.M + BM - 1) / BM) * a.ntiles;
+  // (only so many ranges can hold more than min_rows rows)
+  const int ranges = (int)std::min<int64_t>(a.experts, a.M / (a.min_rows + 1));
+  int64_t tiles = (a.offsets ? tile_bound(a.M, ranges, BM) : (a.M + BM - 1) / BM) * a.ntiles;
   if (a.rest && BM < 256) tiles = kRestMax * (256 / BM) * (256 / BN);
   if (tiles <= 0) return hipSuccess;
   if (tiles > INT32_MAX - 8) return hipErrorInvalidValue;
@@ -894,8 +904,8 @@ hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
 // The tile shape, from the sizes the host knows (the rows of an expert only by their
 // mean).  256 x 256 tiles multiply most per byte moved and watt, but need a
 // round of them to fill the 256 CUs and ranges of a few hundred rows to be
-// full: at 8192 x 4096 x 4096 in 8 ranges with 4-bit codes they took 359 us, 128 x 128 ones 434 and 64 x 128 ones
-// 629; at 777 rows in 64 ranges of 1408 x 2048 (2-bit) 55, 27 and 23 us.
+// full: at 8192 x 4096 x 4096 in 8 ranges with 4-bit codes (all tiles written from registers then) they took 359 us, 128 x
+// 128 ones 434 and 64 x 128 ones 629; at 777 rows in 64 ranges of 1408 x 2048 (2-bit) 55, 27 and 23 us.
 template <int KIND, int BITS>
 hipError_t launch_tile(TileArgs a, const Levels& lv, hipStream_t s) {
   const int64_t no = KIND == TILE_TR ? a.K : a.N;
