@@ -208,7 +208,10 @@ qlr_status qlr_qweight_sizes(int64_t rows, int64_t cols, int32_t bits, int32_t b
  * splits, rounded up to 256 bytes (0 bytes when M or r is 0).
  * QLR_OP_LINEAR_BWD (N = rows, K = cols of the weight): the partial sums of
  * x A^T and dy B, B transposed, and float32 partials of the adapter gradients
- * (0 bytes when r is 0).  Contents need no initialisation.  Host only.
+ * (0 bytes when r is 0).  QLR_OP_LINEAR_I8: the tokens as integers with their
+ * scales, and t for M rows and rank r.  The grouped calls have a function of
+ * their own (qlr_grouped_workspace_bytes).  Contents need no initialisation.
+ * Host only.
  */
 qlr_status qlr_workspace_bytes(qlr_op op, int64_t M, int64_t N, int64_t K, int32_t r,
                                size_t* bytes);
