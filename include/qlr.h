@@ -20,7 +20,8 @@
  *     A is r x K, B is N x r, all row-major and densely packed.
  *   - Pointers marked (device) are HIP device pointers; the caller owns every
  *     buffer.  The library allocates nothing and keeps no per-call state; it
- *     holds no handle.  Device pointers must be 16-byte aligned.
+ *     holds no handle.  Device pointers must be 16-byte aligned (offsets:
+ *     4-byte).
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).  All
  *     calls are asynchronous on that stream unless stated otherwise.
  *   - Every call returns a qlr_status; nothing is thrown across the ABI.

@@ -382,7 +382,8 @@ hipError_t launch_t(const TJobs& J, int jobs, hipStream_t s) {
 hipError_t launch_t_jobs(const TJobs& J, int jobs, hipStream_t s) {
   // Few row tiles: 16 waves, 8 steps of loads in flight each (a decode call waits for one round trip).  Many: 32 rows
   // against up to 64 adapter columns, which halves the reads of A; 64 rows where the ranges fill them and A is wide (8192
-  // rows of 4096, r = 64: 37 us with 32 rows, 30 with 64, of 13 for reading x).
+  // rows of 4096, r = 64: 37 us with 32 rows, 30 with 64, of 13 for reading x).  Narrow A: 8 waves with 2 steps in flight
+  // (4096 rows of x and dy, r = 16: 19.0 us, 4 waves with 4 steps 19.4; 4096 rows of 2048: 7.0 and 7.8).
   const bool few = tile_bound(J.M, J.experts, 16) * ((J.r + 15) / 16) <= 256;
   if (few) return launch_t<1, 1, 16, 4>(J, jobs, s);
   if (J.r <= 16) return launch_t<2, 1, 8, 2>(J, jobs, s);

@@ -145,6 +145,9 @@ __global__ __launch_bounds__(kLtWaves * 64) void k_i8_prep(const uint16_t* __res
   else lora_t_small_body(x, M, K, A, r, t, (b % jtiles) * 16, splits, b / jtiles, red);
 }
 
+// Long rows: 1024 threads a row while there is at most a row per CU (16 rows of 8192: 5.1 us, with 256 threads 7.7),
+// 256 threads for more (4096 rows of 11008: 38 us, with 1024 threads 42; 2048 rows of 4096 in 10.5 us are read and written at 2.4
+// TB/s, the bound of larger calls).
 template <int DT>
 hipError_t launch_quantize_dt(const void* X, int64_t rows, int64_t cols, int8_t* q, float* scale, hipStream_t s) {
   for (int64_t r0 = 0; r0 < rows; r0 += 1 << 30) {  // the grid's x dimension holds 2^31 - 1 workgroups
@@ -153,7 +156,8 @@ hipError_t launch_quantize_dt(const void* X, int64_t rows, int64_t cols, int8_t*
     int8_t* q0 = q + r0 * cols;
     if (cols % 8 != 0) hipLaunchKernelGGL((k_quantize_i8<DT, false, 1, 256>), n, dim3(256), 0, s, x0, cols, q0, scale + r0);
     else if (cols <= 2 * 2048) hipLaunchKernelGGL((k_quantize_i8<DT, true, 2, 256>), n, dim3(256), 0, s, x0, cols, q0, scale + r0);
-    else hipLaunchKernelGGL((k_quantize_i8<DT, true, 2, 1024>), n, dim3(1024), 0, s, x0, cols, q0, scale + r0);
+    else if (rows <= 256) hipLaunchKernelGGL((k_quantize_i8<DT, true, 2, 1024>), n, dim3(1024), 0, s, x0, cols, q0, scale + r0);
+    else hipLaunchKernelGGL((k_quantize_i8<DT, true, 8, 256>), n, dim3(256), 0, s, x0, cols, q0, scale + r0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
