@@ -54,7 +54,7 @@ typedef enum {
   QLR_ERR_ALIGN = 6,     /* a device pointer is not 16-byte aligned */
   QLR_ERR_NONFINITE = 7, /* quantize: W holds NaN or Inf */
   QLR_ERR_WORKSPACE = 8, /* workspace NULL or smaller than qlr_workspace_bytes() */
-  QLR_ERR_ALIAS = 9,     /* mixed: an output overlaps an input or another output */
+  QLR_ERR_ALIAS = 9,     /* an output overlaps an input or another output (where a call checks it) */
   QLR_ERR_HIP = 10,      /* a HIP runtime call or launch failed (text in qlr_last_error) */
   QLR_ERR_FORMAT = 11,   /* qlr_qweight.format_version unknown */
   QLR_ERR_PATH = 12      /* forced path cannot run these arguments */
@@ -455,7 +455,7 @@ qlr_status qlr_linear_bwd(const void* dy, qlr_dtype dydt, const void* x, qlr_dty
  * holds a NaN or an Inf gets a NaN scale and q = 0, so that every product with
  * it is NaN.  rows may be 0 (nothing is launched).  Asynchronous, no workspace.
  * Errors: QLR_ERR_NULL, QLR_ERR_SHAPE, QLR_ERR_DTYPE, QLR_ERR_ALIGN,
- * QLR_ERR_HIP.
+ * QLR_ERR_ALIAS (X, q and scale overlap), QLR_ERR_HIP.
  */
 qlr_status qlr_quantize_i8(const void* X, qlr_dtype dt, int64_t rows, int64_t cols, qlr_i8rows* out,
                            void* stream);
@@ -471,7 +471,7 @@ qlr_status qlr_quantize_i8(const void* X, qlr_dtype dt, int64_t rows, int64_t co
  * be NULL (and xdt is ignored) when xq is given and r == 0.  A, B bf16 as in
  * qlr_linear_fwd (abdt must be QLR_BF16 when r > 0); y (device) M x N in ydt
  * (f32 or bf16).  K % 16 == 0 and K <= 131072 (the integer sums stay below
- * 2^31); M may be 0.  Integer sums are exact; each
+ * 2^31); M <= 2^27, M may be 0.  Integer sums are exact; each
  * result takes three float32 roundings (within 2e-7 of it, plus half a bf16
  * ulp for a bf16 y; intermediate results beyond float32's range overflow),
  * and the adapter term 1e-4 of the sum of its terms' absolute values.
@@ -480,7 +480,8 @@ qlr_status qlr_quantize_i8(const void* X, qlr_dtype dt, int64_t rows, int64_t co
  * (device) >= qlr_workspace_bytes(QLR_OP_LINEAR_I8, M, N, K, r).
  * Asynchronous, allocation-free.
  * Errors: QLR_ERR_NULL, QLR_ERR_SHAPE, QLR_ERR_DTYPE, QLR_ERR_ALIGN,
- * QLR_ERR_WORKSPACE, QLR_ERR_PATH, QLR_ERR_HIP.
+ * QLR_ERR_WORKSPACE, QLR_ERR_ALIAS (y overlaps an input), QLR_ERR_PATH,
+ * QLR_ERR_HIP.
  */
 qlr_status qlr_linear_fwd_i8(const void* x, qlr_dtype xdt, int64_t M, const qlr_i8rows* xq, const qlr_i8rows* w,
                              const void* A, const void* B, qlr_dtype abdt, int32_t r, float scale, void* y,
@@ -511,7 +512,7 @@ qlr_status qlr_grouped_workspace_bytes(qlr_op op, int64_t T, int64_t rows, int64
  * nothing outside the buffers is touched, the rows concerned get wrong values.)
  * x (device) T x cols bf16; A (device) experts x r x cols and B (device) experts
  * x N x r bf16, both NULL when r == 0; y (device) T x N in ydt (f32 or bf16).
- * 1 <= experts <= QLR_MAX_EXPERTS, T <= 2^30, T may be 0.  Error bound per
+ * 1 <= experts <= QLR_MAX_EXPERTS, T <= 2^27, T may be 0.  Error bound per
  * element as QLR_PATH_GEMM of qlr_linear_fwd: 5e-3 * S + 1e-5 (the weight enters
  * rounded to bf16; sums are float32), plus half a bf16 ulp for a bf16 y.
  * qlr_force_path: QLR_PATH_GEMM runs every expert on the tiled kernel (by

@@ -7,6 +7,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -306,7 +307,19 @@ Span span_of(const void* p, size_t n) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
   return {a, a + n};
 }
-bool overlaps(const Span& p, const Span& q) { return p.first < q.second && q.first < p.second; }
+// (an empty span overlaps nothing)
+bool overlaps(const Span& p, const Span& q) {
+  return p.first < p.second && q.first < q.second && p.first < q.second && q.first < p.second;
+}
+
+bool overlaps_any(const Span& p, std::initializer_list<Span> others) {
+  for (const Span& q : others)
+    if (overlaps(p, q)) return true;
+  return false;
+}
+
+// The largest T (M) of the grouped calls and of the 8-bit linear: launches of a few rows per workgroup stay below 2^32 threads.
+constexpr int64_t kMaxRows = INT64_C(1) << 27;
 
 qlr_status check_i8rows(const qlr_i8rows* q, const char* what) {
   if (!q->q || !q->scale) return fail(QLR_ERR_NULL, "%s: a buffer is NULL", what);
@@ -319,7 +332,7 @@ qlr_status check_grouped(int64_t T, const qlr_qweight* w, int32_t experts, const
                          qlr_dtype xdt, qlr_dtype abdt, qlr_dtype odt) {
   qlr_status st = check_qweight(w);
   if (st != QLR_OK) return st;
-  if (T < 0 || T > (INT64_C(1) << 30)) return fail(QLR_ERR_SHAPE, "T %lld not in [0, 2^30]", (long long)T);
+  if (T < 0 || T > kMaxRows) return fail(QLR_ERR_SHAPE, "T %lld not in [0, 2^27]", (long long)T);
   if (r < 0 || r > (1 << 20)) return fail(QLR_ERR_SHAPE, "r %d not in [0, 2^20]", r);
   if (experts < 1 || experts > QLR_MAX_EXPERTS)
     return fail(QLR_ERR_SHAPE, "experts %d not in [1, %d]", experts, QLR_MAX_EXPERTS);
@@ -1077,6 +1090,9 @@ qlr_status qlr_quantize_i8(const void* X, qlr_dtype dt, int64_t rows, int64_t co
   const qlr_status st = check_i8rows(out, "out");
   if (st != QLR_OK) return st;
   if (!aligned16(X)) return fail(QLR_ERR_ALIGN, "X must be 16-byte aligned");
+  const Span in = span_of(X, (size_t)(rows * cols) * dtype_size(dt)), q = span_of(out->q, (size_t)(rows * cols)),
+             sc = span_of(out->scale, (size_t)rows * 4);
+  if (overlaps(q, sc) || overlaps_any(in, {q, sc})) return fail(QLR_ERR_ALIAS, "X, q and scale overlap");
   const hipError_t e = qlr::launch_quantize_i8(X, (int)dt, rows, cols, out->q, out->scale, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "row quantization launch");
   return QLR_OK;
@@ -1086,8 +1102,8 @@ qlr_status qlr_linear_fwd_i8(const void* x, qlr_dtype xdt, int64_t M, const qlr_
                              const void* A, const void* B, qlr_dtype abdt, int32_t r, float scale, void* y,
                              qlr_dtype ydt, void* ws, size_t ws_bytes, void* stream) {
   if (!w) return fail(QLR_ERR_NULL, "w is NULL");
-  if (M < 0 || M > (INT64_C(1) << 30)) return fail(QLR_ERR_SHAPE, "M %lld not in [0, 2^30]", (long long)M);
-  if (r < 0) return fail(QLR_ERR_SHAPE, "r < 0");
+  if (M < 0 || M > kMaxRows) return fail(QLR_ERR_SHAPE, "M %lld not in [0, 2^27]", (long long)M);
+  if (r < 0 || r > (1 << 20)) return fail(QLR_ERR_SHAPE, "r %d not in [0, 2^20]", r);
   const int64_t N = w->rows, K = w->cols;
   if (N <= 0 || K <= 0) return fail(QLR_ERR_SHAPE, "empty weight");
   if (N > (INT64_C(1) << 30)) return fail(QLR_ERR_SHAPE, "rows %lld above 2^30", (long long)N);
@@ -1108,6 +1124,14 @@ qlr_status qlr_linear_fwd_i8(const void* x, qlr_dtype xdt, int64_t M, const qlr_
   if (r > 0) {
     if (!A || !B) return fail(QLR_ERR_NULL, "A or B is NULL with r > 0");
     if (!aligned16(A) || !aligned16(B)) return fail(QLR_ERR_ALIGN, "A and B must be 16-byte aligned");
+  }
+  if (M > 0) {
+    const Span none = {0, 0}, out = span_of(y, (size_t)(M * N) * dtype_size(ydt));
+    if (overlaps_any(out, {span_of(w->q, (size_t)(N * K)), span_of(w->scale, (size_t)N * 4),
+                           need_x ? span_of(x, (size_t)(M * K) * dtype_size(xdt)) : none,
+                           xq ? span_of(xq->q, (size_t)(M * K)) : none, xq ? span_of(xq->scale, (size_t)M * 4) : none,
+                           span_of(A, (size_t)r * (size_t)K * 2), span_of(B, (size_t)N * (size_t)r * 2)}))
+      return fail(QLR_ERR_ALIAS, "y overlaps an input");
   }
   const I8Layout lay = i8_layout(M, K, r);
   if (lay.total > 0 && (!ws || ws_bytes < lay.total))
@@ -1185,14 +1209,13 @@ qlr_status qlr_linear_fwd_grouped(const void* x, qlr_dtype xdt, int64_t T, const
     if (!aligned16(A) || !aligned16(B)) return fail(QLR_ERR_ALIGN, "A and B must be 16-byte aligned");
   }
   if (T > 0) {
-    const Span out = span_of(y, (size_t)(T * N) * dtype_size(ydt));
-    std::vector<Span> ins = {span_of(x, (size_t)(T * K) * 2), span_of(offsets, ((size_t)experts + 1) * 4)};
-    if (r > 0) {
-      ins.push_back(span_of(A, (size_t)experts * (size_t)r * (size_t)K * 2));
-      ins.push_back(span_of(B, (size_t)w->rows * (size_t)r * 2));
-    }
-    for (const Span& in : ins)
-      if (overlaps(out, in)) return fail(QLR_ERR_ALIAS, "y overlaps an input");
+    size_t wb[3];
+    if ((st = qlr_qweight_sizes(w->rows, K, w->bits, w->block, &wb[0], &wb[1], &wb[2])) != QLR_OK) return st;
+    if (overlaps_any(span_of(y, (size_t)(T * N) * dtype_size(ydt)),
+                     {span_of(x, (size_t)(T * K) * 2), span_of(offsets, ((size_t)experts + 1) * 4), span_of(w->codes, wb[0]),
+                      span_of(w->absmax_q8, wb[1]), span_of(w->absmax_c, wb[2]),
+                      span_of(A, (size_t)experts * (size_t)r * (size_t)K * 2), span_of(B, (size_t)w->rows * (size_t)r * 2)}))
+      return fail(QLR_ERR_ALIAS, "y overlaps an input");
   }
   const GroupedLayout lay = grouped_layout(false, T, w->rows, K, experts, r);
   if (lay.total > 0 && (!ws || ws_bytes < lay.total))
@@ -1252,23 +1275,19 @@ qlr_status qlr_linear_bwd_grouped(const void* dy, qlr_dtype dydt, const void* x,
       return fail(QLR_ERR_ALIGN, "dy, x and dx must be 16-byte aligned");
   }
   {
-    std::vector<Span> outs, ins = {span_of(offsets, ((size_t)experts + 1) * 4)};
+    size_t wb[3];
+    if ((st = qlr_qweight_sizes(w->rows, K, w->bits, w->block, &wb[0], &wb[1], &wb[2])) != QLR_OK) return st;
     const size_t ab = (size_t)experts * (size_t)r * (size_t)K, bb = (size_t)w->rows * (size_t)r;
-    if (T > 0 && dx) outs.push_back(span_of(dx, (size_t)(T * K) * dtype_size(dxdt)));
-    if (r > 0) {
-      outs.push_back(span_of(dA, ab * 4));
-      outs.push_back(span_of(dB, bb * 4));
-      ins.push_back(span_of(A, ab * 2));
-      ins.push_back(span_of(B, bb * 2));
-      if (T > 0) ins.push_back(span_of(x, (size_t)(T * K) * 2));
-    }
-    if (T > 0) ins.push_back(span_of(dy, (size_t)(T * N) * 2));
-    for (size_t i = 0; i < outs.size(); ++i) {
-      for (size_t j = i + 1; j < outs.size(); ++j)
-        if (overlaps(outs[i], outs[j])) return fail(QLR_ERR_ALIAS, "two outputs overlap");
-      for (const Span& in : ins)
-        if (overlaps(outs[i], in)) return fail(QLR_ERR_ALIAS, "an output overlaps an input");
-    }
+    const Span none = {0, 0};
+    const Span outs[3] = {dx ? span_of(dx, (size_t)(T * K) * dtype_size(dxdt)) : none, r > 0 ? span_of(dA, ab * 4) : none,
+                          r > 0 ? span_of(dB, bb * 4) : none};
+    if (overlaps(outs[0], outs[1]) || overlaps(outs[0], outs[2]) || overlaps(outs[1], outs[2]))
+      return fail(QLR_ERR_ALIAS, "two outputs overlap");
+    for (const Span& out : outs)
+      if (overlaps_any(out, {span_of(dy, (size_t)(T * N) * 2), r > 0 ? span_of(x, (size_t)(T * K) * 2) : none,
+                             span_of(offsets, ((size_t)experts + 1) * 4), span_of(w->codes, wb[0]),
+                             span_of(w->absmax_q8, wb[1]), span_of(w->absmax_c, wb[2]), span_of(A, ab * 2), span_of(B, bb * 2)}))
+        return fail(QLR_ERR_ALIAS, "an output overlaps an input");
   }
   const GroupedLayout lay = grouped_layout(true, T, w->rows, K, experts, r);
   if (lay.total > 0 && (!ws || ws_bytes < lay.total))

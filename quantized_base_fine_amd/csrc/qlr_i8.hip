@@ -150,8 +150,8 @@ __global__ __launch_bounds__(kLtWaves * 64) void k_i8_prep(const uint16_t* __res
 // TB/s, the bound of larger calls).
 template <int DT>
 hipError_t launch_quantize_dt(const void* X, int64_t rows, int64_t cols, int8_t* q, float* scale, hipStream_t s) {
-  for (int64_t r0 = 0; r0 < rows; r0 += 1 << 30) {  // the grid's x dimension holds 2^31 - 1 workgroups
-    const dim3 n((unsigned)std::min<int64_t>(rows - r0, 1 << 30));
+  for (int64_t r0 = 0; r0 < rows; r0 += 1 << 23) {  // (a launch holds fewer than 2^32 threads)
+    const dim3 n((unsigned)std::min<int64_t>(rows - r0, 1 << 23));
     const char* x0 = reinterpret_cast<const char*>(X) + r0 * cols * (DT == DT_F32 ? 4 : 2);
     int8_t* q0 = q + r0 * cols;
     if (cols % 8 != 0) hipLaunchKernelGGL((k_quantize_i8<DT, false, 1, 256>), n, dim3(256), 0, s, x0, cols, q0, scale + r0);

@@ -71,6 +71,17 @@ def test_quantize_agrees_with_torch_on_the_gpu():
     assert torch.equal(q.q.double(), torch.round(x.double() / s.double()[:, None]).clamp(-127, 127))
 
 
+def test_quantize_more_rows_than_one_launch_holds():
+    x = torch.randn((2 ** 23 + 5, 16), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)).to(torch.bfloat16)
+    q = qlr.quantize_i8(x)
+    torch.cuda.synchronize()
+    for a, b in ((0, 300), (2 ** 23 - 100, 2 ** 23 + 5)):
+        rq, rs = ref_rows(x[a:b].cpu())
+        assert np.array_equal(q.scale[a:b].cpu().numpy(), rs)
+        assert np.array_equal(q.q[a:b].cpu().numpy().astype(np.float64), rq)
+    assert torch.equal(q.scale, x.float().abs().amax(1) / 127)
+
+
 def test_quantize_extreme_rows():
     x = torch.zeros((8, 72), dtype=torch.float32)
     x[1, 5] = float("nan")

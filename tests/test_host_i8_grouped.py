@@ -28,6 +28,8 @@ def test_quantize_refusals():
     assert quant(rows=-1) == "ERR_SHAPE" and quant(cols=0) == "ERR_SHAPE" and quant(out=(5, 64, P["xq"], P["xs"])) == "ERR_SHAPE"
     assert quant(X=P["x"] + 8) == "ERR_ALIGN" and quant(out=(4, 64, P["xq"] + 1, P["xs"])) == "ERR_ALIGN"
     assert quant(X=None, rows=0, out=(0, 64, None, None)) == "OK"
+    assert quant(out=(4, 64, P["x"], P["xs"])) == "ERR_ALIAS" and quant(out=(4, 64, P["xq"], P["x"] + 1008)) == "ERR_ALIAS"
+    assert quant(out=(4, 64, P["xq"], P["xq"] + 240)) == "ERR_ALIAS"
 
 
 def i8(x=P["x"], xdt=BF, M=4, xq=None, w=(32, 64, P["w"], P["s"]), A=P["A"], B=P["B"], abdt=BF, r=4, y=P["y"], ydt=BF,
@@ -55,6 +57,11 @@ def test_linear_i8_refusals():
     with qlr.path(qlr.PATH_GEMV):
         assert i8(M=17) == "ERR_PATH"
     assert i8(M=0, x=None, y=None) == "OK"
+    assert i8(M=(1 << 27) + 1) == "ERR_SHAPE" and i8(r=(1 << 20) + 1) == "ERR_SHAPE"
+    for n in ("x", "w", "s", "A", "B"):
+        assert i8(y=P[n]) == "ERR_ALIAS", n
+    for n in ("xq", "xs"):
+        assert i8(xq=(4, 64, P["xq"], P["xs"]), y=P[n]) == "ERR_ALIAS", n
 
 
 def grouped(x=P["x"], xdt=BF, T=4, w=None, E=2, off=P["off"], A=P["A"], B=P["B"], abdt=BF, r=4, y=P["y"], ydt=BF,
@@ -88,8 +95,9 @@ def test_grouped_refusals(call):
 
 def test_forward_only_refusals():
     assert grouped(y=None) == "ERR_NULL" and grouped(ydt=F16) == "ERR_DTYPE" and grouped(y=P["y"] + 2) == "ERR_ALIGN"
-    for n in ("x", "A", "B", "off"):
+    for n in ("x", "A", "B", "off", "w", "s", "xs"):  # (w, s, xs: the weight's codes, absmax codes and constants)
         assert grouped(y=P[n]) == "ERR_ALIAS", n
+    assert grouped(T=(1 << 27) + 1) == "ERR_SHAPE"
     assert grouped(T=0, x=None, y=None) == "OK"
 
 
@@ -98,7 +106,8 @@ def test_backward_only_refusals():
     assert bwd(rows=2 * 12) == "ERR_SHAPE"  # 12 rows of an expert
     assert bwd(dydt=F32) == "ERR_DTYPE" and bwd(dxdt=F16) == "ERR_DTYPE"
     assert bwd(dx=P["dx"] + 2) == "ERR_ALIGN" and bwd(dA=P["dA"] + 4) == "ERR_ALIGN"
-    for o, i in (("dx", "dy"), ("dx", "x"), ("dA", "A"), ("dB", "B"), ("dB", "off"), ("dA", "x")):
+    for o, i in (("dx", "dy"), ("dx", "x"), ("dA", "A"), ("dB", "B"), ("dB", "off"), ("dA", "x"), ("dx", "w"), ("dA", "s"),
+                 ("dB", "xs")):
         assert bwd(**{o: P[i]}) == "ERR_ALIAS", (o, i)
     assert bwd(dA=P["dB"]) == "ERR_ALIAS" and bwd(dx=P["dA"]) == "ERR_ALIAS"
 
