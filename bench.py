@@ -147,9 +147,9 @@ TRAFFIC_KERNELS = {
     "decode": ("k_gemv<4, 2, true, false, 2, true, false, 0, false, false>",
                [_CSRC + f for f in ("qlr_gemv.hip", "qlr_lut.h", "qlr_device.h", "qlr_internal.h")]),
     "prefill": ("k_gemm<4, 2, false, false, false>",
-                [_CSRC + f for f in ("qlr_gemm.hip", "qlr_lut.h", "qlr_device.h", "qlr_internal.h")]),
+                [_CSRC + f for f in ("qlr_gemm.hip", "qlr_dequant.h", "qlr_lut.h", "qlr_device.h", "qlr_internal.h")]),
     "backward": ("k_gemm<4, 2, false, true, false>",
-                 [_CSRC + f for f in ("qlr_gemm.hip", "qlr_lut.h", "qlr_device.h", "qlr_internal.h")]),
+                 [_CSRC + f for f in ("qlr_gemm.hip", "qlr_dequant.h", "qlr_lut.h", "qlr_device.h", "qlr_internal.h")]),
 }
 COPY_BYTES = 256 << 20  # the calibration copy reads and writes this many bytes
 
