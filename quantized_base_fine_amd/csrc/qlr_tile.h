@@ -909,6 +909,10 @@ hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
 // round of them to fill the 256 CUs and ranges of a few hundred rows to be
 // full: at 8192 x 4096 x 4096 in 8 ranges with 4-bit codes (all tiles written from registers then) they took 359 us, 128 x
 // 128 ones 434 and 64 x 128 ones 629; at 777 rows in 64 ranges of 1408 x 2048 (2-bit) 55, 27 and 23 us.
+// Between 256 x 256 and 128 x 128 tiles of expert ranges the estimated times decide, in rounds of the former: a rest of at most
+// kRestMax takes half a round, 512 of the latter (two to a CU) 0.79.  3000 rows in 8 ranges of 4096 x 4096: 129
+// us and 168 (the rule 1.0 and 1.33), 5000 in 16 of 2816 x 2048 105 and 114 (1.5 and 1.6), 4096 in 16 of 2816 x 2048 116
+// and 111 (1.5 and 1.36).
 template <int KIND, int BITS>
 hipError_t launch_tile(TileArgs a, const Levels& lv, hipStream_t s) {
   const int64_t no = KIND == TILE_TR ? a.K : a.N;
@@ -918,13 +922,15 @@ hipError_t launch_tile(TileArgs a, const Levels& lv, hipStream_t s) {
     return a.offsets ? (a.M / b + (std::min<int64_t>(a.experts, a.M) + 1) / 2) * nt : (a.M + b - 1) / b * nt;
   };
   const bool short_ranges = a.offsets && a.M < (int64_t)a.experts * 96;
-  if (!short_ranges && count(256, 256) >= (a.offsets ? 320 : 192)) {  // (an even split has fewer tiles than the estimate)
+  const int64_t n256 = count(256, 256), over = n256 % kCus;
+  const double t256 = (double)(n256 / kCus) + (over == 0 ? 0.0 : n256 > kCus && over <= kRestMax ? 0.5 : 1.0);
+  const double t128 = 0.79 / 512 * (double)count(128, 128);
+  if (!short_ranges && (a.offsets ? t256 < t128 : n256 >= 192)) {
     a.rest = 1;
     const hipError_t e = launch_tile_t<KIND, BITS, 256, 256>(a, lv, s);
     if (e != hipSuccess) return e;
     // the rest kernel: known not to be needed only without offsets
-    const int64_t total = a.offsets ? INT_MAX : count(256, 256);
-    if (!a.offsets && tile_split((int)total) == (int)total) return hipSuccess;
+    if (!a.offsets && tile_split((int)n256) == (int)n256) return hipSuccess;
     return launch_tile_t<KIND, BITS, 128, 128>(a, lv, s);
   }
   a.rest = 0;
