@@ -176,6 +176,13 @@ def test_wide_adapters_and_half_filled_tiles(r):
     check_forward(L)
 
 
+@pytest.mark.parametrize("counts", [[350] * 8, [350] * 7 + [600], [250] * 8 + [750]], ids=["16", "17", "11"])
+@pytest.mark.parametrize("bits", [3, 4])
+def test_about_one_round_of_large_tiles(bits, counts):
+    """Input gradient: 16 column tiles of 256 and 16, 17 and 11 row tiles, so a whole round, one and 16 tiles, part of one."""
+    check_backward(Layer(counts, 64, 4096, bits, 16, seed=sum(counts) + bits, pad=1))
+
+
 def test_no_rows():
     L = Layer([0, 0], 24, 128, 4, 8, seed=1)
     assert qlr.linear_grouped(L.xd, L.qw, L.offsets, L.Ad, L.Bd, 1.0).shape == (0, 24)
