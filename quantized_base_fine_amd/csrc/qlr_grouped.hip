@@ -358,11 +358,12 @@ __global__ __launch_bounds__(64 * W) void k_grouped_t(TJobs J) {
   constexpr uint32_t kSlice = 16 * RT * kTRowB + (kA > kB ? kA : kB), kSum = RT * 16 * JT * 16 * 4;
   __shared__ __attribute__((aligned(16))) char lds[W * (kSlice > kSum ? kSlice : kSum)];
   int e = 0, row0 = 0, row_end = 0;
-  const int total = tile_scan(J.offsets, J.experts, (int)J.M, 0, 16 * RT, -1, e, row0, row_end);
+  ScanChunk c0;
+  const int total = tile_count(J.offsets, J.experts, (int)J.M, 0, 16 * RT, c0);
   // each XCD a contiguous range of row tiles (the grid's rows are a multiple of 8): an expert's adapter in few L2s
   const int per = (total + 7) / 8, loc = (int)(blockIdx.x >> 3), tile = (int)(blockIdx.x & 7) * per + loc;
   if (loc >= per || tile >= total) return;  // the whole workgroup
-  tile_scan(J.offsets, J.experts, (int)J.M, 0, 16 * RT, tile, e, row0, row_end);
+  tile_find(J.offsets, J.experts, (int)J.M, 0, 16 * RT, c0, tile, e, row0, row_end);
   e = __builtin_amdgcn_readfirstlane(e);
   row0 = __builtin_amdgcn_readfirstlane(row0);
   row_end = __builtin_amdgcn_readfirstlane(row_end);

@@ -88,56 +88,68 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// Tiles of BM rows over the ranges holding more than min_rows rows: with
-// `want` < 0 returns the tile count, else finds tile `want` (expert and its
-// first and end row).  Called by whole waves.
-__device__ __forceinline__ int tile_scan(const int32_t* offsets, int E, int M, int min_rows, int BM, int want,
-                                         int& e_out, int& row0, int& row_end) {
+// 64 ranges of a scan, one to a lane: first and end row, tiles of BM rows (0 of a range of at most min_rows rows), and the
+// tiles up to it.
+struct ScanChunk { int a, b, nt, inc; };
+__device__ __forceinline__ ScanChunk scan_chunk(const int32_t* offsets, int E, int M, int min_rows, int BM, int e) {
+  ScanChunk c{0, 0, 0, 0};
+  if (e < E) {
+    if (offsets) expert_range(offsets, e, M, c.a, c.b);
+    else c.b = M;
+  }
+  c.nt = c.b - c.a > min_rows ? (c.b - c.a + BM - 1) / BM : 0;
+  c.inc = wave_scan(c.nt);
+  return c;
+}
+
+// Tiles of BM rows over the ranges holding more than min_rows rows: tile_count
+// returns their number and the first chunk of the scan, tile_find the expert of tile `want` and its
+// first and end row (as they are given if there is none).  Called by whole waves.
+__device__ __forceinline__ int tile_count(const int32_t* offsets, int E, int M, int min_rows, int BM, ScanChunk& c0) {
+  const int lane = threadIdx.x & 63;
+  c0 = scan_chunk(offsets, E, M, min_rows, BM, lane);
+  int total = __builtin_amdgcn_readlane(c0.inc, 63);
+  for (int e0 = 64; e0 < E; e0 += 64)
+    total += __builtin_amdgcn_readlane(scan_chunk(offsets, E, M, min_rows, BM, e0 + lane).inc, 63);
+  return total;
+}
+__device__ __forceinline__ void tile_find(const int32_t* offsets, int E, int M, int min_rows, int BM, const ScanChunk& c0,
+                                          int want, int& e_out, int& row0, int& row_end) {
   const int lane = threadIdx.x & 63;
   int before = 0;
+  ScanChunk c = c0;
   for (int e0 = 0; e0 < E; e0 += 64) {
-    int a = 0, b = 0;
-    if (e0 + lane < E) expert_range(offsets, e0 + lane, M, a, b);
-    const int nt = b - a > min_rows ? (b - a + BM - 1) / BM : 0;
-    const int inc = wave_scan(nt);
-    const int last = __builtin_amdgcn_readlane(inc, 63);
-    if (want >= 0 && want < before + last) {
-      const uint64_t hit = __ballot(before + inc > want);
+    if (e0 > 0) c = scan_chunk(offsets, E, M, min_rows, BM, e0 + lane);
+    const int last = __builtin_amdgcn_readlane(c.inc, 63);
+    if (want < before + last) {
+      const uint64_t hit = __ballot(before + c.inc > want);
       const int src = __ffsll((unsigned long long)hit) - 1;  // the first expert whose tiles reach past `want`
-      const int t0 = before + __builtin_amdgcn_readlane(inc - nt, src);
       e_out = e0 + src;
-      row0 = __builtin_amdgcn_readlane(a, src) + (want - t0) * BM;
-      row_end = __builtin_amdgcn_readlane(b, src);
-      return 0;
+      row0 = __builtin_amdgcn_readlane(c.a, src) + (want - before - __builtin_amdgcn_readlane(c.inc - c.nt, src)) * BM;
+      row_end = __builtin_amdgcn_readlane(c.b, src);
+      return;
     }
     before += last;
   }
-  return before;
 }
 
 // A workgroup's part of the rest: the 128 x 128 quarters of the 256 x 256 tiles split .. total - 1
 // that hold a row and a column, counted through (workgroups that find nothing to do must come last: among the
 // others they would leave some CUs two workgroups and others none, 80 us instead of 64 for a 4096 x 4096 backward of 8
 // ragged ranges).  ntiles: column tiles of 256; ncols: of 128; half: kRestRows words of LDS for each wave.  Returns the
-// tile, or -1.  Called by whole waves.
+// tile, or -1.  c: the first chunk of the scan of tiles of 256 rows.  Called by whole waves.
 constexpr int kRestRows = kRestMax + kGroupM;  // at most that many row tiles have tiles in the rest
-__device__ __forceinline__ int rest_tile(const int32_t* offsets, int E, int M, int min_rows, int split, int total,
+__device__ __forceinline__ int rest_tile(const int32_t* offsets, int E, int M, int min_rows, ScanChunk c, int split, int total,
                                          int ntiles, int ncols, uint32_t* half, int& row_half, int& col_half) {
   const int lane = threadIdx.x & 63;
   const int lo = split / (kGroupM * ntiles) * kGroupM, mt_total = total / ntiles;
   for (int i = lane; i < kRestRows; i += 64) half[i] = 2;
   int before = 0;
   for (int e0 = 0; e0 < E; e0 += 64) {
-    int a = 0, b = 0;
-    if (e0 + lane < E) {
-      if (offsets) expert_range(offsets, e0 + lane, M, a, b);
-      else b = M;
-    }
-    const int nt = b - a > min_rows ? (b - a + 255) / 256 : 0;
-    const int inc = wave_scan(nt);
-    const int at = before + inc - 1 - lo;  // the range's last row tile
-    if (nt > 0 && b - a - (nt - 1) * 256 <= 128 && at >= 0 && at < kRestRows) half[at] = 1;
-    before += __builtin_amdgcn_readlane(inc, 63);
+    if (e0 > 0) c = scan_chunk(offsets, E, M, min_rows, 256, e0 + lane);
+    const int at = before + c.inc - 1 - lo;  // the range's last row tile
+    if (c.nt > 0 && c.b - c.a - (c.nt - 1) * 256 <= 128 && at >= 0 && at < kRestRows) half[at] = 1;
+    before += __builtin_amdgcn_readlane(c.inc, 63);
   }
   __builtin_amdgcn_wave_barrier();
   // quarters of a lane's tiles, the tile's row and column halves
@@ -238,14 +250,15 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     constexpr int kBig = 256;
     const bool sub = BM == 128 && P.rest;  // the 128 x 128 kernel on the rest of the 256 x 256 tiles
     const int step_m = sub ? kBig : BM, ntiles = sub ? (P.ntiles + kBig / BN - 1) / (kBig / BN) : P.ntiles;
-    const int mt_total = P.offsets ? tile_scan(P.offsets, P.experts, (int)P.M, P.min_rows, step_m, -1, e, row0, row_end)
-                                   : (int)((P.M + step_m - 1) / step_m);
+    const int ranges = P.offsets ? P.experts : 1;
+    ScanChunk c0;
+    const int mt_total = tile_count(P.offsets, ranges, (int)P.M, P.min_rows, step_m, c0);
     const int total = mt_total * ntiles;
     const int split = P.rest ? tile_split(total) : total;
     int big, row_half = 0, col_half = 0;
     if (sub) {
       // (its words lie in a buffer that no wave writes before the first barrier, which every wave reaches after reading them)
-      big = rest_tile(P.offsets, P.offsets ? P.experts : 1, (int)P.M, P.min_rows, split, total, ntiles, P.ntiles,
+      big = rest_tile(P.offsets, ranges, (int)P.M, P.min_rows, c0, split, total, ntiles, P.ntiles,
                       reinterpret_cast<uint32_t*>(sW1) + wave * kRestRows, row_half, col_half);
       if (big < 0) return;  // (as below)
     } else {
@@ -258,12 +271,8 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     const int gm = min(kGroupM, mt_total - grp * kGroupM);
     const int mi = grp * kGroupM + in % gm;
     tile_n = in / gm;
-    if (P.offsets) {
-      row_end = 0;
-      tile_scan(P.offsets, P.experts, (int)P.M, P.min_rows, step_m, mi, e, row0, row_end);
-    } else {
-      row0 = mi * step_m;
-    }
+    row_end = 0;
+    tile_find(P.offsets, ranges, (int)P.M, P.min_rows, step_m, c0, mi, e, row0, row_end);
     if (sub) {
       row0 += row_half * BM;
       tile_n = tile_n * (kBig / BN) + col_half;
