@@ -266,6 +266,16 @@ def test_calls_on_two_streams():
             close(dB, rB, SB, 1e-4, 1e-6, "dB")
 
 
+def test_many_long_experts():
+    """More experts than a wave has lanes, on large tiles and their rest: 70 ranges of 1 to 520 rows, 8 column tiles."""
+    counts = [1 + (97 * i * i + 31 * i) % 520 for i in range(70)]
+    assert sum(counts) >= 96 * 70
+    L = Layer(counts, 2048, 64, 4, 8, seed=11, pad=2, lead=3)
+    check_forward(L)
+    L = Layer(counts, 64, 2048, 4, 8, seed=12)
+    check_backward(L)
+
+
 def test_many_experts():
     rng = np.random.RandomState(3)
     counts = rng.randint(0, 4, size=150)
