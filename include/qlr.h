@@ -515,6 +515,9 @@ qlr_status qlr_grouped_workspace_bytes(qlr_op op, int64_t T, int64_t rows, int64
  * 1 <= experts <= QLR_MAX_EXPERTS, T <= 2^27, T may be 0.  Error bound per
  * element as QLR_PATH_GEMM of qlr_linear_fwd: 5e-3 * S + 1e-5 (the weight enters
  * rounded to bf16; sums are float32), plus half a bf16 ulp for a bf16 y.
+ * Infinities and NaN in a live row or an adapter give what the formula gives
+ * (intermediate results beyond float32's range overflow), in that row only or
+ * where that adapter enters.
  * qlr_force_path: QLR_PATH_GEMM runs every expert on the tiled kernel (by
  * default experts of few rows run on a kernel of their own); the others are
  * refused.  ws (device) >= qlr_grouped_workspace_bytes(QLR_OP_LINEAR_GROUPED, ...).

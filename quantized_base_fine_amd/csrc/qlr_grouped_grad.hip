@@ -10,7 +10,7 @@ namespace {
 // Both are out[j][c] = s sum_m P[m][j] Q[m][c] with (P, Q, C) = (u, x, K) and
 // (t, dy, N), computed as out^T[c][j] on 16x16x32 bf16 MFMA: Q^T as the A
 // operand and P^T as B, both read from row-major LDS tiles with the transpose
-// read.  P enters as three bf16 parts (hi, mid, lo: 24 significant bits), so the
+// read.  P enters as three bf16 parts (hi, mid, lo: 24 significant bits, see split_rest), so the
 // products are those of float32 P; the extra products are cheap beside the reads
 // of Q, which bound the kernel.
 //
@@ -145,13 +145,14 @@ __global__ __launch_bounds__(256) void k_grouped_grad(GroupGrads G) {
       uint32_t part[3][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const float p0 = s.p[i][2 * t], p1 = s.p[i][2 * t + 1];
-        const uint32_t h0 = f32_to_bf16_bits(p0), h1 = f32_to_bf16_bits(p1);
-        const float r0 = p0 - bf16_bits_to_f32(h0), r1 = p1 - bf16_bits_to_f32(h1);
-        const uint32_t m0 = f32_to_bf16_bits(r0), m1 = f32_to_bf16_bits(r1);
-        part[0][t] = h0 | (h1 << 16);
-        part[1][t] = m0 | (m1 << 16);
-        part[2][t] = pack_bf16x2(r0 - bf16_bits_to_f32(m0), r1 - bf16_bits_to_f32(m1));
+        float v0 = s.p[i][2 * t], v1 = s.p[i][2 * t + 1];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {  // (the third part is the whole rest: at most 8 bits)
+          const float r0 = k < 2 ? split_rest(v0) : 0.0f, r1 = k < 2 ? split_rest(v1) : 0.0f;
+          part[k][t] = (__float_as_uint(v0) >> 16) | (__float_as_uint(v1) & 0xFFFF0000u);
+          v0 = r0;
+          v1 = r1;
+        }
       }
 #pragma unroll
       for (int k = 0; k < 3; ++k)

@@ -31,7 +31,7 @@
 //
 // Adapter.  t = x A_e^T (float32 partial sums) enters after the last step as
 // blocks of 32 adapter columns: the x side holds [hi(s t) | lo(s t)] (two bf16
-// halves, about 16 significant bits of s t), the weight side [B | B].
+// parts, about 16 significant bits of s t, see split_rest), the weight side [B | B].
 //
 // Ranges.  Expert e's rows are [offsets[e], offsets[e + 1]); every offset is
 // clamped into [0, M] and to its predecessor, so no offset can lead out of
@@ -201,6 +201,20 @@ struct TileLds {
   static_assert(BM != 128 || kW >= 8 * kRestRows * 4, "rest_tile's words overlay a buffer");
   static_assert(kXBufs * kX + kWBufs * kW + kTabBytes <= 160 * 1024, "LDS budget");
 };
+
+// v as a sum of bf16 parts for products on bf16 MFMA: v becomes the next part (its low 16 bits zero), the result the rest
+// (v's other significant bits, 16 of float32's 24).  The parts have v's sign and none but a zero's is zero, so that their
+// products add up to v's own with an infinity on either side too: Inf B = Inf B + Inf B and v Inf = hi Inf + lo Inf.  (The
+// nearest part would leave a rest of either sign or none, whose products with an infinity, and an infinite v's rest
+// Inf - Inf, are NaN; and it rounds the largest values to infinity.)  A v of 8 significant bits is halved.  The rest
+// is that of the rounded v: contracted with a product that formed v, it could have the other sign.
+__device__ __forceinline__ float split_rest(float& v) {
+#pragma clang fp contract(off)
+  const float half = 0.5f * v, hi = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u), rest = v - hi;
+  const bool whole = !(fabsf(rest) > 0.0f);  // or v is infinite or NaN
+  v = whole ? half : hi;
+  return whole ? half : rest;
+}
 
 __device__ __forceinline__ f32x16_t tile_mfma(u32x4_t a, u32x4_t b, f32x16_t c) {
   return mfma32x32x16(as_bf16x8(a), as_bf16x8(b), c);
@@ -703,10 +717,10 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
         u32x4_t hv, lo;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float u0 = P.scale * tv[2 * i], u1 = P.scale * tv[2 * i + 1];
-          const uint32_t h0 = f32_to_bf16_bits(u0), h1 = f32_to_bf16_bits(u1);
-          hv[i] = h0 | (h1 << 16);
-          lo[i] = pack_bf16x2(u0 - bf16_bits_to_f32(h0), u1 - bf16_bits_to_f32(h1));
+          float u0 = P.scale * tv[2 * i], u1 = P.scale * tv[2 * i + 1];
+          const float l0 = split_rest(u0), l1 = split_rest(u1);
+          hv[i] = (__float_as_uint(u0) >> 16) | (__float_as_uint(u1) & 0xFFFF0000u);
+          lo[i] = pack_bf16x2(l0, l1);
         }
         const uint32_t xrow = (uint32_t)row * 128u;
         st16(sX0 + xrow + ((((uint32_t)c) ^ swz((uint32_t)row & 15u)) << 4), hv);
