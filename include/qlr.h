@@ -471,7 +471,7 @@ qlr_status qlr_quantize_i8(const void* X, qlr_dtype dt, int64_t rows, int64_t co
  * be NULL (and xdt is ignored) when xq is given and r == 0.  A, B bf16 as in
  * qlr_linear_fwd (abdt must be QLR_BF16 when r > 0); y (device) M x N in ydt
  * (f32 or bf16).  K % 16 == 0 and K <= 131072 (the integer sums stay below
- * 2^31); M <= 2^27, M may be 0.  Integer sums are exact; each
+ * 2^31); N <= 2^30, M <= 2^27, M may be 0; M N and M K at most 2^40.  Integer sums are exact; each
  * result takes three float32 roundings (within 2e-7 of it, plus half a bf16
  * ulp for a bf16 y; intermediate results beyond float32's range overflow),
  * and the adapter term 1e-4 of the sum of its terms' absolute values.
@@ -512,7 +512,8 @@ qlr_status qlr_grouped_workspace_bytes(qlr_op op, int64_t T, int64_t rows, int64
  * nothing outside the buffers is touched, the rows concerned get wrong values.)
  * x (device) T x cols bf16; A (device) experts x r x cols and B (device) experts
  * x N x r bf16, both NULL when r == 0; y (device) T x N in ydt (f32 or bf16).
- * 1 <= experts <= QLR_MAX_EXPERTS, T <= 2^27, T may be 0.  Error bound per
+ * 1 <= experts <= QLR_MAX_EXPERTS, N <= 2^20, cols <= 2^20, T <= 2^27, T may
+ * be 0; T N and T cols at most 2^40.  Error bound per
  * element as QLR_PATH_GEMM of qlr_linear_fwd: 5e-3 * S + 1e-5 (the weight enters
  * rounded to bf16; sums are float32), plus half a bf16 ulp for a bf16 y.
  * Infinities and NaN in a live row or an adapter give what the formula gives

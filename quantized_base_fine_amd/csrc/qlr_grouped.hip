@@ -396,10 +396,11 @@ hipError_t launch_t_jobs(const TJobs& J, int jobs, hipStream_t s) {
 // Bt[e][j][n] = B[e][n][j]
 __global__ __launch_bounds__(256) void k_grouped_transpose(const uint16_t* __restrict__ B, int64_t N, int r,
                                                            uint16_t* __restrict__ Bt) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= N * r) return;
-  const int64_t j = i / N, n = i % N, base = (int64_t)blockIdx.y * N * r;
-  Bt[base + i] = B[base + n * r + j];
+  const int64_t base = (int64_t)blockIdx.y * N * r;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < N * r; i += (int64_t)gridDim.x * 256) {
+    const int64_t j = i / N, n = i % N;
+    Bt[base + i] = B[base + n * r + j];
+  }
 }
 
 }  // namespace
@@ -439,8 +440,8 @@ hipError_t launch_grouped_tu(const uint16_t* x, const uint16_t* dy, int64_t M, i
 }
 
 hipError_t launch_grouped_transpose(const uint16_t* B, int experts, int64_t N, int r, uint16_t* Bt, hipStream_t s) {
-  hipLaunchKernelGGL(k_grouped_transpose, dim3((unsigned)((N * r + 255) / 256), (unsigned)experts), dim3(256), 0, s, B, N,
-                     r, Bt);
+  hipLaunchKernelGGL(k_grouped_transpose, dim3((unsigned)std::min((N * r + 255) / 256, kLaunchBlocks), (unsigned)experts), dim3(256),
+                     0, s, B, N, r, Bt);
   return hipGetLastError();
 }
 

@@ -32,6 +32,7 @@ struct GroupGrads {
   int64_t C[2];
   int ct0, ct;  // column tiles of job 0 and of both
   int extra;    // slots of extra chunks in part
+  int block0;   // the launch's first workgroup among the call's
   int64_t M;
   int r, experts;
   const int32_t* offsets;
@@ -89,7 +90,7 @@ __global__ __launch_bounds__(256) void k_grouped_grad(GroupGrads G) {
   __shared__ __attribute__((aligned(16))) char lds[2 * kGBuf];
   const int M = (int)G.M, r = G.r;
   // workgroups: per expert (its first chunk), then per extra chunk, the column tiles of both jobs
-  const int by = (int)(blockIdx.x / G.ct), bx = (int)(blockIdx.x % G.ct);
+  const int block = G.block0 + (int)blockIdx.x, by = block / G.ct, bx = block % G.ct;
   int e = by, chunk = 0;
   if (e >= G.experts) {
     const int want = e - G.experts;
@@ -291,10 +292,12 @@ hipError_t launch_grouped_grads(const float* u, const float* t, const uint16_t* 
   G.extra = (int)extra;
   const int64_t wgs = (int64_t)G.ct * (experts + (int64_t)extra);
   if (wgs > INT_MAX) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)wgs, (unsigned)((r + 63) / 64));
-  if (r % 4 == 0) hipLaunchKernelGGL(k_grouped_grad<true>, grid, dim3(256), 0, s, G);
-  else hipLaunchKernelGGL(k_grouped_grad<false>, grid, dim3(256), 0, s, G);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = launch_blocks(wgs, [&](unsigned n, int b0) {
+    const dim3 grid(n, (unsigned)((r + 63) / 64));
+    G.block0 = b0;
+    if (r % 4 == 0) hipLaunchKernelGGL(k_grouped_grad<true>, grid, dim3(256), 0, s, G);
+    else hipLaunchKernelGGL(k_grouped_grad<false>, grid, dim3(256), 0, s, G);
+  });
   if (e != hipSuccess || extra == 0) return e;
   const int64_t n = (N + K) * r;
   hipLaunchKernelGGL(k_grouped_grad_add, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 256), (unsigned)experts),

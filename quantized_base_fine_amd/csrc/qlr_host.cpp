@@ -318,8 +318,9 @@ bool overlaps_any(const Span& p, std::initializer_list<Span> others) {
   return false;
 }
 
-// The largest T (M) of the grouped calls and of the 8-bit linear: launches of a few rows per workgroup stay below 2^32 threads.
-constexpr int64_t kMaxRows = INT64_C(1) << 27;
+// The largest T (M) of the grouped calls and of the 8-bit linear, and the most elements of their inputs and outputs: rows
+// and tiles are numbered in 32 bits.
+constexpr int64_t kMaxRows = INT64_C(1) << 27, kMaxElems = INT64_C(1) << 40;
 
 qlr_status check_i8rows(const qlr_i8rows* q, const char* what) {
   if (!q->q || !q->scale) return fail(QLR_ERR_NULL, "%s: a buffer is NULL", what);
@@ -342,6 +343,7 @@ qlr_status check_grouped(int64_t T, const qlr_qweight* w, int32_t experts, const
   if (w->cols % QLR_BLOCK != 0) return fail(QLR_ERR_SHAPE, "cols %lld is not a multiple of 64", (long long)w->cols);
   if (w->cols > (1 << 20) || w->rows / experts > (1 << 20))
     return fail(QLR_ERR_SHAPE, "an expert's weight is larger than 2^20 x 2^20");
+  if (T > kMaxElems / std::max(w->cols, w->rows / experts)) return fail(QLR_ERR_SHAPE, "x or y holds more than 2^40 elements");
   if (xdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "x (dy) must be bf16");
   if (r > 0 && abdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "the adapters must be bf16");
   if (!(odt == QLR_F32 || odt == QLR_BF16)) return fail(QLR_ERR_DTYPE, "y (dx) dtype must be f32 or bf16");
@@ -1109,6 +1111,7 @@ qlr_status qlr_linear_fwd_i8(const void* x, qlr_dtype xdt, int64_t M, const qlr_
   if (N > (INT64_C(1) << 30)) return fail(QLR_ERR_SHAPE, "rows %lld above 2^30", (long long)N);
   if (K % 16 != 0 || K > 131072)
     return fail(QLR_ERR_SHAPE, "cols %lld must be a multiple of 16 and at most 131072", (long long)K);
+  if (M > kMaxElems / std::max(N, K)) return fail(QLR_ERR_SHAPE, "x or y holds more than 2^40 elements");
   qlr_status st = check_i8rows(w, "w");
   if (st != QLR_OK) return st;
   const bool need_x = !xq || r > 0;

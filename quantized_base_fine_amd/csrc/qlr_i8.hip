@@ -180,12 +180,12 @@ hipError_t launch_quantize_dt(const void* X, int64_t rows, int64_t cols, int8_t*
 constexpr int kFewWaves = 8;
 
 template <int NB>
-__global__ __launch_bounds__(512) void k_i8_few(TileArgs P) {
+__global__ __launch_bounds__(512) void k_i8_few(TileArgs P, int block0) {
   typedef FewAdapter<16, 4096> Adapter;
   __shared__ __attribute__((aligned(16))) char ad_lds[Adapter::kBytes];
   __shared__ int red[kFewWaves][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = (block0 + (int)blockIdx.x) * 16;
   const int M = (int)P.M;
   const int64_t K = P.K, N = P.N;
   // weight: load 2 s + i of a step, rows n0 + 8 i + lane / 8, bytes 16 (lane % 8) of the step's 128
@@ -280,8 +280,8 @@ hipError_t launch_i8_prep(const void* x, int64_t M, int64_t K, int8_t* q, float*
 
 hipError_t launch_i8_few(const TileArgs& a, hipStream_t s) {
   if (a.M < 1 || a.M > kFewRows || a.K % 16 != 0) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_i8_few<1>), dim3((unsigned)((a.N + 15) / 16)), dim3(512), 0, s, a);
-  return hipGetLastError();
+  return launch_blocks((a.N + 15) / 16,
+                       [&](unsigned n, int b0) { hipLaunchKernelGGL((k_i8_few<1>), dim3(n), dim3(512), 0, s, a, b0); });
 }
 
 hipError_t launch_i8_gemm(const TileArgs& a, hipStream_t s) {

@@ -314,6 +314,16 @@ hipError_t launch_lora_t(const void* x, int xdt, int64_t M, int64_t K, const voi
                        K, reinterpret_cast<const uint16_t*>(A), r, t);
     return hipGetLastError();
   }
+  // (a launch holds fewer than 2^32 threads, 64 for each of the M r sums: parts of 2^25 of them)
+  const int64_t part = std::max<int64_t>(1, (int64_t(1) << 25) / r);
+  if (M > part) {
+    for (int64_t m = 0; m < M; m += part) {
+      const char* xm = reinterpret_cast<const char*>(x) + m * K * (xdt == DT_F32 ? 4 : 2);
+      const hipError_t e = launch_lora_t(xm, xdt, std::min(part, M - m), K, A, abdt, r, t + m * r, splits, s);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
   const int64_t items = M * r;
   dim3 grid((unsigned)((items + 3) / 4)), block(256);
   if (xdt == DT_F32 && abdt == DT_F32)
@@ -376,6 +386,23 @@ hipError_t launch_lora_t_group(const LoraTItem* items, int n, int64_t M, hipStre
   int64_t jt = 0;
   for (int i = 0; i < n; ++i)
     if (items[i].r > 0) jt += (items[i].r + 15) / 16;
+  // (a launch holds fewer than 2^32 threads: a product of more tiles in two halves)
+  if ((M + 15) / 16 * jt > (int64_t(1) << 22) && M > 64) {
+    const int64_t half = (M / 2 + 15) / 16 * 16;
+    LoraTItem part[kTGroupMax];
+    for (int h = 0; h < 2; ++h) {
+      for (int i = 0; i < n; ++i) {
+        part[i] = items[i];
+        if (h == 1) {
+          part[i].x = reinterpret_cast<const uint16_t*>(items[i].x) + half * items[i].K;
+          part[i].t = items[i].t + half * items[i].r;
+        }
+      }
+      const hipError_t e = launch_lora_t_group(part, n, h == 0 ? half : M - half, s);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
   // 8-row tiles when 16-row ones would give fewer workgroups than CUs
   G.mt = ((M + 15) / 16) * jt < 256 ? 8 : 16;
   int64_t t0 = 0;

@@ -234,8 +234,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void* p, uint3
                                            (int)__builtin_amdgcn_readfirstlane(n), 0x00020000);
 }
 
+// block0: the launch's first workgroup among the call's (a multiple of 8)
 template <int KIND, int BITS, int BM, int BN>
-__global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(TileArgs P, Levels lv) {
+__global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(TileArgs P, Levels lv, int block0) {
   using L = TileLds<KIND, BITS, BM, BN>;
   constexpr int WM = (BN == 256 || BM == 64) ? 2 : 4, WN = 8 / WM;
   constexpr int MT = BM / WM / 32, NT = BN / WN / 32;  // MFMA tiles of a wave
@@ -276,7 +277,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
                       reinterpret_cast<uint32_t*>(sW1) + wave * kRestRows, row_half, col_half);
       if (big < 0) return;  // (as below)
     } else {
-      const int per = (split + 7) / 8, loc = (int)(blockIdx.x >> 3);
+      const int per = (split + 7) / 8, loc = (block0 + (int)blockIdx.x) >> 3;
       big = (int)(blockIdx.x & 7) * per + loc;
       if (loc >= per || big >= split) return;  // the whole workgroup, before any barrier
     }
@@ -909,6 +910,19 @@ struct FewAdapter {
   }
 };
 
+// A launch of 2^32 threads or more runs the excess only, without an error: grids whose sizes allow that are launched in parts
+// of at most kLaunchBlocks workgroups (of up to 512 threads), launch(n, b0) workgroups b0 .. b0 + n - 1.
+constexpr int64_t kLaunchBlocks = 1 << 22;
+template <typename F>
+hipError_t launch_blocks(int64_t blocks, F launch) {
+  for (int64_t b0 = 0; b0 < blocks; b0 += kLaunchBlocks) {
+    launch((unsigned)std::min(kLaunchBlocks, blocks - b0), (int)b0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 // Upper bound of the row tiles of any `experts` ranges over M rows.
 inline int64_t tile_bound(int64_t M, int experts, int BM) { return M / BM + std::min<int64_t>(experts, M); }
 
@@ -923,8 +937,7 @@ hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
   if (a.rest && BM < 256) tiles = kRestMax * (256 / BM) * (256 / BN);
   if (tiles <= 0) return hipSuccess;
   if (tiles > INT32_MAX - 8) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(8 * ((tiles + 7) / 8))), dim3(512), 0, s, a, lv);
-  return hipGetLastError();
+  return launch_blocks(8 * ((tiles + 7) / 8), [&](unsigned n, int b0) { hipLaunchKernelGGL(kern, dim3(n), dim3(512), 0, s, a, lv, b0); });
 }
 
 // The tile shape, from the sizes the host knows (the rows of an expert only by their
