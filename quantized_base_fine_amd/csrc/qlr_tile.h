@@ -540,13 +540,20 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   __syncthreads();
   // The end of a step: every wave's share of the next one is in LDS.  Behind the loads that must have arrived there are those
   // of the kAhead - 1 steps after the next: XL (+ WL) direct loads each and, from the next step's on, at least three of codes,
-  // scale and constant (loads return in order).
+  // scale and constant (loads return in order).  That count holds while each step issues its loads within the step: keep
+  // stops the compiler from moving a memory access past it (the three loads come from three arrays, so they cannot be
+  // one), and tests/test_host_tile_waits.py counts the loads in the compiled loops.
+  auto keep = [] {
+    if constexpr (kAhead > 1) asm volatile("" ::: "memory");
+  };
   auto step_barrier = [&] {
     if constexpr (kAhead > 1) {
       constexpr int kOpen = (kAhead - 1) * (XL + (KIND == TILE_I8 ? WL : 0)) + (KIND == TILE_I8 ? 0 : 3 * kAhead);
       static_assert(kOpen < 16, "wait count");
+      keep();
       __builtin_amdgcn_s_waitcnt(0x0070 | kOpen);  // and no LDS access open
       __builtin_amdgcn_s_barrier();
+      keep();
     } else {
       __syncthreads();
     }
@@ -559,8 +566,10 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     __builtin_amdgcn_sched_barrier(0);
     read_frags(bx, bw, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
+    keep();
     direct(xr, ox, k + kAhead, xloads);
     if constexpr (KIND == TILE_I8) direct(wr, ow, k + kAhead, wloads);
+    keep();
     __builtin_amdgcn_sched_barrier(0);
     Lut4 lut{};
     float ap = 0.0f;
@@ -597,7 +606,9 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       }
       if constexpr (S == 1 && KIND != TILE_I8) {
         __builtin_amdgcn_sched_barrier(0);
+        keep();
         load_w(k + kSets, nxt);
+        keep();
       }
       __builtin_amdgcn_sched_barrier(0);
     };
