@@ -193,9 +193,18 @@ __global__ __launch_bounds__(512, 4) void k_grouped_few(TileArgs P, Levels lv) {
 template <int BITS, int RS>
 hipError_t launch_few_r(const TileArgs& a, const Levels& lv, hipStream_t s) {
   auto kern = k_grouped_few<BITS, RS>;
+  static bool checked = false;
+  hipError_t e;
+  if (!checked) {
+    // the level table is read at LDS addresses from 0: the kernel must not have static LDS
+    hipFuncAttributes fa;
+    e = hipFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern));
+    if (e != hipSuccess) return e;
+    if (fa.sharedSizeBytes != 0) return hipErrorInvalidKernelFile;
+    checked = true;
+  }
   const size_t shmem = FewTab<BITS>::kBytes + kFewWaves * kXSlice + (a.r > 0 ? FewAdapter<16 * RS, 1024>::kBytes : 0);
-  const hipError_t e =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)shmem);
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)shmem);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)((a.N + 16 * RS - 1) / (16 * RS)), (unsigned)a.experts), dim3(512), shmem, s, a, lv);
   return hipGetLastError();
