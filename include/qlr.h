@@ -161,7 +161,8 @@ typedef struct {
 
 /*
  * Rows held in 8-bit integers with one scale per row (tokens, or the output
- * channels of a weight): row i stands for scale[i] * q[i][:].
+ * channels of a weight): row i stands for scale[i] * q[i][:].  qlr_quantize_i8
+ * writes values within [-127, 127].
  */
 typedef struct {
   int64_t rows;
@@ -470,11 +471,13 @@ qlr_status qlr_quantize_i8(const void* X, qlr_dtype dt, int64_t rows, int64_t co
  * quantization and for the adapter, which multiplies the unquantized x; it may
  * be NULL (and xdt is ignored) when xq is given and r == 0.  A, B bf16 as in
  * qlr_linear_fwd (abdt must be QLR_BF16 when r > 0); y (device) M x N in ydt
- * (f32 or bf16).  K % 16 == 0 and K <= 131072 (the integer sums stay below
- * 2^31); N <= 2^30, M <= 2^27, M may be 0; M N and M K at most 2^40.  Integer sums are exact; each
- * result takes three float32 roundings (within 2e-7 of it, plus half a bf16
- * ulp for a bf16 y; intermediate results beyond float32's range overflow),
- * and the adapter term 1e-4 of the sum of its terms' absolute values.
+ * (f32 or bf16).  K % 16 == 0 and K <= 131072, which keeps the integer sums
+ * below 2^31 while xq or w holds no -128 (values a caller made: -128 in both
+ * is exact up to K = 131056); N <= 2^30, M <= 2^27, M may be 0; M N and M K at
+ * most 2^40.  Integer sums are exact; each result takes three float32 roundings
+ * (within 2e-7 of it, plus half a bf16 ulp for a bf16 y; intermediate results
+ * beyond float32's range overflow), and the adapter term 1e-4 of the sum of its
+ * terms' absolute values.
  * qlr_force_path: QLR_PATH_GEMV (M <= 16) and QLR_PATH_GEMM select the decode
  * and the tiled kernel (the same values without an adapter); QLR_PATH_F32 is refused.  ws
  * (device) >= qlr_workspace_bytes(QLR_OP_LINEAR_I8, M, N, K, r).

@@ -665,7 +665,9 @@ class _Launch:
 
 @dataclass
 class I8Rows:
-    """Rows in 8-bit integers: q (rows, cols) int8 and scale (rows,) float32, both on the GPU."""
+    """Rows in 8-bit integers: q (rows, cols) int8 and scale (rows,) float32, both on the GPU.
+    quantize_i8 writes values within [-127, 127]; products of two operands that both hold -128 (made
+    elsewhere) are exact up to 131056 columns."""
     rows: int
     cols: int
     q: "object"
