@@ -203,17 +203,16 @@ struct TileLds {
 };
 
 // v as a sum of bf16 parts for products on bf16 MFMA: v becomes the next part (its low 16 bits zero), the result the rest
-// (v's other significant bits, 16 of float32's 24).  The parts have v's sign and none but a zero's is zero, so that their
-// products add up to v's own with an infinity on either side too: Inf B = Inf B + Inf B and v Inf = hi Inf + lo Inf.  (The
-// nearest part would leave a rest of either sign or none, whose products with an infinity, and an infinite v's rest
-// Inf - Inf, are NaN; and it rounds the largest values to infinity.)  A v of 8 significant bits is halved.  The rest
-// is that of the rounded v: contracted with a product that formed v, it could have the other sign.
+// (16 of float32's 24 significant bits at most).  The part is the largest one below v in magnitude, so the parts have v's sign and
+// none but a zero's is zero: their products add up to v's own with an infinity on either side too (Inf B = hi B + Inf B, v Inf =
+// hi Inf + lo Inf).  The nearest part would leave a rest of either sign or none, whose products with an infinity, and an
+// infinite v's rest Inf - Inf, are NaN; and it rounds the largest values to infinity.  The rest is that of the rounded v, not
+// contracted with a product that formed v.
 __device__ __forceinline__ float split_rest(float& v) {
 #pragma clang fp contract(off)
-  const float half = 0.5f * v, hi = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u), rest = v - hi;
-  const bool whole = !(fabsf(rest) > 0.0f);  // or v is infinite or NaN
-  v = whole ? half : hi;
-  return whole ? half : rest;
+  const float hi = __uint_as_float((__float_as_uint(v) - (v != 0.0f ? 1u : 0u)) & 0xFFFF0000u), rest = v - hi;
+  v = hi;
+  return rest;
 }
 
 __device__ __forceinline__ f32x16_t tile_mfma(u32x4_t a, u32x4_t b, f32x16_t c) {
