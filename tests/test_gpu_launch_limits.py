@@ -10,6 +10,12 @@ from quantized_base_fine_amd import qlr  # noqa: E402
 BF, F32 = torch.bfloat16, torch.float32
 
 
+@pytest.fixture(autouse=True)
+def free_memory():
+    yield
+    torch.cuda.empty_cache()  # (tens of GB)
+
+
 def gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 

@@ -1,6 +1,6 @@
 """GPU tests of tile shapes and borders that the other tests of the 8-bit-integer and expert-grouped calls do not reach:
-128 x 128 tiles as a whole call, malformed offsets over long ranges, and the largest integer sums with -128.  Oracles and
-tolerances of test_gpu_grouped.py and test_gpu_i8.py."""
+128 x 128 tiles as a whole call, malformed offsets over long ranges, the largest integer sums with -128, the most experts, wide
+adapters and the longest rows.  Oracles and tolerances of test_gpu_grouped.py and test_gpu_i8.py."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -74,3 +74,32 @@ def test_malformed_offsets_over_long_ranges(bad, r):
     torch.cuda.synchronize()
     for buf, size, _ in bufs:
         assert (buf[:guard] == 0xA5).all() and (buf[guard + size:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("path", ["auto", "gemm"])
+def test_the_most_experts(path):
+    """4096 experts: most without rows, some of 1 to 5, one of 17 and one of 700 (two gradient chunks)."""
+    counts = [(i * i) % 7 % 6 if i % 9 == 0 else 0 for i in range(qlr.MAX_EXPERTS)]
+    counts[1000], counts[4095] = 17, 700
+    print(f"grouped, {len(counts)} experts, {sum(counts)} rows, {path}", flush=True)
+    L = Layer(counts, 8, 64, 4, 4, seed=17, pad=2)
+    check_forward(L, path)
+    check_backward(L)
+
+
+@pytest.mark.parametrize("r", [136, 257])
+def test_wide_ranks(r):
+    """More than two blocks of 64 adapter columns, and a rank that is no multiple of 8."""
+    print(f"grouped r={r}", flush=True)
+    L = Layer([9, 0, 16, 200, 530], 72, 192, 4, r, seed=r, pad=1)
+    check_forward(L)
+    check_backward(L)
+
+
+@pytest.mark.parametrize("K,N", [(1 << 20, 16), (64, 1 << 20)])
+def test_longest_rows(K, N):
+    """The longest rows of x and of dy (2^21 bytes): the few-rows kernel, the tiles and the gradients."""
+    print(f"grouped N={N} K={K}", flush=True)
+    L = Layer([12, 30], N, K, 4, 8, seed=23)
+    check_forward(L)
+    check_backward(L)
