@@ -57,7 +57,8 @@ typedef enum {
   QLR_ERR_ALIAS = 9,     /* an output overlaps an input or another output (where a call checks it) */
   QLR_ERR_HIP = 10,      /* a HIP runtime call or launch failed (text in qlr_last_error) */
   QLR_ERR_FORMAT = 11,   /* qlr_qweight.format_version unknown */
-  QLR_ERR_PATH = 12      /* forced path cannot run these arguments */
+  QLR_ERR_PATH = 12,     /* forced path cannot run these arguments */
+  QLR_ERR_VALUE = 13     /* a number or a choice is outside its range (dropout probability, activation) */
 } qlr_status;
 
 typedef enum { QLR_F32 = 0, QLR_F16 = 1, QLR_BF16 = 2 } qlr_dtype;
@@ -80,7 +81,11 @@ typedef enum {
   QLR_OP_LINEAR_WHA = 6, /* r is ignored */
   QLR_OP_LINEAR_I8 = 7,
   QLR_OP_LINEAR_GROUPED = 8,    /* these two: qlr_grouped_workspace_bytes */
-  QLR_OP_LINEAR_GROUPED_BWD = 9
+  QLR_OP_LINEAR_GROUPED_BWD = 9,
+  QLR_OP_LINEAR_DROPOUT = 10,
+  QLR_OP_LINEAR_DROPOUT_BWD = 11,
+  QLR_OP_GATED = 12,     /* these two: N = the output's columns (half the stacked weight's rows) */
+  QLR_OP_GATED_BWD = 13
 } qlr_op;
 
 /*
@@ -171,6 +176,31 @@ typedef struct {
   float* scale; /* device, rows */
 } qlr_i8rows;
 
+/*
+ * Dropout of an adapter's input by a mask that is never stored: the calls of one
+ * step form it anew from these numbers.  Element (m, k) of an M x K input (K % 8
+ * == 0) belongs to group g = (m K + k) / 8.  Philox4x32-10 (Salmon, Moraes, Dror,
+ * Shaw, SC 2011) of the counter words (g low, g high, c low, c high), each 32
+ * bits, under the key (seed low, seed high) gives four words, eight 16-bit numbers
+ * from the low half of the first on; the element is kept if number k % 8 is at
+ * least t = p 65536 rounded to the nearest integer (ties to even, at most 65535),
+ * and a kept one is multiplied by 65536 / (65536 - t).  c = counter + *step modulo
+ * 2^64.  A dropped element counts as 0 whatever it holds.  p = 0 drops nothing.
+ */
+typedef struct {
+  double p;             /* probability of dropping, 0 <= p < 1 */
+  uint64_t seed;
+  uint64_t counter;     /* a number of its own for every mask of a seed */
+  const uint64_t* step; /* device, 8-byte aligned, or NULL (0): read when the call runs, so that a captured call follows it */
+} qlr_dropout;
+
+/* Activation of the gated block: act(g) = g q(g). */
+typedef enum {
+  QLR_ACT_SILU = 0,     /* q = 1 / (1 + exp(-g)) */
+  QLR_ACT_GELU = 1,     /* q = Phi(g), the normal distribution function */
+  QLR_ACT_GELU_TANH = 2 /* q = (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+} qlr_act;
+
 /* Most experts of a grouped call. */
 #define QLR_MAX_EXPERTS 4096
 
@@ -211,7 +241,10 @@ qlr_status qlr_qweight_sizes(int64_t rows, int64_t cols, int32_t bits, int32_t b
  * QLR_OP_LINEAR_BWD (N = rows, K = cols of the weight): the partial sums of
  * x A^T and dy B, B transposed, and float32 partials of the adapter gradients
  * (0 bytes when r is 0).  QLR_OP_LINEAR_I8: the tokens as integers with their
- * scales, and t for M rows and rank r.  The grouped calls have a function of
+ * scales, and t for M rows and rank r.  QLR_OP_LINEAR_DROPOUT, QLR_OP_GATED: the
+ * adapters' products (0 bytes when M or r is 0); their backward ops also the
+ * partials of the adapter gradients, and QLR_OP_GATED_BWD the gradients of the
+ * pre-activations (M x 2N bf16).  The grouped calls have a function of
  * their own (qlr_grouped_workspace_bytes).  Contents need no initialisation.
  * Host only.
  */
@@ -554,6 +587,104 @@ qlr_status qlr_linear_bwd_grouped(const void* dy, qlr_dtype dydt, const void* x,
                                   const qlr_qweight* w, int32_t experts, const int32_t* offsets, const void* A,
                                   const void* B, qlr_dtype abdt, int32_t r, float scale, void* dx, qlr_dtype dxdt,
                                   float* dA, float* dB, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Forward with dropout on the adapter's input (fine-tuning of the adapter beside
+ * the frozen base): y = x W'^T + scale (drop(x) A^T) B^T.  x and the adapter bf16;
+ * drop may be NULL (nothing is dropped).  Arguments, kernel families and error
+ * bound otherwise as qlr_linear_fwd, with S extended by scale sum_j |B[n][j]|
+ * sum_k |drop(x)[m][k] A[j][k]|.  rows, cols and r at most 2^20, M <= 2^27, M N and
+ * M K at most 2^40.
+ * ws (device) >= qlr_workspace_bytes(QLR_OP_LINEAR_DROPOUT, M, rows, cols, r).
+ * Asynchronous, allocation-free; results do not depend on timing.
+ * Errors: as qlr_linear_fwd, plus QLR_ERR_VALUE (p) and QLR_ERR_ALIAS (y overlaps
+ * an input).
+ */
+qlr_status qlr_linear_fwd_dropout(const void* x, qlr_dtype xdt, int64_t M, const qlr_qweight* w, const void* A,
+                                  const void* B, qlr_dtype abdt, int32_t r, float scale, const qlr_dropout* drop,
+                                  void* y, qlr_dtype ydt, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward of qlr_linear_fwd_dropout for an upstream gradient dy (M x N bf16), with
+ * the mask of the same drop, q = 65536 / (65536 - t), u = dy B and t = drop(x) A^T:
+ *     dx = dy W' + scale q mask (u A)   (M x K, f32 or bf16; NULL: skipped)
+ *     dA = scale u^T drop(x)            (r x K float32)
+ *     dB = scale dy^T t                 (N x r float32)
+ * dA and dB are overwritten (zero when M == 0) and required when r > 0; x is not
+ * read when r == 0 and may be NULL.  rows % 8 == 0, cols % 64 == 0, both at most
+ * 2^20, M <= 2^27, M N and M K at most 2^40.  Per element dx is within 5e-3 * S + 1e-5
+ * (plus half a bf16 ulp for a bf16 dx; the weight enters rounded to bf16), dA and
+ * dB within 1e-4 * S + 1e-6 of the exact value, S the sum of the absolute values
+ * of the terms that define it.  Infinities and NaN give what the formula gives, in
+ * the results that they enter.  qlr_force_path: QLR_PATH_GEMM is the only family.
+ * ws (device) >= qlr_workspace_bytes(QLR_OP_LINEAR_DROPOUT_BWD, M, rows, cols, r).
+ * Asynchronous, allocation-free; results do not depend on timing.
+ * Errors: QLR_ERR_NULL, QLR_ERR_SHAPE, QLR_ERR_DTYPE, QLR_ERR_BITS, QLR_ERR_BLOCK,
+ * QLR_ERR_ALIGN, QLR_ERR_FORMAT, QLR_ERR_WORKSPACE, QLR_ERR_ALIAS, QLR_ERR_PATH,
+ * QLR_ERR_VALUE, QLR_ERR_HIP.
+ */
+qlr_status qlr_linear_bwd_dropout(const void* dy, qlr_dtype dydt, const void* x, qlr_dtype xdt, int64_t M,
+                                  const qlr_qweight* w, const void* A, const void* B, qlr_dtype abdt, int32_t r,
+                                  float scale, const qlr_dropout* drop, void* dx, qlr_dtype dxdt, float* dA, float* dB,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * First half of a gated feed-forward block on the quantized base: with the gate's
+ * and the up projection's weights Wg and Wu and an unmerged adapter on each,
+ *     g = x Wg'^T + scale (drop(x) Ag^T) Bg^T,   v = x Wu'^T + scale (drop'(x) Au^T) Bu^T,
+ *     h = act(g) v.
+ * w holds the two weights stacked by rows (quantized as one matrix: w->rows = 2 N,
+ * the first N the gate's; cols % 64 == 0).  x (device) M x cols bf16; A (device) 2 x
+ * r x cols and B (device) 2 x N x r bf16, the gate's first, both NULL when r == 0;
+ * h (device) M x N in hdt (f32 or bf16).  gu (device, M x 2N bf16, or NULL) gets g
+ * and v, [g | v] by row, rounded to bf16, for the backward; h is formed from the
+ * unrounded values.  drop (or NULL) with counter c gives the gate's adapter the mask of
+ * c and the up projection's the mask of c + 1, as two calls of qlr_linear_fwd_dropout
+ * with these counters have them.  N <= 2^19, cols <= 2^20, r <= 2^20, M <= 2^27, M may be
+ * 0; M N and M cols at most 2^39.  g and v are within 5e-3 * S + 1e-5 of the exact
+ * values (S the sum of the absolute values of the terms; the weight enters
+ * rounded to bf16, sums are float32), the activation within 1e-6 of itself and
+ * h one float32 rounding (plus half a bf16 ulp for a bf16 h) of their product.
+ * An infinity or NaN stays in its row, one in an adapter in that adapter's side of the
+ * columns that it enters; act of an infinity is what g q(g) gives (NaN where
+ * that is infinity times 0).
+ * qlr_force_path: QLR_PATH_GEMV (M <= 16) and QLR_PATH_GEMM select the decode and the
+ * tiled kernel, QLR_PATH_F32 is refused.  ws (device) >=
+ * qlr_workspace_bytes(QLR_OP_GATED, M, N, cols, r).  Asynchronous,
+ * allocation-free; results do not depend on timing.
+ * Errors: QLR_ERR_NULL, QLR_ERR_SHAPE, QLR_ERR_DTYPE, QLR_ERR_BITS, QLR_ERR_BLOCK,
+ * QLR_ERR_ALIGN, QLR_ERR_FORMAT, QLR_ERR_WORKSPACE, QLR_ERR_ALIAS (h and gu overlap
+ * each other or an input), QLR_ERR_PATH, QLR_ERR_VALUE, QLR_ERR_HIP.
+ */
+qlr_status qlr_gated_fwd(const void* x, qlr_dtype xdt, int64_t M, const qlr_qweight* w, qlr_act act, const void* A,
+                         const void* B, qlr_dtype abdt, int32_t r, float scale, const qlr_dropout* drop, void* h,
+                         qlr_dtype hdt, void* gu, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward of qlr_gated_fwd for an upstream gradient dh (M x N bf16) at the
+ * pre-activations gu = [g | v] (M x 2N bf16) that the forward left:
+ *     dg = dh v act'(g),   dv = dh act(g),
+ *     dx = dg Wg' + dv Wu' + scale (q mask (dg Bg) Ag + q mask' (dv Bu) Au)   (M x cols; NULL: skipped)
+ *     dA = scale ((dg Bg)^T drop(x), (dv Bu)^T drop'(x))                      (2 x r x cols float32)
+ *     dB = scale (dg^T (drop(x) Ag^T), dv^T (drop'(x) Au^T))                  (2 x N x r float32)
+ * In the products with the base dg and dv enter rounded to bf16 (a second bf16 part
+ * would double the matrix work), in those with the adapters in two bf16 parts.  dA and dB
+ * are overwritten (zero when M == 0) and required when r > 0; x is not read when
+ * r == 0 and may be NULL.  N % 8 == 0; sizes otherwise as the forward.  Per
+ * element dx is within 1e-2 * S + 1e-5 (plus half a bf16 ulp for a bf16 dx; the
+ * weight and dg, dv rounded to bf16), dA and dB within 1e-4 * S + 1e-6, S the sum
+ * of the absolute values of the terms that define it at the exact dg and dv of
+ * the given gu, |act| and |act'| counted as they are.  An infinity or NaN
+ * enters every result that its term enters (and where dg or dv passes bf16's largest
+ * value, dx is infinite).  qlr_force_path: QLR_PATH_GEMM is the only family.
+ * ws (device) >= qlr_workspace_bytes(QLR_OP_GATED_BWD, M, N, cols, r).
+ * Asynchronous, allocation-free; results do not depend on timing.  Errors: as the
+ * forward.
+ */
+qlr_status qlr_gated_bwd(const void* dh, qlr_dtype dhdt, const void* gu, const void* x, qlr_dtype xdt, int64_t M,
+                         const qlr_qweight* w, qlr_act act, const void* A, const void* B, qlr_dtype abdt, int32_t r,
+                         float scale, const qlr_dropout* drop, void* dx, qlr_dtype dxdt, float* dA, float* dB, void* ws,
+                         size_t ws_bytes, void* stream);
 
 /*
  * Force the kernel family used by qlr_linear_fwd, qlr_linear_fwd_mixed,

@@ -27,6 +27,9 @@ Pages (titles as printed):
   * "QWHA" (gist.science summary), section 2.1: the Walsh-Hadamard adapter
     (``wha``).
 
+Beside the pages: the dropout mask of an adapter's input (``dropout``, the generator of
+Salmon et al., SC 2011) and the gated feed-forward block (``gated``).
+
 Every function here is pinned by a ``-m "not gpu"`` test against something
 other than itself (closed forms, brute force over exact rationals, invariants,
 page arithmetic); no function is "parity unpinned".
@@ -37,6 +40,8 @@ from .quant import (widen, block_absmax, nearest_codes, pack_codes, unpack_codes
                     qweight_sizes, QuantizedWeight)
 from .linear import (lora_t, linear, linear_tolerance, linear_backward,
                      linear_backward_tolerance, adapter_grads, adapter_grads_tolerance)
+from .dropout import dropout_factors, dropout_threshold, philox4x32
+from .gated import gate, gated_backward, gated_forward
 from . import dba, outliers, wha
 
 __all__ = [
@@ -44,5 +49,6 @@ __all__ = [
     "pack_codes", "unpack_codes", "double_quantize", "dequantize_scales", "dequantize",
     "quantize", "qweight_sizes", "QuantizedWeight", "lora_t", "linear",
     "linear_tolerance", "linear_backward", "linear_backward_tolerance", "adapter_grads",
-    "adapter_grads_tolerance", "dba", "outliers", "wha",
+    "adapter_grads_tolerance", "dropout_factors", "dropout_threshold", "philox4x32",
+    "gate", "gated_backward", "gated_forward", "dba", "outliers", "wha",
 ]

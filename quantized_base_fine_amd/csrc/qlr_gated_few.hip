@@ -1,0 +1,218 @@
+// Gated block of up to 16 rows (decoding): bound by the stream of both projections' codes.
+#include "qlr_tile.h"
+
+namespace qlr {
+
+namespace {
+
+// As the few-rows kernel of the expert products: levels from a table in LDS (pairs of codes as bf16, 32 copies), the
+// block's scale on its products, a wave's rows of x through a slice of LDS of its own.  A level is held as one bf16 (half a
+// step, 2^-8 of it; the scale stays float32): two parts would double the lookups and products that bound the kernel beside the stream.
+// A workgroup of 8 waves takes 8 RS output columns: RS sets of 16 weight rows, 8 of the gate and the up rows of the same columns, the
+// 8 / RS waves of a set sharing K in ranges of 64-element blocks.  The waves' sums are added through LDS in wave order, then
+// each thread forms one output: both adapters' terms, the activation and the product.
+constexpr int kWaves = 8, kChunk = 2;
+constexpr uint32_t kXRow = 256 + 16, kXSlice = 16 * kXRow;  // a wave's slice: two blocks of 16 rows, padded
+constexpr uint32_t kRedBytes = kWaves * 16 * 16 * 4;        // the waves' sums, over the slices
+
+template <int BITS>
+struct FewTab {
+  static constexpr int kEntries = BITS == 8 ? 256 : 1 << (2 * BITS);
+  static constexpr uint32_t kBytes = kEntries * 128;
+};
+template <int BITS>
+constexpr int kWords = BITS == 8 ? 4 : BITS == 2 ? 1 : 2;  // words of a lane's 16 codes
+
+// bf16 levels of the lane's 16 codes, pairs in code order; tl = 4 (lane % 32).
+template <int BITS>
+__device__ __forceinline__ void few_levels(const uint32_t (&w)[kWords<BITS>], uint32_t tl, uint32_t (&o)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (BITS == 8) {
+      const uint32_t v = w[j >> 1] >> (16 * (j & 1));
+      o[j] = __builtin_amdgcn_perm(lds_word(((v >> 8) & 255u) << 7 | tl), lds_word((v & 255u) << 7 | tl), 0x05040100u);
+    } else if constexpr (BITS == 3) {
+      const int bit = 6 * j, wd = bit >> 5, sh = bit & 31;
+      const uint32_t v = sh + 6 > 32 ? __builtin_amdgcn_alignbit(w[wd < 1 ? wd + 1 : wd], w[wd], sh) : w[wd] >> sh;
+      o[j] = lds_word((v & 63u) << 7 | tl);
+    } else {
+      constexpr uint32_t mask = (1u << (2 * BITS)) - 1;
+      o[j] = lds_word(((w[(2 * BITS * j) >> 5] >> ((2 * BITS * j) & 31)) & mask) << 7 | tl);
+    }
+  }
+}
+
+// P.t: the gate's t_splits x M x r partial sums, then the up projection's.
+template <int BITS, int RS>
+__global__ __launch_bounds__(512, 4) void k_gated_few(TrainArgs P, Levels lv) {
+  constexpr int NR = 16 * RS, NO = NR / 2, KS = kWaves / RS, NW = kWords<BITS>;
+  typedef FewAdapter<NO, 2048> Adapter;
+  constexpr uint32_t kRed = FewTab<BITS>::kBytes;
+  static_assert(kRedBytes + 2 * Adapter::kBytes <= kWaves * kXSlice, "the adapters' operands overlay the slices");
+  extern __shared__ uint32_t smem[];
+  const int rows = (int)P.M;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t N = P.N, K = P.K, nb = K >> 6, n0 = (int64_t)blockIdx.x * NO;
+  const int rs = wave / KS, ks = wave % KS;
+  const int row = lane >> 2, g = lane & 3, src = (4 * (lane & 15) + (lane >> 4)) << 2;  // of the loads; the permute's source
+  const int frow = lane & 15, fg = lane >> 4;                                           // of the fragments
+  const int64_t b0 = nb * ks / KS, b1 = nb * (ks + 1) / KS;
+  const int64_t wblk = ((int64_t)(row >> 3) * N + min<int64_t>(n0 + 8 * rs + (row & 7), N - 1)) * nb;
+  // x loads: piece lane % 16 of rows lane / 16 + 4 i of the two blocks
+  const int xr = lane >> 4, xc = lane & 15;
+  const uint16_t* xp = reinterpret_cast<const uint16_t*>(P.x) + 8 * xc;
+  struct Ld {
+    uint32_t c[kChunk][NW];
+    uint32_t q8[kChunk];
+    float sc[kChunk];
+  };
+  const u32x4_t zero4 = {0u, 0u, 0u, 0u};
+  auto load = [&](int64_t bl, Ld& d) {  // (blocks past the wave's range repeat its last one and are not used)
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      const int64_t blk = wblk + max<int64_t>(min<int64_t>(bl + i, b1 - 1), 0);
+      Codes32<BITS> c = load_codes16<BITS>(P.w + blk * (8 * BITS), g);
+      place_codes16<BITS>(c, g);
+#pragma unroll
+      for (int j = 0; j < NW; ++j) d.c[i][j] = c.w[j];
+      d.q8[i] = P.q8[blk];
+      d.sc[i] = P.cst[blk >> 8];
+    }
+  };
+  u32x4_t xv[4];
+  auto load_x = [&](int64_t bl) {
+    const int64_t k = bl * 64;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * i < rows)  // (the same for the whole workgroup)
+        xv[i] = 4 * i + xr < rows && k + 8 * xc < K && bl < b1 ? *reinterpret_cast<const u32x4_t*>(xp + (int64_t)(4 * i + xr) * K + k)
+                                                               : zero4;
+  };
+  Ld d0, d1;
+  load(b0, d0);
+  load_x(b0);
+  Adapter ad[2];
+  const int live = (int)min<int64_t>(NO, N - n0);
+  const int64_t tside = (int64_t)P.t_splits * rows * P.r;
+#pragma unroll
+  for (int sd = 0; sd < 2; ++sd)
+    ad[sd].load(P.t + sd * tside, P.t_splits, P.M, 0, rows, P.ab + (int64_t)sd * N * P.r, n0, live, P.r);
+  // the level table, while the first loads are on their way
+  {
+    float* sL = reinterpret_cast<float*>(smem) + kRed / 4;
+    stage_levels<1 << BITS>(lv, sL);
+    __syncthreads();
+    constexpr int NL = 1 << BITS;
+    for (int i = tid; i < FewTab<BITS>::kEntries * 32; i += 512) {
+      const int en = i >> 5;
+      smem[i] = BITS == 8 ? f32_to_bf16_bits(sL[en]) : pack_bf16x2(sL[en & (NL - 1)], sL[en >> BITS]);
+    }
+    __syncthreads();
+  }
+  const uint32_t tl = 4u * (lane & 31);
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  char* const xs = reinterpret_cast<char*>(smem) + kRed + wave * kXSlice;
+  auto compute = [&](int64_t bl, const Ld& d) {
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      if (bl + i >= b1) return;  // (the same for the whole wave)
+      if (i % 2 == 0) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (4 * t < rows) *reinterpret_cast<u32x4_t*>(xs + (4 * t + xr) * kXRow + 16 * xc) = xv[t];
+        load_x(bl + i + 2);
+      }
+      uint32_t w[NW], o[8];
+#pragma unroll
+      for (int j = 0; j < NW; ++j) w[j] = (uint32_t)__builtin_amdgcn_ds_bpermute(src, (int)d.c[i][j]);
+      const float ap = __int_as_float(__builtin_amdgcn_ds_bpermute(src, __float_as_int((float)d.q8[i] * d.sc[i])));
+      few_levels<BITS>(w, tl, o);
+      const char* xf = xs + frow * kXRow + 128 * (i % 2) + 32 * fg;
+      // (rows past M hold anything: they only reach results that are dropped)
+      f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+      s = mfma16x16x32(as_bf16x8(*reinterpret_cast<const u32x4_t*>(xf)), as_bf16x8(u32x4_t{o[0], o[1], o[2], o[3]}), s);
+      s = mfma16x16x32(as_bf16x8(*reinterpret_cast<const u32x4_t*>(xf + 16)), as_bf16x8(u32x4_t{o[4], o[5], o[6], o[7]}), s);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[v] = fmaf(ap, s[v], acc[v]);
+    }
+  };
+  for (int64_t bl = b0; bl < b1; bl += 2 * kChunk) {
+    load(bl + kChunk, d1);
+    compute(bl, d0);
+    if (bl + kChunk >= b1) break;
+    load(bl + 2 * kChunk, d0);
+    compute(bl + kChunk, d1);
+  }
+  __syncthreads();  // (the sums and the adapters' operands overlay the waves' slices)
+  // [K range][token][weight row]: the lane's tokens 4 fg + v of weight row frow
+  float* red = reinterpret_cast<float*>(smem) + kRed / 4;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) red[(ks * 16 + 4 * fg + v) * NR + 16 * rs + frow] = acc[v];
+  char* const ad_lds = reinterpret_cast<char*>(smem) + kRed + kRedBytes;
+#pragma unroll
+  for (int sd = 0; sd < 2; ++sd) ad[sd].stage(ad_lds + sd * Adapter::kBytes, P.t_splits, rows, P.r);
+  __syncthreads();
+  if (tid >= rows * NO) return;  // (16 rows x 32 columns at most: one output a thread)
+  const int m = tid / NO, c = tid % NO;
+  const int64_t n = n0 + c;
+  if (n >= N) return;
+  float gv[2];
+#pragma unroll
+  for (int sd = 0; sd < 2; ++sd) {
+    float y = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) y += red[(k * 16 + m) * NR + 16 * (c >> 3) + 8 * sd + (c & 7)];
+    if (P.r > 0)
+      y = fmaf(P.scale, ad[sd].dot(ad_lds + sd * Adapter::kBytes, P.t + sd * tside, P.t_splits, P.M, 0, m,
+                                   P.ab + (int64_t)sd * N * P.r, n0, c, P.r), y);
+    gv[sd] = y;
+    if (P.gu) P.gu[(int64_t)m * 2 * N + sd * N + n] = (uint16_t)f32_to_bf16_bits(y);
+  }
+  const float a = P.act == ACT_SILU ? act_f<ACT_SILU>(gv[0]) : P.act == ACT_GELU ? act_f<ACT_GELU>(gv[0]) : act_f<ACT_GELU_TANH>(gv[0]);
+  const int64_t o = (int64_t)m * N + n;
+  if (P.ydt == DT_F32) reinterpret_cast<float*>(P.y)[o] = a * gv[1];
+  else reinterpret_cast<uint16_t*>(P.y)[o] = (uint16_t)f32_to_bf16_bits(a * gv[1]);
+}
+
+template <int BITS, int RS>
+hipError_t launch_few_r(const TrainArgs& a, const Levels& lv, hipStream_t s) {
+  auto kern = k_gated_few<BITS, RS>;
+  static bool checked = false;
+  hipError_t e;
+  if (!checked) {
+    // the level table is read at LDS addresses from 0: the kernel must not have static LDS
+    hipFuncAttributes fa;
+    e = hipFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern));
+    if (e != hipSuccess) return e;
+    if (fa.sharedSizeBytes != 0) return hipErrorInvalidKernelFile;
+    checked = true;
+  }
+  const size_t shmem = FewTab<BITS>::kBytes + kWaves * kXSlice;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)shmem);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)((a.N + 8 * RS - 1) / (8 * RS))), dim3(512), shmem, s, a, lv);
+  return hipGetLastError();
+}
+
+template <int BITS>
+hipError_t launch_few_b(const TrainArgs& a, const Levels& lv, hipStream_t s) {
+  // as many rows to a workgroup (one level table) as still gives 512 of them
+  const int64_t sets = (a.N + 7) / 8;
+  if (sets >= 4 * 512) return launch_few_r<BITS, 4>(a, lv, s);
+  if (sets >= 2 * 512) return launch_few_r<BITS, 2>(a, lv, s);
+  return launch_few_r<BITS, 1>(a, lv, s);
+}
+
+}  // namespace
+
+hipError_t launch_gated_few(const TrainArgs& a, const Levels& lv, hipStream_t s) {
+  if (a.M > kFewRows) return hipErrorInvalidValue;
+  switch (a.bits) {
+    case 2: return launch_few_b<2>(a, lv, s);
+    case 3: return launch_few_b<3>(a, lv, s);
+    case 4: return launch_few_b<4>(a, lv, s);
+    default: return launch_few_b<8>(a, lv, s);
+  }
+}
+
+}  // namespace qlr

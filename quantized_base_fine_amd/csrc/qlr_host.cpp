@@ -194,6 +194,43 @@ GroupedLayout grouped_layout(bool bwd, int64_t T, int64_t rows, int64_t K, int32
   return L;
 }
 
+// Workspace of the calls under adapter dropout and of the gated block: the adapters' products as float32 partial sums (as many
+// as the call may choose, with a mask or without), for the backward u beside t, the partials of the adapter
+// gradients, and the gated block's dgu.
+struct TrainLayout {
+  size_t t, u, dgu, part, total;
+  int t_splits, u_splits;  // of the masked product, and of the gated block's u
+};
+TrainLayout train_layout(qlr_op op, int64_t M, int64_t N, int64_t K, int32_t r) {
+  TrainLayout L{};
+  L.t_splits = L.u_splits = 1;
+  if (M <= 0) return L;
+  auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
+  const bool gated = op == QLR_OP_GATED || op == QLR_OP_GATED_BWD, bwd = op == QLR_OP_LINEAR_DROPOUT_BWD || op == QLR_OP_GATED_BWD;
+  const int two = gated ? 2 : 1;
+  const size_t row = (size_t)two * (size_t)r * sizeof(float);
+  size_t at = 0;
+  if (gated && bwd) L.u_splits = qlr::gated_u_splits(M, N, r);
+  if (r > 0) {
+    const int64_t kmin = op == QLR_OP_LINEAR_DROPOUT_BWD ? std::min(N, K) : K;
+    L.t_splits = qlr::train_t_splits(M, kmin, r, op == QLR_OP_LINEAR_DROPOUT ? 1 : 2);
+    size_t parts = (size_t)L.t_splits;
+    if (!bwd) parts = std::max(parts, (size_t)qlr::lora_t_splits(M, K, r, qlr::DT_BF16, qlr::DT_BF16));
+    at = L.t + up(parts * (size_t)M * row);
+    if (bwd) {
+      L.u = at;
+      if (!gated) L.u_splits = L.t_splits;
+      at = L.u + up((size_t)L.u_splits * (size_t)M * row);
+      L.part = at;
+      at = L.part + up(qlr::train_grad_floats(M, (int64_t)two * (N + K), r) * sizeof(float));
+    }
+  }
+  L.dgu = at;
+  if (op == QLR_OP_GATED_BWD) at = L.dgu + up((size_t)M * (size_t)(2 * N) * 2);
+  L.total = at;
+  return L;
+}
+
 // choose the kernel family for a linear call
 // The Walsh-Hadamard branch is merged into the weight on the prefill GEMM when
 // the bf16 copy fits the dense-weight GEMM's 32-bit offsets.
@@ -352,6 +389,87 @@ qlr_status check_grouped(int64_t T, const qlr_qweight* w, int32_t experts, const
   return QLR_OK;
 }
 
+// The dropout of a call as the kernels take it; *q: the factor of the kept values, which the call puts into its scale.
+qlr_status drop_args(const qlr_dropout* d, int32_t r, qlr::DropArgs* out, double* q) {
+  *out = qlr::DropArgs{0, 0, nullptr, 0};
+  *q = 1.0;
+  if (!d) return QLR_OK;
+  if (!(d->p >= 0.0 && d->p < 1.0)) return fail(QLR_ERR_VALUE, "dropout probability %g not in [0, 1)", d->p);
+  if ((reinterpret_cast<uintptr_t>(d->step) & 7u) != 0) return fail(QLR_ERR_ALIGN, "step must be 8-byte aligned");
+  const long long t = std::min<long long>(std::llrint(d->p * 65536.0), 65535);
+  if (t == 0 || r == 0) return QLR_OK;
+  *out = qlr::DropArgs{d->seed, d->counter, d->step, (uint32_t)t};
+  *q = 65536.0 / (double)(65536 - t);
+  return QLR_OK;
+}
+
+// The checks that the calls under adapter dropout and the gated block share: sides = 2 for the gated block's stacked weight.
+qlr_status check_train(int64_t M, const qlr_qweight* w, int sides, int32_t r, qlr_dtype xdt, qlr_dtype abdt, qlr_dtype odt) {
+  qlr_status st = check_qweight(w);
+  if (st != QLR_OK) return st;
+  if (M < 0 || M > kMaxRows) return fail(QLR_ERR_SHAPE, "M %lld not in [0, 2^27]", (long long)M);
+  if (r < 0 || r > (1 << 20)) return fail(QLR_ERR_SHAPE, "r %d not in [0, 2^20]", r);
+  if (w->rows == 0 || w->cols == 0) return fail(QLR_ERR_SHAPE, "empty weight");
+  if (w->rows % sides != 0) return fail(QLR_ERR_SHAPE, "the stacked weight's %lld rows are odd", (long long)w->rows);
+  if (w->cols % QLR_BLOCK != 0) return fail(QLR_ERR_SHAPE, "cols %lld is not a multiple of 64", (long long)w->cols);
+  if (w->cols > (1 << 20) || w->rows > (1 << 20)) return fail(QLR_ERR_SHAPE, "the weight is larger than 2^20 x 2^20");
+  if (M > kMaxElems / std::max(sides * w->cols, w->rows)) return fail(QLR_ERR_SHAPE, "x or y holds too many elements");
+  if (xdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "x (dy, dh) must be bf16");
+  if (r > 0 && abdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "the adapters must be bf16");
+  if (!(odt == QLR_F32 || odt == QLR_BF16)) return fail(QLR_ERR_DTYPE, "output dtype must be f32 or bf16");
+  return QLR_OK;
+}
+
+qlr_status check_adapters(const void* A, const void* B, int32_t r) {
+  if (r == 0) return QLR_OK;
+  if (!A || !B) return fail(QLR_ERR_NULL, "A or B is NULL with r > 0");
+  if (!aligned16(A) || !aligned16(B)) return fail(QLR_ERR_ALIGN, "A and B must be 16-byte aligned");
+  return QLR_OK;
+}
+
+qlr_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(QLR_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", need, ws ? ws_bytes : (size_t)0);
+  if (need > 0 && !aligned16(ws)) return fail(QLR_ERR_ALIGN, "workspace must be 16-byte aligned");
+  return QLR_OK;
+}
+
+qlr_status check_act(qlr_act act) {
+  if (act < QLR_ACT_SILU || act > QLR_ACT_GELU_TANH) return fail(QLR_ERR_VALUE, "unknown activation %d", (int)act);
+  return QLR_OK;
+}
+
+// No output may overlap another, the workspace or an input.
+qlr_status check_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* a = outs.begin(); a != outs.end(); ++a) {
+    for (const Span* b = a + 1; b != outs.end(); ++b)
+      if (overlaps(*a, *b)) return fail(QLR_ERR_ALIAS, "two outputs overlap");
+    if (overlaps_any(*a, ins)) return fail(QLR_ERR_ALIAS, "an output overlaps an input");
+  }
+  return QLR_OK;
+}
+
+Span step_span(const qlr_dropout* d) { return d && d->step ? span_of(d->step, 8) : Span{0, 0}; }
+
+// The weight's part of a tiled call's arguments.
+qlr::TrainArgs train_args(int64_t M, const qlr_qweight* w, int64_t N, int32_t r, float scale, const qlr::DropArgs& drop) {
+  qlr::TrainArgs a{};
+  a.M = M;
+  a.experts = 1;
+  a.N = N;
+  a.K = w->cols;
+  a.bits = w->bits;
+  a.w = reinterpret_cast<const uint8_t*>(w->codes);
+  a.q8 = w->absmax_q8;
+  a.cst = w->absmax_c;
+  a.t_splits = 1;
+  a.r = r;
+  a.scale = scale;
+  a.drop = drop;
+  a.halves = 1;
+  return a;
+}
+
 qlr::TileArgs grouped_args(int64_t T, const qlr_qweight* w, int32_t experts, const int32_t* offsets, int32_t r, float scale) {
   qlr::TileArgs a{};
   a.M = T;
@@ -463,6 +581,7 @@ const char* qlr_status_string(qlr_status s) {
     case QLR_ERR_HIP: return "HIP error";
     case QLR_ERR_FORMAT: return "unknown qweight format";
     case QLR_ERR_PATH: return "path cannot run these arguments";
+    case QLR_ERR_VALUE: return "value outside its range";
   }
   return "unknown status";
 }
@@ -527,6 +646,11 @@ qlr_status qlr_workspace_bytes(qlr_op op, int64_t M, int64_t N, int64_t K, int32
   if (op == QLR_OP_LINEAR_I8) {
     if (M < 0 || N < 0 || K < 0 || r < 0) return fail(QLR_ERR_SHAPE, "negative size");
     *bytes = i8_layout(M, K, r).total;
+    return QLR_OK;
+  }
+  if (op >= QLR_OP_LINEAR_DROPOUT && op <= QLR_OP_GATED_BWD) {
+    if (M < 0 || N < 0 || K < 0 || r < 0) return fail(QLR_ERR_SHAPE, "negative size");
+    *bytes = train_layout(op, M, N, K, r).total;
     return QLR_OK;
   }
   if (op != QLR_OP_LINEAR && op != QLR_OP_LINEAR_BWD) return fail(QLR_ERR_SHAPE, "unknown op %d", (int)op);
@@ -1334,6 +1458,266 @@ qlr_status qlr_linear_bwd_grouped(const void* dy, qlr_dtype dydt, const void* x,
   if (r > 0) {
     e = qlr::launch_grouped_grads(u, t, xp, dyp, T, N, K, r, offsets, experts, scale, dA, dB,
                                   reinterpret_cast<float*>(wsp + lay.part), s);
+    if (e != hipSuccess) return hip_fail(e, "adapter-gradient launch");
+  }
+  return QLR_OK;
+}
+
+qlr_status qlr_linear_fwd_dropout(const void* x, qlr_dtype xdt, int64_t M, const qlr_qweight* w, const void* A,
+                                  const void* B, qlr_dtype abdt, int32_t r, float scale, const qlr_dropout* drop,
+                                  void* y, qlr_dtype ydt, void* ws, size_t ws_bytes, void* stream) {
+  qlr_status st = check_train(M, w, 1, r, xdt, abdt, ydt);
+  if (st != QLR_OK) return st;
+  const LinearCheck c{x, xdt, M, w, A, B, abdt, r, y, ydt};
+  if ((st = check_linear(c)) != QLR_OK) return st;
+  qlr::DropArgs d;
+  double q;
+  if ((st = drop_args(drop, r, &d, &q)) != QLR_OK) return st;
+  const int64_t N = w->rows, K = w->cols;
+  size_t wb[3];
+  sizes_of(N, K, w->bits, &wb[0], &wb[1], &wb[2]);
+  const TrainLayout lay = train_layout(QLR_OP_LINEAR_DROPOUT, M, N, K, r);
+  if ((st = check_overlap({span_of(y, (size_t)(M * N) * dtype_size(ydt))},
+                          {span_of(x, (size_t)(M * K) * 2), span_of(w->codes, wb[0]), span_of(w->absmax_q8, wb[1]),
+                           span_of(w->absmax_c, wb[2]), span_of(A, (size_t)r * (size_t)K * 2),
+                           span_of(B, (size_t)N * (size_t)r * 2), step_span(drop), span_of(ws, ws ? lay.total : 0)})) != QLR_OK)
+    return st;
+  if ((st = check_ws(ws, ws_bytes, lay.total)) != QLR_OK) return st;
+  qlr_path path;
+  if ((st = pick_path(M, xdt, abdt, r, &path)) != QLR_OK) return st;
+  if (M == 0) return QLR_OK;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  char* wsp = reinterpret_cast<char*>(ws);
+  if (d.thr == 0) return run_linear(c, scale, wsp, path, s);
+  float* t = reinterpret_cast<float*>(wsp + lay.t);
+  const qlr::TrainProd job{reinterpret_cast<const uint16_t*>(x), reinterpret_cast<const uint16_t*>(A), K, t, r, r, 0, 0, false};
+  hipError_t e = qlr::launch_train_t(&job, 1, M, lay.t_splits, d, s);
+  if (e != hipSuccess) return hip_fail(e, "masked adapter product launch");
+  qlr::LinearArgs a = make_args(c, (float)((double)scale * q), wsp + lay.t, lay.t_splits);
+  a.A = nullptr;  // (the decode kernel would form x A^T itself)
+  const qlr::Levels lv = levels_arg(w->bits);
+  switch (path) {
+    case QLR_PATH_F32: e = qlr::launch_linear_f32(a, lv, s); break;
+    case QLR_PATH_GEMV: e = qlr::launch_gemv(a, lv, s); break;
+    default: e = qlr::launch_gemm(a, lv, s); break;
+  }
+  if (e != hipSuccess) return hip_fail(e, "linear launch");
+  return QLR_OK;
+}
+
+qlr_status qlr_linear_bwd_dropout(const void* dy, qlr_dtype dydt, const void* x, qlr_dtype xdt, int64_t M,
+                                  const qlr_qweight* w, const void* A, const void* B, qlr_dtype abdt, int32_t r,
+                                  float scale, const qlr_dropout* drop, void* dx, qlr_dtype dxdt, float* dA, float* dB,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  qlr_status st = check_train(M, w, 1, r, dydt, abdt, dx ? dxdt : QLR_F32);
+  if (st != QLR_OK) return st;
+  const int64_t N = w->rows, K = w->cols;
+  if (N % 8 != 0) return fail(QLR_ERR_SHAPE, "rows %lld is not a multiple of 8", (long long)N);
+  if (r > 0 && xdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "x must be bf16");
+  if ((st = check_adapters(A, B, r)) != QLR_OK) return st;
+  if (r > 0 && (!dA || !dB)) return fail(QLR_ERR_NULL, "dA or dB is NULL with r > 0");
+  if (r > 0 && (!aligned16(dA) || !aligned16(dB))) return fail(QLR_ERR_ALIGN, "dA and dB must be 16-byte aligned");
+  if (M > 0) {
+    if (!dy) return fail(QLR_ERR_NULL, "dy is NULL");
+    if (r > 0 && !x) return fail(QLR_ERR_NULL, "x is NULL with r > 0");
+    if (!aligned16(dy) || (dx && !aligned16(dx)) || (r > 0 && !aligned16(x)))
+      return fail(QLR_ERR_ALIGN, "dy, x and dx must be 16-byte aligned");
+  }
+  qlr::DropArgs d;
+  double q;
+  if ((st = drop_args(drop, r, &d, &q)) != QLR_OK) return st;
+  const TrainLayout lay = train_layout(QLR_OP_LINEAR_DROPOUT_BWD, M, N, K, r);
+  size_t wb[3];
+  sizes_of(N, K, w->bits, &wb[0], &wb[1], &wb[2]);
+  const Span none = {0, 0};
+  const size_t ab = (size_t)r * (size_t)K, bb = (size_t)N * (size_t)r;
+  if ((st = check_overlap({dx ? span_of(dx, (size_t)(M * K) * dtype_size(dxdt)) : none, span_of(dA, ab * 4), span_of(dB, bb * 4)},
+                          {span_of(dy, (size_t)(M * N) * 2), r > 0 ? span_of(x, (size_t)(M * K) * 2) : none,
+                           span_of(w->codes, wb[0]), span_of(w->absmax_q8, wb[1]), span_of(w->absmax_c, wb[2]),
+                           span_of(A, ab * 2), span_of(B, bb * 2), step_span(drop), span_of(ws, ws ? lay.total : 0)})) != QLR_OK)
+    return st;
+  if ((st = check_ws(ws, ws_bytes, lay.total)) != QLR_OK) return st;
+  if (t_path != QLR_PATH_AUTO && t_path != QLR_PATH_GEMM)
+    return fail(QLR_ERR_PATH, "the backward under dropout has no float32 or single-row family");
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  char* wsp = reinterpret_cast<char*>(ws);
+  float *t = reinterpret_cast<float*>(wsp + lay.t), *u = reinterpret_cast<float*>(wsp + lay.u);
+  const uint16_t *xp = reinterpret_cast<const uint16_t*>(x), *dyp = reinterpret_cast<const uint16_t*>(dy);
+  const float sq = (float)((double)scale * q);
+  hipError_t e;
+  if (r > 0 && M > 0) {
+    const qlr::TrainProd jobs[2] = {{xp, reinterpret_cast<const uint16_t*>(A), K, t, r, r, 0, 0, false},
+                                    {dyp, reinterpret_cast<const uint16_t*>(B), N, u, r, r, 0, -1, true}};
+    e = qlr::launch_train_t(jobs, 2, M, lay.t_splits, d, s);
+    if (e != hipSuccess) return hip_fail(e, "adapter products (x A^T, dy B) launch");
+  }
+  if (dx && M > 0) {
+    qlr::TrainArgs a = train_args(M, w, N, r, sq, d);
+    a.x = dy;
+    a.t = u;
+    a.t_splits = lay.t_splits;
+    a.ab = reinterpret_cast<const uint16_t*>(A);
+    a.y = dx;
+    a.ydt = (int)dxdt;
+    const qlr::Levels lv = levels_arg(w->bits);
+    e = d.thr > 0 ? qlr::launch_drop_dx(a, lv, s) : qlr::launch_grouped_dx(a, lv, s);
+    if (e != hipSuccess) return hip_fail(e, "input-gradient launch");
+  }
+  if (r > 0) {
+    const qlr::TrainGrad jobs[2] = {{u, lay.t_splits, r, 0, xp, K, dA, 0, 0, false}, {t, lay.t_splits, r, 0, dyp, N, dB, 0, -1, true}};
+    e = qlr::launch_train_grads(jobs, 2, M, r, nullptr, 0, 0, sq, d, reinterpret_cast<float*>(wsp + lay.part), s);
+    if (e != hipSuccess) return hip_fail(e, "adapter-gradient launch");
+  }
+  return QLR_OK;
+}
+
+qlr_status qlr_gated_fwd(const void* x, qlr_dtype xdt, int64_t M, const qlr_qweight* w, qlr_act act, const void* A,
+                         const void* B, qlr_dtype abdt, int32_t r, float scale, const qlr_dropout* drop, void* h,
+                         qlr_dtype hdt, void* gu, void* ws, size_t ws_bytes, void* stream) {
+  qlr_status st = check_train(M, w, 2, r, xdt, abdt, hdt);
+  if (st != QLR_OK) return st;
+  if ((st = check_act(act)) != QLR_OK) return st;
+  const int64_t N = w->rows / 2, K = w->cols;
+  if ((st = check_adapters(A, B, r)) != QLR_OK) return st;
+  if (M > 0) {
+    if (!x || !h) return fail(QLR_ERR_NULL, "x or h is NULL");
+    if (!aligned16(x) || !aligned16(h) || (gu && !aligned16(gu))) return fail(QLR_ERR_ALIGN, "x, h and gu must be 16-byte aligned");
+  }
+  qlr::DropArgs d;
+  double q;
+  if ((st = drop_args(drop, r, &d, &q)) != QLR_OK) return st;
+  const TrainLayout lay = train_layout(QLR_OP_GATED, M, N, K, r);
+  size_t wb[3];
+  sizes_of(w->rows, K, w->bits, &wb[0], &wb[1], &wb[2]);
+  const Span none = {0, 0};
+  if ((st = check_overlap({span_of(h, (size_t)(M * N) * dtype_size(hdt)), gu ? span_of(gu, (size_t)(M * N) * 4) : none},
+                          {span_of(x, (size_t)(M * K) * 2), span_of(w->codes, wb[0]), span_of(w->absmax_q8, wb[1]),
+                           span_of(w->absmax_c, wb[2]), span_of(A, (size_t)r * (size_t)K * 4),
+                           span_of(B, (size_t)w->rows * (size_t)r * 2), step_span(drop), span_of(ws, ws ? lay.total : 0)})) != QLR_OK)
+    return st;
+  if ((st = check_ws(ws, ws_bytes, lay.total)) != QLR_OK) return st;
+  qlr_path path = t_path;
+  if (path == QLR_PATH_AUTO) path = M <= qlr::kFewRows ? QLR_PATH_GEMV : QLR_PATH_GEMM;
+  if (path == QLR_PATH_F32) return fail(QLR_ERR_PATH, "the gated block has no float32 family");
+  if (path == QLR_PATH_GEMV && M > qlr::kFewRows) return fail(QLR_ERR_PATH, "the GEMV path takes M <= %d", qlr::kFewRows);
+  if (M == 0) return QLR_OK;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  float* t = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + lay.t);
+  const uint16_t *xp = reinterpret_cast<const uint16_t*>(x), *Ap = reinterpret_cast<const uint16_t*>(A);
+  const bool few = path == QLR_PATH_GEMV;
+  qlr::TrainArgs a = train_args(M, w, N, r, (float)((double)scale * q), d);
+  hipError_t e = hipSuccess;
+  if (r > 0) {
+    // the gate's and the up projection's products: side by side in rows of 2 r columns, for the decode kernel one after the other
+    if (d.thr > 0 || (!few && M <= 16)) {
+      a.t_splits = lay.t_splits;
+      const size_t side = (size_t)a.t_splits * (size_t)M * (size_t)r;
+      qlr::TrainProd jobs[2];
+      for (int i = 0; i < 2; ++i)
+        jobs[i] = qlr::TrainProd{xp, Ap + (int64_t)i * r * K, K, few ? t + i * side : t, r, few ? r : 2 * r, few ? 0 : i * r, i, false};
+      e = qlr::launch_train_t(jobs, 2, M, a.t_splits, d, s);
+    } else if (few) {
+      a.t_splits = qlr::lora_t_splits(M, K, r, qlr::DT_BF16, qlr::DT_BF16);
+      const size_t side = (size_t)a.t_splits * (size_t)M * (size_t)r;
+      const qlr::LoraTItem items[2] = {{xp, Ap, t, K, r, false}, {xp, Ap + (int64_t)r * K, t + side, K, r, false}};
+      e = qlr::launch_lora_t_small_group(items, 2, M, s);
+    } else {
+      e = qlr::launch_lora_t(x, qlr::DT_BF16, M, K, A, qlr::DT_BF16, 2 * r, t, 1, s);
+    }
+    if (e != hipSuccess) return hip_fail(e, "adapter products launch");
+  }
+  a.x = x;
+  a.t = t;
+  a.ab = reinterpret_cast<const uint16_t*>(B);
+  a.y = h;
+  a.ydt = (int)hdt;
+  a.act = (int)act;
+  a.gu = reinterpret_cast<uint16_t*>(gu);
+  const qlr::Levels lv = levels_arg(w->bits);
+  e = few ? qlr::launch_gated_few(a, lv, s) : qlr::launch_gated_gemm(a, lv, s);
+  if (e != hipSuccess) return hip_fail(e, "gated product launch");
+  return QLR_OK;
+}
+
+qlr_status qlr_gated_bwd(const void* dh, qlr_dtype dhdt, const void* gu, const void* x, qlr_dtype xdt, int64_t M,
+                         const qlr_qweight* w, qlr_act act, const void* A, const void* B, qlr_dtype abdt, int32_t r,
+                         float scale, const qlr_dropout* drop, void* dx, qlr_dtype dxdt, float* dA, float* dB, void* ws,
+                         size_t ws_bytes, void* stream) {
+  qlr_status st = check_train(M, w, 2, r, dhdt, abdt, dx ? dxdt : QLR_F32);
+  if (st != QLR_OK) return st;
+  if ((st = check_act(act)) != QLR_OK) return st;
+  const int64_t N = w->rows / 2, K = w->cols;
+  if (N % 8 != 0) return fail(QLR_ERR_SHAPE, "%lld columns of h are not a multiple of 8", (long long)N);
+  if (r > 0 && xdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "x must be bf16");
+  if ((st = check_adapters(A, B, r)) != QLR_OK) return st;
+  if (r > 0 && (!dA || !dB)) return fail(QLR_ERR_NULL, "dA or dB is NULL with r > 0");
+  if (r > 0 && (!aligned16(dA) || !aligned16(dB))) return fail(QLR_ERR_ALIGN, "dA and dB must be 16-byte aligned");
+  if (M > 0) {
+    if (!dh || !gu) return fail(QLR_ERR_NULL, "dh or gu is NULL");
+    if (r > 0 && !x) return fail(QLR_ERR_NULL, "x is NULL with r > 0");
+    if (!aligned16(dh) || !aligned16(gu) || (dx && !aligned16(dx)) || (r > 0 && !aligned16(x)))
+      return fail(QLR_ERR_ALIGN, "dh, gu, x and dx must be 16-byte aligned");
+  }
+  qlr::DropArgs d;
+  double q;
+  if ((st = drop_args(drop, r, &d, &q)) != QLR_OK) return st;
+  const TrainLayout lay = train_layout(QLR_OP_GATED_BWD, M, N, K, r);
+  size_t wb[3];
+  sizes_of(w->rows, K, w->bits, &wb[0], &wb[1], &wb[2]);
+  const Span none = {0, 0};
+  const size_t ab = 2 * (size_t)r * (size_t)K, bb = (size_t)w->rows * (size_t)r;
+  if ((st = check_overlap({dx ? span_of(dx, (size_t)(M * K) * dtype_size(dxdt)) : none, span_of(dA, ab * 4), span_of(dB, bb * 4)},
+                          {span_of(dh, (size_t)(M * N) * 2), span_of(gu, (size_t)(M * N) * 4),
+                           r > 0 ? span_of(x, (size_t)(M * K) * 2) : none, span_of(w->codes, wb[0]), span_of(w->absmax_q8, wb[1]),
+                           span_of(w->absmax_c, wb[2]), span_of(A, ab * 2), span_of(B, bb * 2), step_span(drop),
+                           span_of(ws, ws ? lay.total : 0)})) != QLR_OK)
+    return st;
+  if ((st = check_ws(ws, ws_bytes, lay.total)) != QLR_OK) return st;
+  if (t_path != QLR_PATH_AUTO && t_path != QLR_PATH_GEMM)
+    return fail(QLR_ERR_PATH, "the gated block's backward has no float32 or single-row family");
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  char* wsp = reinterpret_cast<char*>(ws);
+  float *t = reinterpret_cast<float*>(wsp + lay.t), *u = r > 0 ? reinterpret_cast<float*>(wsp + lay.u) : nullptr;
+  uint16_t* dgu = reinterpret_cast<uint16_t*>(wsp + lay.dgu);
+  const uint16_t *xp = reinterpret_cast<const uint16_t*>(x), *Ap = reinterpret_cast<const uint16_t*>(A);
+  const uint16_t *dhp = reinterpret_cast<const uint16_t*>(dh), *gup = reinterpret_cast<const uint16_t*>(gu);
+  const float sq = (float)((double)scale * q);
+  hipError_t e;
+  if (M > 0 && (dx || r > 0)) {
+    e = qlr::launch_gated_u(dhp, gup, (int)act, M, N, reinterpret_cast<const uint16_t*>(B), r, dgu, u, lay.u_splits, s);
+    if (e != hipSuccess) return hip_fail(e, "pre-activation gradient launch");
+  }
+  if (r > 0 && M > 0) {
+    qlr::TrainProd jobs[2];
+    for (int i = 0; i < 2; ++i) jobs[i] = qlr::TrainProd{xp, Ap + (int64_t)i * r * K, K, t, r, 2 * r, i * r, i, false};
+    e = qlr::launch_train_t(jobs, 2, M, lay.t_splits, d, s);
+    if (e != hipSuccess) return hip_fail(e, "adapter products launch");
+  }
+  if (dx && M > 0) {
+    qlr::TrainArgs a = train_args(M, w, 2 * N, r, sq, d);
+    a.x = dgu;
+    a.t = u;
+    a.t_splits = lay.u_splits;
+    a.ab = Ap;
+    a.y = dx;
+    a.ydt = (int)dxdt;
+    const qlr::Levels lv = levels_arg(w->bits);
+    if (d.thr > 0) {
+      a.halves = 2;
+      e = qlr::launch_drop_dx(a, lv, s);
+    } else {
+      a.r = 2 * r;  // the two adapters are one of 2 r columns
+      e = qlr::launch_grouped_dx(a, lv, s);
+    }
+    if (e != hipSuccess) return hip_fail(e, "input-gradient launch");
+  }
+  if (r > 0) {
+    const int64_t aside = (int64_t)r * K, bside = N * r;
+    const qlr::TrainGrad jobs[4] = {{u, lay.u_splits, 2 * r, 0, xp, K, dA, 0, 0, false},
+                                    {u, lay.u_splits, 2 * r, r, xp, K, dA + aside, 0, 1, false},
+                                    {t, lay.t_splits, 2 * r, 0, dhp, N, dB, 1, -1, true},
+                                    {t, lay.t_splits, 2 * r, r, dhp, N, dB + bside, 2, -1, true}};
+    e = qlr::launch_train_grads(jobs, 4, M, r, gup, N, (int)act, sq, d, reinterpret_cast<float*>(wsp + lay.part), s);
     if (e != hipSuccess) return hip_fail(e, "adapter-gradient launch");
   }
   return QLR_OK;

@@ -225,6 +225,21 @@ struct TileArgs {
   int min_rows;            // experts with at most this many rows are left out (the few-rows kernel takes them)
   int ntiles, rest;        // set by the launcher: column tiles; whether a last partial round is split finer
 };
+// Dropout of an adapter's input (see qlr_philox.h); thr = 0: none.
+struct DropArgs {
+  uint64_t seed, counter;
+  const uint64_t* step;  // device, added to counter when a kernel runs, or null
+  uint32_t thr;          // an element is kept iff its 16-bit number is at least thr
+};
+enum { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
+// The products of a training step and of the gated block.  Gated: N is one projection's rows, w the two stacked (gate, up),
+// t and u hold 2 r columns (gate's, up's), ab is B as 2 x N x r.
+struct TrainArgs : TileArgs {
+  DropArgs drop;
+  int halves;  // transposed with dropout: adapters side by side, each with r columns of t, rows of ab and a mask of its own
+  int act;
+  uint16_t* gu;  // gated: M x 2N bf16 pre-activations, or null
+};
 // Rows up to which the few-rows kernels take an expert, or a call of the 8-bit product.
 constexpr int kFewRows = 16;
 
@@ -252,6 +267,46 @@ hipError_t launch_grouped_tu(const uint16_t* x, const uint16_t* dy, int64_t M, i
                              hipStream_t s);
 // Bt (experts x r x N) = B^T per expert, B experts x N x r bf16.
 hipError_t launch_grouped_transpose(const uint16_t* B, int experts, int64_t N, int r, uint16_t* Bt, hipStream_t s);
+// ---- adapter dropout and the gated block (no offsets: one range of M rows)
+// h = act(gate) up, M x N (and gu): rows of x from 17 on, and up to kFewRows rows.
+hipError_t launch_gated_gemm(const TrainArgs& a, const Levels& lv, hipStream_t s);
+hipError_t launch_gated_few(const TrainArgs& a, const Levels& lv, hipStream_t s);
+// dx = dy W' + sum over the halves of mask (scale u A): K % 64 == 0, N % 8 == 0.
+hipError_t launch_drop_dx(const TrainArgs& a, const Levels& lv, hipStream_t s);
+
+// One product t = src A^T over K columns, as `splits` float32 partial sums of M x ldt floats each, columns col0 .. col0 + r - 1.
+struct TrainProd {
+  const uint16_t* x;   // M x K bf16
+  const uint16_t* A;   // r x K, or K x r (bt)
+  int64_t K;
+  float* t;
+  int r, ldt, col0;
+  int mask;            // >= 0: x under mask number `mask`
+  bool bt;
+};
+// Up to four products of one M, rank and number of partial sums, in one launch; K % 8 == 0.
+int train_t_splits(int64_t M, int64_t K, int r, int jobs);
+hipError_t launch_train_t(const TrainProd* jobs, int n, int64_t M, int splits, const DropArgs& drop, hipStream_t s);
+// The gated block's backward up to the products: from dh (M x N) and gu (M x 2N) dgu = [dg | dv] (M x 2N bf16, rounded to
+// nearest) and, where u is given, u (splits x M x 2r) = [dg Bg | dv Bu] from unrounded dg and dv.
+int gated_u_splits(int64_t M, int64_t N, int r);
+hipError_t launch_gated_u(const uint16_t* dh, const uint16_t* gu, int act, int64_t M, int64_t N, const uint16_t* B, int r,
+                          uint16_t* dgu, float* u, int splits, hipStream_t s);
+// Adapter gradients: out = scale P^T Q (r x C), or its transpose, for up to four jobs of one M and rank.
+struct TrainGrad {
+  const float* P;      // p_splits x M x ldp, columns col0 .. col0 + r - 1
+  int p_splits, ldp, col0;
+  const uint16_t* Q;   // M x C (kinds 1 and 2: dh, with gu)
+  int64_t C;
+  float* out;
+  int kind;            // 0: Q; 1, 2: dg, dv formed from dh and gu
+  int mask;            // >= 0: Q under mask number `mask` (kind 0)
+  bool cols_major;     // out is C x r
+};
+size_t train_grad_floats(int64_t M, int64_t C_total, int r);
+hipError_t launch_train_grads(const TrainGrad* jobs, int n, int64_t M, int r, const uint16_t* gu, int64_t N, int act, float scale,
+                              const DropArgs& drop, float* part, hipStream_t s);
+
 // dA (experts x r x K) = scale u^T x and dB (experts x N x r) = scale dy^T t, float32, zero for experts
 // without rows; K % 8 == 0 and N % 8 == 0.  part: grouped_grad_floats() floats of scratch.
 size_t grouped_grad_floats(int64_t M, int64_t N, int64_t K, int r, int experts);

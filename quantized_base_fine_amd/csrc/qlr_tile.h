@@ -5,6 +5,8 @@
 //   KIND TILE_I8    y = (sum_k xq wq) sx[m] sw[n]          (+ adapter)
 //   KIND TILE_CODED y[m] = x[m] W'_e^T, e the row's expert  (+ adapter)
 //   KIND TILE_TR    y[m] = x[m] W'_e (x = dy, y = dx)       (+ adapter)
+//   KIND TILE_GATED y[m] = act(x[m] Wg'^T) (x[m] Wu'^T)      (+ adapters; Wg and Wu stacked; one range)
+//   KIND TILE_TRD   as TILE_TR, the adapter's part under a dropout mask (one or two adapters; one range)
 //
 // Tiling.  A workgroup of 8 waves owns BM rows x BN columns (256 x 256 down to 64
 // x 128), divided among WM x WN waves in 32 x 32 MFMA tiles.  A step contracts 128 bytes of each row of x: 64 bf16 or 128
@@ -37,6 +39,12 @@
 // blocks of 32 adapter columns: the x side holds [hi(s t) | lo(s t)] (two bf16
 // parts, about 16 significant bits of s t, see split_rest), the weight side [B | B].
 //
+// Gated.  Of each 32 weight rows of a tile 16 are gate rows and 16 the up rows of the same columns, so that a lane's results
+// hold both sides of 8 outputs and the epilogue needs no exchange; a wave loads rows of one side only.
+//
+// Dropout.  dx = dy W' + s mask (u A): a block of 32 adapter columns is multiplied into sums of its own, which are added where the
+// mask keeps the element.  The mask's bits are formed once per tile and adapter (16 a lane and MFMA tile).
+//
 // Ranges.  Expert e's rows are [offsets[e], offsets[e + 1]); every offset is
 // clamped into [0, M] and to its predecessor, so no offset can lead out of
 // bounds.  Each workgroup finds its tile by a wave scan over the experts' tile
@@ -47,12 +55,14 @@
 #include <climits>
 #include <type_traits>
 
+#include "qlr_act.h"
 #include "qlr_dequant.h"
 #include "qlr_internal.h"
+#include "qlr_philox.h"
 
 namespace qlr {
 
-enum { TILE_I8 = 0, TILE_CODED = 1, TILE_TR = 2 };
+enum { TILE_I8 = 0, TILE_CODED = 1, TILE_TR = 2, TILE_GATED = 3, TILE_TRD = 4 };
 
 namespace {
 
@@ -239,9 +249,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void* p, uint3
 
 // block0: the launch's first workgroup among the call's (a multiple of 8); before the levels, whose kilobyte lies
 // in cache lines of its own (behind them, its load took 0.3 us of 333 x 5003 x 4096)
+template <int KIND>
+struct TileParams {
+  typedef typename std::conditional<(KIND >= TILE_GATED), TrainArgs, TileArgs>::type T;
+};
+
 template <int KIND, int BITS, int BM, int BN>
-__global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(TileArgs P, int block0, Levels lv) {
+__global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(typename TileParams<KIND>::T P, int block0, Levels lv) {
   using L = TileLds<KIND, BITS, BM, BN>;
+  constexpr bool kTR = KIND == TILE_TR || KIND == TILE_TRD;
+  constexpr int BO = KIND == TILE_GATED ? BN / 2 : BN;  // output columns
   constexpr int WM = (BN == 256 || BM == 64) ? 2 : 4, WN = 8 / WM;
   constexpr int MT = BM / WM / 32, NT = BN / WN / 32;  // MFMA tiles of a wave
   constexpr int XL = BM / 64;  // direct loads of x per wave and step
@@ -305,9 +322,9 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   }
   const int mrows = min(BM, row_end - row0);
   const int64_t N = P.N, K = P.K;
-  const int64_t NO = KIND == TILE_TR ? K : N;            // output columns
-  const int n0 = tile_n * BN;
-  const uint32_t kbytes = (uint32_t)(KIND == TILE_I8 ? K : KIND == TILE_TR ? 2 * N : 2 * K);  // bytes of one x row
+  const int64_t NO = kTR ? K : N;                        // output columns
+  const int n0 = tile_n * BO;
+  const uint32_t kbytes = (uint32_t)(KIND == TILE_I8 ? K : kTR ? 2 * N : 2 * K);  // bytes of one x row
   const int nsteps = (int)((kbytes + 127) / 128);
 
   if constexpr (L::kTabBytes > 0) {
@@ -359,6 +376,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   // ---- weight loads
   // I8: as x, the rows from n0 (rows past N zero).
   // CODED: thread = row tid / TPB, codes [CPT dh, + CPT) of the step's block (TPB threads share a block).
+  // GATED: as CODED; of the tile's rows the first half of the threads takes the gate's, the second the up's.
   // TR: thread = weight row 64 k + tid / 8, codes [CPT dh, + CPT) of block column n0 / 64 + bq.
   struct Ws {
     Codes32<BITS> c;
@@ -369,17 +387,20 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   const char* wbase = reinterpret_cast<const char*>(P.w) + (int64_t)n0 * K;
   const __amdgpu_buffer_rsrc_t wr = tile_rsrc(KIND == TILE_I8 ? wbase : nullptr, KIND == TILE_I8 ? (uint32_t)wrows * kbytes : 0u);
   constexpr int TPB = 64 / CPT;
-  const int rr = KIND == TILE_TR ? (tid >> 3) : tid / TPB, dh = tid % TPB, bq = KIND == TILE_TR ? (tid & 7) / TPB : 0;
+  const int wcol = KIND == TILE_GATED ? (tid / TPB) % BO : tid / TPB;  // the thread's weight row, from n0
+  const int side = KIND == TILE_GATED && wave >= 4 ? 1 : 0;
+  const int rr = kTR ? (tid >> 3) : KIND == TILE_GATED ? 32 * (wcol >> 4) + 16 * side + (wcol & 15) : wcol;  // its row in the tile
+  const int dh = tid % TPB, bq = kTR ? (tid & 7) / TPB : 0;
   // Addresses of a coded weight's blocks: a scalar part (the tile's first block and the step) plus a 32-bit part
   // per lane, fixed for all steps but TR's last, whose rows past N read row N - 1 with scale 0.
   const int64_t nbK = K >> 6;
-  const int64_t gb = KIND == TILE_TR ? (int64_t)e * N * nbK + (n0 >> 6) : ((int64_t)e * N + n0) * nbK;
+  const int64_t gb = kTR ? (int64_t)e * N * nbK + (n0 >> 6) : ((int64_t)(e + side) * N + n0) * nbK;
   bool wv = true, wv_last = true;
   uint32_t lb = 0, lb_last = 0;  // the lane's block, relative
-  if constexpr (KIND == TILE_CODED) {
-    wv = wv_last = n0 + rr < N;
-    lb = lb_last = (uint32_t)(min<int64_t>(rr, N - 1 - n0) * nbK);
-  } else if constexpr (KIND == TILE_TR) {
+  if constexpr (KIND == TILE_CODED || KIND == TILE_GATED) {
+    wv = wv_last = n0 + wcol < N;
+    lb = lb_last = (uint32_t)(min<int64_t>(wcol, N - 1 - n0) * nbK);
+  } else if constexpr (kTR) {
     wv = (n0 >> 6) + bq < nbK;
     const uint32_t col = (uint32_t)min<int64_t>(bq, nbK - 1 - (n0 >> 6));
     const int64_t nl = N - 64 * (int64_t)(nsteps - 1);  // rows of the last step
@@ -394,7 +415,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   uint32_t wst[WL];
 #pragma unroll
   for (int q = 0; q < WL; ++q) {
-    if constexpr (KIND == TILE_TR)
+    if constexpr (kTR)
       wst[q] = (uint32_t)(bq >> 1) * 16384u + (uint32_t)rr * 256u +
                (tr_chunk((uint32_t)(8 * (bq & 1) + WL * dh + q), (uint32_t)rr) << 4);
     else
@@ -406,7 +427,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     if constexpr (KIND != TILE_I8) {
       const int kk = min(k, nsteps - 1);
       const bool last = kk == nsteps - 1;  // (scalar)
-      const int64_t ks = KIND == TILE_TR ? 64 * (int64_t)kk * nbK : kk;  // the step's first block
+      const int64_t ks = kTR ? 64 * (int64_t)kk * nbK : kk;  // the step's first block
       const uint32_t l = last ? lb_last : lb;
       const uint8_t* const wk = wb8 + ks * (8 * BITS);
       if constexpr (CPT == 32) s.c = load_codes32<BITS>(wk + l * (uint32_t)(8 * BITS) + dh * (4 * BITS));
@@ -475,20 +496,22 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
     }
   }
   u32x4_t fx[2][MT], fw[2][NT];
+  auto frag_x = [&](const char* bx, int s, int i) { return ld16(bx + xb[s] + 4096u * i); };
+  auto frag_w = [&](char* bw, int s, int c) {
+    if constexpr (kTR) {
+      char* const ad = bw + tbo[c] + 4096u * s;
+      const u16x4_t lo = ld_tr(ad), hi = ld_tr(ad + 1024u);
+      return u32x4_t{__builtin_bit_cast(uint2, lo).x, __builtin_bit_cast(uint2, lo).y, __builtin_bit_cast(uint2, hi).x,
+                     __builtin_bit_cast(uint2, hi).y};
+    } else {
+      return ld16(bw + wb[s] + 4096u * c);
+    }
+  };
   auto read_frags = [&](const char* bx, char* bw, int s, int slot) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) fx[slot][i] = ld16(bx + xb[s] + 4096u * i);
+    for (int i = 0; i < MT; ++i) fx[slot][i] = frag_x(bx, s, i);
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      if constexpr (KIND == TILE_TR) {
-        char* const ad = bw + tbo[c] + 4096u * s;
-        const u16x4_t lo = ld_tr(ad), hi = ld_tr(ad + 1024u);
-        fw[slot][c] = u32x4_t{__builtin_bit_cast(uint2, lo).x, __builtin_bit_cast(uint2, lo).y,
-                              __builtin_bit_cast(uint2, hi).x, __builtin_bit_cast(uint2, hi).y};
-      } else {
-        fw[slot][c] = ld16(bw + wb[s] + 4096u * c);
-      }
-    }
+    for (int c = 0; c < NT; ++c) fw[slot][c] = frag_w(bw, s, c);
   };
   f32x16_t acc[MT][NT];
 #pragma unroll
@@ -676,11 +699,18 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
   }
 
   // ---- adapter blocks (buffer 0 is free: the last barrier has passed)
+  // GATED, TRD: the adapters one after the other, each multiplied into sums of its own, of which its side's rows or the
+  // elements that its mask keeps are added (so that an infinity of one adapter stays out of the other's results).
   if (P.r > 0) {
+    int halves = KIND == TILE_GATED ? 2 : 1;
+    if constexpr (KIND == TILE_TRD) halves = P.halves;
     const int r = P.r;
+    const int64_t rt = (int64_t)halves * r;  // columns of t
     const bool r8 = (r & 7) == 0;
     const u32x4_t zero4 = {0u, 0u, 0u, 0u};
-    for (int j0 = 0; j0 < r; j0 += 32) {
+    // TRD: the mask of the lane's results, bit 4 q + i of tile (i, c) for its columns 8 q + 4 h + i
+    uint32_t keep[KIND == TILE_TRD ? MT : 1][KIND == TILE_TRD ? NT : 1];
+    auto block = [&](int hf, int j0) {
       // the weight side's pieces first, so that both sides' loads are on their way together
       constexpr int kAP = BN / 128;
       u32x4_t av[kAP];
@@ -688,14 +718,16 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
       for (int u = 0; u < kAP; ++u) {
         const int idx = tid + 512 * u;
         av[u] = zero4;
-        if constexpr (KIND == TILE_TR) {  // A[j0 + row][n0 + 8 c ..]
+        if constexpr (kTR) {  // A[j0 + row][n0 + 8 c ..]
           const int row = idx / (BN / 8);
           const int64_t col = n0 + 8 * (idx % (BN / 8));
-          if (j0 + row < r && col < K) av[u] = *reinterpret_cast<const u32x4_t*>(P.ab + ((int64_t)e * r + j0 + row) * K + col);
+          if (j0 + row < r && col < K)
+            av[u] = *reinterpret_cast<const u32x4_t*>(P.ab + ((int64_t)(e + hf) * r + j0 + row) * K + col);
         } else {  // B[n0 + row][j0 + 8 c ..]
-          const int row = idx >> 2, jb = j0 + 8 * (idx & 3);
-          if (n0 + row < N && jb < r) {
-            const uint16_t* bp = P.ab + ((int64_t)e * N + n0 + row) * r + jb;
+          // (GATED: rows of the other side zero)
+          const int row = idx >> 2, jb = j0 + 8 * (idx & 3), n = KIND == TILE_GATED ? 16 * (row >> 5) + (row & 15) : row;
+          if (n0 + n < N && jb < r && (KIND != TILE_GATED || ((row >> 4) & 1) == hf)) {
+            const uint16_t* bp = P.ab + ((int64_t)(e + hf) * N + n0 + n) * r + jb;
             if (r8) {
               av[u] = *reinterpret_cast<const u32x4_t*>(bp);
             } else {
@@ -716,7 +748,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
         for (int i = 0; i < 8; ++i) tv[i] = 0.0f;
         if (row < mrows && jb < r) {
           for (int sp = 0; sp < P.t_splits; ++sp) {
-            const float* tq = P.t + ((int64_t)sp * P.M + row0 + row) * r + jb;
+            const float* tq = P.t + ((int64_t)sp * P.M + row0 + row) * rt + hf * r + jb;
             if (r8) {
               const f32x4_t v0 = *reinterpret_cast<const f32x4_t*>(tq), v1 = *reinterpret_cast<const f32x4_t*>(tq + 4);
 #pragma unroll
@@ -747,7 +779,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
 #pragma unroll
       for (int u = 0; u < kAP; ++u) {
         const int idx = tid + 512 * u;
-        if constexpr (KIND == TILE_TR) {
+        if constexpr (kTR) {
           const int row = idx / (BN / 8), c = idx % (BN / 8);
           const uint32_t base = (uint32_t)(c >> 4) * 16384u;
           st16(sW0 + base + (uint32_t)row * 256u + (tr_chunk((uint32_t)(c & 15), (uint32_t)row) << 4), av[u]);
@@ -760,16 +792,120 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(Tile
         }
       }
       __syncthreads();
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        read_frags(sX0, sW0, s, 0);
+      if constexpr (KIND >= TILE_GATED) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int c = 0; c < NT; ++c) acc[i][c] = tile_mfma(fw[0][c], fx[0][i], acc[i][c]);
+          for (int c = 0; c < NT; ++c) {
+            f32x16_t part;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) part[v] = 0.0f;
+            // (opaque: the compiler would form the 16 comparisons of every tile ahead and spill them)
+            if constexpr (KIND == TILE_TRD) asm volatile("" : "+v"(keep[i][c]));
+#pragma unroll
+            for (int s = 0; s < 4; ++s) part = tile_mfma(frag_w(sW0, s, c), frag_x(sX0, s, i), part);
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+              if constexpr (KIND == TILE_GATED) acc[i][c][v] += (v >> 3) == hf ? part[v] : 0.0f;
+              else acc[i][c][v] += (keep[i][c] >> v) & 1u ? part[v] : 0.0f;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+      } else {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          read_frags(sX0, sW0, s, 0);
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int c = 0; c < NT; ++c) acc[i][c] = tile_mfma(fw[0][c], fx[0][i], acc[i][c]);
+        }
       }
       __syncthreads();
+    };
+    for (int hf = 0; hf < halves; ++hf) {
+      if constexpr (KIND == TILE_TRD) {
+        // lane h = 0 forms the groups q = 0, 1 of its row, lane h = 1 q = 2, 3
+        const uint64_t ctr = drop_counter(P.drop, hf);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int c = 0; c < NT; ++c) {
+            const uint64_t g = (uint64_t)(row0 + mh * (BM / WM) + 32 * i + fr) * (uint64_t)(K >> 3) +
+                               (uint32_t)((n0 + nh * (BN / WN) + 32 * c) >> 3) + 2u * h;
+            const uint32_t own = drop_bits(g, ctr, P.drop) | drop_bits(g + 1, ctr, P.drop) << 8;
+            const uint32_t other = (uint32_t)__shfl_xor((int)own, 32, 64);
+            const uint32_t lo = h ? other >> 4 : own, hi = h ? own >> 4 : other;  // the lane's nibbles of groups 0, 1 and 2, 3
+            keep[i][c] = (lo & 15u) | ((lo >> 4) & 0xF0u) | (hi & 15u) << 8 | ((hi >> 4) & 0xF0u) << 8;
+            __builtin_amdgcn_sched_barrier(0);  // (one tile's rounds at a time: together they would spill the sums)
+          }
+      }
+      for (int j0 = 0; j0 < r; j0 += 32) block(hf, j0);
     }
+  }
+
+  // ---- gated output: g and up of the lane's 8 columns are results v and v + 8 of each MFMA tile
+  if constexpr (KIND == TILE_GATED) {
+    // rows of BO values, as many to a buffer as fit (the weight's first), 16-byte pieces XOR-swizzled by the row
+    auto emit = [&](auto value, void* out, int64_t ld, int es) {
+      const uint32_t rowb = (uint32_t)(BO * es);
+      const int rpb = (int)(L::kW / rowb), cpr = (int)rowb / 16;
+      const uint32_t mask = (uint32_t)min(31, cpr - 1);
+      auto sbuf = [&](int b) { return b == 0 ? sW0 : b == 1 ? sW1 : b == 2 ? sX0 : sX1; };
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int row = mh * (BM / WM) + 32 * i + fr;
+        char* const st = sbuf(row / rpb) + (uint32_t)(row % rpb) * rowb;
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t col = (uint32_t)(nh * (BO / WN) + 16 * c + 8 * q);
+            float o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = value(acc[i][c][4 * q + j], acc[i][c][8 + 4 * q + j]);
+            if (es == 4)
+              *reinterpret_cast<f32x4_t*>(st + 16u * ((col / 4 + h) ^ ((uint32_t)row & mask))) = f32x4_t{o[0], o[1], o[2], o[3]};
+            else
+              *reinterpret_cast<u32x2v_t*>(st + 16u * ((col / 8) ^ ((uint32_t)row & mask)) + 8u * h) =
+                  u32x2v_t{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+          }
+      }
+      __syncthreads();
+      const bool vec = (ld * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+      for (int idx = tid; idx < mrows * cpr; idx += 512) {
+        const int row = idx / cpr, c = idx % cpr;
+        const int64_t col = n0 + c * (16 / es);
+        const u32x4_t v = ld16(sbuf(row / rpb) + (uint32_t)(row % rpb) * rowb + 16u * ((uint32_t)c ^ ((uint32_t)row & mask)));
+        char* dst = reinterpret_cast<char*>(out) + ((int64_t)(row0 + row) * ld + col) * es;
+        if (vec && col + 16 / es <= NO) {
+          *reinterpret_cast<u32x4_t*>(dst) = v;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = v[i];
+            if (es == 4) {
+              if (col + i < NO) reinterpret_cast<uint32_t*>(dst)[i] = w;
+            } else {
+              if (col + 2 * i < NO) reinterpret_cast<uint16_t*>(dst)[2 * i] = (uint16_t)w;
+              if (col + 2 * i + 1 < NO) reinterpret_cast<uint16_t*>(dst)[2 * i + 1] = (uint16_t)(w >> 16);
+            }
+          }
+        }
+      }
+      __syncthreads();
+    };
+    if (P.gu) {
+      emit([](float g, float) { return g; }, P.gu, 2 * N, 2);
+      emit([](float, float v) { return v; }, P.gu + N, 2 * N, 2);
+    }
+    const int es = P.ydt == DT_F32 ? 4 : 2;
+    switch (P.act) {
+      case ACT_SILU: emit([](float g, float v) { return act_f<ACT_SILU>(g) * v; }, P.y, N, es); break;
+      case ACT_GELU: emit([](float g, float v) { return act_f<ACT_GELU>(g) * v; }, P.y, N, es); break;
+      default: emit([](float g, float v) { return act_f<ACT_GELU_TANH>(g) * v; }, P.y, N, es); break;
+    }
+    return;
   }
 
   // ---- output: staged row-major in LDS, stored in 16-byte pieces
@@ -942,10 +1078,14 @@ hipError_t launch_blocks(int64_t blocks, F launch) {
 // Upper bound of the row tiles of any `experts` ranges over M rows.
 inline int64_t tile_bound(int64_t M, int experts, int BM) { return M / BM + std::min<int64_t>(experts, M); }
 
+// (GATED: columns of the two sides together, as the tiles hold them)
+template <int KIND>
+int64_t tile_cols(const TileArgs& a) { return KIND == TILE_TR || KIND == TILE_TRD ? a.K : KIND == TILE_GATED ? 2 * a.N : a.N; }
+
 template <int KIND, int BITS, int BM, int BN>
-hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
+hipError_t launch_tile_t(typename TileParams<KIND>::T a, const Levels& lv, hipStream_t s) {
   auto kern = k_tile<KIND, BITS, BM, BN>;
-  const int64_t no = KIND == TILE_TR ? a.K : a.N;
+  const int64_t no = tile_cols<KIND>(a);
   a.ntiles = (int)((no + BN - 1) / BN);
   // (only so many ranges can hold more than min_rows rows)
   const int ranges = (int)std::min<int64_t>(a.experts, a.M / (a.min_rows + 1));
@@ -966,8 +1106,8 @@ hipError_t launch_tile_t(TileArgs a, const Levels& lv, hipStream_t s) {
 // us and 168 (the rule 1.0 and 1.33), 5000 in 16 of 2816 x 2048 105 and 114 (1.5 and 1.6), 4096 in 16 of 2816 x 2048 116
 // and 111 (1.5 and 1.36).
 template <int KIND, int BITS>
-hipError_t launch_tile(TileArgs a, const Levels& lv, hipStream_t s) {
-  const int64_t no = KIND == TILE_TR ? a.K : a.N;
+hipError_t launch_tile(typename TileParams<KIND>::T a, const Levels& lv, hipStream_t s) {
+  const int64_t no = tile_cols<KIND>(a);
   // tiles of b x c: whole ones, and half a partial one per range
   auto count = [&](int64_t b, int64_t c) {
     const int64_t nt = (no + c - 1) / c;

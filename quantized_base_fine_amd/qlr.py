@@ -26,12 +26,15 @@ PATH_AUTO, PATH_F32, PATH_GEMV, PATH_GEMM = 0, 1, 2, 3
 OP_QUANTIZE, OP_LINEAR, OP_LINEAR_BWD, OP_LINEAR_DBA = 0, 1, 2, 3
 OP_QUANTIZE_OUTLIERS, OP_LINEAR_OUTLIERS, OP_LINEAR_WHA = 4, 5, 6
 OP_LINEAR_I8, OP_LINEAR_GROUPED, OP_LINEAR_GROUPED_BWD = 7, 8, 9
+OP_LINEAR_DROPOUT, OP_LINEAR_DROPOUT_BWD, OP_GATED, OP_GATED_BWD = 10, 11, 12, 13
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 MAX_EXPERTS = 4096
 
 STATUS = {
     0: "QLR_OK", 1: "QLR_ERR_NULL", 2: "QLR_ERR_SHAPE", 3: "QLR_ERR_DTYPE", 4: "QLR_ERR_BITS",
     5: "QLR_ERR_BLOCK", 6: "QLR_ERR_ALIGN", 7: "QLR_ERR_NONFINITE", 8: "QLR_ERR_WORKSPACE",
     9: "QLR_ERR_ALIAS", 10: "QLR_ERR_HIP", 11: "QLR_ERR_FORMAT", 12: "QLR_ERR_PATH",
+    13: "QLR_ERR_VALUE",
 }
 
 
@@ -73,6 +76,10 @@ class CSparse(C.Structure):
 
 class CI8Rows(C.Structure):
     _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("q", C.c_void_p), ("scale", C.c_void_p)]
+
+
+class CDropout(C.Structure):
+    _fields_ = [("p", C.c_double), ("seed", C.c_uint64), ("counter", C.c_uint64), ("step", C.c_void_p)]
 
 
 EXPORTS = {
@@ -127,6 +134,19 @@ EXPORTS = {
                                          C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_float,
                                          C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
                                          C.c_void_p]),
+    "qlr_linear_fwd_dropout": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.POINTER(CQWeight), C.c_void_p, C.c_void_p,
+                                         C.c_int, C.c_int32, C.c_float, C.POINTER(CDropout), C.c_void_p, C.c_int,
+                                         C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qlr_linear_bwd_dropout": (C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_int, C.c_int64, C.POINTER(CQWeight),
+                                         C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_float, C.POINTER(CDropout),
+                                         C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
+                                         C.c_void_p]),
+    "qlr_gated_fwd": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.POINTER(CQWeight), C.c_int, C.c_void_p, C.c_void_p,
+                                C.c_int, C.c_int32, C.c_float, C.POINTER(CDropout), C.c_void_p, C.c_int, C.c_void_p,
+                                C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qlr_gated_bwd": (C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_int, C.c_int64, C.POINTER(CQWeight),
+                                C.c_int, C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_float, C.POINTER(CDropout),
+                                C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
     "qlr_force_path": (C.c_int, [C.c_int]),
 }
 
@@ -870,3 +890,245 @@ def linear_grouped_bwd(dy, x, qw: QWeight, offsets, A=None, B=None, scale: float
                        need_dx: bool = True):
     """Gradients (dx, dA, dB) of linear_grouped for an upstream gradient dy; see GroupedBwdCall."""
     return GroupedBwdCall(dy, x, qw, offsets, A, B, scale, dx_dtype=dx_dtype, need_dx=need_dx)()
+
+
+# ---------------------------------------------------------------- adapter dropout, gated feed-forward block
+
+@dataclass
+class Dropout:
+    """Dropout of an adapter's input by a mask that is never stored: a function of ``seed`` and of
+    ``counter`` + ``step`` (see qlr_dropout in the header).  The forward and the backward of one step are
+    given the same numbers; every mask of a seed needs a counter of its own (a linear takes one, a gated
+    block two: counter and counter + 1).  ``step``: an int64 tensor of one element on the GPU, read when a call
+    runs, so that calls captured into a graph follow it; or None."""
+    p: float
+    seed: int
+    counter: int = 0
+    step: "object" = None
+
+    def c_struct(self) -> CDropout:
+        torch = _torch()
+        if self.step is not None:
+            _require_cuda(self.step)
+            if self.step.dtype != torch.int64 or self.step.numel() != 1:
+                raise ValueError("step must be an int64 tensor of one element")
+        mask = (1 << 64) - 1
+        return CDropout(float(self.p), int(self.seed) & mask, int(self.counter) & mask, _ptr(self.step))
+
+
+def _bf16(t, what: str, shape):
+    torch = _torch()
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous bfloat16 tensor of shape {tuple(shape)}")
+    return t
+
+
+def _train_operands(qw: QWeight, A, B, lead):
+    """(columns of the output, rank) of a call under dropout (lead: ()) or of a gated block ((2,)), checked."""
+    if lead and qw.rows % 2 != 0:
+        raise ValueError(f"the stacked weight's {qw.rows} rows are odd")
+    N = qw.rows // 2 if lead else qw.rows
+    if (A is None) != (B is None):
+        raise ValueError("A and B come together")
+    r = 0
+    if A is not None:
+        r = A.shape[-2] if A.dim() == len(lead) + 2 else -1
+        _bf16(A, "A", (*lead, r, qw.cols))
+        _bf16(B, "B", (*lead, N, r))
+    return N, r
+
+
+def _train_output(out, what: str, rows: int, cols: int, dtype, device):
+    """The given output, checked, or a new one."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=device)
+    if _rows2d(out, what, cols, (torch.float32, torch.bfloat16)).shape[0] != rows:
+        raise ValueError(f"{what} must have {rows} rows")
+    return out
+
+
+def _train_grads(dA, dB, shapeA, shapeB, device):
+    torch = _torch()
+    out = []
+    for name, t, shape in (("dA", dA, shapeA), ("dB", dB, shapeB)):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.float32, device=device)
+        if tuple(t.shape) != tuple(shape) or t.dtype != torch.float32 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)}")
+        out.append(t)
+    return out
+
+
+def _train_ws(ws, op: int, M: int, N: int, K: int, r: int, device):
+    torch = _torch()
+    need = workspace_bytes(op, M, N, K, r)
+    if ws is None and need > 0:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def _drop_arg(dropout: Optional[Dropout]):
+    """(the C structure, what the call takes)"""
+    c = None if dropout is None else dropout.c_struct()
+    return c, None if c is None else C.byref(c)
+
+
+def _step(dropout: Optional[Dropout]):
+    return None if dropout is None else dropout.step
+
+
+class LinearDropoutCall:
+    """A prepared ``qlr_linear_fwd_dropout`` call: y = x W'^T + scale (drop(x) A^T) B^T, x and the
+    adapter bfloat16.  Marshalled once (the stream current at construction is used; the dropout's step is
+    read on the GPU at every call); the tensors are kept alive by the object, and two calls that can
+    overlap in time need workspaces of their own."""
+
+    def __init__(self, x, qw: QWeight, A=None, B=None, scale: float = 0.0, dropout: Optional[Dropout] = None,
+                 out_dtype=None, out=None, ws=None):
+        torch = _torch()
+        _require_cuda(x, A, B, out, ws)
+        N, r = _train_operands(qw, A, B, ())
+        M, dev = _rows2d(x, "x", qw.cols, (torch.bfloat16,)).shape[0], x.device
+        self.y = out = _train_output(out, "out", M, N, out_dtype, dev)
+        ws, ws_bytes = _train_ws(ws, OP_LINEAR_DROPOUT, M, N, qw.cols, r, dev)
+        _same_device(x, weight=qw.codes, A=A, B=B, out=out, ws=ws, step=_step(dropout))
+        cw, (cd, drop) = qw.c_struct(), _drop_arg(dropout)
+        self._keep = (x, qw, A, B, ws, cw, cd, dropout)
+        self._run = _Launch(lib().qlr_linear_fwd_dropout,
+                            (x.data_ptr(), _dt(x), M, C.byref(cw), _ptr(A), _ptr(B), QLR_BF16, r, float(scale), drop,
+                             out.data_ptr(), _dt(out), _ptr(ws), ws_bytes, _stream(dev)), dev)
+
+    def __call__(self):
+        self._run()
+        return self.y
+
+
+def linear_dropout(x, qw: QWeight, A=None, B=None, scale: float = 0.0, dropout: Optional[Dropout] = None, out_dtype=None,
+                   out=None):
+    """y = x W'^T + scale (drop(x) A^T) B^T; see LinearDropoutCall."""
+    return LinearDropoutCall(x, qw, A, B, scale, dropout, out_dtype=out_dtype, out=out)()
+
+
+class LinearDropoutBwdCall:
+    """A prepared ``qlr_linear_bwd_dropout`` call for an upstream gradient dy (M, N) and the dropout of
+    the forward: dx = dy W' + scale drop'((dy B) A), dA = scale (dy B)^T drop(x), dB = scale dy^T
+    (drop(x) A^T), drop' the mask and its factor.  dA and dB are float32; ``need_dx=False`` skips the input
+    gradient; without an adapter x may be None.  Marshalled once, as LinearDropoutCall."""
+
+    def __init__(self, dy, x, qw: QWeight, A=None, B=None, scale: float = 0.0, dropout: Optional[Dropout] = None,
+                 dx_dtype=None, need_dx: bool = True, dx=None, dA=None, dB=None, ws=None):
+        torch = _torch()
+        _require_cuda(dy, x, A, B, dx, dA, dB, ws)
+        N, r = _train_operands(qw, A, B, ())
+        M, dev = _rows2d(dy, "dy", N, (torch.bfloat16,)).shape[0], dy.device
+        if x is None and r > 0:
+            raise ValueError("x is needed for the adapter's gradients")
+        if x is not None:
+            _bf16(x, "x", (M, qw.cols))
+        self.dx = _train_output(dx, "dx", M, qw.cols, dx_dtype, dev) if need_dx else None
+        self.dA, self.dB = _train_grads(dA, dB, (r, qw.cols), (N, r), dev) if r > 0 else (None, None)
+        ws, ws_bytes = _train_ws(ws, OP_LINEAR_DROPOUT_BWD, M, N, qw.cols, r, dev)
+        _same_device(dy, x=x, weight=qw.codes, A=A, B=B, dx=self.dx, dA=self.dA, dB=self.dB, ws=ws, step=_step(dropout))
+        cw, (cd, drop) = qw.c_struct(), _drop_arg(dropout)
+        self._keep = (dy, x, qw, A, B, ws, cw, cd, dropout)
+        self._run = _Launch(lib().qlr_linear_bwd_dropout,
+                            (dy.data_ptr(), _dt(dy), _ptr(x), QLR_BF16, M, C.byref(cw), _ptr(A), _ptr(B), QLR_BF16, r,
+                             float(scale), drop, _ptr(self.dx), _dt(self.dx) if self.dx is not None else QLR_F32,
+                             _ptr(self.dA), _ptr(self.dB), _ptr(ws), ws_bytes, _stream(dev)), dev)
+
+    def __call__(self):
+        self._run()
+        return self.dx, self.dA, self.dB
+
+
+def linear_dropout_bwd(dy, x, qw: QWeight, A=None, B=None, scale: float = 0.0, dropout: Optional[Dropout] = None,
+                       dx_dtype=None, need_dx: bool = True):
+    """Gradients (dx, dA, dB) of linear_dropout for an upstream gradient dy; see LinearDropoutBwdCall."""
+    return LinearDropoutBwdCall(dy, x, qw, A, B, scale, dropout, dx_dtype=dx_dtype, need_dx=need_dx)()
+
+
+def _activation(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {tuple(ACTIVATIONS)}, not {act!r}")
+    return ACTIVATIONS[act]
+
+
+class GatedCall:
+    """A prepared ``qlr_gated_fwd`` call, the first half of a gated feed-forward block: h = act(g) v with
+    g and v the linears of the two halves (N rows each) of the stacked weight, A (2, r, K) and B (2, N, r) their
+    adapters, the gate's first.  ``save=True`` (or a ``gu`` tensor) also keeps [g | v] (M, 2 N) in
+    bfloat16 for the backward; the call then returns (h, gu).  Marshalled once (the stream current at
+    construction is used); the tensors are kept alive by the object, and two calls that can overlap in
+    time need workspaces of their own."""
+
+    def __init__(self, x, qw: QWeight, A=None, B=None, scale: float = 0.0, act: str = "silu",
+                 dropout: Optional[Dropout] = None, out_dtype=None, save: bool = False, out=None, gu=None, ws=None):
+        torch = _torch()
+        _require_cuda(x, A, B, out, gu, ws)
+        N, r = _train_operands(qw, A, B, (2,))
+        M, dev = _rows2d(x, "x", qw.cols, (torch.bfloat16,)).shape[0], x.device
+        self.h = out = _train_output(out, "out", M, N, out_dtype, dev)
+        if gu is None and save:
+            gu = torch.empty((M, 2 * N), dtype=torch.bfloat16, device=dev)
+        if gu is not None:
+            _bf16(gu, "gu", (M, 2 * N))
+        self.gu = gu
+        ws, ws_bytes = _train_ws(ws, OP_GATED, M, N, qw.cols, r, dev)
+        _same_device(x, weight=qw.codes, A=A, B=B, out=out, gu=gu, ws=ws, step=_step(dropout))
+        cw, (cd, drop) = qw.c_struct(), _drop_arg(dropout)
+        self._keep = (x, qw, A, B, ws, cw, cd, dropout)
+        self._run = _Launch(lib().qlr_gated_fwd,
+                            (x.data_ptr(), _dt(x), M, C.byref(cw), _activation(act), _ptr(A), _ptr(B), QLR_BF16, r,
+                             float(scale), drop, out.data_ptr(), _dt(out), _ptr(gu), _ptr(ws), ws_bytes, _stream(dev)), dev)
+
+    def __call__(self):
+        self._run()
+        return self.h if self.gu is None else (self.h, self.gu)
+
+
+def gated(x, qw: QWeight, A=None, B=None, scale: float = 0.0, act: str = "silu", dropout: Optional[Dropout] = None,
+          out_dtype=None, save: bool = False):
+    """h = act(x Wg'^T + ...) (x Wu'^T + ...), with ``save=True`` (h, [g | v]); see GatedCall."""
+    return GatedCall(x, qw, A, B, scale, act, dropout, out_dtype=out_dtype, save=save)()
+
+
+class GatedBwdCall:
+    """A prepared ``qlr_gated_bwd`` call for an upstream gradient dh (M, N) at the pre-activations gu (M,
+    2 N) that the forward kept, with its activation and dropout: dx (M, K), dA (2, r, K) and dB (2, N, r)
+    float32.  ``need_dx=False`` skips the input gradient; without an adapter x may be None.  Marshalled
+    once, as GatedCall."""
+
+    def __init__(self, dh, gu, x, qw: QWeight, A=None, B=None, scale: float = 0.0, act: str = "silu",
+                 dropout: Optional[Dropout] = None, dx_dtype=None, need_dx: bool = True, dx=None, dA=None, dB=None, ws=None):
+        torch = _torch()
+        _require_cuda(dh, gu, x, A, B, dx, dA, dB, ws)
+        N, r = _train_operands(qw, A, B, (2,))
+        M, dev = _rows2d(dh, "dh", N, (torch.bfloat16,)).shape[0], dh.device
+        _bf16(gu, "gu", (M, 2 * N))
+        if x is None and r > 0:
+            raise ValueError("x is needed for the adapters' gradients")
+        if x is not None:
+            _bf16(x, "x", (M, qw.cols))
+        self.dx = _train_output(dx, "dx", M, qw.cols, dx_dtype, dev) if need_dx else None
+        self.dA, self.dB = _train_grads(dA, dB, (2, r, qw.cols), (2, N, r), dev) if r > 0 else (None, None)
+        ws, ws_bytes = _train_ws(ws, OP_GATED_BWD, M, N, qw.cols, r, dev)
+        _same_device(dh, gu=gu, x=x, weight=qw.codes, A=A, B=B, dx=self.dx, dA=self.dA, dB=self.dB, ws=ws,
+                     step=_step(dropout))
+        cw, (cd, drop) = qw.c_struct(), _drop_arg(dropout)
+        self._keep = (dh, gu, x, qw, A, B, ws, cw, cd, dropout)
+        self._run = _Launch(lib().qlr_gated_bwd,
+                            (dh.data_ptr(), _dt(dh), gu.data_ptr(), _ptr(x), QLR_BF16, M, C.byref(cw), _activation(act),
+                             _ptr(A), _ptr(B), QLR_BF16, r, float(scale), drop, _ptr(self.dx),
+                             _dt(self.dx) if self.dx is not None else QLR_F32, _ptr(self.dA), _ptr(self.dB), _ptr(ws),
+                             ws_bytes, _stream(dev)), dev)
+
+    def __call__(self):
+        self._run()
+        return self.dx, self.dA, self.dB
+
+
+def gated_bwd(dh, gu, x, qw: QWeight, A=None, B=None, scale: float = 0.0, act: str = "silu",
+              dropout: Optional[Dropout] = None, dx_dtype=None, need_dx: bool = True):
+    """Gradients (dx, dA, dB) of gated for an upstream gradient dh; see GatedBwdCall."""
+    return GatedBwdCall(dh, gu, x, qw, A, B, scale, act, dropout, dx_dtype=dx_dtype, need_dx=need_dx)()
