@@ -198,9 +198,13 @@ GroupedLayout grouped_layout(bool bwd, int64_t T, int64_t rows, int64_t K, int32
 // as the call may choose, with a mask or without), for the backward u beside t, the partials of the adapter
 // gradients, and the gated block's dgu.
 struct TrainLayout {
-  size_t t, u, dgu, part, total;
+  size_t t, u, dgu, bits, part, total;
   int t_splits, u_splits;  // of the masked product, and of the gated block's u
+  bool dense;              // the product of many rows, through a dense copy of the weight at wd; xt, wt, sums: see qlr_dense.hip
+  size_t wd, xt, wt, sums;
 };
+// Rows from which the adapters' partial sums are added once, before the kernels that read them many times.
+constexpr int64_t kSumRows = 256;
 TrainLayout train_layout(qlr_op op, int64_t M, int64_t N, int64_t K, int32_t r) {
   TrainLayout L{};
   L.t_splits = L.u_splits = 1;
@@ -221,12 +225,26 @@ TrainLayout train_layout(qlr_op op, int64_t M, int64_t N, int64_t K, int32_t r) 
       L.u = at;
       if (!gated) L.u_splits = L.t_splits;
       at = L.u + up((size_t)L.u_splits * (size_t)M * row);
-      L.part = at;
+      L.bits = at;
+      L.part = L.bits + up((size_t)two * (size_t)M * (size_t)(K / 8));
       at = L.part + up(qlr::train_grad_floats(M, (int64_t)two * (N + K), r) * sizeof(float));
     }
   }
   L.dgu = at;
   if (op == QLR_OP_GATED_BWD) at = L.dgu + up((size_t)M * (size_t)(2 * N) * 2);
+  if (op != QLR_OP_LINEAR_DROPOUT) {
+    // forward: h of x and the 2 N x K weight; backward: dx of dy (dgu) and the weight's transpose
+    const int64_t NO = bwd ? K : N, KC = bwd ? two * N : K, wrows = bwd ? K : two * N, nb = (r + 31) / 32;
+    const qlr::DensePlan p = qlr::dense_plan(M, NO, KC, !bwd);
+    L.dense = p.ok;
+    if (L.dense) {
+      L.wd = at;
+      L.xt = L.wd + up((size_t)wrows * (size_t)KC * 2);
+      L.wt = L.xt + up((size_t)two * (size_t)nb * (size_t)M * 128);
+      L.sums = L.wt + up((size_t)(bwd ? two : 1) * (size_t)nb * (size_t)wrows * 128);
+      at = L.sums + (size_t)p.rest * (size_t)p.splits * qlr::kDensePartFloats * sizeof(float);
+    }
+  }
   L.total = at;
   return L;
 }
@@ -391,14 +409,14 @@ qlr_status check_grouped(int64_t T, const qlr_qweight* w, int32_t experts, const
 
 // The dropout of a call as the kernels take it; *q: the factor of the kept values, which the call puts into its scale.
 qlr_status drop_args(const qlr_dropout* d, int32_t r, qlr::DropArgs* out, double* q) {
-  *out = qlr::DropArgs{0, 0, nullptr, 0};
+  *out = qlr::DropArgs{0, 0, nullptr, 0, nullptr};
   *q = 1.0;
   if (!d) return QLR_OK;
   if (!(d->p >= 0.0 && d->p < 1.0)) return fail(QLR_ERR_VALUE, "dropout probability %g not in [0, 1)", d->p);
   if ((reinterpret_cast<uintptr_t>(d->step) & 7u) != 0) return fail(QLR_ERR_ALIGN, "step must be 8-byte aligned");
   const long long t = std::min<long long>(std::llrint(d->p * 65536.0), 65535);
   if (t == 0 || r == 0) return QLR_OK;
-  *out = qlr::DropArgs{d->seed, d->counter, d->step, (uint32_t)t};
+  *out = qlr::DropArgs{d->seed, d->counter, d->step, (uint32_t)t, nullptr};
   *q = 65536.0 / (double)(65536 - t);
   return QLR_OK;
 }
@@ -468,6 +486,45 @@ qlr::TrainArgs train_args(int64_t M, const qlr_qweight* w, int64_t N, int32_t r,
   a.drop = drop;
   a.halves = 1;
   return a;
+}
+
+// The product of a, of NO columns over KC, through a dense copy of the weight: h of the gated block, or (tr) dx.
+hipError_t run_dense(const qlr::TrainArgs& a, int64_t NO, int64_t KC, char* ws, const TrainLayout& lay, bool gated, bool tr,
+                     const qlr::Levels& lv, hipStream_t s) {
+  uint16_t *wd = reinterpret_cast<uint16_t*>(ws + lay.wd), *xt = reinterpret_cast<uint16_t*>(ws + lay.xt),
+           *wt = reinterpret_cast<uint16_t*>(ws + lay.wt);
+  const int64_t rows = gated ? 2 * NO : tr ? KC : NO, cols = tr ? NO : KC;
+  const qlr::DenseWeight w{a.w, a.q8, a.cst, rows, cols, a.bits, wd};
+  hipError_t e = qlr::launch_dense_weight(w, tr, lv, s);
+  if (e != hipSuccess) return e;
+  const int halves = gated ? 2 : a.halves;
+  qlr::DenseArgs d{};
+  if (a.r > 0) {
+    const qlr::DenseAdapter ad{a.t, a.t_splits, halves * a.r, a.ab, tr, a.M, gated ? 2 * NO : NO, a.r, (a.r + 31) / 32, halves, a.scale, xt, wt};
+    e = qlr::launch_dense_adapter(ad, s);
+    if (e != hipSuccess) return e;
+    d.nb = ad.nb;
+  }
+  const qlr::DensePlan p = qlr::dense_plan(a.M, NO, KC, gated);
+  d.x = reinterpret_cast<const uint16_t*>(a.x);
+  d.w = wd;
+  d.M = a.M;
+  d.KC = KC;
+  d.NO = NO;
+  d.ntiles = p.ntiles;
+  d.whole = p.whole;
+  d.rest = p.rest;
+  d.splits = p.splits;
+  d.xt = xt;
+  d.wt = wt;
+  d.halves = halves;
+  d.y = a.y;
+  d.ydt = a.ydt;
+  d.act = a.act;
+  d.gu = a.gu;
+  d.drop = a.drop;
+  d.part = reinterpret_cast<float*>(ws + lay.sums);
+  return qlr::launch_dense(d, gated, s);
 }
 
 qlr::TileArgs grouped_args(int64_t T, const qlr_qweight* w, int32_t experts, const int32_t* offsets, int32_t r, float scale) {
@@ -1544,27 +1601,35 @@ qlr_status qlr_linear_bwd_dropout(const void* dy, qlr_dtype dydt, const void* x,
   float *t = reinterpret_cast<float*>(wsp + lay.t), *u = reinterpret_cast<float*>(wsp + lay.u);
   const uint16_t *xp = reinterpret_cast<const uint16_t*>(x), *dyp = reinterpret_cast<const uint16_t*>(dy);
   const float sq = (float)((double)scale * q);
+  d.bits = reinterpret_cast<uint8_t*>(wsp + lay.bits);
+  int t_splits = lay.t_splits;
   hipError_t e;
   if (r > 0 && M > 0) {
     const qlr::TrainProd jobs[2] = {{xp, reinterpret_cast<const uint16_t*>(A), K, t, r, r, 0, 0, false},
                                     {dyp, reinterpret_cast<const uint16_t*>(B), N, u, r, r, 0, -1, true}};
     e = qlr::launch_train_t(jobs, 2, M, lay.t_splits, d, s);
+    if (e == hipSuccess && M >= kSumRows) {
+      const qlr::TrainSum sums[2] = {{t, t_splits, r}, {u, t_splits, r}};
+      e = qlr::launch_train_sum(sums, 2, M, s);
+      t_splits = 1;
+    }
     if (e != hipSuccess) return hip_fail(e, "adapter products (x A^T, dy B) launch");
   }
   if (dx && M > 0) {
     qlr::TrainArgs a = train_args(M, w, N, r, sq, d);
     a.x = dy;
     a.t = u;
-    a.t_splits = lay.t_splits;
+    a.t_splits = t_splits;
     a.ab = reinterpret_cast<const uint16_t*>(A);
     a.y = dx;
     a.ydt = (int)dxdt;
     const qlr::Levels lv = levels_arg(w->bits);
-    e = d.thr > 0 ? qlr::launch_drop_dx(a, lv, s) : qlr::launch_grouped_dx(a, lv, s);
+    if (lay.dense) e = run_dense(a, K, N, wsp, lay, false, true, lv, s);
+    else e = d.thr > 0 ? qlr::launch_drop_dx(a, lv, s) : qlr::launch_grouped_dx(a, lv, s);
     if (e != hipSuccess) return hip_fail(e, "input-gradient launch");
   }
   if (r > 0) {
-    const qlr::TrainGrad jobs[2] = {{u, lay.t_splits, r, 0, xp, K, dA, 0, 0, false}, {t, lay.t_splits, r, 0, dyp, N, dB, 0, -1, true}};
+    const qlr::TrainGrad jobs[2] = {{u, t_splits, r, 0, xp, K, dA, 0, 0, false}, {t, t_splits, r, 0, dyp, N, dB, 0, -1, true}};
     e = qlr::launch_train_grads(jobs, 2, M, r, nullptr, 0, 0, sq, d, reinterpret_cast<float*>(wsp + lay.part), s);
     if (e != hipSuccess) return hip_fail(e, "adapter-gradient launch");
   }
@@ -1634,7 +1699,9 @@ qlr_status qlr_gated_fwd(const void* x, qlr_dtype xdt, int64_t M, const qlr_qwei
   a.act = (int)act;
   a.gu = reinterpret_cast<uint16_t*>(gu);
   const qlr::Levels lv = levels_arg(w->bits);
-  e = few ? qlr::launch_gated_few(a, lv, s) : qlr::launch_gated_gemm(a, lv, s);
+  if (few) e = qlr::launch_gated_few(a, lv, s);
+  else if (lay.dense) e = run_dense(a, N, K, reinterpret_cast<char*>(ws), lay, true, false, lv, s);
+  else e = qlr::launch_gated_gemm(a, lv, s);
   if (e != hipSuccess) return hip_fail(e, "gated product launch");
   return QLR_OK;
 }
@@ -1682,6 +1749,8 @@ qlr_status qlr_gated_bwd(const void* dh, qlr_dtype dhdt, const void* gu, const v
   const uint16_t *xp = reinterpret_cast<const uint16_t*>(x), *Ap = reinterpret_cast<const uint16_t*>(A);
   const uint16_t *dhp = reinterpret_cast<const uint16_t*>(dh), *gup = reinterpret_cast<const uint16_t*>(gu);
   const float sq = (float)((double)scale * q);
+  d.bits = reinterpret_cast<uint8_t*>(wsp + lay.bits);
+  int t_splits = lay.t_splits, u_splits = lay.u_splits;
   hipError_t e;
   if (M > 0 && (dx || r > 0)) {
     e = qlr::launch_gated_u(dhp, gup, (int)act, M, N, reinterpret_cast<const uint16_t*>(B), r, dgu, u, lay.u_splits, s);
@@ -1691,32 +1760,34 @@ qlr_status qlr_gated_bwd(const void* dh, qlr_dtype dhdt, const void* gu, const v
     qlr::TrainProd jobs[2];
     for (int i = 0; i < 2; ++i) jobs[i] = qlr::TrainProd{xp, Ap + (int64_t)i * r * K, K, t, r, 2 * r, i * r, i, false};
     e = qlr::launch_train_t(jobs, 2, M, lay.t_splits, d, s);
+    if (e == hipSuccess && M >= kSumRows) {
+      const qlr::TrainSum sums[2] = {{t, t_splits, 2 * r}, {u, u_splits, 2 * r}};
+      e = qlr::launch_train_sum(sums, 2, M, s);
+      t_splits = u_splits = 1;
+    }
     if (e != hipSuccess) return hip_fail(e, "adapter products launch");
   }
   if (dx && M > 0) {
     qlr::TrainArgs a = train_args(M, w, 2 * N, r, sq, d);
     a.x = dgu;
     a.t = u;
-    a.t_splits = lay.u_splits;
+    a.t_splits = u_splits;
     a.ab = Ap;
     a.y = dx;
     a.ydt = (int)dxdt;
     const qlr::Levels lv = levels_arg(w->bits);
-    if (d.thr > 0) {
-      a.halves = 2;
-      e = qlr::launch_drop_dx(a, lv, s);
-    } else {
-      a.r = 2 * r;  // the two adapters are one of 2 r columns
-      e = qlr::launch_grouped_dx(a, lv, s);
-    }
+    if (d.thr > 0) a.halves = 2;
+    else a.r = 2 * r;  // the two adapters are one of 2 r columns
+    if (lay.dense) e = run_dense(a, K, 2 * N, wsp, lay, false, true, lv, s);
+    else e = d.thr > 0 ? qlr::launch_drop_dx(a, lv, s) : qlr::launch_grouped_dx(a, lv, s);
     if (e != hipSuccess) return hip_fail(e, "input-gradient launch");
   }
   if (r > 0) {
     const int64_t aside = (int64_t)r * K, bside = N * r;
-    const qlr::TrainGrad jobs[4] = {{u, lay.u_splits, 2 * r, 0, xp, K, dA, 0, 0, false},
-                                    {u, lay.u_splits, 2 * r, r, xp, K, dA + aside, 0, 1, false},
-                                    {t, lay.t_splits, 2 * r, 0, dhp, N, dB, 1, -1, true},
-                                    {t, lay.t_splits, 2 * r, r, dhp, N, dB + bside, 2, -1, true}};
+    const qlr::TrainGrad jobs[4] = {{u, u_splits, 2 * r, 0, xp, K, dA, 0, 0, false},
+                                    {u, u_splits, 2 * r, r, xp, K, dA + aside, 0, 1, false},
+                                    {t, t_splits, 2 * r, 0, dhp, N, dB, 1, -1, true},
+                                    {t, t_splits, 2 * r, r, dhp, N, dB + bside, 2, -1, true}};
     e = qlr::launch_train_grads(jobs, 4, M, r, gup, N, (int)act, sq, d, reinterpret_cast<float*>(wsp + lay.part), s);
     if (e != hipSuccess) return hip_fail(e, "adapter-gradient launch");
   }

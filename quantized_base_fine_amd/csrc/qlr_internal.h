@@ -230,6 +230,7 @@ struct DropArgs {
   uint64_t seed, counter;
   const uint64_t* step;  // device, added to counter when a kernel runs, or null
   uint32_t thr;          // an element is kept iff its 16-bit number is at least thr
+  uint8_t* bits;         // backward: the masks (which x rows x K / 8 bytes, bit j of a byte its element j), formed once (launch_train_t)
 };
 enum { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 // The products of a training step and of the gated block.  Gated: N is one projection's rows, w the two stacked (gate, up),
@@ -274,6 +275,49 @@ hipError_t launch_gated_few(const TrainArgs& a, const Levels& lv, hipStream_t s)
 // dx = dy W' + sum over the halves of mask (scale u A): K % 64 == 0, N % 8 == 0.
 hipError_t launch_drop_dx(const TrainArgs& a, const Levels& lv, hipStream_t s);
 
+// The same products of many rows through a dense bf16 copy of the weight in the workspace (qlr_dense.hip).
+struct DensePlan {
+  int ntiles, whole, rest, splits;  // column tiles; tiles computed whole; tiles split along the contraction, into how many parts
+  bool ok;
+};
+DensePlan dense_plan(int64_t M, int64_t NO, int64_t KC, bool gated);
+constexpr int64_t kDensePartFloats = 256 * 256;  // of each of the rest x splits sums
+struct DenseWeight {
+  const uint8_t* codes;
+  const uint8_t* q8;
+  const float* cst;
+  int64_t rows, K;
+  int bits;
+  uint16_t* out;  // rows x K, or (tr) K x rows
+};
+hipError_t launch_dense_weight(const DenseWeight& w, bool tr, const Levels& lv, hipStream_t s);
+struct DenseAdapter {
+  const float* t;      // t_splits x M x ldt, half h in columns h r ..
+  int t_splits, ldt;
+  const uint16_t* ab;  // rows x r, or (tr) halves x r x rows
+  bool tr;
+  int64_t M, rows;
+  int r, nb, halves;   // nb = ceil(r / 32)
+  float scale;
+  uint16_t* xt;        // halves nb x M x 64
+  uint16_t* wt;        // (tr ? halves : 1) nb x rows x 64
+};
+hipError_t launch_dense_adapter(const DenseAdapter& a, hipStream_t s);
+struct DenseArgs {
+  const uint16_t* x;   // M x KC
+  const uint16_t* w;   // output columns x KC (gated: 2 NO rows)
+  int64_t M, KC, NO;
+  int ntiles, whole, rest, splits, block0;
+  const uint16_t *xt, *wt;
+  int nb, halves;      // nb = 0: no adapter
+  void* y;
+  int ydt, act;
+  uint16_t* gu;        // gated: M x 2 NO, or null
+  DropArgs drop;
+  float* part;
+};
+hipError_t launch_dense(const DenseArgs& a, bool gated, hipStream_t s);
+
 // One product t = src A^T over K columns, as `splits` float32 partial sums of M x ldt floats each, columns col0 .. col0 + r - 1.
 struct TrainProd {
   const uint16_t* x;   // M x K bf16
@@ -303,6 +347,12 @@ struct TrainGrad {
   int mask;            // >= 0: Q under mask number `mask` (kind 0)
   bool cols_major;     // out is C x r
 };
+// Partial sums t (splits x M x ld) added into the first, for up to two buffers.
+struct TrainSum {
+  float* t;
+  int splits, ld;
+};
+hipError_t launch_train_sum(const TrainSum* jobs, int n, int64_t M, hipStream_t s);
 size_t train_grad_floats(int64_t M, int64_t C_total, int r);
 hipError_t launch_train_grads(const TrainGrad* jobs, int n, int64_t M, int r, const uint16_t* gu, int64_t N, int act, float scale,
                               const DropArgs& drop, float* part, hipStream_t s);

@@ -37,6 +37,15 @@ __device__ __forceinline__ u32x4_t philox(uint64_t g, uint64_t c, uint64_t seed)
   return u32x4_t{x0, x1, x2, x3};
 }
 
+// Eight bits, element j at bit j, as 16-bit lanes, all ones where the bit is set.
+__device__ __forceinline__ u32x4_t bit_lanes(uint32_t b) {
+  u32x4_t m;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m[i] = ((uint32_t)__builtin_amdgcn_sbfe((int)b, 2 * i, 1) & 0xFFFFu) | ((uint32_t)__builtin_amdgcn_sbfe((int)b, 2 * i + 1, 1) & 0xFFFF0000u);
+  return m;
+}
+
 // The group's eight 16-bit lanes, all ones where the element is kept (thr >= 1).
 __device__ __forceinline__ u32x4_t drop_lanes(uint64_t g, uint64_t c, const DropArgs& d) {
   typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));

@@ -825,19 +825,17 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
     };
     for (int hf = 0; hf < halves; ++hf) {
       if constexpr (KIND == TILE_TRD) {
-        // lane h = 0 forms the groups q = 0, 1 of its row, lane h = 1 q = 2, 3
-        const uint64_t ctr = drop_counter(P.drop, hf);
+        // a lane's 16 columns lie in the four groups of its row's 32: a word of the mask's bits, of which it takes one
+        // nibble a byte (rows and columns past the end repeat the last: their results are dropped)
+        const uint8_t* const bits = P.drop.bits + (int64_t)hf * P.M * (K >> 3);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int c = 0; c < NT; ++c) {
-            const uint64_t g = (uint64_t)(row0 + mh * (BM / WM) + 32 * i + fr) * (uint64_t)(K >> 3) +
-                               (uint32_t)((n0 + nh * (BN / WN) + 32 * c) >> 3) + 2u * h;
-            const uint32_t own = drop_bits(g, ctr, P.drop) | drop_bits(g + 1, ctr, P.drop) << 8;
-            const uint32_t other = (uint32_t)__shfl_xor((int)own, 32, 64);
-            const uint32_t lo = h ? other >> 4 : own, hi = h ? own >> 4 : other;  // the lane's nibbles of groups 0, 1 and 2, 3
-            keep[i][c] = (lo & 15u) | ((lo >> 4) & 0xF0u) | (hi & 15u) << 8 | ((hi >> 4) & 0xF0u) << 8;
-            __builtin_amdgcn_sched_barrier(0);  // (one tile's rounds at a time: together they would spill the sums)
+            const int64_t row = min<int64_t>(row0 + mh * (BM / WM) + 32 * i + fr, P.M - 1);
+            const int64_t col = min<int64_t>(n0 + nh * (BN / WN) + 32 * c, K - 32);
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(bits + row * (K >> 3) + (col >> 3)) >> (4 * h);
+            keep[i][c] = (w & 15u) | ((w >> 4) & 0xF0u) | ((w >> 8) & 0xF00u) | ((w >> 12) & 0xF000u);
           }
       }
       for (int j0 = 0; j0 < r; j0 += 32) block(hf, j0);

@@ -17,11 +17,17 @@ __device__ __forceinline__ bf16x8_t tr_frag(const char* lo, const char* hi) {
 }
 __device__ __forceinline__ u32x4_t ld16g(const void* p) { return *reinterpret_cast<const u32x4_t*>(p); }
 
-// Eight (dg, dv) from dh, g and v, as bf16 pieces: rounded to nearest (gn, vn), and as a part and its rest (see split_rest;
-// 16 bits together) for the products whose results are float32.
+// Eight (dg, dv) from dh, g and v, as bf16 pieces: rounded to nearest (gn, vn), and as three parts (8 bits each, the third the whole
+// rest: see split_rest) for the products whose results are float32.
 struct Dgu {
-  u32x4_t gn, vn, g[2], v[2];
+  u32x4_t gn, vn, g[3], v[3];
 };
+__device__ __forceinline__ void three_parts(float a, float b, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+  float a1 = split_rest(a), b1 = split_rest(b), a2 = split_rest(a1), b2 = split_rest(b1);
+  p0 = (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xFFFF0000u);
+  p1 = (__float_as_uint(a1) >> 16) | (__float_as_uint(b1) & 0xFFFF0000u);
+  p2 = (__float_as_uint(a2) >> 16) | (__float_as_uint(b2) & 0xFFFF0000u);
+}
 template <int ACT, bool NEAREST, bool G, bool V>
 __device__ __forceinline__ void form_dgu(u32x4_t dh, u32x4_t gate, u32x4_t up, Dgu& o) {
 #pragma unroll
@@ -41,15 +47,14 @@ __device__ __forceinline__ void form_dgu(u32x4_t dh, u32x4_t gate, u32x4_t up, D
       o.gn[i] = pack_bf16x2(dg[0], dg[1]);
       o.vn[i] = pack_bf16x2(dv[0], dv[1]);
     }
+    uint32_t p0, p1, p2;
     if constexpr (G) {
-      const float r0 = split_rest(dg[0]), r1 = split_rest(dg[1]);
-      o.g[0][i] = (__float_as_uint(dg[0]) >> 16) | (__float_as_uint(dg[1]) & 0xFFFF0000u);
-      o.g[1][i] = pack_bf16x2(r0, r1);
+      three_parts(dg[0], dg[1], p0, p1, p2);
+      o.g[0][i] = p0, o.g[1][i] = p1, o.g[2][i] = p2;
     }
     if constexpr (V) {
-      const float r0 = split_rest(dv[0]), r1 = split_rest(dv[1]);
-      o.v[0][i] = (__float_as_uint(dv[0]) >> 16) | (__float_as_uint(dv[1]) & 0xFFFF0000u);
-      o.v[1][i] = pack_bf16x2(r0, r1);
+      three_parts(dv[0], dv[1], p0, p1, p2);
+      o.v[0][i] = p0, o.v[1][i] = p1, o.v[2][i] = p2;
     }
   }
 }
@@ -98,6 +103,8 @@ __device__ __forceinline__ void prod_tile(const TrainProd& job, const TrainProds
   const bool r8 = (r & 7) == 0;
   const bool masked = job.mask >= 0 && J.drop.thr > 0;
   const uint64_t ctr = masked ? drop_counter(J.drop, job.mask) : 0;
+  // (the workgroups of the first adapter columns leave the mask's bits for the kernels behind)
+  uint8_t* const keep = masked && J.drop.bits && j0 == 0 ? J.drop.bits + (int64_t)job.mask * M * (K >> 3) : nullptr;
   const int64_t nst = (K + 31) / 32;
   const int64_t a0 = nst * split / J.splits, a1 = nst * (split + 1) / J.splits;
   const int64_t s0 = a0 + (a1 - a0) * wave / W, s1 = a0 + (a1 - a0) * (wave + 1) / W;
@@ -134,7 +141,16 @@ __device__ __forceinline__ void prod_tile(const TrainProd& job, const TrainProds
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       u32x4_t v = d.x[i];
-      if (masked) v &= drop_lanes((uint64_t)(xrow[i] * (K >> 3) + 4 * st + g), ctr, J.drop);
+      if (masked) {
+        const int64_t group = xrow[i] * (K >> 3) + 4 * st + g;
+        if (keep) {
+          const uint32_t b = drop_bits((uint64_t)group, ctr, J.drop);
+          if (16 * i + row < rows && 32 * st + 8 * g < K) keep[group] = (uint8_t)b;
+          v &= bit_lanes(b);
+        } else {
+          v &= drop_lanes((uint64_t)group, ctr, J.drop);
+        }
+      }
       *reinterpret_cast<u32x4_t*>(sl + (16 * i + row) * kRowB + 16 * g) = v;
     }
 #pragma unroll
@@ -232,7 +248,7 @@ struct GatedU {
 
 template <int ACT, int RT, int JT, int W>
 __global__ __launch_bounds__(64 * W) void k_gated_u(GatedU G) {
-  constexpr uint32_t kXs = 16u * RT * kRowB, kBs = 32u * kBtRow<JT>, kSlice = JT ? 4u * kXs + 2u * kBs : 16u;
+  constexpr uint32_t kXs = 16u * RT * kRowB, kBs = 32u * kBtRow<JT>, kSlice = JT ? 6u * kXs + 2u * kBs : 16u;
   constexpr uint32_t kSum = RT * 16 * JT * 16 * 4 * 2;
   __shared__ __attribute__((aligned(16))) char lds[W * (kSlice > kSum ? kSlice : kSum)];
   const int64_t N = G.N, M = G.M, row0 = (int64_t)blockIdx.x * 16 * RT;
@@ -277,7 +293,7 @@ __global__ __launch_bounds__(64 * W) void k_gated_u(GatedU G) {
 #pragma unroll
       for (int c = 0; c < JA; ++c) acc[sd][i][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   char* const sl = lds + wave * kSlice;
-  char* const sb = sl + 4 * kXs;
+  char* const sb = sl + 6 * kXs;
   auto compute = [&](int64_t st, const Ld& d) {
     const int64_t k = 32 * st + 8 * g;
 #pragma unroll
@@ -290,10 +306,11 @@ __global__ __launch_bounds__(64 * W) void k_gated_u(GatedU G) {
       }
       if constexpr (JT > 0) {
         char* const p = sl + (16 * i + row) * kRowB + 16 * g;
-        *reinterpret_cast<u32x4_t*>(p) = o.g[0];
-        *reinterpret_cast<u32x4_t*>(p + kXs) = o.g[1];
-        *reinterpret_cast<u32x4_t*>(p + 2 * kXs) = o.v[0];
-        *reinterpret_cast<u32x4_t*>(p + 3 * kXs) = o.v[1];
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          *reinterpret_cast<u32x4_t*>(p + q * kXs) = o.g[q];
+          *reinterpret_cast<u32x4_t*>(p + (3 + q) * kXs) = o.v[q];
+        }
       }
     }
     if constexpr (JT > 0) {
@@ -306,12 +323,12 @@ __global__ __launch_bounds__(64 * W) void k_gated_u(GatedU G) {
       }
 #pragma unroll
       for (int sd = 0; sd < 2; ++sd) {
-        bf16x8_t xf[RT][2], bf[JA];
+        bf16x8_t xf[RT][3], bf[JA];
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            xf[i][q] = as_bf16x8(*reinterpret_cast<const u32x4_t*>(sl + (2 * sd + q) * kXs + (16 * i + frow) * kRowB + 16 * fg));
+          for (int q = 0; q < 3; ++q)
+            xf[i][q] = as_bf16x8(*reinterpret_cast<const u32x4_t*>(sl + (3 * sd + q) * kXs + (16 * i + frow) * kRowB + 16 * fg));
 #pragma unroll
         for (int c = 0; c < JT; ++c) {
           const char* p = sb + sd * kBs + (8u * fg + (frow >> 2)) * kBtRow<JT> + 32u * c + 8u * (frow & 3);
@@ -322,7 +339,7 @@ __global__ __launch_bounds__(64 * W) void k_gated_u(GatedU G) {
 #pragma unroll
           for (int c = 0; c < JT; ++c)
 #pragma unroll
-            for (int q = 1; q >= 0; --q) acc[sd][i][c] = mfma16x16x32(xf[i][q], bf[c], acc[sd][i][c]);
+            for (int q = 2; q >= 0; --q) acc[sd][i][c] = mfma16x16x32(xf[i][q], bf[c], acc[sd][i][c]);
       }
     }
   };
@@ -382,11 +399,16 @@ hipError_t launch_u_act(const GatedU& G, hipStream_t s) {
 //
 // out[j][c] = s sum_m P[m][j] Q[m][c], computed as out^T[c][j] on 16x16x32 bf16 MFMA: Q^T as the A operand and P^T as B, both
 // read from row-major LDS tiles with the transpose read.  P (float32) enters as three bf16 parts (24 bits); Q is bf16, under
-// its mask where it has one, or dg or dv formed from dh, g and v, in two parts (16 bits; the smallest product of parts is
-// left out).  A workgroup of 4 waves takes 128 columns x 64 adapter rows x up to kChunk rows, 32 rows per step in one of two LDS
-// buffers, the next two steps' loads in registers.  The first chunk goes to the output itself, the others to float32 partials
-// that a second kernel adds in chunk order: results do not depend on timing.
-constexpr int kChunk = 512;
+// its mask where it has one, or dg or dv formed from dh, g and v, in three parts too (the three smallest products of parts, 2^-24 and
+// less, are left out).  A workgroup of 4 waves takes 128 columns x 64 adapter rows x one chunk of rows, 32 rows per step in one of two
+// LDS buffers, the next two steps' loads in registers.  The first chunk goes to the output itself, the others to float32 partials
+// in the outputs' order that a second kernel adds in chunk order: results do not depend on timing.
+//
+// Chunk: as many as give about 256 workgroups, of at most 512 rows.
+int64_t grad_chunk(int64_t M, int64_t CC) {
+  const int64_t tiles = (CC + 127) / 128, chunks = std::max<int64_t>(1, (256 + tiles - 1) / tiles);
+  return std::max<int64_t>(64, std::min<int64_t>(512, ((M + chunks - 1) / chunks + 31) / 32 * 32));
+}
 constexpr uint32_t kQ = 32 * 256, kP = 32 * 128;
 
 struct TrainGrads {
@@ -395,10 +417,10 @@ struct TrainGrads {
   int tile0[5];   // first column tile of each job
   const uint16_t* gu;
   int64_t M, N, CC;
-  int n, r, block0;
+  int n, r, block0, chunk;
   float scale;
   DropArgs drop;
-  float* part;    // extra chunks x r x CC
+  float* part;    // extra chunks x (the jobs' outputs)
 };
 
 __device__ __forceinline__ uint32_t q_off(uint32_t row, uint32_t chunk) {
@@ -414,21 +436,21 @@ __device__ __forceinline__ uint32_t p_off(uint32_t row, uint32_t chunk) {
 template <int SRC, int ACT>
 __device__ __forceinline__ void grad_tile(const TrainGrads& G, const TrainGrad& job, int ji, int64_t mb, int chunk, int cb, int j0,
                                           char* lds) {
-  constexpr int QP = SRC == 0 ? 1 : 2;  // parts of Q
+  constexpr int QP = SRC == 0 ? 1 : 3;  // parts of Q
   constexpr uint32_t kBuf = QP * kQ + 3 * kP;
   const int r = G.r;
   const int64_t C = job.C, M = G.M;
-  const int rows = (int)min<int64_t>(kChunk, M - mb);
+  const int rows = (int)min<int64_t>(G.chunk, M - mb);
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int jt = min(4, (r - j0 + 15) / 16);
   const bool r4 = (r & 3) == 0;
   const bool masked = SRC == 0 && job.mask >= 0 && G.drop.thr > 0;
-  const uint64_t ctr = masked ? drop_counter(G.drop, job.mask) : 0;
+  const uint8_t* const keep = masked ? G.drop.bits + ((int64_t)job.mask * M + mb) * (C >> 3) : nullptr;
   const __amdgpu_buffer_rsrc_t qr = tile_rsrc(job.Q + mb * C, (uint32_t)(rows * C * 2));
   const __amdgpu_buffer_rsrc_t gr = tile_rsrc(SRC ? G.gu + mb * 2 * C : nullptr, SRC ? (uint32_t)(rows * C * 4) : 0u);
   const uint32_t qrow = (uint32_t)tid >> 4, qch = (uint32_t)tid & 15u;
   const int64_t qcol = min<int64_t>(cb + 8 * qch, C - 8);  // clamped: outputs past C are dropped
-  struct Stage { u32x4_t q[2], g[2], v[2]; f32x4_t p[2]; };
+  struct Stage { u32x4_t q[2], g[2], v[2]; f32x4_t p[2]; uint32_t keep[2]; };
   auto ld = [](__amdgpu_buffer_rsrc_t rs, int64_t elem) {
     return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (uint32_t)(elem * 2), 0, 0));
   };
@@ -439,12 +461,14 @@ __device__ __forceinline__ void grad_tile(const TrainGrads& G, const TrainGrad& 
       s.q[i] = ld(qr, row * C + qcol);
       if constexpr (SRC > 0) s.g[i] = ld(gr, row * 2 * C + qcol);
       if constexpr (SRC == 1) s.v[i] = ld(gr, row * 2 * C + C + qcol);
+      if constexpr (SRC == 0) s.keep[i] = masked && row < rows ? keep[row * (C >> 3) + (qcol >> 3)] : 255u;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = m0 + (int)qrow + 16 * i, jb = j0 + 4 * (int)qch;
       f32x4_t v = {0.f, 0.f, 0.f, 0.f};
       if (m < rows && jb < r) {
+#pragma unroll 4
         for (int sp = 0; sp < job.p_splits; ++sp) {
           const float* p = job.P + ((int64_t)sp * M + mb + m) * job.ldp + job.col0 + jb;
           if (r4) {
@@ -468,26 +492,17 @@ __device__ __forceinline__ void grad_tile(const TrainGrads& G, const TrainGrad& 
       char* const at = buf + q_off(row, qch);
       if constexpr (SRC == 0) {
         u32x4_t q = s.q[i];
-        if (masked) q &= drop_lanes((uint64_t)((mb + m0 + row) * (C >> 3) + (qcol >> 3)), ctr, G.drop);
+        if (masked) q &= bit_lanes(s.keep[i]);
         *reinterpret_cast<u32x4_t*>(at) = q;
       } else {
         Dgu o;
         form_dgu<ACT, false, SRC == 1, SRC == 2>(s.q[i], s.g[i], SRC == 1 ? s.v[i] : s.g[i], o);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) *reinterpret_cast<u32x4_t*>(at + k * kQ) = SRC == 1 ? o.g[k] : o.v[k];
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4_t*>(at + k * kQ) = SRC == 1 ? o.g[k] : o.v[k];
       }
       uint32_t part[3][2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float v0 = s.p[i][2 * t], v1 = s.p[i][2 * t + 1];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {  // (the third part is the whole rest: at most 8 bits)
-          const float r0 = k < 2 ? split_rest(v0) : 0.0f, r1 = k < 2 ? split_rest(v1) : 0.0f;
-          part[k][t] = (__float_as_uint(v0) >> 16) | (__float_as_uint(v1) & 0xFFFF0000u);
-          v0 = r0;
-          v1 = r1;
-        }
-      }
+      for (int t = 0; t < 2; ++t) three_parts(s.p[i][2 * t], s.p[i][2 * t + 1], part[0][t], part[1][t], part[2][t]);
 #pragma unroll
       for (int k = 0; k < 3; ++k)
         *reinterpret_cast<uint2*>(buf + QP * kQ + k * kP + p_off(row, qch >> 1) + 8u * (qch & 1u)) = uint2{part[k][0], part[k][1]};
@@ -536,10 +551,9 @@ __device__ __forceinline__ void grad_tile(const TrainGrads& G, const TrainGrad& 
         const bf16x8_t p = tr_frag(buf + k * kP + pa[t][0], buf + k * kP + pa[t][1]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if constexpr (QP == 2) {
-            if (k < 2) acc[c][t] = mfma16x16x32(q[1][c], p, acc[c][t]);
-          }
-          acc[c][t] = mfma16x16x32(q[0][c], p, acc[c][t]);
+#pragma unroll
+          for (int l = QP - 1; l >= 0; --l)
+            if (k + l < 3) acc[c][t] = mfma16x16x32(q[l][c], p, acc[c][t]);
         }
       }
     }
@@ -559,14 +573,13 @@ __device__ __forceinline__ void grad_tile(const TrainGrads& G, const TrainGrad& 
       const int64_t c0 = cb + 32 * w + 16 * c + 4 * (int64_t)g;
       if (c0 >= C) continue;  // C % 4 == 0: whole pieces
       const f32x4_t v = acc[c][t];
-      if (chunk > 0) {
-        *reinterpret_cast<f32x4_t*>(G.part + ((int64_t)(chunk - 1) * r + j) * G.CC + G.at[ji] + c0) = v;
-      } else if (!job.cols_major) {
-        *reinterpret_cast<f32x4_t*>(job.out + (int64_t)j * C + c0) =
-            f32x4_t{G.scale * v[0], G.scale * v[1], G.scale * v[2], G.scale * v[3]};
+      float* const out = chunk > 0 ? G.part + ((int64_t)(chunk - 1) * G.CC + G.at[ji]) * r : job.out;
+      const float f = chunk > 0 ? 1.0f : G.scale;
+      if (!job.cols_major) {
+        *reinterpret_cast<f32x4_t*>(out + (int64_t)j * C + c0) = f32x4_t{f * v[0], f * v[1], f * v[2], f * v[3]};
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) job.out[(c0 + i) * r + j] = G.scale * v[i];
+        for (int i = 0; i < 4; ++i) out[(c0 + i) * r + j] = f * v[i];
       }
     }
   }
@@ -575,13 +588,13 @@ __device__ __forceinline__ void grad_tile(const TrainGrads& G, const TrainGrad& 
 // ACT < 0: no job forms dg or dv
 template <int ACT>
 __global__ __launch_bounds__(256) void k_train_grad(TrainGrads G) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * ((ACT < 0 ? 1 : 2) * kQ + 3 * kP)];
+  __shared__ __attribute__((aligned(16))) char lds[2 * ((ACT < 0 ? 1 : 3) * kQ + 3 * kP)];
   const int ct = G.tile0[G.n];
   const int block = G.block0 + (int)blockIdx.x, chunk = block / ct, bx = block % ct;
   int ji = 0;
   while (ji + 1 < G.n && bx >= G.tile0[ji + 1]) ++ji;
   const TrainGrad& job = G.j[ji];
-  const int64_t mb = (int64_t)chunk * kChunk;
+  const int64_t mb = (int64_t)chunk * G.chunk;
   const int cb = (bx - G.tile0[ji]) * 128, j0 = blockIdx.y * 64;
   if constexpr (ACT >= 0) {
     if (job.kind == 1) return grad_tile<1, ACT>(G, job, ji, mb, chunk, cb, j0, lds);
@@ -592,17 +605,48 @@ __global__ __launch_bounds__(256) void k_train_grad(TrainGrads G) {
 
 // out += scale * (the further chunks, in order)
 __global__ __launch_bounds__(256) void k_train_grad_add(TrainGrads G, int chunks) {
-  const int64_t n = G.CC * G.r;
+  const int64_t n = G.CC * G.r / 4;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    float v = 0.0f;
-    for (int c = 0; c < chunks; ++c) v += G.part[(int64_t)c * n + i];
-    const int64_t j = i / G.CC, cc = i % G.CC;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int c = 0; c < chunks; ++c) {
+      const f32x4_t p = reinterpret_cast<const f32x4_t*>(G.part)[(int64_t)c * n + i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += p[k];
+    }
     int ji = 0;
-    while (ji + 1 < G.n && cc >= G.at[ji + 1]) ++ji;
-    const TrainGrad& job = G.j[ji];
-    const int64_t c = cc - G.at[ji];
-    float* o = job.cols_major ? job.out + c * G.r + j : job.out + j * job.C + c;
-    *o += G.scale * v;
+    while (ji + 1 < G.n && 4 * i >= G.at[ji + 1] * G.r) ++ji;
+    f32x4_t* const o = reinterpret_cast<f32x4_t*>(G.j[ji].out + 4 * i - G.at[ji] * G.r);
+    f32x4_t w = *o;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] += G.scale * v[k];
+    *o = w;
+  }
+}
+
+struct TrainSums {
+  TrainSum j[2];
+};
+__global__ __launch_bounds__(256) void k_train_sum(TrainSums S, int64_t M) {
+  const TrainSum& job = S.j[blockIdx.y];
+  const int64_t n = M * job.ld;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+    if (n % 4 == 0) {
+      f32x4_t v = *reinterpret_cast<const f32x4_t*>(job.t + i);
+#pragma unroll 4
+      for (int c = 1; c < job.splits; ++c) {
+        const f32x4_t p = *reinterpret_cast<const f32x4_t*>(job.t + c * n + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] += p[k];
+      }
+      *reinterpret_cast<f32x4_t*>(job.t + i) = v;
+    } else {
+      for (int k = 0; k < 4 && i + k < n; ++k) {
+        float v = job.t[i + k];
+        for (int c = 1; c < job.splits; ++c) v += job.t[c * n + i + k];
+        job.t[i + k] = v;
+      }
+    }
   }
 }
 
@@ -648,8 +692,21 @@ hipError_t launch_gated_u(const uint16_t* dh, const uint16_t* gu, int act, int64
   }
 }
 
+hipError_t launch_train_sum(const TrainSum* jobs, int n, int64_t M, hipStream_t s) {
+  TrainSums S{};
+  int live = 0, ld = 0;
+  for (int i = 0; i < n; ++i) {
+    if (jobs[i].splits < 2 || live == 2) continue;
+    S.j[live++] = jobs[i];
+    ld = std::max(ld, jobs[i].ld);
+  }
+  if (live == 0 || M == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_train_sum, dim3((unsigned)std::min<int64_t>((M * ld + 1023) / 1024, 2048), (unsigned)live), dim3(256), 0, s, S, M);
+  return hipGetLastError();
+}
+
 size_t train_grad_floats(int64_t M, int64_t C_total, int r) {
-  return M > kChunk ? (size_t)((M - 1) / kChunk) * (size_t)r * (size_t)C_total : 0;
+  return M > 0 ? (size_t)((M - 1) / grad_chunk(M, C_total)) * (size_t)r * (size_t)C_total : 0;
 }
 
 hipError_t launch_train_grads(const TrainGrad* jobs, int n, int64_t M, int r, const uint16_t* gu, int64_t N, int act, float scale,
@@ -674,7 +731,8 @@ hipError_t launch_train_grads(const TrainGrad* jobs, int n, int64_t M, int r, co
   G.scale = scale;
   G.drop = drop;
   G.part = part;
-  const int64_t chunks = std::max<int64_t>(1, (M + kChunk - 1) / kChunk), wgs = chunks * G.tile0[n];
+  G.chunk = (int)grad_chunk(M, G.CC);
+  const int64_t chunks = std::max<int64_t>(1, (M + G.chunk - 1) / G.chunk), wgs = chunks * G.tile0[n];
   if (wgs > INT_MAX) return hipErrorInvalidValue;
   const hipError_t e = launch_blocks(wgs, [&](unsigned blocks, int b0) {
     const dim3 grid(blocks, (unsigned)((r + 63) / 64));
@@ -685,7 +743,7 @@ hipError_t launch_train_grads(const TrainGrad* jobs, int n, int64_t M, int r, co
     else hipLaunchKernelGGL(k_train_grad<ACT_GELU_TANH>, grid, dim3(256), 0, s, G);
   });
   if (e != hipSuccess || chunks == 1) return e;
-  hipLaunchKernelGGL(k_train_grad_add, dim3((unsigned)std::min<int64_t>((G.CC * r + 255) / 256, 2048)), dim3(256), 0, s, G,
+  hipLaunchKernelGGL(k_train_grad_add, dim3((unsigned)std::min<int64_t>((G.CC * r + 1023) / 1024, 2048)), dim3(256), 0, s, G,
                      (int)(chunks - 1));
   return hipGetLastError();
 }
