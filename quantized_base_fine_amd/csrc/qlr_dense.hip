@@ -35,6 +35,8 @@ enum { DENSE_PLAIN = 0, DENSE_GATED = 1, DENSE_DROP = 2 };
 
 constexpr uint32_t kPiece = 128 * 128;  // bytes: 128 rows of 64 bf16
 constexpr int kTileFloats = 256 * 256;
+// Of a split contraction of the tiled product: steps of 64 in a range at least, and ranges at most.
+constexpr int64_t kSplitSteps = 4, kMaxSplits = 8;
 
 struct FragX { u32x4_t f[4][2]; };
 struct FragW { u32x4_t f[2][2]; };
@@ -561,6 +563,27 @@ __global__ __launch_bounds__(512) void k_dense_rest_drop(DenseArgs P) {
   });
 }
 
+// The sums of a tiled product's ranges (64 x 128 and 128 x 128 tiles, qlr_tile.h) added in order, 8 output columns of a row to a thread.
+template <int KIND>
+__global__ __launch_bounds__(256) void k_tile_sum(DenseArgs P, int64_t ld) {
+  const int64_t items = (P.NO + 7) / 8, id = (int64_t)blockIdx.x * 256 + threadIdx.x, row = id / items, col = id % items * 8;
+  if (row >= P.M) return;
+  const float* p = P.part + row * ld + col;
+  const bool two = col + 4 < P.NO;  // (the columns' second four are there, a row's end rounded up to four)
+  f32x4_t s[4] = {};
+#pragma unroll 4
+  for (int k = 0; k < P.splits; ++k, p += P.M * ld) {
+#pragma unroll
+    for (int h = 0; h < (KIND == DENSE_GATED ? 4 : 2); ++h) {
+      f32x4_t u = {0.f, 0.f, 0.f, 0.f};
+      if ((h & 1) == 0 || two) u = *reinterpret_cast<const f32x4_t*>(p + (h >> 1) * (ld / 2) + 4 * (h & 1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[h][j] += u[j];
+    }
+  }
+  result8<KIND>(P, row, col, s[0], s[1], s[2], s[3]);
+}
+
 // ---------------------------------------------------------------- the weight
 //
 // Wd = bf16(level scale), row by row (rows x K), or transposed (K x rows); each weight rounded once to nearest.
@@ -711,6 +734,37 @@ hipError_t launch_dense_k(DenseArgs a, hipStream_t s) {
 unsigned grid_of(int64_t items) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + 255) / 256, 256 * 16)); }
 
 }  // namespace
+
+// A step of a tile is bound by its workgroup's LDS traffic (dequantized weights in and fragments out), so more rows a tile and all
+// CUs at work are what counts: up to 64 rows 64 x 128 tiles, from there on 128 x 128 ones, in ranges that make about 512
+// workgroups, two to a CU.  Input gradient of 777 rows, 2048 columns over 5632 (2-bit): 40 us and 6.5 for the sums, as 64 x 128 tiles
+// 55, in two ranges of those 47 and 5; of 333, 4096 over 4096 (8-bit): 37 and 6.6, 57, 50 and 5; of 64, 1024 over 2048: 11 and 4,
+// unsplit 24.  A tile of a few steps more than fills the GPU by itself: 333 rows, 1403 gated columns over 2048 unsplit
+// 22 us, in 3 to 7 ranges 24 to 27.
+int train_tile_splits(int64_t M, int64_t cols, int64_t KC) {
+  // (256 x 256 tiles: see launch_tile)
+  if ((M + 255) / 256 * ((cols + 255) / 256) >= 192) return 1;
+  const int64_t nt = (cols + 127) / 128, steps = (KC + 63) / 64;
+  if (steps <= 32 && (M + 63) / 64 * nt >= 128) return 1;
+  const int64_t bm = M <= 64 ? 64 : 128, tiles = (M + bm - 1) / bm * nt;
+  return (int)std::max<int64_t>(1, std::min({(int64_t)512 / tiles, steps / kSplitSteps, (int64_t)kMaxSplits}));
+}
+
+hipError_t launch_tile_sum(const TrainArgs& a, int64_t NO, bool gated, hipStream_t s) {
+  DenseArgs d{};
+  d.M = a.M;
+  d.NO = NO;
+  d.y = a.y;
+  d.ydt = a.ydt;
+  d.act = a.act;
+  d.gu = a.gu;
+  d.splits = a.splits;
+  d.part = a.part;
+  const dim3 grid((unsigned)((a.M * ((NO + 7) / 8) + 255) / 256));
+  if (gated) hipLaunchKernelGGL(k_tile_sum<DENSE_GATED>, grid, dim3(256), 0, s, d, train_part_cols(NO, true));
+  else hipLaunchKernelGGL(k_tile_sum<DENSE_PLAIN>, grid, dim3(256), 0, s, d, train_part_cols(NO, false));
+  return hipGetLastError();
+}
 
 constexpr int64_t kDenseRows = 1024;
 

@@ -202,6 +202,7 @@ struct TrainLayout {
   int t_splits, u_splits;  // of the masked product, and of the gated block's u
   bool dense;              // the product of many rows, through a dense copy of the weight at wd; xt, wt, sums: see qlr_dense.hip
   size_t wd, xt, wt, sums;
+  int k_splits;            // the others: ranges of the contraction, their sums at sums
 };
 // Rows from which the adapters' partial sums are added once, before the kernels that read them many times.
 constexpr int64_t kSumRows = 256;
@@ -243,6 +244,10 @@ TrainLayout train_layout(qlr_op op, int64_t M, int64_t N, int64_t K, int32_t r) 
       L.wt = L.xt + up((size_t)two * (size_t)nb * (size_t)M * 128);
       L.sums = L.wt + up((size_t)(bwd ? two : 1) * (size_t)nb * (size_t)wrows * 128);
       at = L.sums + (size_t)p.rest * (size_t)p.splits * qlr::kDensePartFloats * sizeof(float);
+    } else {
+      L.k_splits = qlr::train_tile_splits(M, bwd ? K : two * N, KC);
+      L.sums = at;
+      if (L.k_splits > 1) at = L.sums + (size_t)L.k_splits * (size_t)M * (size_t)qlr::train_part_cols(NO, !bwd) * sizeof(float);
     }
   }
   L.total = at;
@@ -485,7 +490,16 @@ qlr::TrainArgs train_args(int64_t M, const qlr_qweight* w, int64_t N, int32_t r,
   a.scale = scale;
   a.drop = drop;
   a.halves = 1;
+  a.splits = 1;
   return a;
+}
+
+// h of the gated block, or dx, on the tiled product.
+hipError_t run_tiles(qlr::TrainArgs& a, int64_t NO, char* ws, const TrainLayout& lay, bool gated, const qlr::Levels& lv, hipStream_t s) {
+  a.splits = lay.k_splits;
+  a.part = reinterpret_cast<float*>(ws + lay.sums);
+  const hipError_t e = gated ? qlr::launch_gated_gemm(a, lv, s) : qlr::launch_drop_dx(a, lv, s);
+  return e == hipSuccess && a.splits > 1 ? qlr::launch_tile_sum(a, NO, gated, s) : e;
 }
 
 // The product of a, of NO columns over KC, through a dense copy of the weight: h of the gated block, or (tr) dx.
@@ -1625,7 +1639,7 @@ qlr_status qlr_linear_bwd_dropout(const void* dy, qlr_dtype dydt, const void* x,
     a.ydt = (int)dxdt;
     const qlr::Levels lv = levels_arg(w->bits);
     if (lay.dense) e = run_dense(a, K, N, wsp, lay, false, true, lv, s);
-    else e = d.thr > 0 ? qlr::launch_drop_dx(a, lv, s) : qlr::launch_grouped_dx(a, lv, s);
+    else e = run_tiles(a, K, wsp, lay, false, lv, s);
     if (e != hipSuccess) return hip_fail(e, "input-gradient launch");
   }
   if (r > 0) {
@@ -1701,7 +1715,7 @@ qlr_status qlr_gated_fwd(const void* x, qlr_dtype xdt, int64_t M, const qlr_qwei
   const qlr::Levels lv = levels_arg(w->bits);
   if (few) e = qlr::launch_gated_few(a, lv, s);
   else if (lay.dense) e = run_dense(a, N, K, reinterpret_cast<char*>(ws), lay, true, false, lv, s);
-  else e = qlr::launch_gated_gemm(a, lv, s);
+  else e = run_tiles(a, N, reinterpret_cast<char*>(ws), lay, true, lv, s);
   if (e != hipSuccess) return hip_fail(e, "gated product launch");
   return QLR_OK;
 }
@@ -1779,7 +1793,7 @@ qlr_status qlr_gated_bwd(const void* dh, qlr_dtype dhdt, const void* gu, const v
     if (d.thr > 0) a.halves = 2;
     else a.r = 2 * r;  // the two adapters are one of 2 r columns
     if (lay.dense) e = run_dense(a, K, 2 * N, wsp, lay, false, true, lv, s);
-    else e = d.thr > 0 ? qlr::launch_drop_dx(a, lv, s) : qlr::launch_grouped_dx(a, lv, s);
+    else e = run_tiles(a, K, wsp, lay, false, lv, s);
     if (e != hipSuccess) return hip_fail(e, "input-gradient launch");
   }
   if (r > 0) {

@@ -240,7 +240,14 @@ struct TrainArgs : TileArgs {
   int halves;  // transposed with dropout: adapters side by side, each with r columns of t, rows of ab and a mask of its own
   int act;
   uint16_t* gu;  // gated: M x 2N bf16 pre-activations, or null
+  int splits;    // ranges of the contraction whose sums go to part (splits x M x train_part_cols floats), or 1
+  float* part;
 };
+// Ranges of the contraction (KC) for the calls that run as 64 x 128 or 128 x 128 tiles of `cols` columns (gated: both sides'): see launch_tile.
+int train_tile_splits(int64_t M, int64_t cols, int64_t KC);
+constexpr int64_t train_part_cols(int64_t NO, bool gated) { return gated ? 2 * ((NO + 3) / 4 * 4) : NO; }
+// y (and gu) from the ranges' sums.
+hipError_t launch_tile_sum(const TrainArgs& a, int64_t NO, bool gated, hipStream_t s);
 // Rows up to which the few-rows kernels take an expert, or a call of the 8-bit product.
 constexpr int kFewRows = 16;
 
@@ -272,7 +279,7 @@ hipError_t launch_grouped_transpose(const uint16_t* B, int experts, int64_t N, i
 // h = act(gate) up, M x N (and gu): rows of x from 17 on, and up to kFewRows rows.
 hipError_t launch_gated_gemm(const TrainArgs& a, const Levels& lv, hipStream_t s);
 hipError_t launch_gated_few(const TrainArgs& a, const Levels& lv, hipStream_t s);
-// dx = dy W' + sum over the halves of mask (scale u A): K % 64 == 0, N % 8 == 0.
+// dx = dy W' + sum over the halves of mask (scale u A), of everything without a mask: K % 64 == 0, N % 8 == 0.
 hipError_t launch_drop_dx(const TrainArgs& a, const Levels& lv, hipStream_t s);
 
 // The same products of many rows through a dense bf16 copy of the weight in the workspace (qlr_dense.hip).

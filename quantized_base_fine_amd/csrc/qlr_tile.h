@@ -281,7 +281,10 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
   // ---- which tile.  Workgroup b runs on XCD b % 8; each XCD takes a contiguous range of tiles.
   // With P.rest the tiles are counted in 256 x 256 ones and those of a last partial
   // round are left to the 128 x 128 kernel (tile_split): this kernel takes either part.
-  int e = 0, row0 = 0, row_end = (int)P.M, tile_n;
+  // (kSplit: each tile P.splits times, the ranges of its contraction)
+  constexpr bool kSplit = KIND >= TILE_GATED && BM < 256;
+  int e = 0, row0 = 0, row_end = (int)P.M, tile_n, range = 0, ranges_k = 1;
+  if constexpr (kSplit) ranges_k = P.rest ? 1 : P.splits;
   {
     constexpr int kBig = 256;
     const bool sub = BM == 128 && P.rest;  // the 128 x 128 kernel on the rest of the 256 x 256 tiles
@@ -298,9 +301,13 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
                       reinterpret_cast<uint32_t*>(sW1) + wave * kRestRows, row_half, col_half);
       if (big < 0) return;  // (as below)
     } else {
-      const int per = (split + 7) / 8, loc = (block0 + (int)blockIdx.x) >> 3;
+      const int units = kSplit ? split * ranges_k : split, per = (units + 7) / 8, loc = (block0 + (int)blockIdx.x) >> 3;
       big = (int)(blockIdx.x & 7) * per + loc;
-      if (loc >= per || big >= split) return;  // the whole workgroup, before any barrier
+      if (loc >= per || big >= units) return;  // the whole workgroup, before any barrier
+      if constexpr (kSplit) {
+        range = big / split;
+        big -= range * split;
+      }
     }
     // order: blocks of kGroupM row tiles, their column tiles one after the other, row tiles innermost
     const int grp = big / (kGroupM * ntiles), in = big - grp * kGroupM * ntiles;
@@ -326,6 +333,8 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
   const int n0 = tile_n * BO;
   const uint32_t kbytes = (uint32_t)(KIND == TILE_I8 ? K : kTR ? 2 * N : 2 * K);  // bytes of one x row
   const int nsteps = (int)((kbytes + 127) / 128);
+  const int step0 = kSplit ? __builtin_amdgcn_readfirstlane((int)((int64_t)nsteps * range / ranges_k)) : 0;
+  const int step1 = kSplit ? __builtin_amdgcn_readfirstlane((int)((int64_t)nsteps * (range + 1) / ranges_k)) : nsteps;
 
   if constexpr (L::kTabBytes > 0) {
     float* sL = reinterpret_cast<float*>(sX0);
@@ -534,29 +543,29 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
   // x (and int8 weights) of step k are loaded kAhead steps before, codes kSets steps before.
   constexpr int kAhead = L::kXBufs - 1, kSets = L::kXBufs == 4 ? 4 : 2;
   Ws wa, wb_, wc, wd;
-  direct(xr, sX0, 0, xloads);
+  direct(xr, sX0, step0, xloads);
   if constexpr (KIND == TILE_I8) direct(wr, sW0, 0, wloads);
   if constexpr (kAhead > 1) {
-    direct(xr, sX1, 1, xloads);
+    direct(xr, sX1, step0 + 1, xloads);
     if constexpr (KIND == TILE_I8) direct(wr, sW1, 1, wloads);
   }
-  if constexpr (kAhead > 2) direct(xr, sX2, 2, xloads);
+  if constexpr (kAhead > 2) direct(xr, sX2, step0 + 2, xloads);
   if constexpr (KIND != TILE_I8) {
-    load_w(0, wa);
+    load_w(step0, wa);
     // (loads in the steps' order.  The loop's head waits for all loads, or all but one to three, all the same: in one of four
     // steps of the coded 64 x 128 tiles what was loaded ahead has to have arrived)
     __builtin_amdgcn_sched_barrier(0);
-    load_w(1, wb_);
+    load_w(step0 + 1, wb_);
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (kSets == 4) {
-      load_w(2, wc);
+      load_w(step0 + 2, wc);
       __builtin_amdgcn_sched_barrier(0);
-      load_w(3, wd);
+      load_w(step0 + 3, wd);
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (CPT == 16) place_codes16<BITS>(wa.c, dh);
     Lut4 lut{};
-    const float ap = scale_of(wa, 0);
+    const float ap = scale_of(wa, step0);
     if constexpr (BITS == 4) lut = make_lut4(lv, ap);
     store_w(wa, lut, ap, std::integral_constant<int, 0>{}, sW0);
     store_w(wa, lut, ap, std::integral_constant<int, 1>{}, sW0);
@@ -646,7 +655,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
     sub(std::integral_constant<int, 3>{});
     step_barrier();
   };
-  int k = 0;
+  int k = step0;
   if constexpr (kAhead == 2) {
     for (;;) {
       step(k, sX0, sW0, sX2, sW2, wa, wa);
@@ -659,20 +668,20 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
   } else if constexpr (kAhead == 3) {
     for (;;) {
       step(k, sX0, sW0, sX3, sW1, wb_, wa);
-      if (++k >= nsteps) break;
+      if (++k >= step1) break;
       step(k, sX1, sW1, sX0, sW0, wc, wb_);
-      if (++k >= nsteps) break;
+      if (++k >= step1) break;
       step(k, sX2, sW0, sX1, sW1, wd, wc);
-      if (++k >= nsteps) break;
+      if (++k >= step1) break;
       step(k, sX3, sW1, sX2, sW0, wa, wd);
-      if (++k >= nsteps) break;
+      if (++k >= step1) break;
     }
   } else {
-    for (; k + 1 < nsteps; k += 2) {
+    for (; k + 1 < step1; k += 2) {
       step(k, sX0, sW0, sX1, sW1, wb_, wa);
       step(k + 1, sX1, sW1, sX0, sW0, wa, wb_);
     }
-    if (k < nsteps) step(k, sX0, sW0, sX1, sW1, wb_, wa);
+    if (k < step1) step(k, sX0, sW0, sX1, sW1, wb_, wa);
   }
   if constexpr (kAhead > 1) {
     __builtin_amdgcn_s_waitcnt(0x0070);  // the loads past the last step too, before the buffers are used again
@@ -701,7 +710,8 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
   // ---- adapter blocks (buffer 0 is free: the last barrier has passed)
   // GATED, TRD: the adapters one after the other, each multiplied into sums of its own, of which its side's rows or the
   // elements that its mask keeps are added (so that an infinity of one adapter stays out of the other's results).
-  if (P.r > 0) {
+  // (of a split contraction, in the first range's sums)
+  if (P.r > 0 && range == 0) {
     int halves = KIND == TILE_GATED ? 2 : 1;
     if constexpr (KIND == TILE_TRD) halves = P.halves;
     const int r = P.r;
@@ -827,11 +837,17 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
       if constexpr (KIND == TILE_TRD) {
         // a lane's 16 columns lie in the four groups of its row's 32: a word of the mask's bits, of which it takes one
         // nibble a byte (rows and columns past the end repeat the last: their results are dropped)
+        // (without a mask everything is kept)
+        const bool all = P.drop.thr == 0;
         const uint8_t* const bits = P.drop.bits + (int64_t)hf * P.M * (K >> 3);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int c = 0; c < NT; ++c) {
+            if (all) {
+              keep[i][c] = 0xFFFFu;
+              continue;
+            }
             const int64_t row = min<int64_t>(row0 + mh * (BM / WM) + 32 * i + fr, P.M - 1);
             const int64_t col = min<int64_t>(n0 + nh * (BN / WN) + 32 * c, K - 32);
             const uint32_t w = *reinterpret_cast<const uint32_t*>(bits + row * (K >> 3) + (col >> 3)) >> (4 * h);
@@ -893,6 +909,13 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
       }
       __syncthreads();
     };
+    if (kSplit && ranges_k > 1) {
+      const int64_t ld = train_part_cols(N, true);
+      float* const part = P.part + (int64_t)range * P.M * ld;
+      emit([](float g, float) { return g; }, part, ld, 4);
+      emit([](float, float v) { return v; }, part + ld / 2, ld, 4);
+      return;
+    }
     if (P.gu) {
       emit([](float g, float) { return g; }, P.gu, 2 * N, 2);
       emit([](float, float v) { return v; }, P.gu + N, 2 * N, 2);
@@ -906,14 +929,21 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
     return;
   }
 
-  // ---- output: staged row-major in LDS, stored in 16-byte pieces
-  const int es = P.ydt == DT_F32 ? 4 : 2;
+  // ---- output: staged row-major in LDS, stored in 16-byte pieces (of a split contraction, the range's sums)
+  int es = P.ydt == DT_F32 ? 4 : 2;
+  char* out = reinterpret_cast<char*>(P.y);
+  if constexpr (kSplit && kTR) {
+    if (ranges_k > 1) {
+      es = 4;
+      out = reinterpret_cast<char*>(P.part + (int64_t)range * P.M * NO);
+    }
+  }
   const bool vec = (NO * es) % 16 == 0;
   const int cpr = BN * es / 16;  // 16-byte pieces of a staged row (a power of two)
   auto put = [&](int row, int c, u32x4_t v) {  // piece c of tile row `row`
     const int64_t col = n0 + c * (16 / es);
     if (col >= NO) return;
-    char* dst = reinterpret_cast<char*>(P.y) + ((int64_t)(row0 + row) * NO + col) * es;
+    char* dst = out + ((int64_t)(row0 + row) * NO + col) * es;
     if (vec) {
       *reinterpret_cast<u32x4_t*>(dst) = v;
     } else {
@@ -1089,6 +1119,7 @@ hipError_t launch_tile_t(typename TileParams<KIND>::T a, const Levels& lv, hipSt
   const int ranges = (int)std::min<int64_t>(a.experts, a.M / (a.min_rows + 1));
   int64_t tiles = (a.offsets ? tile_bound(a.M, ranges, BM) : (a.M + BM - 1) / BM) * a.ntiles;
   if (a.rest && BM < 256) tiles = kRestMax * (256 / BM) * (256 / BN);
+  if constexpr (KIND >= TILE_GATED && BM < 256) tiles *= a.rest ? 1 : a.splits;
   if (tiles <= 0) return hipSuccess;
   if (tiles > INT32_MAX - 8) return hipErrorInvalidValue;
   return launch_blocks(8 * ((tiles + 7) / 8), [&](unsigned n, int b0) { hipLaunchKernelGGL(kern, dim3(n), dim3(512), 0, s, a, b0, lv); });
@@ -1124,6 +1155,9 @@ hipError_t launch_tile(typename TileParams<KIND>::T a, const Levels& lv, hipStre
     return launch_tile_t<KIND, BITS, 128, 128>(a, lv, s);
   }
   a.rest = 0;
+  if constexpr (KIND >= TILE_GATED) {
+    if (a.splits > 1) return a.M <= 64 ? launch_tile_t<KIND, BITS, 64, 128>(a, lv, s) : launch_tile_t<KIND, BITS, 128, 128>(a, lv, s);
+  }
   if (a.M < (a.offsets ? (int64_t)a.experts * 64 : 65) || count(128, 128) < 256) return launch_tile_t<KIND, BITS, 64, 128>(a, lv, s);
   return launch_tile_t<KIND, BITS, 128, 128>(a, lv, s);
 }
