@@ -766,14 +766,22 @@ hipError_t launch_tile_sum(const TrainArgs& a, int64_t NO, bool gated, hipStream
   return hipGetLastError();
 }
 
-constexpr int64_t kDenseRows = 1024;
+// When.  The copy costs a fixed time for the weight, 0.5 ns per 1000 weights and two to four launches, and saves the tiled product's own
+// dequantization, whose part grows with the rows; its tiles take longer to begin and to end.  The call through the copy and on
+// the tiled product, 4-bit, r = 16, us: gated forward, K = 4096, rows 1024, 1536, 2048, 4096: N = 4096 108 and 97, 125 and 116,
+// 136 and 135, 244 and 262; N = 11008 224 and 213, 297 and 306, 348 and 365, 636 and 723.  Gated backward under a mask, K = 4096, rows
+// 1536, 2048, 4096: N = 4096 251 and 248, 272 and 272, 430 and 417 (without one 230 and 240, 248 and 264, 389 and 399); N = 11008
+// 519 and 561, 560 and 633, 925 and 954.  Layer backward under a mask, 2048 rows, N x K: 11008 x 4096 267 and 282, 4096 x
+// 4096 157 and 136, 4096 x 11008 333 and 303; 1024 x 1024 80 and 38.  So: from 1536 rows, forward two rounds of tiles, backward a
+// contraction of 8192.
+constexpr int64_t kDenseRows = 1536;
 
 DensePlan dense_plan(int64_t M, int64_t NO, int64_t KC, bool gated) {
   DensePlan p{};
   p.ntiles = (int)((NO + (gated ? 127 : 255)) / (gated ? 128 : 256));
   const int64_t total = (M + 255) / 256 * p.ntiles, rest = total % kCus;
   // (32-bit offsets: 256 rows of x or of the weight stay below 2^31 bytes)
-  p.ok = M >= kDenseRows && KC < (int64_t)1 << 21 && total < INT_MAX - 256;
+  p.ok = M >= kDenseRows && (gated ? total >= 512 : KC >= 8192 && total >= 96) && KC < (int64_t)1 << 21 && total < INT_MAX - 256;
   p.whole = (int)total;
   p.splits = 1;
   const int64_t steps = (KC + 63) / 64, sp = rest > 0 ? std::min({(int64_t)4, kCus / rest, steps / 16}) : 1;

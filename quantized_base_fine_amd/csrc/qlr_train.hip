@@ -227,9 +227,9 @@ hipError_t launch_t(const TrainProds& J, int n, int r, hipStream_t s) {
 }
 
 constexpr int kMaxSplits = 8;
-// Ranges of the contraction so that about 512 workgroups run, each wave with two steps of 32 at least.
-int range_splits(int64_t wgs, int64_t steps, int waves) {
-  const int64_t want = (512 + wgs - 1) / wgs, most = steps / (2 * waves);
+// Ranges of the contraction so that about `target` workgroups run, each wave with two steps at least.
+int range_splits(int64_t wgs, int64_t steps, int waves, int target = 512) {
+  const int64_t want = (target + wgs - 1) / wgs, most = steps / (2 * waves);
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), kMaxSplits));
 }
 
@@ -385,14 +385,105 @@ hipError_t launch_u(const GatedU& G, hipStream_t s) {
                      dim3(64 * W), 0, s, G);
   return hipGetLastError();
 }
-// rows and waves of a workgroup, as gated_u_splits counts them
-int u_rows(int64_t M) { return M >= 512 ? 32 : 16; }
+
+// More than 16 adapter columns: a workgroup of 8 waves takes 64 rows x 64 columns of both sides, 64 columns of dh a step; wave w
+// takes rows 16 (w % 4) .. and half w / 4 of the step.  B's rows are staged once for the workgroup and read with the transpose
+// read; dh, g and v are loaded in the fragments' layout (16 bytes of each of 16 rows a quarter wave) and their parts stay in
+// registers.  The kernel above with four times the columns holds both sides' B per wave: 256 registers, one wave a SIMD, 103 us at
+// 2048 x 11008, r = 64, where this one takes 77 (the arrays' 225 MB: 44).
+template <int ACT>
+__global__ __launch_bounds__(512, 2) void k_gated_u_wide(GatedU G) {
+  constexpr uint32_t kRow = kBtRow<4>, kSide = 64u * kRow, kBuf = 2u * kSide;
+  __shared__ __attribute__((aligned(16))) char lds[2 * kBuf];
+  static_assert(2 * kBuf >= 4 * 32 * 64 * 4, "the second half's sums overlay the buffers");
+  const int64_t N = G.N, M = G.M, row0 = (int64_t)blockIdx.x * 64;
+  const int r = G.r, j0 = blockIdx.y * 64, split = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave & 3, ws = wave >> 2, frow = lane & 15, fg = lane >> 4;
+  const bool r8 = (r & 7) == 0, first = blockIdx.y == 0;
+  const int64_t nst = (N + 63) / 64;
+  const int64_t a0 = nst * split / G.splits, a1 = nst * (split + 1) / G.splits;
+  const u32x4_t zero4 = {0u, 0u, 0u, 0u};
+  const int64_t row = min<int64_t>(row0 + 16 * wr + frow, M - 1);
+  const bool live = row0 + 16 * wr + frow < M;
+  struct Ld { u32x4_t dh, g, v, b[2]; };
+  auto load = [&](int64_t st, Ld& d) {
+    const int64_t k = 64 * st + 32 * ws + 8 * fg, n = 64 * st + (tid >> 3);
+    const bool ok = st < a1 && k < N;
+    d.dh = ok ? ld16g(G.dh + row * N + k) : zero4;
+    d.g = ok ? ld16g(G.gu + row * 2 * N + k) : zero4;
+    d.v = ok ? ld16g(G.gu + row * 2 * N + N + k) : zero4;
+#pragma unroll
+    for (int sd = 0; sd < 2; ++sd) d.b[sd] = st < a1 && n < N ? ld_cols(G.B, sd * N + n, r, j0 + 8 * (tid & 7), r8) : zero4;
+  };
+  f32x4_t acc[2][4];
+#pragma unroll
+  for (int sd = 0; sd < 2; ++sd)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[sd][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](int64_t st, const Ld& d, char* buf) {
+#pragma unroll
+    for (int sd = 0; sd < 2; ++sd) *reinterpret_cast<u32x4_t*>(buf + sd * kSide + (tid >> 3) * kRow + 16 * (tid & 7)) = d.b[sd];
+    Dgu o;
+    form_dgu<ACT, true, true, true>(d.dh, d.g, d.v, o);
+    const int64_t k = 64 * st + 32 * ws + 8 * fg;
+    if (first && live && k < N) {
+      *reinterpret_cast<u32x4_t*>(G.dgu + row * 2 * N + k) = o.gn;
+      *reinterpret_cast<u32x4_t*>(G.dgu + row * 2 * N + N + k) = o.vn;
+    }
+    __syncthreads();
+    const char* const p = buf + (32u * ws + 8u * fg + (frow >> 2)) * kRow + 8u * (frow & 3);
+#pragma unroll
+    for (int sd = 0; sd < 2; ++sd)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bf16x8_t b = tr_frag(p + sd * kSide + 32 * c, p + sd * kSide + 32 * c + 4 * kRow);
+#pragma unroll
+        for (int q = 2; q >= 0; --q) acc[sd][c] = mfma16x16x32(as_bf16x8(sd ? o.v[q] : o.g[q]), b, acc[sd][c]);
+      }
+  };
+  // (a buffer is written again two steps later, behind the barrier that every wave passes past its reads)
+  Ld d0, d1;
+  load(a0, d0);
+  for (int64_t st = a0; st < a1; st += 2) {
+    load(st + 1, d1);
+    compute(st, d0, lds);
+    if (st + 1 >= a1) break;
+    load(st + 2, d0);
+    compute(st + 1, d1, lds + kBuf);
+  }
+  __syncthreads();
+  f32x4_t* const red = reinterpret_cast<f32x4_t*>(lds) + wr * 8 * 64 + lane;
+  if (ws == 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[i * 64] = acc[i >> 2][i & 3];
+  __syncthreads();
+  if (ws == 1) return;
+#pragma unroll
+  for (int sd = 0; sd < 2; ++sd)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const f32x4_t other = red[(4 * sd + c) * 64];
+      const int j = j0 + 16 * c + frow;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int64_t m = row0 + 16 * wr + 4 * fg + v;
+        if (m < M && j < r) G.u[((int64_t)split * M + m) * 2 * r + sd * r + j] = acc[sd][c][v] + other[v];
+      }
+    }
+}
+
+// rows of a workgroup, as gated_u_splits counts them
+int u_rows(int64_t M, int r) { return r > 16 ? 64 : M >= 512 ? 32 : 16; }
 template <int ACT>
 hipError_t launch_u_act(const GatedU& G, hipStream_t s) {
-  const bool two = u_rows(G.M) == 32;
+  if (G.r > 16) {
+    hipLaunchKernelGGL(k_gated_u_wide<ACT>, dim3((unsigned)((G.M + 63) / 64), (unsigned)((G.r + 63) / 64), (unsigned)G.splits), dim3(512), 0, s, G);
+    return hipGetLastError();
+  }
+  const bool two = u_rows(G.M, G.r) == 32;
   if (!G.u) return two ? launch_u<ACT, 2, 0, 4>(G, s) : launch_u<ACT, 1, 0, 4>(G, s);
-  if (G.r <= 16) return two ? launch_u<ACT, 2, 1, 4>(G, s) : launch_u<ACT, 1, 1, 4>(G, s);
-  return two ? launch_u<ACT, 2, 4, 4>(G, s) : launch_u<ACT, 1, 4, 4>(G, s);
+  return two ? launch_u<ACT, 2, 1, 4>(G, s) : launch_u<ACT, 1, 1, 4>(G, s);
 }
 
 // ---------------------------------------------------------------- adapter gradients
@@ -654,7 +745,8 @@ __global__ __launch_bounds__(256) void k_train_sum(TrainSums S, int64_t M) {
 
 int train_t_splits(int64_t M, int64_t K, int r, int jobs) {
   if (M <= 0 || r <= 0) return 1;
-  return range_splits((M + 15) / 16 * jobs * ((r + 63) / 64), (K + 31) / 32, 8);
+  // (one product's sums are added by every tile of the kernel behind: half as many)
+  return range_splits((M + 15) / 16 * jobs * ((r + 63) / 64), (K + 31) / 32, 8, jobs > 1 ? 1024 : 512);
 }
 
 hipError_t launch_train_t(const TrainProd* jobs, int n, int64_t M, int splits, const DropArgs& drop, hipStream_t s) {
@@ -671,13 +763,15 @@ hipError_t launch_train_t(const TrainProd* jobs, int n, int64_t M, int splits, c
   const int r = jobs[0].r;
   const bool two = M >= 512;
   if (r <= 16) return two ? launch_t<2, 1, 8>(J, n, r, s) : launch_t<1, 1, 8>(J, n, r, s);
-  return two ? launch_t<2, 4, 4>(J, n, r, s) : launch_t<1, 4, 8>(J, n, r, s);
+  // (32 rows: 2048 x 11008 under a mask and x 4096, r = 64: 36 us, four waves and 512 workgroups 57, 16 rows 42)
+  return two ? launch_t<2, 4, 8>(J, n, r, s) : launch_t<1, 4, 8>(J, n, r, s);
 }
 
 int gated_u_splits(int64_t M, int64_t N, int r) {
   if (M <= 0) return 1;
-  const int rows = u_rows(M);
-  return range_splits((M + rows - 1) / rows * std::max(1, (r + 63) / 64), (N + 31) / 32, 4);
+  const int rows = u_rows(M, r);
+  if (rows == 64) return range_splits((M + 63) / 64 * ((r + 63) / 64), (N + 63) / 64, 1);
+  return range_splits((M + rows - 1) / rows, (N + 31) / 32, 4);
 }
 
 hipError_t launch_gated_u(const uint16_t* dh, const uint16_t* gu, int act, int64_t M, int64_t N, const uint16_t* B, int r,

@@ -16,7 +16,7 @@ class Train:
         g = torch.Generator().manual_seed(seed)
         self.M, self.N, self.K, self.r, self.sides, self.p = M, N, K, r, sides, p
         self.qw = qlr.quantize((torch.randn((sides * N, K), generator=g) * 0.05).cuda(), bits)
-        self.W = qlr.dequantize(self.qw, F32).cpu().double().view(sides, N, K)
+        self.W = qlr.dequantize(self.qw, F32).double().view(sides, N, K)  # (the references' products run on the GPU in 64 bits)
         lead = (2,) if sides == 2 else ()
         self.x = (torch.randn((M, K), generator=g) * xscale).to(BF)
         self.A = (torch.randn((*lead, r, K), generator=g) * K ** -0.5).to(BF) if r else None
@@ -36,33 +36,34 @@ class Train:
 
     def factors(self, side):
         return torch.from_numpy(oracle.dropout_factors(self.M, self.K, self.p, self.seed,
-                                                       self.counter + side + (self.step or 0)))
+                                                       self.counter + side + (self.step or 0))).cuda()
 
     def ab(self, side):
-        A, B = self.A.double(), self.B.double()
+        A, B = self.Ad.double(), self.Bd.double()
         return (A, B) if self.sides == 1 else (A[side], B[side])
 
     def linear(self, side):
         """(y, S) of one side."""
-        x, W = self.x.double(), self.W[side]
+        x, W = self.x.double().cuda(), self.W[side]
         y, S = x @ W.t(), x.abs() @ W.abs().t()
         if self.r:
             (A, B), xk = self.ab(side), x * self.factors(side)
             y = y + self.scale * (xk @ A.t()) @ B.t()
             S = S + self.scale * (xk.abs() @ A.abs().t()) @ B.abs().t()
-        return y, S
+        return y.cpu(), S.cpu()
 
     def grads(self, side, dy):
         """((dx, S), (dA, S), (dB, S)) of one side for its upstream gradient."""
-        x, W, s = self.x.double(), self.W[side], self.scale
+        x, W, s, dy = self.x.double().cuda(), self.W[side], self.scale, dy.cuda()
         dx, Sx = dy @ W, dy.abs() @ W.abs()
         if not self.r:
-            return (dx, Sx), None, None
+            return (dx.cpu(), Sx.cpu()), None, None
         (A, B), f = self.ab(side), self.factors(side)
         xk = x * f
         u, t, ua, ta = dy @ B, xk @ A.t(), dy.abs() @ B.abs(), xk.abs() @ A.abs().t()
-        return ((dx + s * f * (u @ A), Sx + s * f * (ua @ A.abs())), (s * u.t() @ xk, s * ua.t() @ xk.abs()),
-                (s * dy.t() @ t, s * dy.abs().t() @ ta))
+        out = ((dx + s * f * (u @ A), Sx + s * f * (ua @ A.abs())), (s * u.t() @ xk, s * ua.t() @ xk.abs()),
+               (s * dy.t() @ t, s * dy.abs().t() @ ta))
+        return tuple((a.cpu(), b.cpu()) for a, b in out)
 
     def gated(self, act):
         """(h, tolerance of h without its own rounding, [g | v], S of them)."""
