@@ -796,7 +796,8 @@ DensePlan dense_plan(int64_t M, int64_t NO, int64_t KC, bool gated) {
 hipError_t launch_dense_weight(const DenseWeight& w, bool tr, const Levels& lv, hipStream_t s) {
   if (w.K % 64 != 0 || (tr && w.rows % 8 != 0)) return hipErrorInvalidValue;
   if (tr) {
-    const dim3 grid((unsigned)((w.rows + 127) / 128), (unsigned)std::min<int64_t>(w.K / 64, 65535));
+    const int64_t tiles = (w.rows + 127) / 128;
+    const dim3 grid((unsigned)tiles, (unsigned)std::max<int64_t>(1, std::min<int64_t>(w.K / 64, kLaunchBlocks / tiles)));
     switch (w.bits) {
       case 2: hipLaunchKernelGGL(k_dense_weight_tr<2>, grid, dim3(256), 0, s, w, lv); break;
       case 3: hipLaunchKernelGGL(k_dense_weight_tr<3>, grid, dim3(256), 0, s, w, lv); break;

@@ -75,8 +75,21 @@ struct TrainProds {
   TrainProd j[4];
   int64_t M;
   int splits;
+  int block0;  // the launch's first row tile
   DropArgs drop;
 };
+
+// A launch of 2^32 threads or more runs the excess only (see launch_blocks): row tiles in launches of at most kLaunchBlocks workgroups.
+template <typename F>
+hipError_t launch_rows(int64_t tiles, int64_t others, F launch) {
+  const int64_t per = std::max<int64_t>(1, kLaunchBlocks / others);
+  for (int64_t b0 = 0; b0 < tiles; b0 += per) {
+    launch((unsigned)std::min(per, tiles - b0), (int)b0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 // A piece of 8 adapter columns of row k of a K x r adapter, zeros past r.
 __device__ __forceinline__ u32x4_t ld_cols(const uint16_t* A, int64_t k, int r, int j, bool r8) {
@@ -212,18 +225,19 @@ __global__ __launch_bounds__(64 * W) void k_train_t(TrainProds J) {
   constexpr uint32_t kSlice = 16 * RT * kRowB + (kA > kB ? kA : kB), kSum = RT * 16 * JT * 16 * 4;
   __shared__ __attribute__((aligned(16))) char lds[W * (kSlice > kSum ? kSlice : kSum)];
   const int ji = (int)blockIdx.z / J.splits, split = (int)blockIdx.z % J.splits;
-  const int64_t row0 = (int64_t)blockIdx.x * 16 * RT;
+  const int64_t row0 = (int64_t)(J.block0 + (int)blockIdx.x) * 16 * RT;
   const TrainProd& job = J.j[ji];
   if (job.bt) prod_tile<RT, JT, W, true>(job, J, split, row0, blockIdx.y * 16 * JT, lds);
   else prod_tile<RT, JT, W, false>(job, J, split, row0, blockIdx.y * 16 * JT, lds);
 }
 
 template <int RT, int JT, int W>
-hipError_t launch_t(const TrainProds& J, int n, int r, hipStream_t s) {
-  hipLaunchKernelGGL((k_train_t<RT, JT, W>),
-                     dim3((unsigned)((J.M + 16 * RT - 1) / (16 * RT)), (unsigned)((r + 16 * JT - 1) / (16 * JT)), (unsigned)(n * J.splits)),
-                     dim3(64 * W), 0, s, J);
-  return hipGetLastError();
+hipError_t launch_t(TrainProds J, int n, int r, hipStream_t s) {
+  const unsigned cols = (unsigned)((r + 16 * JT - 1) / (16 * JT)), each = (unsigned)(n * J.splits);
+  return launch_rows((J.M + 16 * RT - 1) / (16 * RT), (int64_t)cols * each, [&](unsigned tiles, int b0) {
+    J.block0 = b0;
+    hipLaunchKernelGGL((k_train_t<RT, JT, W>), dim3(tiles, cols, each), dim3(64 * W), 0, s, J);
+  });
 }
 
 constexpr int kMaxSplits = 8;
@@ -244,6 +258,7 @@ struct GatedU {
   float* u;
   int64_t M, N;
   int r, splits;
+  int block0;  // the launch's first row tile
 };
 
 template <int ACT, int RT, int JT, int W>
@@ -251,7 +266,7 @@ __global__ __launch_bounds__(64 * W) void k_gated_u(GatedU G) {
   constexpr uint32_t kXs = 16u * RT * kRowB, kBs = 32u * kBtRow<JT>, kSlice = JT ? 6u * kXs + 2u * kBs : 16u;
   constexpr uint32_t kSum = RT * 16 * JT * 16 * 4 * 2;
   __shared__ __attribute__((aligned(16))) char lds[W * (kSlice > kSum ? kSlice : kSum)];
-  const int64_t N = G.N, M = G.M, row0 = (int64_t)blockIdx.x * 16 * RT;
+  const int64_t N = G.N, M = G.M, row0 = (int64_t)(G.block0 + (int)blockIdx.x) * 16 * RT;
   const int r = G.r, rows = (int)min<int64_t>(16 * RT, M - row0), j0 = blockIdx.y * 16 * JT, split = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane >> 2, g = lane & 3, frow = lane & 15, fg = lane >> 4;
@@ -379,13 +394,13 @@ __global__ __launch_bounds__(64 * W) void k_gated_u(GatedU G) {
 }
 
 template <int ACT, int RT, int JT, int W>
-hipError_t launch_u(const GatedU& G, hipStream_t s) {
-  hipLaunchKernelGGL((k_gated_u<ACT, RT, JT, W>),
-                     dim3((unsigned)((G.M + 16 * RT - 1) / (16 * RT)), JT ? (unsigned)((G.r + 16 * JT - 1) / (16 * (JT ? JT : 1))) : 1u, (unsigned)G.splits),
-                     dim3(64 * W), 0, s, G);
-  return hipGetLastError();
+hipError_t launch_u(GatedU G, hipStream_t s) {
+  const unsigned cols = JT ? (unsigned)((G.r + 16 * JT - 1) / (16 * (JT ? JT : 1))) : 1u, each = (unsigned)G.splits;
+  return launch_rows((G.M + 16 * RT - 1) / (16 * RT), (int64_t)cols * each, [&](unsigned tiles, int b0) {
+    G.block0 = b0;
+    hipLaunchKernelGGL((k_gated_u<ACT, RT, JT, W>), dim3(tiles, cols, each), dim3(64 * W), 0, s, G);
+  });
 }
-
 // More than 16 adapter columns: a workgroup of 8 waves takes 64 rows x 64 columns of both sides, 64 columns of dh a step; wave w
 // takes rows 16 (w % 4) .. and half w / 4 of the step.  B's rows are staged once for the workgroup and read with the transpose
 // read; dh, g and v are loaded in the fragments' layout (16 bytes of each of 16 rows a quarter wave) and their parts stay in
@@ -396,7 +411,7 @@ __global__ __launch_bounds__(512, 2) void k_gated_u_wide(GatedU G) {
   constexpr uint32_t kRow = kBtRow<4>, kSide = 64u * kRow, kBuf = 2u * kSide;
   __shared__ __attribute__((aligned(16))) char lds[2 * kBuf];
   static_assert(2 * kBuf >= 4 * 32 * 64 * 4, "the second half's sums overlay the buffers");
-  const int64_t N = G.N, M = G.M, row0 = (int64_t)blockIdx.x * 64;
+  const int64_t N = G.N, M = G.M, row0 = (int64_t)(G.block0 + (int)blockIdx.x) * 64;
   const int r = G.r, j0 = blockIdx.y * 64, split = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave & 3, ws = wave >> 2, frow = lane & 15, fg = lane >> 4;
@@ -476,10 +491,13 @@ __global__ __launch_bounds__(512, 2) void k_gated_u_wide(GatedU G) {
 // rows of a workgroup, as gated_u_splits counts them
 int u_rows(int64_t M, int r) { return r > 16 ? 64 : M >= 512 ? 32 : 16; }
 template <int ACT>
-hipError_t launch_u_act(const GatedU& G, hipStream_t s) {
+hipError_t launch_u_act(GatedU G, hipStream_t s) {
   if (G.r > 16) {
-    hipLaunchKernelGGL(k_gated_u_wide<ACT>, dim3((unsigned)((G.M + 63) / 64), (unsigned)((G.r + 63) / 64), (unsigned)G.splits), dim3(512), 0, s, G);
-    return hipGetLastError();
+    const unsigned cols = (unsigned)((G.r + 63) / 64), each = (unsigned)G.splits;
+    return launch_rows((G.M + 63) / 64, (int64_t)cols * each, [&](unsigned tiles, int b0) {
+      G.block0 = b0;
+      hipLaunchKernelGGL(k_gated_u_wide<ACT>, dim3(tiles, cols, each), dim3(512), 0, s, G);
+    });
   }
   const bool two = u_rows(G.M, G.r) == 32;
   if (!G.u) return two ? launch_u<ACT, 2, 0, 4>(G, s) : launch_u<ACT, 1, 0, 4>(G, s);
@@ -778,7 +796,7 @@ hipError_t launch_gated_u(const uint16_t* dh, const uint16_t* gu, int act, int64
                           uint16_t* dgu, float* u, int splits, hipStream_t s) {
   if (M == 0) return hipSuccess;
   if (N % 8 != 0) return hipErrorInvalidValue;
-  const GatedU G{dh, gu, B, dgu, u, M, N, r, splits};
+  const GatedU G{dh, gu, B, dgu, u, M, N, r, splits, 0};
   switch (act) {
     case ACT_SILU: return launch_u_act<ACT_SILU>(G, s);
     case ACT_GELU: return launch_u_act<ACT_GELU>(G, s);
@@ -828,8 +846,9 @@ hipError_t launch_train_grads(const TrainGrad* jobs, int n, int64_t M, int r, co
   G.chunk = (int)grad_chunk(M, G.CC);
   const int64_t chunks = std::max<int64_t>(1, (M + G.chunk - 1) / G.chunk), wgs = chunks * G.tile0[n];
   if (wgs > INT_MAX) return hipErrorInvalidValue;
-  const hipError_t e = launch_blocks(wgs, [&](unsigned blocks, int b0) {
-    const dim3 grid(blocks, (unsigned)((r + 63) / 64));
+  const int64_t jt = (r + 63) / 64;
+  const hipError_t e = launch_rows(wgs, jt, [&](unsigned blocks, int b0) {
+    const dim3 grid(blocks, (unsigned)jt);
     G.block0 = b0;
     if (!gated) hipLaunchKernelGGL(k_train_grad<-1>, grid, dim3(256), 0, s, G);
     else if (act == ACT_SILU) hipLaunchKernelGGL(k_train_grad<ACT_SILU>, grid, dim3(256), 0, s, G);
