@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libqlr.so")
 
 SOURCES = ["qlr_host.cpp", "qlr_quant.hip", "qlr_linear_f32.hip", "qlr_gemv.hip", "qlr_gemm.hip", "qlr_bwd.hip",
            "qlr_dba.hip", "qlr_outliers.hip", "qlr_wha.hip", "qlr_i8.hip", "qlr_grouped.hip", "qlr_grouped_fwd.hip",
-           "qlr_grouped_bwd.hip", "qlr_grouped_grad.hip", "qlr_gated_fwd.hip", "qlr_gated_few.hip", "qlr_drop_dx.hip",
+           "qlr_grouped_bwd.hip", "qlr_grouped_grad.hip", "qlr_gated_fwd.hip", "qlr_gated_few.hip", "qlr_drop_dx.hip", "qlr_drop_fwd.hip",
            "qlr_train.hip", "qlr_dense.hip"]
 
 

@@ -250,6 +250,11 @@ TrainLayout train_layout(qlr_op op, int64_t M, int64_t N, int64_t K, int32_t r) 
       if (L.k_splits > 1) at = L.sums + (size_t)L.k_splits * (size_t)M * (size_t)qlr::train_part_cols(NO, !bwd) * sizeof(float);
     }
   }
+  if (op == QLR_OP_LINEAR_DROPOUT && r > 0 && M > 16) {
+    L.k_splits = qlr::train_tile_splits(M, N, K);
+    L.sums = at;
+    if (L.k_splits > 1) at = L.sums + (size_t)L.k_splits * (size_t)M * (size_t)qlr::train_part_cols(N, false) * sizeof(float);
+  }
   L.total = at;
   return L;
 }
@@ -1567,6 +1572,21 @@ qlr_status qlr_linear_fwd_dropout(const void* x, qlr_dtype xdt, int64_t M, const
   qlr::LinearArgs a = make_args(c, (float)((double)scale * q), wsp + lay.t, lay.t_splits);
   a.A = nullptr;  // (the decode kernel would form x A^T itself)
   const qlr::Levels lv = levels_arg(w->bits);
+  if (path == QLR_PATH_GEMM && lay.k_splits > 1) {
+    qlr::TrainArgs b = train_args(M, w, N, r, a.scale, qlr::DropArgs{});
+    b.x = x;
+    b.t = t;
+    b.t_splits = lay.t_splits;
+    b.ab = reinterpret_cast<const uint16_t*>(B);
+    b.y = y;
+    b.ydt = (int)ydt;
+    b.splits = lay.k_splits;
+    b.part = reinterpret_cast<float*>(wsp + lay.sums);
+    e = qlr::launch_drop_fwd(b, lv, s);
+    if (e == hipSuccess) e = qlr::launch_tile_sum(b, N, false, s);
+    if (e != hipSuccess) return hip_fail(e, "linear launch");
+    return QLR_OK;
+  }
   switch (path) {
     case QLR_PATH_F32: e = qlr::launch_linear_f32(a, lv, s); break;
     case QLR_PATH_GEMV: e = qlr::launch_gemv(a, lv, s); break;

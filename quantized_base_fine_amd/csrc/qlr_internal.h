@@ -245,7 +245,7 @@ struct TrainArgs : TileArgs {
 };
 // Ranges of the contraction (KC) for the calls that run as 64 x 128 or 128 x 128 tiles of `cols` columns (gated: both sides'): see launch_tile.
 int train_tile_splits(int64_t M, int64_t cols, int64_t KC);
-constexpr int64_t train_part_cols(int64_t NO, bool gated) { return gated ? 2 * ((NO + 3) / 4 * 4) : NO; }
+constexpr int64_t train_part_cols(int64_t NO, bool gated) { return (gated ? 2 : 1) * ((NO + 3) / 4 * 4); }
 // y (and gu) from the ranges' sums.
 hipError_t launch_tile_sum(const TrainArgs& a, int64_t NO, bool gated, hipStream_t s);
 // Rows up to which the few-rows kernels take an expert, or a call of the 8-bit product.
@@ -279,6 +279,8 @@ hipError_t launch_grouped_transpose(const uint16_t* B, int experts, int64_t N, i
 // h = act(gate) up, M x N (and gu): rows of x from 17 on, and up to kFewRows rows.
 hipError_t launch_gated_gemm(const TrainArgs& a, const Levels& lv, hipStream_t s);
 hipError_t launch_gated_few(const TrainArgs& a, const Levels& lv, hipStream_t s);
+// y = x W'^T + scale t B^T in a.splits ranges of the contraction.
+hipError_t launch_drop_fwd(const TrainArgs& a, const Levels& lv, hipStream_t s);
 // dx = dy W' + sum over the halves of mask (scale u A), of everything without a mask: K % 64 == 0, N % 8 == 0.
 hipError_t launch_drop_dx(const TrainArgs& a, const Levels& lv, hipStream_t s);
 

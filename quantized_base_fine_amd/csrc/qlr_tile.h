@@ -62,7 +62,7 @@
 
 namespace qlr {
 
-enum { TILE_I8 = 0, TILE_CODED = 1, TILE_TR = 2, TILE_GATED = 3, TILE_TRD = 4 };
+enum { TILE_I8 = 0, TILE_CODED = 1, TILE_TR = 2, TILE_GATED = 3, TILE_TRD = 4, TILE_LIN = 5 };
 
 namespace {
 
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
   const int64_t gb = kTR ? (int64_t)e * N * nbK + (n0 >> 6) : ((int64_t)(e + side) * N + n0) * nbK;
   bool wv = true, wv_last = true;
   uint32_t lb = 0, lb_last = 0;  // the lane's block, relative
-  if constexpr (KIND == TILE_CODED || KIND == TILE_GATED) {
+  if constexpr (KIND == TILE_CODED || KIND == TILE_GATED || KIND == TILE_LIN) {
     wv = wv_last = n0 + wcol < N;
     lb = lb_last = (uint32_t)(min<int64_t>(wcol, N - 1 - n0) * nbK);
   } else if constexpr (kTR) {
@@ -802,7 +802,7 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
         }
       }
       __syncthreads();
-      if constexpr (KIND >= TILE_GATED) {
+      if constexpr (KIND == TILE_GATED || KIND == TILE_TRD) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -932,18 +932,20 @@ __global__ __launch_bounds__(512, BM * BN <= 128 * 128 ? 4 : 1) void k_tile(type
   // ---- output: staged row-major in LDS, stored in 16-byte pieces (of a split contraction, the range's sums)
   int es = P.ydt == DT_F32 ? 4 : 2;
   char* out = reinterpret_cast<char*>(P.y);
-  if constexpr (kSplit && kTR) {
+  int64_t ldo = NO;
+  if constexpr (kSplit) {
     if (ranges_k > 1) {
       es = 4;
-      out = reinterpret_cast<char*>(P.part + (int64_t)range * P.M * NO);
+      ldo = train_part_cols(NO, false);
+      out = reinterpret_cast<char*>(P.part + (int64_t)range * P.M * ldo);
     }
   }
-  const bool vec = (NO * es) % 16 == 0;
+  const bool vec = (ldo * es) % 16 == 0;
   const int cpr = BN * es / 16;  // 16-byte pieces of a staged row (a power of two)
   auto put = [&](int row, int c, u32x4_t v) {  // piece c of tile row `row`
     const int64_t col = n0 + c * (16 / es);
     if (col >= NO) return;
-    char* dst = out + ((int64_t)(row0 + row) * NO + col) * es;
+    char* dst = out + ((int64_t)(row0 + row) * ldo + col) * es;
     if (vec) {
       *reinterpret_cast<u32x4_t*>(dst) = v;
     } else {

@@ -207,3 +207,14 @@ def test_repeats_bit_for_bit():
     for _ in range(3):
         assert all(torch.equal(u, v) for u, v in
                    zip(a, qlr.linear_dropout_bwd(L.dyd, L.xd, L.qw, L.Ad, L.Bd, L.scale, L.drop())))
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+@pytest.mark.parametrize("M", [17, 64, 65, 300])
+@pytest.mark.parametrize("N,K", [(1, 512), (101, 1088), (255, 4096), (1032, 512)])
+def test_ranges_of_the_contraction(bits, M, N, K):
+    """The tiled product in two to eight ranges, odd widths, one step more in some."""
+    print(f"dropout ranges bits={bits} M={M} N={N} K={K}", flush=True)
+    L = Train(M, N, K, bits, 16 if bits == 4 else 5, seed=bits + M, p=0.1)
+    fwd(L)
+    fwd(L, F32)
