@@ -177,8 +177,8 @@ typedef struct {
 } qlr_i8rows;
 
 /*
- * Dropout of an adapter's input by a mask that is never stored: the calls of one
- * step form it anew from these numbers.  Element (m, k) of an M x K input (K % 8
+ * Dropout of an adapter's input by a mask that is never stored between calls: the
+ * calls of one step form it anew from these numbers.  Element (m, k) of an M x K input (K % 8
  * == 0) belongs to group g = (m K + k) / 8.  Philox4x32-10 (Salmon, Moraes, Dror,
  * Shaw, SC 2011) of the counter words (g low, g high, c low, c high), each 32
  * bits, under the key (seed low, seed high) gives four words, eight 16-bit numbers
@@ -668,7 +668,7 @@ qlr_status qlr_gated_fwd(const void* x, qlr_dtype xdt, int64_t M, const qlr_qwei
  *     dA = scale ((dg Bg)^T drop(x), (dv Bu)^T drop'(x))                      (2 x r x cols float32)
  *     dB = scale (dg^T (drop(x) Ag^T), dv^T (drop'(x) Au^T))                  (2 x N x r float32)
  * In the products with the base dg and dv enter rounded to bf16 (a second bf16 part
- * would double the matrix work), in those with the adapters in two bf16 parts.  dA and dB
+ * would double the matrix work), in those with the adapters in three bf16 parts.  dA and dB
  * are overwritten (zero when M == 0) and required when r > 0; x is not read when
  * r == 0 and may be NULL.  N % 8 == 0; sizes otherwise as the forward.  Per
  * element dx is within 1e-2 * S + 1e-5 (plus half a bf16 ulp for a bf16 dx; the

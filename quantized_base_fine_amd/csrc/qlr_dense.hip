@@ -10,7 +10,7 @@
 // go into t and l during the first half (free since the half before) and into r and b during the second, each a
 // step and a half ahead of its first read.  One barrier per half.  Each half's wait leaves the 8 newest loads open.
 //
-// What bounds it (2048 x 22016 x 4096, 688 tiles): 298 us (1.24 PFLOP/s), on zeros 271 (the clock falls with the power).  32 x 32
+// What bounds it (2048 x 22016 x 4096, 688 tiles, the product alone): 298 us (1.24 PFLOP/s), on zeros 271 (the clock falls with the power).  32 x 32
 // MFMA tiles took 310 and 254: they are the faster ones but draw more.  Half steps of 32 elements in a ring of five buffers, rows
 // of 64 bytes, took 352: the loads of half lines bound that loop (without them it ran as fast as without the LDS reads).
 // 128 x 128 results a wave, which would read a third less of LDS, spill.

@@ -7,6 +7,8 @@
 //   KIND TILE_TR    y[m] = x[m] W'_e (x = dy, y = dx)       (+ adapter)
 //   KIND TILE_GATED y[m] = act(x[m] Wg'^T) (x[m] Wu'^T)      (+ adapters; Wg and Wu stacked; one range)
 //   KIND TILE_TRD   as TILE_TR, the adapter's part under a dropout mask (one or two adapters; one range)
+//   KIND TILE_LIN   as TILE_CODED, one range
+// The last three can split the contraction into P.splits ranges, whose float32 sums go to P.part (launch_tile_sum adds them).
 //
 // Tiling.  A workgroup of 8 waves owns BM rows x BN columns (256 x 256 down to 64
 // x 128), divided among WM x WN waves in 32 x 32 MFMA tiles.  A step contracts 128 bytes of each row of x: 64 bf16 or 128
@@ -43,7 +45,8 @@
 // hold both sides of 8 outputs and the epilogue needs no exchange; a wave loads rows of one side only.
 //
 // Dropout.  dx = dy W' + s mask (u A): a block of 32 adapter columns is multiplied into sums of its own, which are added where the
-// mask keeps the element.  The mask's bits are formed once per tile and adapter (16 a lane and MFMA tile).
+// mask keeps the element.  The mask's bits were left by the kernel that formed x A^T; a lane's 16 columns of an MFMA tile's row are one
+// word of them.
 //
 // Ranges.  Expert e's rows are [offsets[e], offsets[e + 1]); every offset is
 // clamped into [0, M] and to its predecessor, so no offset can lead out of
