@@ -2,7 +2,7 @@
 
 Tolerances, per element, S the sum of the absolute values of the terms: g and v 5e-3 S + 1e-5 (the weight enters rounded to
 bf16, 2^-8 = 3.9e-3 of it), h what these allow through act(g) v (|act'| < 1.13); dx 1e-2 S + 1e-5 (the weight and dg, dv each
-rounded to bf16: 2 x 3.9e-3); dA and dB 1e-4 S + 1e-6 (dg and dv in two bf16 parts, float32 sums).  Half a bf16 ulp, 2^-8 of
+rounded to bf16: 2 x 3.9e-3); dA and dB 1e-4 S + 1e-6 (dg and dv in three bf16 parts, float32 sums).  Half a bf16 ulp, 2^-8 of
 the value, is added for bf16 results."""
 import pytest
 
@@ -107,7 +107,7 @@ def test_families(path, M):
 
 @pytest.mark.parametrize("N", [5000, 16500, 33000])
 def test_decode_widths(N):
-    """One, two and four sets of rows to a workgroup."""
+    """One and two sets of rows to a workgroup."""
     for M in (1, 13):
         fwd(Train(M, N, 128, 4, 16, seed=N, sides=2))
 
