@@ -431,17 +431,25 @@ qlr_status drop_args(const qlr_dropout* d, int32_t r, qlr::DropArgs* out, double
   return QLR_OK;
 }
 
-// The checks that the calls under adapter dropout and the gated block share: sides = 2 for the gated block's stacked weight.
+// Sizes that the calls under adapter dropout and the gated block take (sides = 2: N is half the stacked weight's rows).  What they
+// allow stays within 64 bits in every product of the workspace's layout.
+qlr_status check_train_sizes(int64_t M, int64_t N, int64_t K, int sides, int32_t r) {
+  if (M < 0 || M > kMaxRows) return fail(QLR_ERR_SHAPE, "M %lld not in [0, 2^27]", (long long)M);
+  if (r < 0 || r > (1 << 20)) return fail(QLR_ERR_SHAPE, "r %d not in [0, 2^20]", r);
+  if (N < 0 || K < 0) return fail(QLR_ERR_SHAPE, "negative size");
+  if (N > (1 << 20) / sides || K > (1 << 20)) return fail(QLR_ERR_SHAPE, "the weight is larger than 2^20 x 2^20");
+  if (M > kMaxElems / (sides * std::max<int64_t>({N, K, 1}))) return fail(QLR_ERR_SHAPE, "x or y holds too many elements");
+  return QLR_OK;
+}
+
+// The checks that those calls share.
 qlr_status check_train(int64_t M, const qlr_qweight* w, int sides, int32_t r, qlr_dtype xdt, qlr_dtype abdt, qlr_dtype odt) {
   qlr_status st = check_qweight(w);
   if (st != QLR_OK) return st;
-  if (M < 0 || M > kMaxRows) return fail(QLR_ERR_SHAPE, "M %lld not in [0, 2^27]", (long long)M);
-  if (r < 0 || r > (1 << 20)) return fail(QLR_ERR_SHAPE, "r %d not in [0, 2^20]", r);
   if (w->rows == 0 || w->cols == 0) return fail(QLR_ERR_SHAPE, "empty weight");
   if (w->rows % sides != 0) return fail(QLR_ERR_SHAPE, "the stacked weight's %lld rows are odd", (long long)w->rows);
   if (w->cols % QLR_BLOCK != 0) return fail(QLR_ERR_SHAPE, "cols %lld is not a multiple of 64", (long long)w->cols);
-  if (w->cols > (1 << 20) || w->rows > (1 << 20)) return fail(QLR_ERR_SHAPE, "the weight is larger than 2^20 x 2^20");
-  if (M > kMaxElems / std::max(sides * w->cols, w->rows)) return fail(QLR_ERR_SHAPE, "x or y holds too many elements");
+  if ((st = check_train_sizes(M, w->rows / sides, w->cols, sides, r)) != QLR_OK) return st;
   if (xdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "x (dy, dh) must be bf16");
   if (r > 0 && abdt != QLR_BF16) return fail(QLR_ERR_DTYPE, "the adapters must be bf16");
   if (!(odt == QLR_F32 || odt == QLR_BF16)) return fail(QLR_ERR_DTYPE, "output dtype must be f32 or bf16");
@@ -725,8 +733,9 @@ qlr_status qlr_workspace_bytes(qlr_op op, int64_t M, int64_t N, int64_t K, int32
     return QLR_OK;
   }
   if (op >= QLR_OP_LINEAR_DROPOUT && op <= QLR_OP_GATED_BWD) {
-    if (M < 0 || N < 0 || K < 0 || r < 0) return fail(QLR_ERR_SHAPE, "negative size");
-    *bytes = train_layout(op, M, N, K, r).total;
+    const qlr_status st = check_train_sizes(M, N, K, op == QLR_OP_GATED || op == QLR_OP_GATED_BWD ? 2 : 1, r);
+    if (st != QLR_OK) return st;
+    *bytes = N > 0 && K > 0 ? train_layout(op, M, N, K, r).total : 0;  // (no call takes an empty weight)
     return QLR_OK;
   }
   if (op != QLR_OP_LINEAR && op != QLR_OP_LINEAR_BWD) return fail(QLR_ERR_SHAPE, "unknown op %d", (int)op);
