@@ -585,8 +585,8 @@ hipError_t launch_dx_f32(const LinearArgs& a, const Levels& lv, hipStream_t s) {
 // LDS (64 bytes each), so its ranges hold at most kGradRowsMax rows.
 constexpr int64_t kGradRowsMax = 1024;
 void grad_split(int64_t M, int64_t N, int64_t K, int r, bool mfma, int* msplit, int64_t* rows) {
-  const int64_t tiles = mfma ? ((K + 127) / 128 + (N + 127) / 128) * ((r + 63) / 64)
-                             : ((K + 255) / 256 + (N + 255) / 256) * ((r + 15) / 16);
+  const int64_t tiles = std::max<int64_t>(1, mfma ? ((K + 127) / 128 + (N + 127) / 128) * ((r + 63) / 64)
+                                                  : ((K + 255) / 256 + (N + 255) / 256) * ((r + 15) / 16));
   const int64_t max_split = std::max<int64_t>(1, (M + 127) / 128);
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(max_split, (512 + tiles - 1) / tiles));
   int64_t rw = (M + want - 1) / want;

@@ -40,3 +40,9 @@ def test_sizes_past_the_limits_are_refused(op):
     got = sizes(op, good + bad)
     assert all(int(g) > 0 for g in got[:len(good)])
     assert all("ERR_SHAPE" in g for g in got[len(good):]), got
+
+
+def test_plain_backward_of_an_empty_weight():
+    """The plain layer's backward: its size without rows and columns is t, u and B transposed alone, as with either of them."""
+    got = sizes("LINEAR_BWD", [(M, 0, 0, r) for M in (0, 1, 17, 300) for r in (0, 8, 100)])
+    assert [int(g) for g in got] == [0, 0, 0, 0, 512, 1024, 0, 1536, 2 * 6912, 0, 2 * 9728, 2 * 120064]
