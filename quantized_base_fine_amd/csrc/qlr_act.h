@@ -23,9 +23,14 @@ __device__ __forceinline__ float act_gate(float g, float& d) {
     const float e = __expf(-v), q = __builtin_amdgcn_rcpf(1.0f + e);  // (e = Inf: q = 0)
     if constexpr (SLOPE) {
       // act' = q + g q (1 - q) dv/dg; 1 - q = e q where q is near 1
-      const float p = q < 0.5f ? 1.0f - q : e * q;
-      const float dv = ACT == ACT_SILU ? 1.0f : kGeluC * fmaf(0.134145f * g, g, 1.0f);
-      d = fmaf(g * dv, q * p, q);
+      const float w = q * (q < 0.5f ? 1.0f - q : e * q);
+      if constexpr (ACT == ACT_SILU) {
+        d = fmaf(g, w, q);
+      } else {
+        // (powers of g on the small factor: g dv grows as g^3 and is infinite past 1e13, where w has long been 0)
+        const float t = w * g;
+        d = fmaf(kGeluC, fmaf(0.134145f * t * g, g, t), q);
+      }
     }
     return q;
   }
