@@ -16,6 +16,9 @@ namespace {
 // 16 rows of 2 x 22016 x 8192, 4-bit: 75 us (181 MB of codes, 2.4 TB/s) with two sets, one 92 (each set's own x), four 88 (one
 // workgroup to a CU).  Without x's loads and writes it ran in 52, without the lookups in 66, without the codes' loads in 62: no
 // one of them bounds it.  One row of 2 x 11008 x 4096: 20 us of the call's 24; two sets of 8 columns each, one 27.
+// The table holds the levels times 2^-7, the results are multiplied by 2^7 once they are added up: 64 of bf16's largest values times
+// levels of at most 1 stay inside float32 before the scale, and a scale times 2^7 is never formed.
+constexpr float kLevelUnit = 1.0f / 128.0f;
 constexpr int kWaves = 8;
 template <int BITS>
 constexpr int kFewChunk = BITS == 8 ? 2 : 4;  // (four of 8 bits spill)
@@ -121,7 +124,8 @@ __global__ __launch_bounds__(512, 4) void k_gated_few(TrainArgs P, Levels lv) {
     constexpr int NL = 1 << BITS;
     for (int i = tid; i < FewTab<BITS>::kEntries * 8; i += 512) {  // four copies each
       const int en = i >> 3;
-      const uint32_t v = BITS == 8 ? f32_to_bf16_bits(sL[en]) : pack_bf16x2(sL[en & (NL - 1)], sL[en >> BITS]);
+      const uint32_t v = BITS == 8 ? f32_to_bf16_bits(kLevelUnit * sL[en])
+                                   : pack_bf16x2(kLevelUnit * sL[en & (NL - 1)], kLevelUnit * sL[en >> BITS]);
       reinterpret_cast<u32x4_t*>(smem)[i] = u32x4_t{v, v, v, v};
     }
     __syncthreads();
@@ -196,6 +200,7 @@ __global__ __launch_bounds__(512, 4) void k_gated_few(TrainArgs P, Levels lv) {
       float y = 0.0f;
 #pragma unroll
       for (int k = 0; k < kWaves; ++k) y += red[(k * 16 + m) * NR + 16 * (c >> 3) + 8 * sd + (c & 7)];
+      y *= 1.0f / kLevelUnit;
       if (P.r > 0)
         y = fmaf(P.scale, ad[sd].dot(ad_lds + sd * Adapter::kBytes, P.t + sd * tside, P.t_splits, P.M, 0, m,
                                      P.ab + (int64_t)sd * N * P.r, n0, c, P.r), y);
