@@ -248,6 +248,13 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _holding(c, *tensors):
+    """A C structure that keeps the tensors whose addresses it holds: the fields of the object it was made
+    from may be set to others while a prepared call still uses it."""
+    c.tensors = tensors
+    return c
+
+
 def _require_cuda(*tensors):
     for t in tensors:
         if t is not None and not t.is_cuda:
@@ -265,8 +272,9 @@ class QWeight:
     absmax_c: "object"
 
     def c_struct(self) -> CQWeight:
-        return CQWeight(FORMAT_VERSION, self.bits, BLOCK, GROUP, self.rows, self.cols,
-                        self.codes.data_ptr(), self.absmax_q8.data_ptr(), self.absmax_c.data_ptr())
+        return _holding(CQWeight(FORMAT_VERSION, self.bits, BLOCK, GROUP, self.rows, self.cols,
+                                 self.codes.data_ptr(), self.absmax_q8.data_ptr(), self.absmax_c.data_ptr()),
+                        self.codes, self.absmax_q8, self.absmax_c)
 
     @staticmethod
     def empty(rows: int, cols: int, bits: int, device) -> "QWeight":
@@ -536,8 +544,8 @@ class Sparse:
     max_group_nnz: int = -1
 
     def c_struct(self) -> CSparse:
-        return CSparse(self.rows, self.cols, self.nnz, self.row_ptr.data_ptr(), self.col.data_ptr(),
-                       self.val.data_ptr(), self.max_group_nnz)
+        return _holding(CSparse(self.rows, self.cols, self.nnz, self.row_ptr.data_ptr(), self.col.data_ptr(),
+                                self.val.data_ptr(), self.max_group_nnz), self.row_ptr, self.col, self.val)
 
     @staticmethod
     def empty(rows: int, cols: int, nnz: int, device) -> "Sparse":
@@ -701,7 +709,7 @@ class I8Rows:
         if self.scale.dtype != torch.float32 or self.scale.numel() != self.rows or not self.scale.is_contiguous():
             raise ValueError("scale must be a contiguous float32 tensor of rows values")
         _same_device(self.q, scale=self.scale)
-        return CI8Rows(self.rows, self.cols, self.q.data_ptr(), self.scale.data_ptr())
+        return _holding(CI8Rows(self.rows, self.cols, self.q.data_ptr(), self.scale.data_ptr()), self.q, self.scale)
 
     @staticmethod
     def empty(rows: int, cols: int, device) -> "I8Rows":
@@ -913,7 +921,7 @@ class Dropout:
             if self.step.dtype != torch.int64 or self.step.numel() != 1:
                 raise ValueError("step must be an int64 tensor of one element")
         mask = (1 << 64) - 1
-        return CDropout(float(self.p), int(self.seed) & mask, int(self.counter) & mask, _ptr(self.step))
+        return _holding(CDropout(float(self.p), int(self.seed) & mask, int(self.counter) & mask, _ptr(self.step)), self.step)
 
 
 def _bf16(t, what: str, shape):
