@@ -248,6 +248,14 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _ws_bytes(ws) -> int:
+    if ws is None:
+        return 0
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")  # (an expanded tensor has fewer bytes than its elements would)
+    return ws.numel() * ws.element_size()
+
+
 def _holding(c, *tensors):
     """A C structure that keeps the tensors whose addresses it holds: the fields of the object it was made
     from may be set to others while a prepared call still uses it."""
@@ -298,7 +306,7 @@ def quantize(W, bits: int, out: Optional[QWeight] = None, ws=None, blocking: boo
     cw = qw.c_struct()
     fn = lib().qlr_quantize if blocking else lib().qlr_quantize_async
     check(fn(W.data_ptr(), _dt(W), rows, cols, bits, BLOCK, C.byref(cw), ws.data_ptr(),
-             ws.numel(), _stream(W.device)))
+             _ws_bytes(ws), _stream(W.device)))
     return qw
 
 
@@ -329,7 +337,7 @@ def linear(x, qw: QWeight, A=None, B=None, scale: float = 0.0, out_dtype=None, o
     cw = qw.c_struct()
     check(lib().qlr_linear_fwd(x.data_ptr(), _dt(x), M, C.byref(cw), _ptr(A), _ptr(B), abdt, r,
                                float(scale), y.data_ptr(), _dt(y), _ptr(ws),
-                               0 if ws is None else ws.numel(), _stream(x.device)))
+                               _ws_bytes(ws), _stream(x.device)))
     return y
 
 
@@ -381,7 +389,7 @@ class LinearCall:
         self._cw = qw.c_struct()
         abdt = _dt(A) if r > 0 else QLR_BF16
         self._args = (x.data_ptr(), _dt(x), M, C.byref(self._cw), _ptr(A), _ptr(B), abdt, r, float(scale),
-                      self.y.data_ptr(), _dt(self.y), _ptr(ws), 0 if ws is None else ws.numel(),
+                      self.y.data_ptr(), _dt(self.y), _ptr(ws), _ws_bytes(ws),
                       _stream(x.device))
         self._fn = lib().qlr_linear_fwd
 
@@ -427,7 +435,7 @@ class MixedCall:
             ws = torch.empty(need, dtype=torch.uint8, device=x0.device)
         self._keep = (list(entries), cws, arr, ws)
         self._args = (arr, len(entries), M, _dt(x0), abdt, _dt(self.ys[0]), _ptr(ws),
-                      0 if ws is None else ws.numel(), _stream(x0.device))
+                      _ws_bytes(ws), _stream(x0.device))
         self._fn = lib().qlr_linear_fwd_mixed
 
     def __call__(self):
@@ -476,7 +484,7 @@ class LinearBwdCall:
         xdt = _dt(x) if x is not None else _dt(dy)
         self._args = (dy.data_ptr(), _dt(dy), _ptr(x), xdt, M, C.byref(self._cw), _ptr(A), _ptr(B), abdt, r,
                       float(scale), _ptr(self.dx), _dt(self.dx) if self.dx is not None else QLR_F32,
-                      _ptr(self.dA), _ptr(self.dB), _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev))
+                      _ptr(self.dA), _ptr(self.dB), _ptr(ws), _ws_bytes(ws), _stream(dev))
         self._fn = lib().qlr_linear_bwd
 
     def __call__(self):
@@ -516,7 +524,7 @@ class DbaCall:
         self._cw = qw.c_struct()
         self._ad = CDba(R, ell, *[t.data_ptr() for t in tensors])
         self._args = (x.data_ptr(), _dt(x), M, C.byref(self._cw), C.byref(self._ad), self.y.data_ptr(),
-                      _dt(self.y), ws.data_ptr(), ws.numel(), _stream(x.device))
+                      _dt(self.y), ws.data_ptr(), _ws_bytes(ws), _stream(x.device))
         self._fn = lib().qlr_linear_fwd_dba
 
     def __call__(self):
@@ -569,7 +577,7 @@ def quantize_outliers(W, bits: int, k: int, out: Optional[QWeight] = None, spars
                          device=W.device)
     cw, cs = qw.c_struct(), sp.c_struct()
     check(lib().qlr_quantize_outliers(W.data_ptr(), _dt(W), rows, cols, bits, BLOCK, k, C.byref(cw), C.byref(cs),
-                                      ws.data_ptr(), ws.numel(), _stream(W.device)))
+                                      ws.data_ptr(), _ws_bytes(ws), _stream(W.device)))
     sp.max_group_nnz = int(cs.max_group_nnz)
     return qw, sp
 
@@ -597,7 +605,7 @@ class OutliersCall:
         self._cw, self._cs = qw.c_struct(), sp.c_struct()
         abdt = _dt(A) if r > 0 else QLR_BF16
         self._args = (x.data_ptr(), _dt(x), M, C.byref(self._cw), C.byref(self._cs), _ptr(A), _ptr(B), abdt, r,
-                      float(scale), self.y.data_ptr(), _dt(self.y), _ptr(ws), 0 if ws is None else ws.numel(),
+                      float(scale), self.y.data_ptr(), _dt(self.y), _ptr(ws), _ws_bytes(ws),
                       _stream(x.device))
         self._fn = lib().qlr_linear_fwd_outliers
 
@@ -630,7 +638,7 @@ class WhaCall:
         self._keep = (x, qw, F, ws)
         self._cw, self._cf = qw.c_struct(), F.c_struct()
         self._args = (x.data_ptr(), _dt(x), M, C.byref(self._cw), C.byref(self._cf), int(hblock), self.y.data_ptr(),
-                      _dt(self.y), _ptr(ws), 0 if ws is None else ws.numel(), _stream(x.device))
+                      _dt(self.y), _ptr(ws), _ws_bytes(ws), _stream(x.device))
         self._fn = lib().qlr_linear_fwd_wha
 
     def __call__(self):
@@ -770,7 +778,7 @@ class LinearI8Call:
         self._run = _Launch(lib().qlr_linear_fwd_i8,
                             (_ptr(x), _dt(x) if x is not None else QLR_BF16, M, None if cq is None else C.byref(cq),
                              C.byref(cw), _ptr(A), _ptr(B), QLR_BF16, r, float(scale), out.data_ptr(), _dt(out), _ptr(ws),
-                             0 if ws is None else ws.numel() * ws.element_size(), _stream(src.device)), src.device)
+                             _ws_bytes(ws), _stream(src.device)), src.device)
 
     def __call__(self):
         self._run()
@@ -834,7 +842,7 @@ class GroupedCall:
         self._run = _Launch(lib().qlr_linear_fwd_grouped,
                             (x.data_ptr(), _dt(x), T, C.byref(cw), E, offsets.data_ptr(), _ptr(A), _ptr(B), QLR_BF16, r,
                              float(scale), out.data_ptr(), _dt(out), _ptr(ws),
-                             0 if ws is None else ws.numel() * ws.element_size(), _stream(x.device)), x.device)
+                             _ws_bytes(ws), _stream(x.device)), x.device)
 
     def __call__(self):
         self._run()
@@ -887,7 +895,7 @@ class GroupedBwdCall:
                             (dy.data_ptr(), _dt(dy), _ptr(x), QLR_BF16, T, C.byref(cw), E, offsets.data_ptr(), _ptr(A),
                              _ptr(B), QLR_BF16, r, float(scale), _ptr(self.dx),
                              _dt(self.dx) if self.dx is not None else QLR_F32, _ptr(self.dA), _ptr(self.dB), _ptr(ws),
-                             0 if ws is None else ws.numel() * ws.element_size(), _stream(dev)), dev)
+                             _ws_bytes(ws), _stream(dev)), dev)
 
     def __call__(self):
         self._run()
@@ -973,7 +981,7 @@ def _train_ws(ws, op: int, M: int, N: int, K: int, r: int, device):
     need = workspace_bytes(op, M, N, K, r)
     if ws is None and need > 0:
         ws = torch.empty(need, dtype=torch.uint8, device=device)
-    return ws, 0 if ws is None else ws.numel() * ws.element_size()
+    return ws, _ws_bytes(ws)
 
 
 def _drop_arg(dropout: Optional[Dropout]):
