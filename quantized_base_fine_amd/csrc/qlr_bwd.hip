@@ -610,7 +610,7 @@ size_t grad_partial_floats(int64_t M, int64_t N, int64_t K, int r) {
 
 template <int QDT, bool VEC>
 hipError_t launch_grad_k(const GradParams& G, int64_t tiles, size_t shmem, hipStream_t s) {
-  static bool attr = false;
+  static std::atomic<bool> attr{false};  // (host threads may come here at once: each sets the same)
   if (!attr) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_lora_grad<QDT, VEC>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)(kGradRowsMax * 64));

@@ -216,7 +216,7 @@ hipError_t launch_dba_prep(const DbaArgs& d, const void* x, int xdt, int64_t M, 
     gd.kspan = 32 * ((nsteps + splits - 1) / splits + 1);
     const size_t shmem = (size_t)gd.kspan * 4;
     if (shmem > 96 * 1024) return hipErrorInvalidValue;
-    static bool attr = false;
+    static std::atomic<bool> attr{false};  // (host threads may come here at once: each sets the same)
     if (!attr) {
       const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_dba_prep),
                                                hipFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);

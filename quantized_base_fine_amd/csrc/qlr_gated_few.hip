@@ -217,7 +217,7 @@ __global__ __launch_bounds__(512, 4) void k_gated_few(TrainArgs P, Levels lv) {
 template <int BITS, int NS>
 hipError_t launch_few_r(const TrainArgs& a, const Levels& lv, hipStream_t s) {
   auto kern = k_gated_few<BITS, NS>;
-  static bool checked = false;
+  static std::atomic<bool> checked{false};  // (host threads may come here at once: each sets the same)
   hipError_t e;
   if (!checked) {
     // the level table is read at LDS addresses from 0: the kernel must not have static LDS

@@ -834,7 +834,7 @@ hipError_t launch_gemm_t(const LinearArgs* ls, int n, const Levels& lv, hipStrea
   // SPF (the outlier side channel added to the weight tiles): its staging takes the rest of LDS
   const size_t shmem = SPF ? kLdsAll : gemm_lds_bytes<BITS>();
   auto kern = k_gemm<BITS, YDT, ADP, TR, SPF>;
-  static bool attr = false;
+  static std::atomic<bool> attr{false};  // (host threads may come here at once: each sets the same)
   if (!attr) {
     // the kernel addresses LDS from 0: it must not have static LDS
     hipFuncAttributes fa;

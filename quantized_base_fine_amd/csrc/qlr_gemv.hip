@@ -1623,7 +1623,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemv_group(GvParams P, Levels l
 constexpr size_t kLdsMax = 160 * 1024;
 
 int device_cus() {
-  static int cus = 0;  // one device per process
+  static std::atomic<int> cus{0};  // one device per process
   if (cus == 0) {
     int dev = 0, n = 0;
     if (hipGetDevice(&dev) == hipSuccess &&
@@ -1639,7 +1639,7 @@ template <int BITS, int YDT, bool XLDS, bool ADP, int D, bool DOT = false, bool 
           bool DBA = false, bool XR = false>
 hipError_t launch_k(const Params& P, int64_t grid, size_t shmem, const Levels& lv, hipStream_t s) {
   auto kern = k_gemv<BITS, YDT, XLDS, ADP, D, DOT, TF, SPX, DBA, XR>;
-  static bool attr = false;
+  static std::atomic<bool> attr{false};  // (host threads may come here at once: each sets the same)
   if (!attr) {
     // the kernel addresses LDS from 0: it must not have static LDS
     hipFuncAttributes fa;
@@ -1870,7 +1870,7 @@ namespace {
 template <int BITS, int YDT, bool ADP, int D>
 hipError_t launch_gv_group_k(const GvParams& P, int64_t grid, size_t shmem, const Levels& lv, hipStream_t s) {
   auto kern = k_gemv_group<BITS, YDT, ADP, D>;
-  static bool attr = false;
+  static std::atomic<bool> attr{false};  // (host threads may come here at once: each sets the same)
   if (!attr) {
     hipFuncAttributes fa;
     hipError_t e = hipFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern));

@@ -195,7 +195,7 @@ __global__ __launch_bounds__(512, 4) void k_grouped_few(TileArgs P, Levels lv) {
 template <int BITS, int RS>
 hipError_t launch_few_r(const TileArgs& a, const Levels& lv, hipStream_t s) {
   auto kern = k_grouped_few<BITS, RS>;
-  static bool checked = false;
+  static std::atomic<bool> checked{false};  // (host threads may come here at once: each sets the same)
   hipError_t e;
   if (!checked) {
     // the level table is read at LDS addresses from 0: the kernel must not have static LDS

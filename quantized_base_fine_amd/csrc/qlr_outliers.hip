@@ -566,7 +566,7 @@ hipError_t sparse_addend_t(int64_t cap, const void* x, int64_t M, int64_t K, int
   const int64_t nchunk = (N + nch - 1) / nch;
   const size_t es = XDT == DT_F32 ? 4 : 2;
   const size_t shmem = MR > 0 ? (size_t)MR * K * es : 0;
-  static bool attr = false;
+  static std::atomic<bool> attr{false};  // (host threads may come here at once: each sets the same)
   if (!attr) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_sparse_addend<XDT, MR, TB>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, kSparseLds);

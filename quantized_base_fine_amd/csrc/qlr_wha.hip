@@ -335,7 +335,7 @@ hipError_t wha_t(const void* x, int64_t M, int64_t K, int64_t N, int lp, const i
   nch = std::max<int64_t>(nch, (N + max_rows - 1) / max_rows);
   const int64_t nchunk = (N + nch - 1) / nch;
   const size_t shmem = (size_t)rec + (size_t)nchunk * 4;
-  static bool attr = false;
+  static std::atomic<bool> attr{false};  // (host threads may come here at once: each sets the same)
   if (!attr) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_wha_addend<XDT, MR, G, RB, TB, VL>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)(kWhaLdsAll - 256));
@@ -557,7 +557,7 @@ hipError_t wha_merge_b(const uint8_t* codes, const uint8_t* q8, const float* cst
                        int64_t K, int lp, const int32_t* row_ptr, const int32_t* col, const float* val, int64_t nnz,
                        uint16_t* out, hipStream_t s) {
   const size_t shmem = (size_t)((1 << BITS) + K) * 4;
-  static bool attr = false;
+  static std::atomic<bool> attr{false};  // (host threads may come here at once: each sets the same)
   if (!attr) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_wha_merge<BITS>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)kWhaLdsAll);
