@@ -55,7 +55,7 @@ __device__ __forceinline__ void few_levels(const uint32_t (&w)[kWords<BITS>], ui
 
 // The adapters' operands of 8 NS columns, and all of the kernel's dynamic LDS.
 template <int NS>
-using FewAd = FewAdapter<8 * NS, 2048>;
+using FewAd = FewAdapter<8 * NS, kGatedFewT>;
 template <int BITS, int NS>
 constexpr uint32_t kFewBytes = FewTab<BITS>::kBytes + (kWaves * kXSlice > kRedBytes<NS> + 2 * FewAd<NS>::kBytes ? kWaves * kXSlice : kRedBytes<NS> + 2 * FewAd<NS>::kBytes);
 

@@ -206,6 +206,15 @@ struct TrainLayout {
 };
 // Rows from which the adapters' partial sums are added once, before the kernels that read them many times.
 constexpr int64_t kSumRows = 256;
+// Partial sums of x A^T of up to kFewRows rows: no more than the decode kernel behind holds at once, so that an output does not
+// read them from memory one by one.
+int few_splits(int splits, int64_t M, int32_t r, bool gated) {
+  const int64_t most = (gated ? qlr::kGatedFewT : qlr::kTPartsMax) / (M * std::max(r, 1));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(splits, most));
+}
+int gated_lora_splits(int64_t M, int64_t K, int32_t r) {
+  return few_splits(qlr::lora_t_splits(M, K, r, qlr::DT_BF16, qlr::DT_BF16), M, r, true);
+}
 TrainLayout train_layout(qlr_op op, int64_t M, int64_t N, int64_t K, int32_t r) {
   TrainLayout L{};
   L.t_splits = L.u_splits = 1;
@@ -219,8 +228,9 @@ TrainLayout train_layout(qlr_op op, int64_t M, int64_t N, int64_t K, int32_t r) 
   if (r > 0) {
     const int64_t kmin = op == QLR_OP_LINEAR_DROPOUT_BWD ? std::min(N, K) : K;
     L.t_splits = qlr::train_t_splits(M, kmin, r, op == QLR_OP_LINEAR_DROPOUT ? 1 : 2);
+    if (!bwd && M <= qlr::kFewRows) L.t_splits = few_splits(L.t_splits, M, r, gated);
     size_t parts = (size_t)L.t_splits;
-    if (!bwd) parts = std::max(parts, (size_t)qlr::lora_t_splits(M, K, r, qlr::DT_BF16, qlr::DT_BF16));
+    if (!bwd) parts = std::max(parts, (size_t)(gated ? gated_lora_splits(M, K, r) : qlr::lora_t_splits(M, K, r, qlr::DT_BF16, qlr::DT_BF16)));
     at = L.t + up(parts * (size_t)M * row);
     if (bwd) {
       L.u = at;
@@ -1725,9 +1735,9 @@ qlr_status qlr_gated_fwd(const void* x, qlr_dtype xdt, int64_t M, const qlr_qwei
         jobs[i] = qlr::TrainProd{xp, Ap + (int64_t)i * r * K, K, few ? t + i * side : t, r, few ? r : 2 * r, few ? 0 : i * r, i, false};
       e = qlr::launch_train_t(jobs, 2, M, a.t_splits, d, s);
     } else if (few) {
-      a.t_splits = qlr::lora_t_splits(M, K, r, qlr::DT_BF16, qlr::DT_BF16);
+      a.t_splits = gated_lora_splits(M, K, r);
       const size_t side = (size_t)a.t_splits * (size_t)M * (size_t)r;
-      const qlr::LoraTItem items[2] = {{xp, Ap, t, K, r, false}, {xp, Ap + (int64_t)r * K, t + side, K, r, false}};
+      const qlr::LoraTItem items[2] = {{xp, Ap, t, K, r, false, a.t_splits}, {xp, Ap + (int64_t)r * K, t + side, K, r, false, a.t_splits}};
       e = qlr::launch_lora_t_small_group(items, 2, M, s);
     } else {
       e = qlr::launch_lora_t(x, qlr::DT_BF16, M, K, A, qlr::DT_BF16, 2 * r, t, 1, s);

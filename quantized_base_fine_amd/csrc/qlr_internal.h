@@ -46,11 +46,12 @@ struct LoraTItem {
   int64_t K;
   int r;
   bool bt;
+  int splits;      // M <= 16: partial sums, or 0 (lora_t_splits)
 };
 int lora_t_group_max();
 hipError_t launch_lora_t_group(const LoraTItem* items, int n, int64_t M, hipStream_t s);
 // The same for M <= 16 (bf16, K % 64 == 0, not bt): each item written as
-// lora_t_splits(M, K, r) partial sums, as launch_lora_t would; up to
+// its number of partial sums (lora_t_splits(M, K, r), as launch_lora_t would, where it names none); up to
 // lora_t_small_group_max() items per launch.
 int lora_t_small_group_max();
 hipError_t launch_lora_t_small_group(const LoraTItem* items, int n, int64_t M, hipStream_t s);
@@ -278,6 +279,8 @@ hipError_t launch_grouped_tu(const uint16_t* x, const uint16_t* dy, int64_t M, i
 // Bt (experts x r x N) = B^T per expert, B experts x N x r bf16.
 hipError_t launch_grouped_transpose(const uint16_t* B, int experts, int64_t N, int r, uint16_t* Bt, hipStream_t s);
 // ---- adapter dropout and the gated block (no offsets: one range of M rows)
+// Floats of a side's partial sums of t that the gated block's decode kernel stages.
+constexpr int kGatedFewT = 2048;
 // h = act(gate) up, M x N (and gu): rows of x from 17 on, and up to kFewRows rows.
 hipError_t launch_gated_gemm(const TrainArgs& a, const Levels& lv, hipStream_t s);
 hipError_t launch_gated_few(const TrainArgs& a, const Levels& lv, hipStream_t s);

@@ -367,7 +367,7 @@ hipError_t launch_lora_t_small_group(const LoraTItem* items, int n, int64_t M, h
     L.t = it.t;
     L.K = it.K;
     L.r = it.r;
-    L.splits = lora_t_splits(M, it.K, it.r, DT_BF16, DT_BF16);
+    L.splits = it.splits > 0 ? it.splits : lora_t_splits(M, it.K, it.r, DT_BF16, DT_BF16);
     L.jtiles = (it.r + 15) / 16;
     L.wg0 = wg;
     wg += L.jtiles * L.splits;
