@@ -1715,7 +1715,7 @@ qlr_status qlr_gated_fwd(const void* x, qlr_dtype xdt, int64_t M, const qlr_qwei
     return st;
   if ((st = check_ws(ws, ws_bytes, lay.total)) != QLR_OK) return st;
   qlr_path path = t_path;
-  if (path == QLR_PATH_AUTO) path = M <= qlr::kFewRows ? QLR_PATH_GEMV : QLR_PATH_GEMM;
+  if (path == QLR_PATH_AUTO) path = M <= qlr::kFewRows && qlr::gated_few_takes(r) ? QLR_PATH_GEMV : QLR_PATH_GEMM;
   if (path == QLR_PATH_F32) return fail(QLR_ERR_PATH, "the gated block has no float32 family");
   if (path == QLR_PATH_GEMV && M > qlr::kFewRows) return fail(QLR_ERR_PATH, "the GEMV path takes M <= %d", qlr::kFewRows);
   if (M == 0) return QLR_OK;

@@ -281,6 +281,11 @@ hipError_t launch_grouped_transpose(const uint16_t* B, int experts, int64_t N, i
 // ---- adapter dropout and the gated block (no offsets: one range of M rows)
 // Floats of a side's partial sums of t that the gated block's decode kernel stages.
 constexpr int kGatedFewT = 2048;
+// Ranks at which up to kFewRows rows run on the decode kernel.  It stages ranks of 8, 16 .. 64; at any other each output reads its t and
+// B from memory one by one, and the tiles are faster from rank 3 on.  Decode kernel and tiles, 4-bit, us, one row of 2 x 11008 x 4096: r = 1
+// 29 and 42, r = 2 37 and 43, r = 3 45 and 44, r = 12 115 and 47, r = 16 24 and 41, r = 128 540 and 55; 16 rows: 41 and 42, 56 and 44, 57 and 44,
+// 59 and 48, 28 and 41, 162 and 57; one row of 2 x 1024 x 1024: r = 2 10 and 15, r = 3 11 and 15, r = 12 21 and 17, r = 128 156 and 23.
+constexpr bool gated_few_takes(int r) { return r <= 2 || (r <= 64 && r % 8 == 0); }
 // h = act(gate) up, M x N (and gu): rows of x from 17 on, and up to kFewRows rows.
 hipError_t launch_gated_gemm(const TrainArgs& a, const Levels& lv, hipStream_t s);
 hipError_t launch_gated_few(const TrainArgs& a, const Levels& lv, hipStream_t s);
