@@ -241,12 +241,20 @@ qlr_status qlr_qweight_sizes(int64_t rows, int64_t cols, int32_t bits, int32_t b
  * QLR_OP_LINEAR_BWD (N = rows, K = cols of the weight): the partial sums of
  * x A^T and dy B, B transposed, and float32 partials of the adapter gradients
  * (0 bytes when r is 0).  QLR_OP_LINEAR_I8: the tokens as integers with their
- * scales, and t for M rows and rank r.  QLR_OP_LINEAR_DROPOUT, QLR_OP_GATED: the
- * adapters' products (0 bytes when M or r is 0); their backward ops also the
- * partials of the adapter gradients, and QLR_OP_GATED_BWD the gradients of the
- * pre-activations (M x 2N bf16).  The grouped calls have a function of
- * their own (qlr_grouped_workspace_bytes).  Contents need no initialisation.
- * Host only.
+ * scales, and t for M rows and rank r.  QLR_OP_LINEAR_DROPOUT and QLR_OP_GATED
+ * (N and K: see the calls), of which each size has those parts that its kernels
+ * use: the adapters' products as float32 partial sums; float32 sums of the
+ * result (M x N; of the gated block M x 2N) over up to 8 ranges of the
+ * contraction; for many rows of the gated block a bf16 copy of the weight (2
+ * bytes a weight) with the adapters' operands beside it.  The last two do not
+ * depend on r: the gated block needs them without an adapter too, also for a few rows
+ * (for QLR_PATH_GEMM).  Their backward ops: the same for dx, both adapter
+ * products, the masks' bits (M x K / 8 bytes each), the partials of the adapter
+ * gradients, and QLR_OP_GATED_BWD the gradients of the pre-activations (M x 2N
+ * bf16).  0 bytes when M, N or K is 0, and for QLR_OP_LINEAR_DROPOUT when r is 0;
+ * sizes past the calls' limits are refused (QLR_ERR_SHAPE).  The grouped calls
+ * have a function of their own (qlr_grouped_workspace_bytes).  Contents need no
+ * initialisation.  Host only.
  */
 qlr_status qlr_workspace_bytes(qlr_op op, int64_t M, int64_t N, int64_t K, int32_t r,
                                size_t* bytes);
