@@ -651,8 +651,10 @@ qlr_status qlr_linear_bwd_dropout(const void* dy, qlr_dtype dydt, const void* x,
  * with these counters have them.  N <= 2^19, cols <= 2^20, r <= 2^20, M <= 2^27, M may be
  * 0; M N and M cols at most 2^39.  g and v are within 5e-3 * S + 1e-5 of the exact
  * values (S the sum of the absolute values of the terms; the weight enters
- * rounded to bf16, sums are float32), the activation within 1e-6 of itself and
- * h one float32 rounding (plus half a bf16 ulp for a bf16 h) of their product.
+ * rounded to bf16, sums are float32), the activation within 1e-6 (1 + w) of itself
+ * plus 2e-36 (float32's exp of an argument of size w: |g|, for the tanh form sqrt(8 / pi)
+ * |g + 0.044715 g^3|, for GELU g^2 / 2), and h one float32 rounding (plus half a
+ * bf16 ulp for a bf16 h) of their product.
  * An infinity or NaN stays in its row, one in an adapter in that adapter's side of the
  * columns that it enters; act of an infinity is what g q(g) gives (NaN where
  * that is infinity times 0).
