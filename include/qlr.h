@@ -684,9 +684,9 @@ qlr_status qlr_gated_fwd(const void* x, qlr_dtype xdt, int64_t M, const qlr_qwei
  * element dx is within 1e-2 * S + 1e-5 (plus half a bf16 ulp for a bf16 dx; the
  * weight and dg, dv rounded to bf16), dA and dB within 1e-4 * S + 1e-6, S the sum
  * of the absolute values of the terms that define it at the exact dg and dv of
- * the given gu, |act| and |act'| counted as they are.  An infinity or NaN
- * enters every result that its term enters (and where dg or dv passes bf16's largest
- * value, dx is infinite).  qlr_force_path: QLR_PATH_GEMM is the only family.
+ * the given gu, |act| counted as it is and |act'| as |q| + |g q'| + 1e-32, the
+ * sizes of the two terms that make it up.  An infinity or NaN enters every result
+ * that its term enters (and where dg or dv passes bf16's largest value, dx is infinite).  qlr_force_path: QLR_PATH_GEMM is the only family.
  * ws (device) >= qlr_workspace_bytes(QLR_OP_GATED_BWD, M, N, cols, r).
  * Asynchronous, allocation-free; results do not depend on timing.  Errors: as the
  * forward.
