@@ -770,12 +770,20 @@ hipError_t launch_tile_sum(const TrainArgs& a, int64_t NO, bool gated, hipStream
 
 // When.  The copy costs a fixed time for the weight, 0.5 ns per 1000 weights and two to four launches, and saves the tiled product's own
 // dequantization, whose part grows with the rows; its tiles take longer to begin and to end.  The call through the copy and on
-// the tiled product, 4-bit, r = 16, us: gated forward, K = 4096, rows 1024, 1536, 2048, 4096: N = 4096 108 and 97, 125 and 116,
-// 136 and 135, 244 and 262; N = 11008 224 and 213, 297 and 306, 348 and 365, 636 and 723.  Gated backward under a mask, K = 4096, rows
-// 1536, 2048, 4096: N = 4096 251 and 248, 272 and 272, 430 and 417 (without one 230 and 240, 248 and 264, 389 and 399); N = 11008
-// 519 and 561, 560 and 633, 925 and 954.  Layer backward under a mask, 2048 rows, N x K: 11008 x 4096 267 and 282, 4096 x
-// 4096 157 and 136, 4096 x 11008 333 and 303; 1024 x 1024 80 and 38.  So: from 1536 rows, forward two rounds of tiles, backward a
-// contraction of 8192.
+// the tiled product, 4-bit, r = 16, us.
+// Gated forward, two rounds of its tiles at least.  2048 rows, N = 11008, K = 64, 512, 2048, 8192: 59 and 62, 98 and 103, 213 and 228, 725 and
+// 749; 4096 rows 102 and 115, 175 and 198, 397 and 450, 1315 and 1490; 4096 rows, N = 4096: 46 and 46, 73 and 74, 148 and 164, 479 and 537.
+// At the border, 1536 rows, N = 11008 (two rounds and four tiles), K = 512, 1024, 2048, 4096, 8192: 95 and 88, 129 and 120, 188 and 189, 297 and
+// 306, 574 and 615.  Less than two rounds: 2048 rows, N = 4096, K = 512, 1024, 2048, 4096, 8192 45 and 39, 57 and 53, 83 and 84, 136 and 135,
+// 257 and 270; 1024 rows, N = 11008, K = 4096 224 and 213.
+// Backward, a contraction of 8192 at least, under a mask and without one.  Gated, K = 4096, rows 1536, 2048, 4096: N = 4096 242 and 251, 272 and
+// 277, 438 and 424 (214 and 244, 248 and 269, 396 and 403); N = 5632 350 and 370 at 2048, 568 and 567 at 4096; N = 11008 511 and 565 at 1536,
+// 959 and 997 at 4096.  Layer, 2048 rows, N x K: 8192 x 4096 208 and 230, 11008 x 4096 265 and 293; 4096 x 4096 157 and 136, 4096 x 11008 333
+// and 303, 1024 x 1024 80 and 38.
+// Not where the input gradient's tiles fill most of one round and no second one: there the tiled product has 256 x 256 tiles on every CU
+// too, and the copy saves it little up to 2048 rows.  Layer, 8192 x 8192, 1536, 1800 and 2048 rows (192 and 256 tiles): 292 and 262, 327 and 304, 330 and
+// 310 (264 and 256, 307 and 297, 311 and 303); gated N = 4096, K = 8192 379 and 333, 417 and 379, 422 and 388.  But 2048 rows of 8192 x 5632 (176
+// tiles) 263 and 312, of 8192 x 11008 (344) 474 and 479, 3500 rows of 8192 x 4096 403 and 424, 4096 rows of it (256) 305 and 314.
 constexpr int64_t kDenseRows = 1536;
 
 DensePlan dense_plan(int64_t M, int64_t NO, int64_t KC, bool gated) {
@@ -783,7 +791,8 @@ DensePlan dense_plan(int64_t M, int64_t NO, int64_t KC, bool gated) {
   p.ntiles = (int)((NO + (gated ? 127 : 255)) / (gated ? 128 : 256));
   const int64_t total = (M + 255) / 256 * p.ntiles, rest = total % kCus;
   // (32-bit offsets: 256 rows of x or of the weight stay below 2^31 bytes)
-  p.ok = M >= kDenseRows && (gated ? total >= 512 : KC >= 8192 && total >= 96) && KC < (int64_t)1 << 21 && total < INT_MAX - 256;
+  const bool round = M <= 2048 && total >= 192 && total <= kCus;
+  p.ok = M >= kDenseRows && (gated ? total >= 512 : KC >= 8192 && total >= 96 && !round) && KC < (int64_t)1 << 21 && total < INT_MAX - 256;
   p.whole = (int)total;
   p.splits = 1;
   const int64_t steps = (KC + 63) / 64, sp = rest > 0 ? std::min({(int64_t)4, kCus / rest, steps / 16}) : 1;
