@@ -739,15 +739,18 @@ unsigned grid_of(int64_t items) { return (unsigned)std::max<int64_t>(1, std::min
 // CUs at work are what counts: up to 64 rows 64 x 128 tiles, from there on 128 x 128 ones, in ranges that make about 512
 // workgroups, two to a CU.  Input gradient of 777 rows, 2048 columns over 5632 (2-bit): 40 us and 6.5 for the sums, as 64 x 128 tiles
 // 55, in two ranges of those 47 and 5; of 333, 4096 over 4096 (8-bit): 37 and 6.6, 57, 50 and 5; of 64, 1024 over 2048: 11 and 4,
-// unsplit 24.  A tile of a few steps more than fills the GPU by itself: 333 rows, 1403 gated columns over 2048 unsplit
-// 22 us, in 3 to 7 ranges 24 to 27.  The layer's forward under dropout (r = 16, 4-bit), whole call, ranges and the prefill
+// unsplit 24.  Up to 40 steps, 128 tiles of 64 x 128 and more run unsplit (the sums' kernel and the ranges' ends cost 6 to 10 us).  Gated
+// forward, r = 8, 4-bit, whole call, unsplit and in the 2 to 8 ranges that 512 workgroups would make, 32, 40 and 64 steps: 333 rows x 1403 (132
+// tiles) 29 and 37, 33 and 32, 47 and 37; 333 x 2048 (192) 27 and 32, 31 and 35, 44 and 40; 600 x 1024 (160) 27 and 32, 31 and 33,
+// 45 and 38; 130 x 4096 (192) 26 and 31, 31 and 34, 43 and 41; 64 x 11008 (172) 27 and 32, 32 and 36, 44 and 45.  With 66 tiles (333 x
+// 700) 28 and 27, 32 and 28, 44 and 32.  Layer's backward, 333 rows, 4096 columns (192 tiles) 38 and 45, 44 and 46, 58 and 52.  The layer's forward under dropout (r = 16, 4-bit), whole call, ranges and the prefill
 // kernel without them: 64 rows of 1024 x 1024 15 and 25 us, of 4096 x 4096 21 and 64; 333 rows 18 and 25, 37 and 64; 777 rows
 // 21 and 27, 60 and 67.
 int train_tile_splits(int64_t M, int64_t cols, int64_t KC) {
   // (256 x 256 tiles: see launch_tile)
   if ((M + 255) / 256 * ((cols + 255) / 256) >= 192) return 1;
   const int64_t nt = (cols + 127) / 128, steps = (KC + 63) / 64;
-  if (steps <= 32 && (M + 63) / 64 * nt >= 128) return 1;
+  if (steps <= 40 && (M + 63) / 64 * nt >= 128) return 1;
   const int64_t bm = M <= 64 ? 64 : 128, tiles = (M + bm - 1) / bm * nt;
   return (int)std::max<int64_t>(1, std::min({(int64_t)512 / tiles, steps / kSplitSteps, (int64_t)kMaxSplits}));
 }

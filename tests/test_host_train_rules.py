@@ -1,5 +1,5 @@
-"""Host-side test of when the input gradients of many rows go through a dense copy of the weight, read off the workspace (the copy is
-its largest part, and there is nothing else without an adapter)."""
+"""Host-side tests of when the input gradients of many rows go through a dense copy of the weight, and of when a product's contraction is
+split, read off the workspace: without an adapter it holds nothing else."""
 import pytest
 
 from quantized_base_fine_amd import qlr
@@ -29,3 +29,15 @@ def test_other_gradients_of_many_rows_do(op, N):
         assert copies(op, M, N, K), (M, K)
     for M, K in ((1535, 4096), (1024, 8192)):
         assert not copies(op, M, N, K), (M, K)
+
+
+@pytest.mark.parametrize("M,N", [(333, 1403), (333, 2048), (600, 1024), (130, 4096), (64, 11008)])
+def test_many_short_tiles_are_not_split(M, N):
+    """128 tiles of 64 x 128 and more: unsplit up to 40 steps of 64."""
+    for K, split in ((1024, False), (2048, False), (2560, False), (2624, True), (4096, True)):
+        assert (qlr.workspace_bytes(qlr.OP_GATED, M, N, K, 0) > 0) == split, K
+
+
+def test_few_tiles_are():
+    for K, split in ((256, False), (512, True), (2048, True), (4096, True)):
+        assert (qlr.workspace_bytes(qlr.OP_GATED, 333, 700, K, 0) > 0) == split, K
