@@ -1,5 +1,5 @@
 // Gated block of up to 16 rows (decoding): bound by the stream of both projections' codes.
-#include "qlr_tile.h"
+#include "qlr_few.h"
 
 namespace qlr {
 
@@ -22,36 +22,8 @@ constexpr float kLevelUnit = 1.0f / 128.0f;
 constexpr int kWaves = 8;
 template <int BITS>
 constexpr int kFewChunk = BITS == 8 ? 2 : 4;  // (four of 8 bits spill)
-constexpr uint32_t kXRow = 256 + 16, kXSlice = 16 * kXRow;  // a wave's slice: two blocks of 16 rows, padded
 template <int NS>
 constexpr uint32_t kRedBytes = kWaves * 16 * 16 * NS * 4;   // the waves' sums, over the slices
-
-template <int BITS>
-struct FewTab {
-  static constexpr int kEntries = BITS == 8 ? 256 : 1 << (2 * BITS);
-  static constexpr uint32_t kBytes = kEntries * 128;
-};
-template <int BITS>
-constexpr int kWords = BITS == 8 ? 4 : BITS == 2 ? 1 : 2;  // words of a lane's 16 codes
-
-// bf16 levels of the lane's 16 codes, pairs in code order; tl = 4 (lane % 32).
-template <int BITS>
-__device__ __forceinline__ void few_levels(const uint32_t (&w)[kWords<BITS>], uint32_t tl, uint32_t (&o)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if constexpr (BITS == 8) {
-      const uint32_t v = w[j >> 1] >> (16 * (j & 1));
-      o[j] = __builtin_amdgcn_perm(lds_word(((v >> 8) & 255u) << 7 | tl), lds_word((v & 255u) << 7 | tl), 0x05040100u);
-    } else if constexpr (BITS == 3) {
-      const int bit = 6 * j, wd = bit >> 5, sh = bit & 31;
-      const uint32_t v = sh + 6 > 32 ? __builtin_amdgcn_alignbit(w[wd < 1 ? wd + 1 : wd], w[wd], sh) : w[wd] >> sh;
-      o[j] = lds_word((v & 63u) << 7 | tl);
-    } else {
-      constexpr uint32_t mask = (1u << (2 * BITS)) - 1;
-      o[j] = lds_word(((w[(2 * BITS * j) >> 5] >> ((2 * BITS * j) & 31)) & mask) << 7 | tl);
-    }
-  }
-}
 
 // The adapters' operands of 8 NS columns, and all of the kernel's dynamic LDS.
 template <int NS>
@@ -62,7 +34,7 @@ constexpr uint32_t kFewBytes = FewTab<BITS>::kBytes + (kWaves * kXSlice > kRedBy
 // P.t: the gate's t_splits x M x r partial sums, then the up projection's.
 template <int BITS, int NS>
 __global__ __launch_bounds__(512, 4) void k_gated_few(TrainArgs P, Levels lv) {
-  constexpr int NR = 16 * NS, NO = NR / 2, NW = kWords<BITS>, kChunk = kFewChunk<BITS>;
+  constexpr int NR = 16 * NS, NO = NR / 2, NW = kFewWords<BITS>, kChunk = kFewChunk<BITS>;
   typedef FewAd<NS> Adapter;
   constexpr uint32_t kRed = FewTab<BITS>::kBytes;
   extern __shared__ uint32_t smem[];
@@ -217,18 +189,9 @@ __global__ __launch_bounds__(512, 4) void k_gated_few(TrainArgs P, Levels lv) {
 template <int BITS, int NS>
 hipError_t launch_few_r(const TrainArgs& a, const Levels& lv, hipStream_t s) {
   auto kern = k_gated_few<BITS, NS>;
-  static std::atomic<bool> checked{false};  // (host threads may come here at once: each sets the same)
-  hipError_t e;
-  if (!checked) {
-    // the level table is read at LDS addresses from 0: the kernel must not have static LDS
-    hipFuncAttributes fa;
-    e = hipFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern));
-    if (e != hipSuccess) return e;
-    if (fa.sharedSizeBytes != 0) return hipErrorInvalidKernelFile;
-    checked = true;
-  }
+  static std::atomic<bool> checked{false};
   constexpr size_t shmem = kFewBytes<BITS, NS>;
-  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)shmem);
+  const hipError_t e = few_prepare(reinterpret_cast<const void*>(kern), shmem, checked);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)(a.N + 8 * NS - 1) / (8 * NS)), dim3(512), shmem, s, a, lv);
   return hipGetLastError();

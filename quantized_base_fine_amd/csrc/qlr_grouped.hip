@@ -2,7 +2,7 @@
 // sorted by expert, device offsets, one stacked weight, one adapter per expert.
 // This file holds the forward for experts with few rows and the adapter
 // products; the tiled products are instantiated per code width elsewhere.
-#include "qlr_tile.h"
+#include "qlr_few.h"
 
 namespace qlr {
 
@@ -39,36 +39,6 @@ __device__ __forceinline__ s16x4_t lds_tr16p(const char* p) {
 // accesses of a wave (levels, permutes, x), which the loads cover only in part.  Whole 128-byte lines through a wave's slice of LDS instead of 32-byte
 // pieces of 16 rows took 57 us from memory and 55 from cache, and 2-bit codes 11 % longer: not kept.
 constexpr int kFewWaves = 8, kFewChunk = 2;
-constexpr uint32_t kXRow = 256 + 16, kXSlice = 16 * kXRow;  // a wave's slice: two blocks of 16 rows, padded
-
-template <int BITS>
-struct FewTab {
-  static constexpr int kEntries = BITS == 8 ? 256 : 1 << (2 * BITS);
-  static constexpr uint32_t kBytes = kEntries * 128;
-};
-
-// Words of a lane's 16 codes.
-template <int BITS>
-constexpr int kFewWords = BITS == 8 ? 4 : BITS == 2 ? 1 : 2;
-
-// bf16 levels of the lane's 16 codes, pairs in code order; tl = 4 (lane % 32).
-template <int BITS>
-__device__ __forceinline__ void few_levels(const uint32_t (&w)[kFewWords<BITS>], uint32_t tl, uint32_t (&o)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if constexpr (BITS == 8) {
-      const uint32_t v = w[j >> 1] >> (16 * (j & 1));
-      o[j] = __builtin_amdgcn_perm(lds_word(((v >> 8) & 255u) << 7 | tl), lds_word((v & 255u) << 7 | tl), 0x05040100u);
-    } else if constexpr (BITS == 3) {
-      const int bit = 6 * j, wd = bit >> 5, sh = bit & 31;
-      const uint32_t v = sh + 6 > 32 ? __builtin_amdgcn_alignbit(w[wd < 1 ? wd + 1 : wd], w[wd], sh) : w[wd] >> sh;
-      o[j] = lds_word((v & 63u) << 7 | tl);
-    } else {
-      constexpr uint32_t mask = (1u << (2 * BITS)) - 1;
-      o[j] = lds_word(((w[(2 * BITS * j) >> 5] >> ((2 * BITS * j) & 31)) & mask) << 7 | tl);
-    }
-  }
-}
 
 template <int BITS, int RS>
 __global__ __launch_bounds__(512, 4) void k_grouped_few(TileArgs P, Levels lv) {
@@ -195,18 +165,9 @@ __global__ __launch_bounds__(512, 4) void k_grouped_few(TileArgs P, Levels lv) {
 template <int BITS, int RS>
 hipError_t launch_few_r(const TileArgs& a, const Levels& lv, hipStream_t s) {
   auto kern = k_grouped_few<BITS, RS>;
-  static std::atomic<bool> checked{false};  // (host threads may come here at once: each sets the same)
-  hipError_t e;
-  if (!checked) {
-    // the level table is read at LDS addresses from 0: the kernel must not have static LDS
-    hipFuncAttributes fa;
-    e = hipFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern));
-    if (e != hipSuccess) return e;
-    if (fa.sharedSizeBytes != 0) return hipErrorInvalidKernelFile;
-    checked = true;
-  }
+  static std::atomic<bool> checked{false};
   const size_t shmem = FewTab<BITS>::kBytes + kFewWaves * kXSlice + (a.r > 0 ? FewAdapter<16 * RS, 1024>::kBytes : 0);
-  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)shmem);
+  const hipError_t e = few_prepare(reinterpret_cast<const void*>(kern), shmem, checked);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)((a.N + 16 * RS - 1) / (16 * RS)), (unsigned)a.experts), dim3(512), shmem, s, a, lv);
   return hipGetLastError();

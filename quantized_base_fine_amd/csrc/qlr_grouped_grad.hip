@@ -1,7 +1,7 @@
 // Adapter gradients of the expert products: with e's rows R_e,
 //     dA_e = s u_e^T x_e   (r x K),   dB_e = s dy_e^T t_e   (N x r),
 // u = dy B_e and t = x A_e^T in float32.
-#include "qlr_tile.h"
+#include "qlr_grad_tile.h"
 
 namespace qlr {
 
@@ -23,7 +23,7 @@ namespace {
 // 4096 rows in 8 ranges of 4096 x 4096, r = 16: 15 us for the 67 MB of x and dy (4.5 TB/s; a device copy moves 5.1)
 // and 5.5 us for the sums of 6 longer ranges' chunks.
 constexpr int kGradChunk = 512;
-constexpr uint32_t kGQ = 32 * 256, kGP = 32 * 128, kGBuf = kGQ + 3 * kGP;
+constexpr uint32_t kGBuf = kQ + 3 * kP;
 
 struct GroupGrads {
   const float* P[2];
@@ -70,18 +70,6 @@ __device__ __forceinline__ int extra_scan(const int32_t* offsets, int E, int M, 
   }
   e = -1;
   return before;
-}
-
-__device__ __forceinline__ uint32_t gq_off(uint32_t row, uint32_t chunk) {
-  const uint32_t h = (row & 3u) | (((row >> 3) & 1u) << 2);
-  return row * 256u + ((chunk ^ (h << 1)) << 4);
-}
-__device__ __forceinline__ uint32_t gp_off(uint32_t row, uint32_t chunk) {
-  const uint32_t h = ((row >> 1) & 1u) | (((row >> 3) & 1u) << 1);
-  return row * 128u + ((chunk ^ (h << 1)) << 4);
-}
-__device__ __forceinline__ s16x4_t grad_tr(const char* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(const_cast<char*>(p)));
 }
 
 // R4: r % 4 == 0 (16-byte loads of P)
@@ -142,22 +130,13 @@ __global__ __launch_bounds__(256) void k_grouped_grad(GroupGrads G) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t row = qrow + 16u * i;
-      *reinterpret_cast<u32x4_t*>(lds + buf + gq_off(row, qch)) = s.q[i];
+      *reinterpret_cast<u32x4_t*>(lds + buf + q_off(row, qch)) = s.q[i];
       uint32_t part[3][2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float v0 = s.p[i][2 * t], v1 = s.p[i][2 * t + 1];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {  // (the third part is the whole rest: at most 8 bits)
-          const float r0 = k < 2 ? split_rest(v0) : 0.0f, r1 = k < 2 ? split_rest(v1) : 0.0f;
-          part[k][t] = (__float_as_uint(v0) >> 16) | (__float_as_uint(v1) & 0xFFFF0000u);
-          v0 = r0;
-          v1 = r1;
-        }
-      }
+      for (int t = 0; t < 2; ++t) three_parts(s.p[i][2 * t], s.p[i][2 * t + 1], part[0][t], part[1][t], part[2][t]);
 #pragma unroll
       for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<uint2*>(lds + buf + kGQ + k * kGP + gp_off(row, qch >> 1) + 8u * (qch & 1u)) =
+        *reinterpret_cast<uint2*>(lds + buf + kQ + k * kP + p_off(row, qch >> 1) + 8u * (qch & 1u)) =
             uint2{part[k][0], part[k][1]};
     }
   };
@@ -171,19 +150,15 @@ __global__ __launch_bounds__(256) void k_grouped_grad(GroupGrads G) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const uint32_t col = 32u * w + 16u * c + 4u * (sp & 3u);
-      qa[c][hf] = gq_off(row, col >> 3) + 2u * (col & 7u);
+      qa[c][hf] = q_off(row, col >> 3) + 2u * (col & 7u);
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const uint32_t col = 16u * t + 4u * (sp & 3u);
-      pa[t][hf] = kGQ + gp_off(row, col >> 3) + 2u * (col & 7u);
+      pa[t][hf] = kQ + p_off(row, col >> 3) + 2u * (col & 7u);
     }
   }
-  auto frag = [&](uint32_t lo, uint32_t hi) {
-    const s16x4_t l = grad_tr(lds + lo), h = grad_tr(lds + hi);
-    return as_bf16x8(u32x4_t{__builtin_bit_cast(uint2, l).x, __builtin_bit_cast(uint2, l).y,
-                             __builtin_bit_cast(uint2, h).x, __builtin_bit_cast(uint2, h).y});
-  };
+  auto frag = [&](uint32_t lo, uint32_t hi) { return tr_frag(lds + lo, lds + hi); };
   f32x4_t acc[2][4];
 #pragma unroll
   for (int c = 0; c < 2; ++c)
@@ -205,7 +180,7 @@ __global__ __launch_bounds__(256) void k_grouped_grad(GroupGrads G) {
       if (t >= jt) break;
 #pragma unroll
       for (int k = 2; k >= 0; --k) {  // smallest part first
-        const bf16x8_t p = frag(buf + k * kGP + pa[t][0], buf + k * kGP + pa[t][1]);
+        const bf16x8_t p = frag(buf + k * kP + pa[t][0], buf + k * kP + pa[t][1]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) acc[c][t] = mfma16x16x32(q[c], p, acc[c][t]);
       }

@@ -1,20 +1,11 @@
 // Adapter products and gradients of a training step: under dropout masks formed on the way (qlr_philox.h), and of the gated
 // block's backward, whose dg = dh up act'(gate) and dv = dh act(gate) are formed on the way too.
-#include "qlr_tile.h"
+#include "qlr_grad_tile.h"
 
 namespace qlr {
 
 namespace {
 
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ s16x4_t train_tr(const char* p) {  // LDS transpose read (see lds_tr16)
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(const_cast<char*>(p)));
-}
-__device__ __forceinline__ bf16x8_t tr_frag(const char* lo, const char* hi) {
-  const s16x4_t l = train_tr(lo), h = train_tr(hi);
-  return as_bf16x8(u32x4_t{__builtin_bit_cast(uint2, l).x, __builtin_bit_cast(uint2, l).y, __builtin_bit_cast(uint2, h).x,
-                           __builtin_bit_cast(uint2, h).y});
-}
 __device__ __forceinline__ u32x4_t ld16g(const void* p) { return *reinterpret_cast<const u32x4_t*>(p); }
 
 // Eight (dg, dv) from dh, g and v, as bf16 pieces: rounded to nearest (gn, vn), and as three parts (8 bits each, the third the whole
@@ -22,12 +13,6 @@ __device__ __forceinline__ u32x4_t ld16g(const void* p) { return *reinterpret_ca
 struct Dgu {
   u32x4_t gn, vn, g[3], v[3];
 };
-__device__ __forceinline__ void three_parts(float a, float b, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
-  float a1 = split_rest(a), b1 = split_rest(b), a2 = split_rest(a1), b2 = split_rest(b1);
-  p0 = (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xFFFF0000u);
-  p1 = (__float_as_uint(a1) >> 16) | (__float_as_uint(b1) & 0xFFFF0000u);
-  p2 = (__float_as_uint(a2) >> 16) | (__float_as_uint(b2) & 0xFFFF0000u);
-}
 template <int ACT, bool NEAREST, bool G, bool V>
 __device__ __forceinline__ void form_dgu(u32x4_t dh, u32x4_t gate, u32x4_t up, Dgu& o) {
 #pragma unroll
@@ -518,7 +503,6 @@ int64_t grad_chunk(int64_t M, int64_t CC) {
   const int64_t tiles = (CC + 127) / 128, chunks = std::max<int64_t>(1, (256 + tiles - 1) / tiles);
   return std::max<int64_t>(64, std::min<int64_t>(512, ((M + chunks - 1) / chunks + 31) / 32 * 32));
 }
-constexpr uint32_t kQ = 32 * 256, kP = 32 * 128;
 
 struct TrainGrads {
   TrainGrad j[4];
@@ -531,15 +515,6 @@ struct TrainGrads {
   DropArgs drop;
   float* part;    // extra chunks x (the jobs' outputs)
 };
-
-__device__ __forceinline__ uint32_t q_off(uint32_t row, uint32_t chunk) {
-  const uint32_t h = (row & 3u) | (((row >> 3) & 1u) << 2);
-  return row * 256u + ((chunk ^ (h << 1)) << 4);
-}
-__device__ __forceinline__ uint32_t p_off(uint32_t row, uint32_t chunk) {
-  const uint32_t h = ((row >> 1) & 1u) | (((row >> 3) & 1u) << 1);
-  return row * 128u + ((chunk ^ (h << 1)) << 4);
-}
 
 // SRC 0: Q as it is or masked; 1: dg; 2: dv
 template <int SRC, int ACT>
