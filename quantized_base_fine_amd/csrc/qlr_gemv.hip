@@ -838,9 +838,18 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemv(Params P, Levels lv) {
       __syncthreads();
     }
   }
-  // sT[i] = sum over parts of src[part][i], in part order, staged through sRed
+  // sT[i] = sum over parts of src[part][i], in part order, staged through sRed (a part longer than that: from memory)
   auto stage_t = [&](const float* src, int nparts) {
-    const int per = mr > 0 ? max(1, (kWaves * 256) / mr) : 1;
+    const int per = mr > 0 ? (kWaves * 256) / mr : 1;
+    if (per == 0) {
+      for (int i = tid; i < mr; i += kThreads) {
+        float acc = 0.0f;
+        for (int q = 0; q < nparts; ++q) acc += src[(int64_t)q * mr + i];
+        sT[i] = acc;
+      }
+      __syncthreads();
+      return;
+    }
     for (int p0 = 0; p0 < nparts; p0 += per) {
       const int np = min(per, nparts - p0);
       for (int idx = tid; idx < np * mr; idx += kThreads) sRed[idx] = src[(int64_t)p0 * mr + idx];
