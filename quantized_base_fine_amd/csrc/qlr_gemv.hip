@@ -131,6 +131,9 @@ struct Params {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
 }
+// Range of B (N x r bf16, loaded in 16-byte pieces): whole words, since a word that the range ends in reads as zero and would lose
+// the last element of an odd number.  (The word begins inside B, and so lies on its page.)
+__device__ __forceinline__ int64_t b_bytes(int64_t N, int64_t r) { return (N * r * 2 + 3) & ~(int64_t)3; }
 constexpr uint32_t kOOB = 0xFFFFFFF0u;  // buffer offset past every resource: reads zero, writes dropped
 
 // `ok ? off : kOOB`, with `off` computed unconditionally: the pin keeps the
@@ -629,7 +632,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemv(Params P, Levels lv) {
   const int bpieces = (ADP && !DBA && (TF || P.bpre)) ? (int)ntl * 2 * r : 0;
   u32x4_t bpv[ADP ? kBPre : 1];
   if constexpr (ADP) {
-    const __amdgpu_buffer_rsrc_t brs = rsrc(a.B, N * r * 2);
+    const __amdgpu_buffer_rsrc_t brs = rsrc(a.B, b_bytes(N, r));
 #pragma unroll
     for (int i = 0; i < kBPre; ++i) {
       const int p = tid + i * kThreads;
@@ -1426,7 +1429,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemv_group(GvParams P, Levels l
     const __amdgpu_buffer_rsrc_t cr = rsrc(L.codes, N * nb * 8 * BITS);
     const __amdgpu_buffer_rsrc_t qr = rsrc(L.q8, N * nb);
     const __amdgpu_buffer_rsrc_t sr = rsrc(L.cst, ((N * nb + 255) >> 8) * 4);
-    const __amdgpu_buffer_rsrc_t brs = rsrc(L.B, ADP ? N * r * 2 : 0);
+    const __amdgpu_buffer_rsrc_t brs = rsrc(L.B, ADP ? b_bytes(N, r) : 0);
     const __amdgpu_buffer_rsrc_t yr = rsrc(L.y, N * ES);
     const uint32_t nb32 = (uint32_t)nb, kb032 = (uint32_t)kb0;
     const uint32_t rowb = nb32 * (8u * BITS);
