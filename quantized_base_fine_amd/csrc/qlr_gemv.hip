@@ -1717,6 +1717,7 @@ Plan plan_gemv(const LinearArgs& a) {
       lds += r16((size_t)(nb + 8) * 4);
     }
     // adapter product: fused, partials prefetched when they fit the registers, else summed by a loop
+    constexpr size_t kRoom = kLdsMax - 128;  // (the zero strip behind them)
     const size_t mr = (size_t)a.M * (size_t)r;
     const size_t tparts = (size_t)a.t_splits * mr;
     P.tmode = T_GLOBAL;
@@ -1729,12 +1730,12 @@ Plan plan_gemv(const LinearArgs& a) {
         lds += r16(mr * 4);
         P.sTP = (uint32_t)lds;
         lds += (size_t)kWaves * kFuseR * 4;
-      } else if (tparts <= (size_t)kTPre * kThreads && lds + r16(mr * 4) + r16(tparts * 4) <= kLdsMax) {
+      } else if (tparts <= (size_t)kTPre * kThreads && lds + r16(mr * 4) + r16(tparts * 4) <= kRoom) {
         P.tmode = T_PREFETCH;
         lds += r16(mr * 4);
         P.sTP = (uint32_t)lds;
         lds += r16(tparts * 4);
-      } else if (lds + r16(mr * 4) <= kLdsMax) {
+      } else if (lds + r16(mr * 4) <= kRoom) {
         P.tmode = T_LOOP;
         lds += r16(mr * 4);
       }
@@ -1742,7 +1743,7 @@ Plan plan_gemv(const LinearArgs& a) {
       // kBPre per thread), from a 16-byte aligned B
       const int64_t tpw = (P.ntiles + pl.grid - 1) / pl.grid;
       if (tpw * 2 * r <= (int64_t)kBPre * kThreads && (reinterpret_cast<uintptr_t>(a.B) & 15) == 0 &&
-          lds + r16((size_t)(32 * r * tpw)) <= kLdsMax) {
+          lds + r16((size_t)(32 * r * tpw)) <= kRoom) {
         P.bpre = 1;
         P.sB = (uint32_t)lds;
         lds += r16((size_t)(32 * r * tpw));
