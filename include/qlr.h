@@ -686,7 +686,8 @@ qlr_status qlr_gated_fwd(const void* x, qlr_dtype xdt, int64_t M, const qlr_qwei
  * of the absolute values of the terms that define it at the exact dg and dv of
  * the given gu, |act| counted as it is and |act'| as |q| + |g q'| + 1e-32, the
  * sizes of the two terms that make it up.  An infinity or NaN enters every result
- * that its term enters (and where dg or dv passes bf16's largest value, dx is infinite).  qlr_force_path: QLR_PATH_GEMM is the only family.
+ * that its term enters (and where dg or dv passes bf16's largest value, dx is
+ * infinite).  qlr_force_path: QLR_PATH_GEMM is the only family.
  * ws (device) >= qlr_workspace_bytes(QLR_OP_GATED_BWD, M, N, cols, r).
  * Asynchronous, allocation-free; results do not depend on timing.  Errors: as the
  * forward.
@@ -698,10 +699,11 @@ qlr_status qlr_gated_bwd(const void* dh, qlr_dtype dhdt, const void* gu, const v
 
 /*
  * Force the kernel family used by qlr_linear_fwd, qlr_linear_fwd_mixed,
- * qlr_linear_fwd_i8 and qlr_linear_fwd_grouped (as each describes) on
- * the calling thread (for tests, measurement, and callers that need a
+ * qlr_linear_fwd_i8, qlr_linear_fwd_grouped, qlr_linear_fwd_dropout and
+ * qlr_gated_fwd (as each describes) on the calling thread (for tests, measurement, and callers that need a
  * family's error bound; see qlr_linear_fwd).  QLR_PATH_AUTO restores the
- * default choice: F32 for float32 x or float32 adapters, GEMV for M <= 16,
+ * default choice: F32 for float32 x or float32 adapters, GEMV for M <= 16 (of
+ * qlr_gated_fwd at ranks its decode kernel holds on chip: 8, 16 .. 64, or at most 2),
  * GEMM otherwise.  Host only.  Errors: QLR_ERR_PATH for an unknown value.
  */
 qlr_status qlr_force_path(qlr_path path);

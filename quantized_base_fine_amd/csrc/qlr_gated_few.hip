@@ -15,7 +15,10 @@ namespace {
 //
 // 16 rows of 2 x 22016 x 8192, 4-bit: 75 us (181 MB of codes, 2.4 TB/s) with two sets, one 92 (each set's own x), four 88 (one
 // workgroup to a CU).  Without x's loads and writes it ran in 52, without the lookups in 66, without the codes' loads in 62: no
-// one of them bounds it.  One row of 2 x 11008 x 4096: 20 us of the call's 24; two sets of 8 columns each, one 27.
+// one of them bounds it.  One row of 2 x 11008 x 4096: 20 us of the call's 24; two sets of 8 columns each, one 27; with
+// r = 64 25. 16 rows of it, r = 16: 28, r = 64: 33 (the products before it write as many partial sums as the kernel stages, see FewAd;
+// read from memory by every output they took 94 and 122).
+//
 // The table holds the levels times 2^-7, the results are multiplied by 2^7 once they are added up: 64 of bf16's largest values times
 // levels of at most 1 stay inside float32 before the scale, and a scale times 2^7 is never formed.
 constexpr float kLevelUnit = 1.0f / 128.0f;
