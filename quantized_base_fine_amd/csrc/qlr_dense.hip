@@ -743,7 +743,8 @@ unsigned grid_of(int64_t items) { return (unsigned)std::max<int64_t>(1, std::min
 // forward, r = 8, 4-bit, whole call, unsplit and in the 2 to 8 ranges that 512 workgroups would make, 32, 40 and 64 steps: 333 rows x 1403 (132
 // tiles) 29 and 37, 33 and 32, 47 and 37; 333 x 2048 (192) 27 and 32, 31 and 35, 44 and 40; 600 x 1024 (160) 27 and 32, 31 and 33,
 // 45 and 38; 130 x 4096 (192) 26 and 31, 31 and 34, 43 and 41; 64 x 11008 (172) 27 and 32, 32 and 36, 44 and 45.  With 66 tiles (333 x
-// 700) 28 and 27, 32 and 28, 44 and 32.  Layer's backward, 333 rows, 4096 columns (192 tiles) 38 and 45, 44 and 46, 58 and 52.  The layer's forward under dropout (r = 16, 4-bit), whole call, ranges and the prefill
+// 700) 28 and 27, 32 and 28, 44 and 32.  Layer's backward, 333 rows, 4096 columns (192 tiles) 38 and 45, 44 and 46, 58 and 52.
+// The layer's forward under dropout (r = 16, 4-bit), whole call, ranges and the prefill
 // kernel without them: 64 rows of 1024 x 1024 15 and 25 us, of 4096 x 4096 21 and 64; 333 rows 18 and 25, 37 and 64; 777 rows
 // 21 and 27, 60 and 67.
 int train_tile_splits(int64_t M, int64_t cols, int64_t KC) {

@@ -14,7 +14,7 @@ N, K = 72, 128
 
 @pytest.mark.parametrize("bits", [2, 3, 4, 8])
 @pytest.mark.parametrize("M", [1, 5, 16, 17, 70])
-@pytest.mark.parametrize("wscale,xscale", [(0.05, 2.0 ** 125), (4e36, 0.5), (1e-36, 2.0 ** 126)])
+@pytest.mark.parametrize("wscale,xscale", [(0.05, 2.0 ** 125), (4e36, 0.5), (1e-36, 2.0 ** 126), (4e36, 2.0 ** -120), (4e36, 2.0 ** -125)])
 def test_sums_before_the_scale(bits, M, wscale, xscale):
     print(f"gated large bits={bits} M={M} w={wscale} x={xscale}", flush=True)
     g = torch.Generator().manual_seed(bits + M)
