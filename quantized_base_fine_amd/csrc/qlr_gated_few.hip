@@ -6,8 +6,8 @@ namespace qlr {
 namespace {
 
 // As the few-rows kernel of the expert products: levels from a table in LDS (pairs of codes as bf16, 32 copies), the
-// block's scale on its products, a wave's rows of x through a slice of LDS of its own.  A level is held as one bf16 (half a
-// step, 2^-8 of it; the scale stays float32): two parts would double the lookups and products that bound the kernel beside the stream.
+// block's scale on its products, a wave's rows of x through a slice of LDS of its own.  A level is held as one bf16 (off by half a
+// step, 2^-8 of it, at most; see kLevelUnit; the scale stays float32): two parts would double the lookups and products that bound the kernel beside the stream.
 // A workgroup of 8 waves takes 8 NS output columns as NS sets of 16 weight rows, 8 of the gate and the up rows of the same columns; each
 // wave multiplies all sets over an eighth of K, so that a block of x is read once for NS sets.  Four blocks of 64 columns a
 // step (of 4-bit codes, one line of 128 bytes a row), the next step's codes in flight.  The waves' sums are added through LDS
@@ -19,9 +19,13 @@ namespace {
 // r = 64 25. 16 rows of it, r = 16: 28, r = 64: 33 (the products before it write as many partial sums as the kernel stages, see FewAd;
 // read from memory by every output they took 94 and 122).
 //
-// The table holds the levels times 2^-7, the results are multiplied by 2^7 once they are added up: 64 of bf16's largest values times
-// levels of at most 1 stay inside float32 before the scale, and a scale times 2^7 is never formed.
-constexpr float kLevelUnit = 1.0f / 128.0f;
+// The table holds the levels times a unit f 2^-7, the results are divided by it once they are added up.  2^-7: 64 of bf16's largest
+// values times levels of at most 1 stay inside float32 before the scale, and a scale times 2^7 is never formed.  f: of the bf16
+// numbers in [1, 2) (so that a level of 1 stays exact) one at which bf16(f level) is close to f level.  What the rounding costs a
+// product with normally distributed weights and rows, in relative 2-norm: 2 bits 4.0e-6 (at f = 1 7.9e-4), 3 bits 1.8e-4 (4.0e-4), 4 bits
+// 7.0e-4 (1.18e-3), 8 bits 1.30e-3 (1.61e-3).
+template <int BITS>
+constexpr float kLevelUnit = (BITS == 2 ? 1.6640625f : BITS == 3 ? 1.1953125f : BITS == 4 ? 1.6015625f : 1.59375f) / 128.0f;
 constexpr int kWaves = 8;
 template <int BITS>
 constexpr int kFewChunk = BITS == 8 ? 2 : 4;  // (four of 8 bits spill)
@@ -99,8 +103,8 @@ __global__ __launch_bounds__(512, 4) void k_gated_few(TrainArgs P, Levels lv) {
     constexpr int NL = 1 << BITS;
     for (int i = tid; i < FewTab<BITS>::kEntries * 8; i += 512) {  // four copies each
       const int en = i >> 3;
-      const uint32_t v = BITS == 8 ? f32_to_bf16_bits(kLevelUnit * sL[en])
-                                   : pack_bf16x2(kLevelUnit * sL[en & (NL - 1)], kLevelUnit * sL[en >> BITS]);
+      const uint32_t v = BITS == 8 ? f32_to_bf16_bits(kLevelUnit<BITS> * sL[en])
+                                   : pack_bf16x2(kLevelUnit<BITS> * sL[en & (NL - 1)], kLevelUnit<BITS> * sL[en >> BITS]);
       reinterpret_cast<u32x4_t*>(smem)[i] = u32x4_t{v, v, v, v};
     }
     __syncthreads();
@@ -175,7 +179,7 @@ __global__ __launch_bounds__(512, 4) void k_gated_few(TrainArgs P, Levels lv) {
       float y = 0.0f;
 #pragma unroll
       for (int k = 0; k < kWaves; ++k) y += red[(k * 16 + m) * NR + 16 * (c >> 3) + 8 * sd + (c & 7)];
-      y *= 1.0f / kLevelUnit;
+      y *= 1.0f / kLevelUnit<BITS>;
       if (P.r > 0)
         y = fmaf(P.scale, ad[sd].dot(ad_lds + sd * Adapter::kBytes, P.t + sd * tside, P.t_splits, P.M, 0, m,
                                      P.ab + (int64_t)sd * N * P.r, n0, c, P.r), y);
